@@ -274,8 +274,8 @@ def _truncate(st, new):
 
 
 def _reserve(st, n):
-    """Room for n more tokens in every stream, lowest free pages first; a partly filled page that others hold too is
-    copied, unless its writers alone hold it and this is the first of them."""
+    """Room for n more tokens in every stream, lowest free pages first; the tokens of a partly filled page that others
+    hold too are copied to a page of the stream's own, unless its writers alone hold it and this is the first of them."""
     table, page, length, held, ref = (st[k] for k in ("table", "page", "length", "held", "refcount"))
     S, MP = table.shape
     j = torch.arange(MP, device="cuda")[None, :]
@@ -299,7 +299,8 @@ def _reserve(st, n):
     ref.scatter_add_(0, table.clamp(min=0).long().view(-1), fresh.int().view(-1))
     held.copy_(torch.maximum(held, need))
     dst = table.gather(1, last.clamp(max=MP - 1).long()[:, None])[:, 0][copy].long()
-    st["pool"][:, :, dst] = st["pool"][:, :, src]
+    filled = torch.arange(page, device="cuda")[None, :] < (length % page)[copy][:, None]
+    st["pool"][:, :, dst] = torch.where(filled[:, None, :, None], st["pool"][:, :, src], st["pool"][:, :, dst])
 
 
 def _append(st):
@@ -472,7 +473,7 @@ class _Book:
                 w = writers[p]
                 if held_by[p] > 1 and not (held_by[p] == len(w) and w[0] == s):
                     to = free.pop()
-                    self.pool[:, :, to] = self.pool[:, :, p]
+                    self.pool[:, :, to, :, :m % self.page] = self.pool[:, :, p, :, :m % self.page]
                     self.ref[p] -= 1
                     self.ref[to] += 1
                     self.table[s][i] = to
