@@ -83,6 +83,10 @@ extern "C" {
 #define MOE_ERR_WORKSPACE   (-6) /* workspace NULL, misaligned (256 B) or too small; on the device:
                                       its state section was overwritten between forwards */
 
+#define MOE_ERR_CACHE_FULL  (-7) /* on the device: fewer free pages than a cache call needs */
+#define MOE_ERR_CACHE_STATE (-8) /* on the device: a cache call its books do not allow (a position that was not
+                                      reserved, a shared or unknown page, a stream that is not empty, ...) */
+
 /* ---- config flags ------------------------------------------------------- */
 #define MOE_FLAG_NORM         (1u << 0) /* pre-norm residual stack (see above) */
 #define MOE_FLAG_OUT_BF16     (1u << 1) /* y is bf16 instead of fp32 */
@@ -322,6 +326,157 @@ int moe_mxfp4_quantize(const float* w_dev, int64_t rows, int64_t cols, uint8_t* 
 int moe_mxfp4_accept(const float* logits_dev, const int32_t* tokens_dev, int32_t num_streams, int32_t block,
                      int64_t vocab, int32_t* target_dev, int32_t* accepted_dev, int32_t* next_token_dev,
                      void* stream);
+
+/* ---- paged key/value cache of a verify forward --------------------------------------
+ * The attention of a verify forward reads, for every stream of the batch, the keys and
+ * values of all tokens it has so far.  They live in pages of a pool that the caller owns;
+ * streams that begin with the same tokens hold the same pages.  A forward of S streams
+ * x B block positions (the block that moe_mxfp4_accept judges) is, on one cache:
+ *   moe_mxfp4_cache_reserve(B)            room for the block, in pages of the stream's own
+ *   per layer: moe_mxfp4_cache_append     the block's keys and values into the pages
+ *              moe_mxfp4_cache_attend     the block's attention over context and block
+ *              moe_mxfp4_forward ...      the MoE layer
+ *   moe_mxfp4_accept -> moe_mxfp4_cache_commit(accepted)   keep the accepted positions
+ * moe_mxfp4_cache_fork starts a stream from another one's tokens without copying them,
+ * moe_mxfp4_cache_truncate shortens or empties streams, and moe_mxfp4_cache_compact moves
+ * the pages in use to the front of the pool.
+ *
+ * Pools: per layer a K and a V pool, [num_pages] pages of [kv_heads, page_tokens, head_dim]
+ * (contiguous; one head's page is one run of memory, read by one copy), page_stride
+ * elements apart, 16-byte aligned, BORROWED until moe_mxfp4_cache_destroy.
+ *
+ * State: int32 words in one device buffer that the caller owns (16-byte aligned,
+ * moe_mxfp4_cache_state_bytes long).  All zero = an empty cache.  With S = num_streams,
+ * M = max_pages, P = num_pages:
+ *   [0]               status code, [1] its detail; [2..15] the library's
+ *   [16, +S)          length: tokens stored per stream
+ *   [.., +S)          held: pages held per stream (at least ceil(length / page_tokens))
+ *   [.., +S*M)        page table: page of the stream's tokens i * page_tokens .., for
+ *                     i < held; entries behind held are not read (given back: -1)
+ *   [.., +P)          refcount: page table entries that hold the page; 0 = free
+ *   the rest          the library's
+ * A caller may write the first four itself between calls (a scheduler with its own page
+ * tables); two tables that hold one page at the same index must then agree in all
+ * entries before it, as they do when only the calls below made them.
+ *
+ * The books change in the order of the stream: every call takes effect as if it ran
+ * alone.  What a call finds wrong on the device (too few free pages, a table entry
+ * outside the pool) is recorded in the status words (the first error is kept until
+ * moe_mxfp4_cache_check) and nothing outside the pools and the state is touched.  Results
+ * do not depend on the timing of threads: two runs of the same calls give the same bits.
+ * A cache (state and workspace) may be used by one stream at a time, captured graphs
+ * included.  Calls run on the handle's device, whichever device is current.  No call
+ * allocates device memory or synchronises, but moe_mxfp4_cache_check. */
+
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+
+typedef struct moe_mxfp4_cache moe_mxfp4_cache; /* opaque, host-side */
+
+typedef struct {
+    int32_t num_layers;   /* 1..1024 */
+    int32_t num_streams;  /* S, 1..65536 */
+    int32_t max_pages;    /* M, pages a stream can hold, >= 1; M * page_tokens below 2^30 */
+    int32_t num_pages;    /* P, 1..2^24 */
+    int32_t page_tokens;  /* 16, 32, 64 or 128 */
+    int32_t kv_heads;     /* 1..256 */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t dtype;        /* MOE_DTYPE_*: of the pools, the queries and the outputs */
+    int64_t page_stride;  /* elements between pages of a pool, a multiple of 8, at least
+                           * kv_heads * page_tokens * head_dim; 0 = exactly that */
+    int32_t timeout_us;   /* bound of every device-side wait in microseconds; 0 = default (200000) */
+} moe_mxfp4_cache_config;
+
+typedef struct {
+    void* k_dev;          /* [P] pages of [kv_heads, page_tokens, head_dim] */
+    void* v_dev;
+} moe_mxfp4_cache_layer;
+
+/* Validates the config and the pools (alignment, device memory, an sm_103 device
+ * current, which becomes the handle's) and makes a handle.  layers: num_layers
+ * descriptors (host memory, copied). */
+int moe_mxfp4_cache_create(const moe_mxfp4_cache_config* cfg, const moe_mxfp4_cache_layer* layers,
+                           moe_mxfp4_cache** out);
+void moe_mxfp4_cache_destroy(moe_mxfp4_cache* c); /* NULL is ignored */
+int moe_mxfp4_cache_state_bytes(const moe_mxfp4_cache* c, size_t* bytes);
+
+/* Makes room for add[s] more tokens in every stream (add_dev: int32 [S], or NULL: `add`
+ * tokens in each; a stream with none, or less, is left alone): it then holds
+ * ceil((length + add) / page_tokens) pages at least.  New pages are taken lowest free
+ * first, for the streams in order.  When the stream's last page is partly filled and
+ * other table entries hold it too, its filled tokens are copied (in every layer) to a new
+ * page first; of the streams of one call that write to the same page and are its only
+ * holders, the first keeps it.  All or nothing: MOE_ERR_CACHE_FULL (detail: pages that
+ * were needed) or MOE_ERR_CACHE_STATE (detail: a stream that would pass max_pages or
+ * whose table is out of the pool) is recorded, and no stream gets a page. */
+int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* add_dev, int32_t add, void* stream);
+
+/* Writes a block's keys and values of one layer: token i < n_s of stream s < streams goes
+ * to position length[s] + i, n_s = lengths_dev ? min(lengths_dev[s], block) : block.
+ * k_dev, v_dev: [streams, block, kv_heads, head_dim], 16-byte aligned, `row_stride`
+ * elements between tokens (a multiple of 8; 0 = kv_heads * head_dim).  length is not
+ * changed.  A position that is not reserved, or whose page other streams hold too, is
+ * skipped, with MOE_ERR_CACHE_STATE (detail: the stream). */
+int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const void* k_dev, const void* v_dev,
+                           int64_t row_stride, int32_t streams, int32_t block, const int32_t* lengths_dev,
+                           void* stream);
+
+/* Sets length[s] to new_length[s] (int32 [S]; negative: the stream is left alone) and
+ * gives back the pages behind it.  A length beyond the pages held is refused for that
+ * stream, with MOE_ERR_CACHE_STATE.  commit is the same with length[s] + accepted[s]
+ * (moe_mxfp4_accept's output; 0 drops the whole block, negative: left alone). */
+int moe_mxfp4_cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* new_length_dev, void* stream);
+int moe_mxfp4_cache_commit(moe_mxfp4_cache* c, void* state_dev, const int32_t* accepted_dev, void* stream);
+
+/* For i < n: the empty stream dst[i] (no pages held) gets src[i]'s tokens, by holding the
+ * same ceil(length / page_tokens) pages.  src and dst are int32 device arrays.  A stream
+ * may be src several times.  All or nothing: MOE_ERR_CACHE_STATE (detail: i) for a number
+ * outside [0, S), a dst that holds pages, appears twice or is also a src. */
+int moe_mxfp4_cache_fork(moe_mxfp4_cache* c, void* state_dev, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
+                         void* stream);
+
+/* With U pages in use: moves those at U and above, ascending, into the free ones below U,
+ * ascending (keys and values of every layer, counts, and every table entry), so that the
+ * pages in use are 0..U-1.  At most one copy of each page. */
+int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
+
+/* Attention of a block, one layer.  Query row (s, b, h) of stream s < streams, position
+ * b < n_s (as in append; the block's keys were appended, length is not yet committed),
+ * head h reads kv head h / (q_heads / kv_heads) and sees the key at position j
+ *   if j < length[s], or
+ *   if j = length[s] + i and i <= b (causal), or, with mask_dev, bit i of mask[s, b].
+ * out = sum_j softmax_j(scale * q.k_j) v_j over the keys it sees, lse = ln sum_j
+ * exp(scale * q.k_j); a row that sees nothing has out = 0, lse = -inf.  Rows of positions
+ * n_s and behind are left as they were.  Keys that a row does not see have no part in
+ * it, whatever their bits (NaN and infinities among them).
+ * shared_tokens (a multiple of page_tokens, 0 = none): the first tokens of stream slot
+ * shared_stream, read once for all the streams that hold the same pages (forked from it,
+ * directly or not); a stream with other pages there, or with fewer tokens, reads its own.
+ * Arithmetic: products of q and k are exact and summed in fp32, as are the statistics of
+ * the softmax; its terms are rounded to the cache's type for their product with v, which
+ * is summed in fp32.
+ * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents. */
+typedef struct {
+    const void* q_dev;           /* [streams, block, q_heads, head_dim], 16-byte aligned */
+    int64_t q_stride;            /* elements between tokens, a multiple of 8; 0 = q_heads * head_dim */
+    void* out_dev;               /* [streams, block, q_heads, head_dim], contiguous, 16-byte aligned */
+    float* lse_dev;              /* [streams, block, q_heads] or NULL */
+    const int32_t* lengths_dev;  /* [streams] or NULL */
+    const uint64_t* mask_dev;    /* [streams, block] or NULL; needs block <= 64 */
+    int32_t streams, block;      /* S_q <= num_streams; block >= 1; streams * block * q_heads below 2^31 */
+    int32_t q_heads;             /* a multiple of kv_heads, at most 256 times as many */
+    int32_t shared_stream;       /* stream slot that holds the shared prefix (read when shared_tokens > 0) */
+    int32_t shared_tokens;
+    float scale;
+} moe_mxfp4_attend_args;
+int moe_mxfp4_cache_attend_bytes(const moe_mxfp4_cache* c, int32_t streams, int32_t block, int32_t q_heads,
+                                 size_t* bytes);
+int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const moe_mxfp4_attend_args* args,
+                           void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* Synchronises the stream, returns the first error recorded in the status words since
+ * they were last read (MOE_OK: none) and clears it. */
+int moe_mxfp4_cache_check(moe_mxfp4_cache* c, void* state_dev, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,8 @@ MOE_ERR_CUDA = -3
 MOE_ERR_TIMEOUT = -4
 MOE_ERR_BAD_SCALE = -5
 MOE_ERR_WORKSPACE = -6
+MOE_ERR_CACHE_FULL = -7
+MOE_ERR_CACHE_STATE = -8
 
 MOE_FLAG_NORM = 1 << 0
 MOE_FLAG_OUT_BF16 = 1 << 1
@@ -28,6 +30,9 @@ MOE_FLAG_MULTI_KERNEL = 1 << 2
 MOE_FLAG_NO_DENSE = 1 << 3
 MOE_FLAG_DEBUG_STALL = 1 << 4
 MOE_FLAG_TRACE = 1 << 5
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
 
 EXPORTED = (
     "moe_mxfp4_create",
@@ -43,6 +48,18 @@ EXPORTED = (
     "moe_mxfp4_packed_bytes",
     "moe_mxfp4_pack",
     "moe_mxfp4_split_terms",
+    "moe_mxfp4_cache_create",
+    "moe_mxfp4_cache_destroy",
+    "moe_mxfp4_cache_state_bytes",
+    "moe_mxfp4_cache_reserve",
+    "moe_mxfp4_cache_append",
+    "moe_mxfp4_cache_truncate",
+    "moe_mxfp4_cache_commit",
+    "moe_mxfp4_cache_fork",
+    "moe_mxfp4_cache_compact",
+    "moe_mxfp4_cache_attend_bytes",
+    "moe_mxfp4_cache_attend",
+    "moe_mxfp4_cache_check",
 )
 
 MOE_MXFP4_STATIC_WORKSPACE_BYTES = 16 << 20
@@ -90,6 +107,42 @@ class moe_mxfp4_debug(ctypes.Structure):
     ]
 
 
+class moe_mxfp4_cache_config(ctypes.Structure):
+    _fields_ = [
+        ("num_layers", ctypes.c_int32),
+        ("num_streams", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("timeout_us", ctypes.c_int32),
+    ]
+
+
+class moe_mxfp4_cache_layer(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p)]
+
+
+class moe_mxfp4_attend_args(ctypes.Structure):
+    _fields_ = [
+        ("q_dev", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("out_dev", ctypes.c_void_p),
+        ("lse_dev", ctypes.c_void_p),
+        ("lengths_dev", ctypes.c_void_p),
+        ("mask_dev", ctypes.c_void_p),
+        ("streams", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("shared_stream", ctypes.c_int32),
+        ("shared_tokens", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -133,6 +186,23 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_mxfp4_pack.restype = ctypes.c_int
     lib.moe_mxfp4_split_terms.argtypes = [P, ctypes.c_int64, P, P, P]
     lib.moe_mxfp4_split_terms.restype = ctypes.c_int
+    I32, I64, SIZE = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+    for name, args in (
+            ("create", [ctypes.POINTER(moe_mxfp4_cache_config), ctypes.POINTER(moe_mxfp4_cache_layer), ctypes.POINTER(P)]),
+            ("state_bytes", [P, SIZE]),
+            ("reserve", [P, P, P, I32, P]),
+            ("append", [P, P, I32, P, P, I64, I32, I32, P, P]),
+            ("truncate", [P, P, P, P]),
+            ("commit", [P, P, P, P]),
+            ("fork", [P, P, P, P, I32, P]),
+            ("compact", [P, P, P]),
+            ("attend_bytes", [P, I32, I32, I32, SIZE]),
+            ("attend", [P, P, I32, ctypes.POINTER(moe_mxfp4_attend_args), P, ctypes.c_size_t, P]),
+            ("check", [P, P, P])):
+        fn = getattr(lib, "moe_mxfp4_cache_" + name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
+    lib.moe_mxfp4_cache_destroy.argtypes = [P]
+    lib.moe_mxfp4_cache_destroy.restype = None
     _lib = lib
     return lib
 
@@ -212,6 +282,65 @@ def moe_mxfp4_pack(hidden, inter, num_experts, layer: moe_mxfp4_layer, packed_pt
 
 def moe_mxfp4_split_terms(x_ptr, n_blocks, codes_ptr, scales_ptr, stream_ptr) -> int:
     return load_library().moe_mxfp4_split_terms(x_ptr, n_blocks, codes_ptr, scales_ptr, stream_ptr)
+
+
+def moe_mxfp4_cache_create(cfg: moe_mxfp4_cache_config, layers) -> tuple[int, int]:
+    """Returns (status, handle).  layers: a sequence of moe_mxfp4_cache_layer."""
+    arr = (moe_mxfp4_cache_layer * len(layers))(*layers)
+    out = ctypes.c_void_p()
+    st = load_library().moe_mxfp4_cache_create(ctypes.byref(cfg), arr, ctypes.byref(out))
+    return st, out.value
+
+
+def moe_mxfp4_cache_destroy(cache) -> None:
+    if cache:
+        load_library().moe_mxfp4_cache_destroy(cache)
+
+
+def moe_mxfp4_cache_state_bytes(cache) -> tuple[int, int]:
+    n = ctypes.c_size_t()
+    st = load_library().moe_mxfp4_cache_state_bytes(cache, ctypes.byref(n))
+    return st, n.value
+
+
+def moe_mxfp4_cache_reserve(cache, state_ptr, add_ptr, add, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_reserve(cache, state_ptr, add_ptr, add, stream_ptr)
+
+
+def moe_mxfp4_cache_append(cache, state_ptr, layer, k_ptr, v_ptr, row_stride, streams, block, lengths_ptr,
+                           stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_append(cache, state_ptr, layer, k_ptr, v_ptr, row_stride, streams, block,
+                                                 lengths_ptr, stream_ptr)
+
+
+def moe_mxfp4_cache_truncate(cache, state_ptr, new_length_ptr, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_truncate(cache, state_ptr, new_length_ptr, stream_ptr)
+
+
+def moe_mxfp4_cache_commit(cache, state_ptr, accepted_ptr, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_commit(cache, state_ptr, accepted_ptr, stream_ptr)
+
+
+def moe_mxfp4_cache_fork(cache, state_ptr, src_ptr, dst_ptr, n, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_fork(cache, state_ptr, src_ptr, dst_ptr, n, stream_ptr)
+
+
+def moe_mxfp4_cache_compact(cache, state_ptr, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_compact(cache, state_ptr, stream_ptr)
+
+
+def moe_mxfp4_cache_attend_bytes(cache, streams, block, q_heads) -> tuple[int, int]:
+    n = ctypes.c_size_t()
+    st = load_library().moe_mxfp4_cache_attend_bytes(cache, streams, block, q_heads, ctypes.byref(n))
+    return st, n.value
+
+
+def moe_mxfp4_cache_attend(cache, state_ptr, layer, args: moe_mxfp4_attend_args, ws_ptr, ws_bytes, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_attend(cache, state_ptr, layer, ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr)
+
+
+def moe_mxfp4_cache_check(cache, state_ptr, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_check(cache, state_ptr, stream_ptr)
 
 
 # ----------------------------------------------------------------------------- torch convenience
@@ -374,6 +503,211 @@ class MoeLayers:
             moe_mxfp4_destroy(self.handle)
             self.handle = None
         self.__dict__.pop("_ws", None)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvCache:
+    """The paged key/value cache of a verify forward (moe_mxfp4.h, "paged key/value cache").
+
+    layers: a list of (k, v) pool tensors [num_pages, kv_heads, page_tokens, head_dim], bf16 or fp16 on one CUDA
+    device, contiguous within a page (all with the same stride between pages); kept alive here.  The books are views of
+    one int32 tensor: length [S], held [S], page_table [S, max_pages], refcount [num_pages].  Every call runs on
+    `stream` (a cudaStream_t as int; default: torch's current stream on the cache's device); device-side errors are
+    raised by check().
+    """
+
+    def __init__(self, *, layers, num_streams, max_pages, timeout_us=0):
+        import torch
+        self.handle = None
+        if not layers:
+            raise ValueError("layers: at least one (k, v) pair")
+        k0 = layers[0][0]
+        if not k0.is_cuda or k0.dim() != 4 or k0.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("a pool is a bf16 or fp16 CUDA tensor [num_pages, kv_heads, page_tokens, head_dim]")
+        pages, heads, tokens, dim = k0.shape
+        for pool in (p for kv in layers for p in kv):
+            if (pool.shape != k0.shape or pool.dtype != k0.dtype or pool.device != k0.device
+                    or pool.stride()[1:] != (tokens * dim, dim, 1) or (pages > 1 and pool.stride(0) != k0.stride(0))):
+                raise ValueError("the pools of a cache have one shape, type, device and page stride")
+        self._keep = layers
+        self.device, self.dtype = k0.device, k0.dtype
+        self.num_layers, self.num_streams, self.max_pages = len(layers), num_streams, max_pages
+        self.num_pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, tokens, dim
+        cfg = moe_mxfp4_cache_config(len(layers), num_streams, max_pages, pages, tokens, heads, dim,
+                                     MOE_DTYPE_BF16 if k0.dtype == torch.bfloat16 else MOE_DTYPE_FP16,
+                                     k0.stride(0) if pages > 1 else 0, timeout_us)
+        with torch.cuda.device(self.device):
+            st, self.handle = moe_mxfp4_cache_create(
+                cfg, [moe_mxfp4_cache_layer(k.data_ptr(), v.data_ptr()) for k, v in layers])
+        _check(st, "moe_mxfp4_cache_create")
+        st, n = moe_mxfp4_cache_state_bytes(self.handle)
+        _check(st, "moe_mxfp4_cache_state_bytes")
+        self.state = torch.zeros(n // 4, dtype=torch.int32, device=self.device)
+        self._state_ptr = self.state.data_ptr()
+        S, at = num_streams, 16
+        self.length, at = self.state[at:at + S], at + S
+        self.held, at = self.state[at:at + S], at + S
+        self.page_table, at = self.state[at:at + S * max_pages].view(S, max_pages), at + S * max_pages
+        self.refcount = self.state[at:at + pages]
+        self._lib = load_library()
+        self._args = moe_mxfp4_attend_args()
+        self._ws, self._ws_bytes, self._ws_kept = None, {}, []
+
+    # -- the books
+
+    def reserve(self, tokens, stream=None):
+        """Room for `tokens` more tokens: an int (in every stream) or an int32 tensor [num_streams]."""
+        if isinstance(tokens, int):
+            if not -(1 << 31) <= tokens < 1 << 31:
+                raise ValueError("tokens: a 32-bit count")
+            add, n = None, tokens
+        else:
+            add, n = self._books("tokens", tokens, self.num_streams), 0
+        _check(self._lib.moe_mxfp4_cache_reserve(self.handle, self._state_ptr, add, n, self._stream(stream)),
+               "moe_mxfp4_cache_reserve")
+
+    def commit(self, accepted, stream=None):
+        """length += accepted (int32 [num_streams]; accept()'s output); the pages behind are given back."""
+        _check(self._lib.moe_mxfp4_cache_commit(self.handle, self._state_ptr,
+                                                self._books("accepted", accepted, self.num_streams), self._stream(stream)),
+               "moe_mxfp4_cache_commit")
+
+    def truncate(self, new_length, stream=None):
+        """length = new_length (int32 [num_streams]; negative: left alone); the pages behind are given back."""
+        _check(self._lib.moe_mxfp4_cache_truncate(self.handle, self._state_ptr,
+                                                  self._books("new_length", new_length, self.num_streams),
+                                                  self._stream(stream)), "moe_mxfp4_cache_truncate")
+
+    def fork(self, src, dst, stream=None):
+        """The empty streams dst[i] get the tokens of src[i], holding the same pages (int32 tensors of one length)."""
+        if src.numel() != dst.numel():
+            raise ValueError("src and dst have one length")
+        n = src.numel()
+        _check(self._lib.moe_mxfp4_cache_fork(self.handle, self._state_ptr, self._books("src", src, n),
+                                              self._books("dst", dst, n), n, self._stream(stream)), "moe_mxfp4_cache_fork")
+
+    def compact(self, stream=None):
+        """Moves the pages in use to the front of the pool."""
+        _check(self._lib.moe_mxfp4_cache_compact(self.handle, self._state_ptr, self._stream(stream)),
+               "moe_mxfp4_cache_compact")
+
+    def check(self, stream=None):
+        """Waits for the stream; raises MoeError for the first error the device recorded, and clears it."""
+        _check(self._lib.moe_mxfp4_cache_check(self.handle, self._state_ptr, self._stream(stream)), "moe_mxfp4_cache_check")
+
+    # -- a layer's keys and values
+
+    def append(self, layer, k, v, lengths=None, stream=None):
+        """k, v: [streams, block, kv_heads, head_dim], contiguous or rows of one wider tensor (a fused projection's
+        output); lengths: int32 [streams], tokens in use of each block."""
+        S, B, H, D = self._rows("k", k)
+        if (H, D) != (self.kv_heads, self.head_dim) or v.shape != k.shape:
+            raise ValueError("k and v are [streams, block, kv_heads, head_dim]")
+        self._rows("v", v)
+        if S * B > 1 and self._row_stride(v) != self._row_stride(k):
+            raise ValueError("k and v have one stride between tokens")
+        _check(self._lib.moe_mxfp4_cache_append(self.handle, self._state_ptr, layer, k.data_ptr(), v.data_ptr(),
+                                                self._row_stride(k), S, B,
+                                                None if lengths is None else self._books("lengths", lengths, S),
+                                                self._stream(stream)), "moe_mxfp4_cache_append")
+
+    def attend(self, layer, q, lengths=None, mask=None, shared_stream=0, shared_tokens=0, scale=None, out=None, lse=None,
+               workspace=None, stream=None):
+        """Attention of a block (moe_mxfp4_cache_attend).  q: [streams, block, q_heads, head_dim], as k in append; mask:
+        int64 [streams, block], bit i = sees block position i (default: causal); scale: default 1 / sqrt(head_dim).
+        Returns (out, lse): out like q, contiguous; lse fp32 [streams, block, q_heads].  Rows that `lengths` leaves
+        out are zero in an out (lse) that is made here and unchanged in one that is given."""
+        import torch
+        S, B, H, D = self._rows("q", q)
+        if D != self.head_dim:
+            raise ValueError("q is [streams, block, q_heads, head_dim]")
+        make = torch.empty if lengths is None else torch.zeros
+        if out is None:
+            out = make((S, B, H, D), dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+            raise ValueError("out: contiguous, of q's shape and type")
+        if lse is None:
+            lse = make((S, B, H), dtype=torch.float32, device=self.device)
+        elif (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != self.device
+              or not lse.is_contiguous()):
+            raise ValueError("lse: contiguous fp32 [streams, block, q_heads]")
+        if mask is not None and (mask.shape != q.shape[:2] or mask.dtype not in (torch.int64, torch.uint64)
+                                 or mask.device != self.device or not mask.is_contiguous()):
+            raise ValueError("mask: contiguous int64 [streams, block]")
+        a = self._args
+        a.q_dev, a.q_stride, a.out_dev, a.lse_dev = q.data_ptr(), self._row_stride(q), out.data_ptr(), lse.data_ptr()
+        a.lengths_dev = None if lengths is None else self._books("lengths", lengths, S)
+        a.mask_dev = None if mask is None else mask.data_ptr()
+        a.streams, a.block, a.q_heads = S, B, H
+        a.shared_stream, a.shared_tokens = shared_stream, shared_tokens
+        a.scale = self.head_dim ** -0.5 if scale is None else scale
+        st = self._stream(stream)
+        ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else \
+            self._workspace(S, B, H)
+        _check(self._lib.moe_mxfp4_cache_attend(self.handle, self._state_ptr, layer, ctypes.byref(a), ws, n, st),
+               "moe_mxfp4_cache_attend")
+        return out, lse
+
+    def attend_bytes(self, streams, block, q_heads) -> int:
+        st, n = moe_mxfp4_cache_attend_bytes(self.handle, streams, block, q_heads)
+        _check(st, "moe_mxfp4_cache_attend_bytes")
+        return n
+
+    # -- arguments
+
+    def _stream(self, stream):
+        if stream is not None:
+            return stream
+        import torch
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _books(self, name, t, n):
+        import torch
+        if t.dtype != torch.int32 or t.device != self.device or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: {n} contiguous int32 values on {self.device}")
+        return t.data_ptr()
+
+    def _rows(self, name, t):
+        if t.dim() != 4 or t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name}: a 4-dimensional {self.dtype} tensor on {self.device}")
+        S, B, H, D = t.shape
+        st = t.stride()
+        if t.numel() and ((D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (S > 1 and B > 1 and st[0] != B * st[1])):
+            raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
+        return t.shape
+
+    @staticmethod
+    def _row_stride(t):
+        S, B, H, D = t.shape
+        if B > 1:
+            return t.stride(1)
+        return t.stride(0) if S > 1 else H * D
+
+    def _workspace(self, S, B, H):
+        """The cache's own workspace, grown when a call needs more; earlier ones are kept, since captured graphs may
+        hold their addresses."""
+        key = (S, B, H)
+        n = self._ws_bytes.get(key)
+        if n is None:
+            n = self._ws_bytes[key] = self.attend_bytes(S, B, H)
+        ws = self._ws
+        if ws is None or ws.numel() < n:
+            import torch
+            raw = torch.empty(n + 256, dtype=torch.uint8, device=self.device)
+            off = (-raw.data_ptr()) % 256
+            ws = self._ws = raw[off:off + n]
+            self._ws_kept.append(ws)
+        return ws.data_ptr(), ws.numel()
+
+    def close(self):
+        if getattr(self, "handle", None):
+            moe_mxfp4_cache_destroy(self.handle)
+            self.handle = None
 
     def __del__(self):
         try:

@@ -1,0 +1,592 @@
+// Page operations of the paged key/value cache: reserve (with copy on write), append,
+// truncate / commit, fork, compact; the handle's life cycle.
+//
+// The books (lengths, page tables, counts) are a few words per stream and page, so the
+// operations that hand out or move pages decide everything in one CTA, in the order of the
+// streams and pages (prefix sums, no atomics whose order matters); what follows from the
+// decision (copying pages in every layer, rewriting tables) is spread over the GPU by a
+// second kernel whose launch overlaps the first.  Atomics are integer sums, minima and
+// maxima, whose order cannot be seen.
+#include <cudaTypedefs.h>
+
+#include <new>
+
+#include "cache.cuh"
+
+namespace moe {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kNoStream = 0x7FFFFFFF;
+
+__device__ __forceinline__ void cache_error(const CacheView& c, int code, int detail) {
+    raise_status(c.state + kCacheStatus, code, detail);
+}
+
+// Exclusive prefix sum over the CTA's kPlanThreads threads; *total: the CTA's sum.
+__device__ __forceinline__ long long block_scan(long long v, long long* total) {
+    __shared__ long long sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        long long t = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, t, o);
+            if (lane >= o) t += y;
+        }
+        sums[lane] = t;
+    }
+    __syncthreads();
+    const long long before = (warp ? sums[warp - 1] : 0) + x - v;
+    *total = sums[31];
+    __syncthreads();
+    return before;
+}
+
+// ---- reserve -------------------------------------------------------------------------
+
+// One CTA.  Every stream's wish; the writers of each shared page; the pages wanted in all;
+// as many free pages, lowest first; and, when there are enough, the books.
+__global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c, const int* __restrict__ add, int add_all) {
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, S = c.L.S, P = c.L.P;
+    int* const writers = c.state + c.L.writers;
+    int* const first = c.state + c.L.first;
+    int* const ref = c.refcount();
+    int* const fl = c.state + c.L.free_list;
+    int* const need = c.state + c.L.need;
+    int* const last = c.state + c.L.last;
+    int* const off = c.state + c.L.off;
+    int* const mv_src = c.state + c.L.move_src;
+    if (tid == 0) s_bad = kNoStream;
+    __syncthreads();
+    for (int s = tid; s < S; s += kPlanThreads) {
+        const int len = c.length()[s], held = c.held()[s], n = add ? add[s] : add_all;
+        int want = held, page = -1;
+        if (n > 0) {
+            const long long tokens = (long long)len + n;
+            bool bad = len < 0 || held < 0 || held > c.L.M || tokens > ((long long)c.L.M << c.page_shift) ||
+                       len > ((long long)held << c.page_shift);
+            if (!bad) {
+                want = max(held, (int)((tokens + c.page - 1) >> c.page_shift));
+                if (len & (c.page - 1)) {
+                    page = c.table(s)[len >> c.page_shift];
+                    bad = (unsigned)page >= (unsigned)P;
+                }
+            }
+            if (bad) {
+                atomicMin(&s_bad, s);
+                want = held;
+                page = -1;
+            }
+        }
+        if (page >= 0 && ref[page] > 1) {
+            atomicAdd(writers + page, 1);
+            atomicMax(first + page, S - s);
+        } else {
+            page = -1;
+        }
+        need[s] = want;
+        last[s] = page < 0 ? -1 : 2 * page;
+    }
+    __syncthreads();
+    // Whether a stream copies its last page: its writers do, but the first of them where
+    // they are its only holders.  Pages and copies are summed in the order of the streams.
+    long long total = 0;
+    int moves = 0;
+    for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int want = 0, copy = 0;
+        if (s < S) {
+            const int page = last[s] >> 1;
+            if (last[s] >= 0) copy = !(ref[page] == writers[page] && first[page] == S - s);
+            want = need[s] - c.held()[s] + copy;
+        }
+        long long sum;
+        const long long at = block_scan(((long long)want << 20) | copy, &sum);
+        if (s < S) {
+            off[s] = (int)min(total + (at >> 20), (long long)P);
+            if (copy) {
+                last[s] |= 1;
+                mv_src[moves + (int)(at & 0xFFFFF)] = s;
+            }
+        }
+        total += sum >> 20;
+        moves += (int)(sum & 0xFFFFF);
+    }
+    bool ok = s_bad == kNoStream;
+    long long found = 0;
+    if (ok && total <= P) {
+        for (int p0 = 0; p0 < P && found < total; p0 += 4 * kPlanThreads) {
+            const int p = p0 + 4 * tid;
+            bool r[4];
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r[i] = p + i < P && ref[p + i] == 0;
+                n += r[i];
+            }
+            long long sum;
+            long long at = found + block_scan(n, &sum);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r[i]) {
+                    if (at < total) fl[at] = p + i;
+                    ++at;
+                }
+            found += sum;
+        }
+    }
+    if (tid == 0) {
+        if (!ok) cache_error(c, MOE_ERR_CACHE_STATE, s_bad);
+        else if (found < total) cache_error(c, MOE_ERR_CACHE_FULL, (int)min(total, (long long)kNoStream));
+        c.state[kCacheMoves] = ok && found >= total ? moves : 0;
+    }
+    ok = ok && found >= total;
+    __syncthreads();
+    for (int s = tid; s < S; s += kPlanThreads)
+        if (last[s] >= 0) {                       // the marks back to rest
+            writers[last[s] >> 1] = 0;
+            first[last[s] >> 1] = 0;
+        }
+    if (!ok) return;
+    for (int m = tid; m < moves; m += kPlanThreads) {
+        const int s = mv_src[m], len = c.length()[s], old = last[s] >> 1, to = fl[off[s]];
+        mv_src[m] = old;
+        c.state[c.L.move_dst + m] = to;
+        c.state[c.L.move_used + m] = len & (c.page - 1);
+        c.table(s)[len >> c.page_shift] = to;
+        atomicSub(ref + old, 1);
+    }
+    for (int i = tid; i < (int)total; i += kPlanThreads) ref[fl[i]] = 1;
+    const int lane = tid & 31;
+    for (int s = tid >> 5; s < S; s += kPlanThreads / 32) {   // a warp per stream
+        const int held = c.held()[s], n = need[s];
+        const int* from = fl + off[s] + (last[s] >= 0 ? last[s] & 1 : 0);
+        for (int i = held + lane; i < n; i += 32) c.table(s)[i] = from[i - held];
+        __syncwarp();
+        if (lane == 0 && n > held) c.held()[s] = n;
+    }
+}
+
+// ---- copying pages -------------------------------------------------------------------
+
+constexpr int kMaxPools = 256;    // pools of one launch (2 KB of kernel parameters)
+struct PoolList {
+    void* base[kMaxPools];
+};
+
+constexpr int kCopyThreads = 512;
+constexpr int kPiece = 4096;      // bytes a warp copies at a time: 8 independent 16-byte loads per lane
+
+// move_src[m] -> move_dst[m] in every pool of the list, the first move_used[m] tokens of
+// every head.  A warp takes pieces of one head's page.
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, __grid_constant__ const PoolList pools, int n_pools) {
+    grid_dependency_wait();
+    const int moves = c.state[kCacheMoves];
+    const int row = c.D * 2, head = c.page * row;            // bytes of a token, of a head's page
+    const int pieces = (head + kPiece - 1) / kPiece;
+    const long long n = (long long)moves * n_pools * c.Hkv * pieces;
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
+    for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < n; u += warps) {
+        long long w = u;
+        const int piece = (int)(w % pieces); w /= pieces;
+        const int h = (int)(w % c.Hkv); w /= c.Hkv;
+        const int pool = (int)(w % n_pools);
+        const int m = (int)(w / n_pools);
+        const int bytes = c.state[c.L.move_used + m] * row;
+        char* const base = static_cast<char*>(pools.base[pool]);
+        const int64_t at = (int64_t)h * head + (int64_t)piece * kPiece;
+        const uint4* src = reinterpret_cast<const uint4*>(base + c.state[c.L.move_src + m] * c.page_stride * 2 + at);
+        uint4* dst = reinterpret_cast<uint4*>(base + c.state[c.L.move_dst + m] * c.page_stride * 2 + at);
+        const int left = (min(bytes, (piece + 1) * kPiece) - piece * kPiece) / 16;   // 16-byte words of this piece
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * 32 + lane < left) v[i] = __ldcs(src + i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * 32 + lane < left) __stcs(dst + i * 32 + lane, v[i]);
+    }
+}
+
+// ---- append --------------------------------------------------------------------------
+
+// A thread per 16 bytes of a token's keys (y = 0) or values (y = 1).
+__global__ void __launch_bounds__(256) cache_append_kernel(CacheView c, const char* __restrict__ k, const char* __restrict__ v,
+                                                           int64_t row_bytes, char* __restrict__ kp, char* __restrict__ vp,
+                                                           int streams, int block, const int* __restrict__ lengths) {
+    const int per_head = c.D / 8, per_token = c.Hkv * per_head;
+    const int64_t n = (int64_t)streams * block * per_token;
+    const char* src = blockIdx.y ? v : k;
+    char* const dst = blockIdx.y ? vp : kp;
+    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < n; u += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t tok = u / per_token;
+        const int w = (int)(u - tok * per_token), h = w / per_head, x = w - h * per_head;
+        const int s = (int)(tok / block), i = (int)(tok - (int64_t)s * block);
+        if (lengths && i >= lengths[s]) continue;
+        const int len = c.length()[s];
+        const int64_t pos = (int64_t)len + i, at = pos >> c.page_shift;
+        int page = -1;
+        if (len >= 0 && at < c.held()[s] && at < c.L.M) page = c.table(s)[at];
+        if ((unsigned)page >= (unsigned)c.L.P || c.refcount()[page] > 1) {
+            if (w == 0) cache_error(c, MOE_ERR_CACHE_STATE, s);
+            continue;
+        }
+        const uint4 val = __ldg(reinterpret_cast<const uint4*>(src + tok * row_bytes + (int64_t)w * 16));
+        const int64_t e = page * c.page_stride + ((int64_t)h * c.page + (pos & (c.page - 1))) * c.D + x * 8;
+        *reinterpret_cast<uint4*>(dst + e * 2) = val;
+    }
+}
+
+// ---- truncate, commit ----------------------------------------------------------------
+
+// A warp per stream: gives back the pages behind its new length.
+__global__ void __launch_bounds__(256) cache_truncate_kernel(CacheView c, const int* __restrict__ value, int relative) {
+    const int s = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (s >= c.L.S || value[s] < 0) return;
+    const int len = c.length()[s], held = c.held()[s];
+    const long long to = (long long)value[s] + (relative ? len : 0);
+    if (len < 0 || held < 0 || held > c.L.M || to > ((long long)held << c.page_shift)) {
+        if (lane == 0) cache_error(c, MOE_ERR_CACHE_STATE, s);
+        return;
+    }
+    const int keep = (int)((to + c.page - 1) >> c.page_shift);
+    for (int i = keep + lane; i < held; i += 32) {
+        const int p = c.table(s)[i];
+        if ((unsigned)p < (unsigned)c.L.P) atomicSub(c.refcount() + p, 1);
+        else cache_error(c, MOE_ERR_CACHE_STATE, s);
+        c.table(s)[i] = -1;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        c.length()[s] = (int)to;
+        if (keep < held) c.held()[s] = keep;
+    }
+}
+
+// ---- fork ----------------------------------------------------------------------------
+
+// A CTA per pair.  Every CTA checks the whole list (against the lengths and the pages held,
+// which no CTA changes before all are done), so that all or none take effect; the last CTA
+// to finish writes the lengths and the pages held.
+__global__ void __launch_bounds__(256) cache_fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ dst, int n) {
+    extern __shared__ unsigned taken[];          // a bit per stream: it is a dst
+    __shared__ int s_bad, s_last;
+    const int tid = threadIdx.x, S = c.L.S;
+    for (int i = tid; i < (S + 31) / 32; i += 256) taken[i] = 0;
+    if (tid == 0) s_bad = kNoStream;
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+        const int a = src[i], b = dst[i];
+        bool bad = (unsigned)a >= (unsigned)S || (unsigned)b >= (unsigned)S;
+        if (!bad) {
+            const int len = c.length()[a], held = c.held()[a];
+            bad = c.held()[b] != 0 || len < 0 || held > c.L.M || len > ((long long)held << c.page_shift);
+            if (atomicOr(taken + (b >> 5), 1u << (b & 31)) >> (b & 31) & 1u) bad = true;   // twice
+        }
+        if (bad) atomicMin(&s_bad, i);
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+        const int a = src[i];
+        if ((unsigned)a < (unsigned)S && (taken[a >> 5] >> (a & 31) & 1u)) atomicMin(&s_bad, i);
+    }
+    __syncthreads();
+    const bool ok = s_bad == kNoStream;
+    if (ok) {
+        const int a = src[blockIdx.x], b = dst[blockIdx.x];
+        const int pages = (c.length()[a] + c.page - 1) >> c.page_shift;
+        for (int i = tid; i < pages; i += 256) {
+            const int p = c.table(a)[i];
+            c.table(b)[i] = p;
+            if ((unsigned)p < (unsigned)c.L.P) atomicAdd(c.refcount() + p, 1);
+            else cache_error(c, MOE_ERR_CACHE_STATE, blockIdx.x);
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(c.state + kCacheArrived, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    if (ok)
+        for (int i = tid; i < n; i += 256) {
+            const int len = c.length()[src[i]];
+            c.length()[dst[i]] = len;
+            c.held()[dst[i]] = (len + c.page - 1) >> c.page_shift;
+        }
+    if (tid == 0) {
+        c.state[kCacheArrived] = 0;
+        if (!ok) cache_error(c, MOE_ERR_CACHE_STATE, s_bad);
+    }
+}
+
+// ---- compact -------------------------------------------------------------------------
+
+// One CTA.  U = pages in use; the i-th used page at U or above goes to the i-th free one
+// below U (there are as many of one as of the other).
+__global__ void __launch_bounds__(kPlanThreads) cache_compact_kernel(CacheView c) {
+    const int tid = threadIdx.x, P = c.L.P;
+    int* const ref = c.refcount();
+    int* const to = c.state + c.L.free_list;     // old page -> new page, for the pages that move
+    int* const src = c.state + c.L.move_src;
+    int* const dst = c.state + c.L.move_dst;
+    long long sum;
+    int mine = 0;
+    for (int p = tid; p < P; p += kPlanThreads) mine += ref[p] != 0;
+    block_scan(mine, &sum);
+    const int U = (int)sum;
+    int n_src = 0, n_dst = 0;
+    for (int p0 = 0; p0 < P; p0 += kPlanThreads) {
+        const int p = p0 + tid;
+        const bool used = p < P && ref[p] != 0;
+        const bool up = used && p >= U, hole = p < U && !used;
+        const long long at = block_scan(((long long)up << 32) | hole, &sum);
+        if (up) src[n_src + (int)(at >> 32)] = p;
+        if (hole) dst[n_dst + (int)(at & 0xFFFFFFFF)] = p;
+        n_src += (int)(sum >> 32);
+        n_dst += (int)(sum & 0xFFFFFFFF);
+    }
+    __syncthreads();
+    for (int m = tid; m < n_src; m += kPlanThreads) {
+        const int a = src[m], b = dst[m];
+        to[a] = b;
+        c.state[c.L.move_used + m] = c.page;
+        ref[b] = ref[a];
+        ref[a] = 0;
+    }
+    if (tid == 0) {
+        c.state[kCacheMoves] = n_src;
+        c.state[kCacheLive] = U;
+    }
+}
+
+// The tables after a compact: entries at U or above have moved.
+__global__ void __launch_bounds__(256) cache_remap_kernel(CacheView c) {
+    grid_dependency_wait();
+    const int U = c.state[kCacheLive];
+    const int* to = c.state + c.L.free_list;
+    for (int s = blockIdx.x; s < c.L.S; s += gridDim.x) {
+        const int held = min(c.held()[s], c.L.M);
+        for (int i = threadIdx.x; i < held; i += 256) {
+            const int p = c.table(s)[i];
+            if (p >= U && p < c.L.P) c.table(s)[i] = to[p];
+            else if ((unsigned)p >= (unsigned)c.L.P) cache_error(c, MOE_ERR_CACHE_STATE, s);
+        }
+    }
+}
+
+}  // namespace moe
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool good_state(const moe_mxfp4_cache* c, const void* state) { return c && state && aligned16(state); }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+bool device_memory(const void* p, int device) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == device);
+}
+
+// A pool as a tensor of [pages][kv_heads * page_tokens][head_dim] 16-bit elements, read in
+// boxes of one head's page (up to 128 tokens) x 64 elements, in the 128-byte swizzle.
+bool encode_pool(CUtensorMap* m, const void* base, const moe_mxfp4_cache_config& c) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.kv_heads * c.page_tokens, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, (cuuint64_t)c.page_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)c.page_tokens, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return enc(m, c.dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// Copies the pages of the move list in every pool, kMaxPools pools a launch.
+int launch_copies(const moe_mxfp4_cache* c, const moe::CacheView& v, cudaStream_t st) {
+    for (int l0 = 0; l0 < c->cfg.num_layers; l0 += moe::kMaxPools / 2) {
+        moe::PoolList pools = {};
+        int n = 0;
+        for (int l = l0; l < c->cfg.num_layers && n < moe::kMaxPools; ++l) {
+            pools.base[n++] = c->layers[l].k_dev;
+            pools.base[n++] = c->layers[l].v_dev;
+        }
+        if (moe::launch_dependent(moe::cache_copy_kernel, dim3(4 * c->sm_count), dim3(moe::kCopyThreads), 0, st, v, pools,
+                                  n) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_mxfp4_cache_create(const moe_mxfp4_cache_config* cfg, const moe_mxfp4_cache_layer* layers, moe_mxfp4_cache** out) {
+    if (!cfg || !layers || !out) return MOE_ERR_INVALID_ARG;
+    *out = nullptr;
+    moe_mxfp4_cache_config c = *cfg;
+    if (c.num_layers < 1 || c.num_layers > 1024 || c.num_streams < 1 || c.num_streams > 65536) return MOE_ERR_INVALID_ARG;
+    if (c.num_pages < 1 || c.num_pages > (1 << 24)) return MOE_ERR_INVALID_ARG;
+    if (c.page_tokens != 16 && c.page_tokens != 32 && c.page_tokens != 64 && c.page_tokens != 128) return MOE_ERR_INVALID_ARG;
+    if (c.max_pages < 1 || (int64_t)c.max_pages * c.page_tokens >= (1 << 30)) return MOE_ERR_INVALID_ARG;
+    if (c.kv_heads < 1 || c.kv_heads > 256) return MOE_ERR_INVALID_ARG;
+    if (c.head_dim != 64 && c.head_dim != 128) return MOE_ERR_INVALID_ARG;
+    if (c.dtype != MOE_DTYPE_BF16 && c.dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
+    const int64_t page = (int64_t)c.kv_heads * c.page_tokens * c.head_dim;
+    if (c.page_stride == 0) c.page_stride = page;
+    if (c.page_stride < page || c.page_stride % 8 || c.page_stride >= ((int64_t)1 << 38)) return MOE_ERR_INVALID_ARG;
+    if (c.timeout_us < 0) return MOE_ERR_INVALID_ARG;
+    if (c.timeout_us == 0) c.timeout_us = 200000;
+    for (int l = 0; l < c.num_layers; ++l)
+        if (!layers[l].k_dev || !layers[l].v_dev || !aligned16(layers[l].k_dev) || !aligned16(layers[l].v_dev))
+            return MOE_ERR_INVALID_ARG;
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+    for (int l = 0; l < c.num_layers; ++l)
+        if (!device_memory(layers[l].k_dev, dev) || !device_memory(layers[l].v_dev, dev)) return MOE_ERR_INVALID_ARG;
+    try {
+        moe_mxfp4_cache* h = new moe_mxfp4_cache();
+        h->cfg = c;
+        h->device = dev;
+        h->sm_count = sms;
+        h->layers.assign(layers, layers + c.num_layers);
+        h->maps.resize(2 * (size_t)c.num_layers);
+        for (int l = 0; l < c.num_layers; ++l)
+            if (!encode_pool(&h->maps[2 * l], layers[l].k_dev, c) || !encode_pool(&h->maps[2 * l + 1], layers[l].v_dev, c)) {
+                delete h;
+                return MOE_ERR_CUDA;
+            }
+        *out = h;
+    } catch (...) {
+        return MOE_ERR_INVALID_ARG;
+    }
+    return MOE_OK;
+}
+
+void moe_mxfp4_cache_destroy(moe_mxfp4_cache* c) { delete c; }
+
+int moe_mxfp4_cache_state_bytes(const moe_mxfp4_cache* c, size_t* bytes) {
+    if (!c || !bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)moe::cache_layout(c->cfg.num_streams, c->cfg.max_pages, c->cfg.num_pages).total * 4;
+    return MOE_OK;
+}
+
+int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* add_dev, int32_t add, void* stream) {
+    if (!good_state(c, state_dev) || !aligned4(add_dev)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const moe::CacheView v = moe::cache_view(c, state_dev);
+    moe::cache_reserve_kernel<<<1, moe::kPlanThreads, 0, st>>>(v, add_dev, add);
+    if (const int r = launch_copies(c, v, st)) return r;
+    return launched();
+}
+
+int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const void* k_dev, const void* v_dev,
+                           int64_t row_stride, int32_t streams, int32_t block, const int32_t* lengths_dev, void* stream) {
+    if (!good_state(c, state_dev) || layer < 0 || layer >= c->cfg.num_layers) return MOE_ERR_INVALID_ARG;
+    if (streams < 0 || streams > c->cfg.num_streams || block < 0 || !aligned4(lengths_dev)) return MOE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)c->cfg.kv_heads * c->cfg.head_dim;
+    if (row_stride == 0) row_stride = row;
+    if (row_stride < row || row_stride % 8) return MOE_ERR_INVALID_ARG;
+    if (streams == 0 || block == 0) return MOE_OK;
+    if (!k_dev || !v_dev || !aligned16(k_dev) || !aligned16(v_dev)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    const int64_t n = (int64_t)streams * block * (row / 8);
+    const int64_t want = (n + 255) / 256, most = 32 * (int64_t)c->sm_count;
+    moe::cache_append_kernel<<<dim3((unsigned)(want < most ? want : most), 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        moe::cache_view(c, state_dev), static_cast<const char*>(k_dev), static_cast<const char*>(v_dev), row_stride * 2,
+        static_cast<char*>(c->layers[layer].k_dev), static_cast<char*>(c->layers[layer].v_dev), streams, block, lengths_dev);
+    return launched();
+}
+
+static int cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* value, int relative, void* stream) {
+    if (!good_state(c, state_dev) || !value || !aligned4(value)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    moe::cache_truncate_kernel<<<(c->cfg.num_streams + 7) / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        moe::cache_view(c, state_dev), value, relative);
+    return launched();
+}
+
+int moe_mxfp4_cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* new_length_dev, void* stream) {
+    return cache_truncate(c, state_dev, new_length_dev, 0, stream);
+}
+
+int moe_mxfp4_cache_commit(moe_mxfp4_cache* c, void* state_dev, const int32_t* accepted_dev, void* stream) {
+    return cache_truncate(c, state_dev, accepted_dev, 1, stream);
+}
+
+int moe_mxfp4_cache_fork(moe_mxfp4_cache* c, void* state_dev, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
+                         void* stream) {
+    if (!good_state(c, state_dev) || n < 0 || n > c->cfg.num_streams) return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    if (!src_dev || !dst_dev || !aligned4(src_dev) || !aligned4(dst_dev)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    const size_t smem = (size_t)((c->cfg.num_streams + 31) / 32) * 4;
+    moe::cache_fork_kernel<<<n, 256, smem, static_cast<cudaStream_t>(stream)>>>(moe::cache_view(c, state_dev), src_dev,
+                                                                              dst_dev, n);
+    return launched();
+}
+
+int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream) {
+    if (!good_state(c, state_dev)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const moe::CacheView v = moe::cache_view(c, state_dev);
+    moe::cache_compact_kernel<<<1, moe::kPlanThreads, 0, st>>>(v);
+    if (const int r = launch_copies(c, v, st)) return r;
+    const int S = c->cfg.num_streams;
+    if (moe::launch_dependent(moe::cache_remap_kernel, dim3(S < 4096 ? S : 4096), dim3(256), 0, st, v) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launched();
+}
+
+int moe_mxfp4_cache_check(moe_mxfp4_cache* c, void* state_dev, void* stream) {
+    if (!good_state(c, state_dev)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int s[2] = {0, 0};
+    if (cudaMemcpyAsync(s, state_dev, sizeof(s), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (s[0] == MOE_OK) return MOE_OK;
+    if (cudaMemsetAsync(state_dev, 0, sizeof(s), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return s[0];
+}
+
+}  // extern "C"

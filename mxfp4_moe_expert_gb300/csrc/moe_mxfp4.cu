@@ -535,6 +535,8 @@ const char* moe_mxfp4_status_string(int s) {
         case MOE_ERR_TIMEOUT: return "device-side wait timed out";
         case MOE_ERR_BAD_SCALE: return "E8M0 scale byte 0xFF (NaN) in a routed expert";
         case MOE_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+        case MOE_ERR_CACHE_FULL: return "not enough free cache pages";
+        case MOE_ERR_CACHE_STATE: return "cache call that the cache's books do not allow";
         default: return "unknown status";
     }
 }

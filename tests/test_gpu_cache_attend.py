@@ -1,0 +1,363 @@
+"""GPU tests of the verify block's attention over the paged cache, against the definition in 64 bits; the tolerance is
+what the stated arithmetic allows, element by element (tests/cache_util.py)."""
+import math
+import os
+import random
+
+import pytest
+import torch
+
+import mxfp4_moe_expert_gb300 as pkg
+from cache_util import Books, assert_attention, ceil_div, gather, write_books
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    if not os.path.exists(pkg.LIB_PATH):
+        from mxfp4_moe_expert_gb300 import build
+        build.build()
+    pkg.load_library()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """Streams with given contexts behind a shared prefix (held by the last stream slot), their block stored."""
+
+    def __init__(self, ctx, B, Hq, Hkv, D=128, page=64, prefix=0, dtype=torch.bfloat16, alone=(), seed=0, interleaved=False,
+                 fill=None):
+        S = len(ctx)
+        self.S, self.B, self.Hq, self.Hkv, self.D, self.page, self.prefix = S, B, Hq, Hkv, D, page, prefix
+        rng = random.Random(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        assert prefix % page == 0
+        npre = prefix // page
+        M = max(ceil_div(max(list(ctx) + [0]) + B, page), npre, 1) + 1
+        P = npre + sum(ceil_div(n + B, page) for n in ctx) + 5
+        free = list(range(P))
+        rng.shuffle(free)
+        b = self.books = Books(S + 1, M, P, page)
+        b.table[S][:npre] = [free.pop() for _ in range(npre)]
+        b.held[S], b.length[S] = npre, prefix
+        for p in b.table[S][:npre]:
+            b.ref[p] += 1
+        for s, n in enumerate(ctx):
+            held = ceil_div(n + B, page)
+            for i in range(held):
+                shared = s not in alone and n >= prefix and i < npre
+                b.table[s][i] = b.table[S][i] if shared else free.pop()
+                b.ref[b.table[s][i]] += 1
+            b.held[s], b.length[s] = held, n
+        shape = (P, 2, Hkv, page, D) if interleaved else (2, P, Hkv, page, D)
+        mem = torch.randn(shape, generator=g, device="cuda").to(dtype)
+        self.k, self.v = (mem[:, 0], mem[:, 1]) if interleaved else (mem[0], mem[1])
+        self.v += torch.randn((1, Hkv, 1, D), generator=g, device="cuda").to(dtype)
+        if fill is not None:                       # what no stream has stored holds `fill`
+            used = torch.zeros((P, page), dtype=torch.bool)
+            for s in range(S + 1):
+                stored = b.length[s] + (B if s < S else 0)
+                for i in range(b.held[s]):
+                    used[b.table[s][i], :max(0, min(page, stored - i * page))] = True
+            hole = (~used).cuda()[:, None, :, None]
+            self.k.masked_fill_(hole, fill)
+            self.v.masked_fill_(hole, fill)
+        self.q = (1.3 * torch.randn((S, B, Hq, D), generator=g, device="cuda")).to(dtype)
+        self.cache = pkg.KvCache(layers=[(self.k, self.v)], num_streams=S + 1, max_pages=M)
+        write_books(self.cache, b)
+
+    def attend(self, **kw):
+        if self.prefix and "shared_tokens" not in kw:
+            kw.update(shared_stream=self.S, shared_tokens=self.prefix)
+        out, lse = self.cache.attend(0, self.q, **kw)
+        torch.cuda.synchronize()
+        self.cache.check()
+        return out, lse
+
+    def check(self, out, lse, used=None, mask=None, scale=None, streams=None):
+        assert_attention(out, lse, self.q, self.k, self.v, self.books, used or [self.B] * self.S,
+                         self.D ** -0.5 if scale is None else scale, mask, streams)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 1, 1), (8, 56, 8), (3, 7, 1), (5, 6, 2), (64, 16, 2), (1, 16, 2), (8, 32, 2), (17, 4, 4)])
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16)])
+def test_heads_and_blocks(B, Hq, Hkv, D, dtype):
+    c = Case([0, 1, 63, 64, 127, 128, 129, 300], B, Hq, Hkv, D=D, dtype=dtype, seed=B)
+    c.check(*c.attend())
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D,dtype,interleaved", [(128, torch.float16, True), (64, torch.bfloat16, False)])
+def test_pages_and_a_shared_prefix(page, D, dtype, interleaved):
+    """Contexts that end inside, at and behind tiles and pages; a stream of its own pages, one shorter than the prefix."""
+    prefix = 384
+    ctx = [prefix, prefix + 1, prefix + page - 1, prefix + page, prefix + 700, 5, 0, prefix + 40]
+    c = Case(ctx, 8, 8, 2, D=D, page=page, prefix=prefix, dtype=dtype, alone=(7,), seed=page, interleaved=interleaved)
+    out, lse = c.attend()
+    c.check(out, lse)
+    out2, lse2 = c.attend(shared_tokens=0)            # the same without sharing
+    c.check(out2, lse2)
+    if page <= 64:
+        c.check(*c.attend(shared_stream=c.S, shared_tokens=page * 2))   # a part of what is shared
+
+
+@pytest.mark.parametrize("S,prefix,lo,hi", [(1, 0, 20000, 20000), (2, 4096, 4096, 4100), (40, 2048, 2048, 2500), (130, 256, 256, 400)])
+def test_long_and_many(S, prefix, lo, hi):
+    rng = random.Random(S)
+    c = Case([rng.randint(lo, hi) for _ in range(S)], 8, 14, 2, prefix=prefix, seed=S)
+    out, lse = c.attend()
+    c.check(out, lse, streams=sorted({0, S - 1, S // 2, S // 3}))
+
+
+def test_padded_positions_are_left_alone():
+    used = [0, 5, 8, 1, 0, 7]
+    c = Case([100, 640, 641, 0, 3000, 700], 8, 8, 2, prefix=640, seed=3)
+    out = torch.full_like(c.q, 7.0)
+    lse = torch.full((c.S, c.B, c.Hq), 7.0, device="cuda")
+    lengths = i32(used)
+    c.attend(lengths=lengths, out=out, lse=lse)
+    c.check(out, lse, used=used)
+    for s in range(c.S):
+        assert (out[s, used[s]:] == 7).all() and (lse[s, used[s]:] == 7).all()
+    out, lse = c.attend(lengths=i32([0] * c.S))
+    assert not out.any() and not lse.any()
+    c.attend(lengths=i32([9, 100, 8, -1, -5, 8]))      # more than the block: all of it; less than none: none
+
+
+@pytest.mark.parametrize("B,prefix", [(11, 0), (64, 128), (1, 0)])
+def test_tree_masks_and_empty_rows(B, prefix):
+    """Masks of random bits, rows that see no block position, and, in streams without a context, nothing at all."""
+    rng = random.Random(B)
+    ctx = [prefix, 0, prefix + 77, 0, prefix + 200]
+    c = Case(ctx, B, 4, 2, D=64, page=16, prefix=prefix, dtype=torch.float16, seed=B)
+    rows = [[rng.getrandbits(B) for _ in range(B)] for _ in ctx]
+    rows[1][0] = 0
+    rows[0][B - 1] = 0
+    rows[3] = [0] * B
+    as_i64 = torch.tensor([[x - (1 << 64) if x >> 63 else x for x in r] for r in rows], dtype=torch.int64, device="cuda")
+    out, lse = c.attend(mask=as_i64)
+    c.check(out, lse, mask=rows)
+    assert not out[3].any() and (lse[3] == -math.inf).all()
+    used = [B, max(1, B - 3), B, B // 2, 1]
+    out, lse = c.attend(mask=as_i64, lengths=i32(used))
+    c.check(out, lse, used=used, mask=rows)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("page,D", [(16, 64), (128, 128)])
+def test_what_is_not_stored_has_no_part(fill, page, D):
+    c = Case([0, 5, 130, 256, 391], 3, 8, 4, D=D, page=page, prefix=0, seed=5, fill=fill)
+    c.check(*c.attend())
+    c = Case([256, 261, 300, 511], 3, 8, 4, D=D, page=page, prefix=256, seed=6, fill=fill)
+    c.check(*c.attend())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_keys_that_a_row_does_not_see_have_no_part(bad):
+    """Non-finite keys and values at a block position: earlier positions are as without them, and later ones get what
+    the sums give."""
+    ctx, B = [0, 61, 126, 200], 6
+    c = Case(ctx, B, 4, 2, prefix=0, seed=9)
+    want, wlse = c.attend()
+    for s in range(c.S):
+        i, off = divmod(ctx[s] + 3, c.page)
+        c.v[c.books.table[s][i], :, off, 5] = bad
+    out, lse = c.attend()
+    assert torch.equal(out[:, :3], want[:, :3]) and torch.equal(lse, wlse)
+    keep = [d for d in range(c.D) if d != 5]
+    assert torch.equal(out[..., keep], want[..., keep])
+    assert torch.equal(out[:, 3:, :, 5].isnan(), torch.full_like(out[:, 3:, :, 5], math.isnan(bad), dtype=torch.bool))
+    assert not out[:, 3:, :, 5].isfinite().any()
+    for s in range(c.S):
+        i, off = divmod(ctx[s] + 3, c.page)
+        c.k[c.books.table[s][i], :, off, 7] = float("nan")
+    out, lse = c.attend()
+    assert torch.equal(out[:, :3], want[:, :3]) and torch.equal(lse[:, :3], wlse[:, :3])
+    assert out[:, 3:].isnan().all() and lse[:, 3:].isnan().all()
+
+
+def test_masks_of_one_row_leave_the_others_alone():
+    """The same with a mask: a bad value is seen by the rows whose bit is set, and by no other."""
+    B = 5
+    c = Case([40, 125], B, 4, 2, seed=10)
+    rows = [[0b00001, 0b10010, 0b00101, 0b01000, 0b10000], [0b11111, 0b00000, 0b00100, 0b01011, 0b00010]]
+    mask = torch.tensor(rows, dtype=torch.int64, device="cuda")
+    want, _ = c.attend(mask=mask)
+    for s, n in enumerate([40, 125]):
+        i, off = divmod(n + 2, c.page)
+        c.v[c.books.table[s][i], :, off] = float("nan")
+    out, _ = c.attend(mask=mask)
+    for s in range(2):
+        for b in range(B):
+            if rows[s][b] >> 2 & 1:
+                assert out[s, b].isnan().all()
+            else:
+                assert torch.equal(out[s, b], want[s, b])
+
+
+def test_extreme_scores():
+    """Scores far apart (the running maximum climbs tile by tile), large equal ones, and a scale of zero."""
+    c = Case([700, 1029], 4, 4, 2, seed=11)
+    ramp = torch.linspace(-3, 3, 1100, device="cuda")
+    for s in range(c.S):
+        for i in range(c.books.held[s]):
+            n = i * c.page
+            c.k[c.books.table[s][i]] = (ramp[n % 1000:n % 1000 + c.page, None] * torch.ones(c.D, device="cuda")).to(c.k.dtype)
+    c.q.fill_(1.0)
+    c.check(*c.attend())
+    c.check(*c.attend(scale=0.0), scale=0.0)
+    c.q.fill_(-2.0)
+    c.check(*c.attend(scale=1.0), scale=1.0)
+
+
+def test_rows_of_a_fused_projection_and_bad_tables():
+    c = Case([100, 259], 4, 4, 2, seed=12)
+    want, wlse = c.attend()
+    fused = torch.zeros((2, 4, 12, c.D), dtype=c.q.dtype, device="cuda")
+    fused[:, :, 3:7] = c.q
+    out, lse = c.cache.attend(0, fused[:, :, 3:7])
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    # entries outside the pool and fewer pages than the length says: read as if absent, no fault, others unharmed
+    c.cache.page_table[0, 0] = 1 << 30
+    c.cache.page_table[0, 1] = -5
+    out, _ = c.cache.attend(0, c.q)
+    assert torch.equal(out[1], want[1])
+    c.cache.held[0] = 0
+    c.cache.length[0] = 1 << 20
+    out, _ = c.cache.attend(0, c.q)
+    torch.cuda.synchronize()
+    assert torch.equal(out[1], want[1])
+    pkg.moe_mxfp4_cache_check(c.cache.handle, c.cache.state.data_ptr(), torch.cuda.current_stream().cuda_stream)
+
+
+def test_prompt_blocks():
+    """Long blocks (a prompt behind a shared one): causal over many row tiles, ragged."""
+    used = [500, 0, 333]
+    c = Case([256, 256, 300], 500, 8, 2, prefix=256, seed=13)
+    out, lse = c.attend(lengths=i32(used))
+    c.check(out, lse, used=used)
+
+
+def test_offsets_beyond_32_bits():
+    P, Hkv, page, D = 16500, 8, 128, 128
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    mem = torch.empty((2, P, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    b = Books(1, 8, P, page)
+    ids = [P - 1, 0, P - 2, 16400, 3]
+    mem[:, ids] = torch.randn((2, len(ids), Hkv, page, D), device="cuda").bfloat16()
+    b.table[0][:5], b.held[0], b.length[0] = ids, 5, 600
+    for p in ids:
+        b.ref[p] = 1
+    cache = pkg.KvCache(layers=[(mem[0], mem[1])], num_streams=1, max_pages=8)
+    write_books(cache, b)
+    q = torch.randn((1, 4, 16, D), device="cuda").bfloat16()
+    out, lse = cache.attend(0, q)
+    cache.check()
+    assert_attention(out, lse, q, mem[0], mem[1], b, [4], D ** -0.5)
+
+
+def test_graph_replay_follows_the_books_and_repeats_bit_for_bit():
+    c = Case([256, 700, 300], 8, 8, 2, prefix=256, seed=14)
+    out, lse = c.attend()
+    out2, lse2 = c.attend()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        gout, glse = c.cache.attend(0, c.q, shared_stream=c.S, shared_tokens=256)
+    with torch.cuda.stream(side):
+        g.replay()
+    side.synchronize()
+    assert torch.equal(gout, out) and torch.equal(glse, lse)
+    c.cache.truncate(i32([256, 440, 299, 256]))        # shorter streams (with other pages), the same graph
+    c.books.truncate([256, 440, 299, 256])
+    c.cache.reserve(i32([8, 8, 8, 0]))
+    c.books.reserve([8, 8, 8, 0])
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(gout, glse)
+
+
+def test_a_verify_forward_from_reserve_to_commit():
+    """The calls as a user makes them: streams fork from a prompt, and blocks are reserved, appended, attended, judged
+    by accept() and committed; the attention then equals that over contiguous keys."""
+    torch.manual_seed(0)
+    S, B, Hq, Hkv, D, page, V = 5, 4, 8, 2, 64, 16, 50
+    mem = torch.zeros((2, 2, 60, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    c = pkg.KvCache(layers=[(mem[i, 0], mem[i, 1]) for i in range(2)], num_streams=S + 1, max_pages=12)
+    prompt = 37
+    c.reserve(i32([0] * S + [prompt]))
+    pk, pv = torch.randn((2, 1, prompt, Hkv, D), device="cuda").bfloat16()
+    allk, allv = [pk[0].clone() for _ in range(S)], [pv[0].clone() for _ in range(S)]
+    slot = torch.zeros((S + 1, prompt, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    slot[S] = pk[0]
+    slotv = torch.zeros_like(slot)
+    slotv[S] = pv[0]
+    for layer in range(2):
+        c.append(layer, slot, slotv, lengths=i32([0] * S + [prompt]))
+    c.commit(i32([0] * S + [prompt]))
+    c.fork(i32([S] * S), i32(list(range(S))))
+    shared = prompt // page * page
+    for step in range(9):
+        c.reserve(i32([B] * S + [0]))
+        k, v = torch.randn((2, S, B, Hkv, D), device="cuda").bfloat16()
+        q = torch.randn((S, B, Hq, D), device="cuda").bfloat16()
+        for layer in range(2):
+            c.append(layer, k, v)
+            out, lse = c.attend(layer, q, shared_stream=S, shared_tokens=shared)
+        logits = torch.randn((S, B, V), device="cuda")
+        target = logits.argmax(-1).int()
+        tokens = torch.zeros((S, B), dtype=torch.int32, device="cuda")
+        tokens[:, 1:] = target[:, :-1]
+        tokens[step % S, 1 + step % (B - 1):] = -1     # one stream's drafts fail early
+        _, acc, _ = pkg.accept(logits, tokens)
+        for s in range(S):
+            kk, vv = torch.cat([allk[s], k[s]]), torch.cat([allv[s], v[s]])
+            flat = Books(1, 1, 1, kk.shape[0])
+            flat.table, flat.held, flat.length = [[0]], [1], [allk[s].shape[0]]
+            assert_attention(out[s:s + 1], lse[s:s + 1], q[s:s + 1], kk.transpose(0, 1)[None], vv.transpose(0, 1)[None],
+                             flat, [B], D ** -0.5)
+            n = int(acc[s])
+            allk[s], allv[s] = torch.cat([allk[s], k[s, :n]]), torch.cat([allv[s], v[s, :n]])
+        c.commit(torch.cat([acc, torch.zeros(1, dtype=torch.int32, device="cuda")]))
+        if step == 4:
+            c.compact()
+        c.check()
+    for s in range(S):
+        n = allk[s].shape[0]
+        assert c.length[s].item() == n
+        assert torch.equal(gather(mem[1, 0], c.page_table[s].tolist(), c.held[s].item(), page)[:, :n], allk[s].transpose(0, 1))
+
+
+def test_refusals():
+    c = Case([10, 20], 4, 4, 2, seed=15)
+    q, cache = c.q, c.cache
+    for call in (lambda: cache.attend(0, q.half()), lambda: cache.attend(0, q[..., :64]), lambda: cache.attend(0, q[0]),
+                 lambda: cache.attend(0, q, out=q[:1]), lambda: cache.attend(0, q, lse=torch.zeros(3, device="cuda")),
+                 lambda: cache.attend(0, q, mask=torch.zeros((2, 4), dtype=torch.int32, device="cuda")),
+                 lambda: cache.attend(0, q, lengths=i32([1])), lambda: cache.attend(0, q.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cache.attend(1, q), lambda: cache.attend(0, q[:, :, :3]),
+                 lambda: cache.attend(0, q, shared_tokens=65), lambda: cache.attend(0, q, shared_tokens=-64),
+                 lambda: cache.attend(0, q, shared_tokens=64, shared_stream=3),
+                 lambda: cache.attend(0, q, shared_tokens=64 * 1000), lambda: cache.attend(0, q, scale=float("nan")),
+                 lambda: cache.attend(0, torch.zeros((2, 65, 4, 128), dtype=q.dtype, device="cuda"),
+                                      mask=torch.zeros((2, 65), dtype=torch.int64, device="cuda")),
+                 lambda: cache.attend(0, torch.zeros((4, 1, 4, 128), dtype=q.dtype, device="cuda"))):
+        with pytest.raises(pkg.MoeError) as e:
+            call()
+        assert e.value.status == pkg.MOE_ERR_INVALID_ARG
+    with pytest.raises(pkg.MoeError) as e:
+        cache.attend(0, q, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == pkg.MOE_ERR_WORKSPACE
+    out, lse = cache.attend(0, q[:0])
+    assert out.numel() == 0 and lse.numel() == 0
