@@ -473,6 +473,7 @@ int moe_mxfp4_cache_create(const moe_mxfp4_cache_config* cfg, const moe_mxfp4_ca
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     for (int l = 0; l < c.num_layers; ++l)
         if (!device_memory(layers[l].k_dev, dev) || !device_memory(layers[l].v_dev, dev)) return MOE_ERR_INVALID_ARG;
+    if (!moe::attend_prepare()) return MOE_ERR_CUDA;
     try {
         moe_mxfp4_cache* h = new moe_mxfp4_cache();
         h->cfg = c;

@@ -1,0 +1,100 @@
+// tcgen05 products of 16-bit operands (kind::f16) and the small pieces around them: TMA boxes
+// of a 3-D tensor, tensor-memory stores, packed fp32 arithmetic, the base-2 exponential.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace moe {
+
+// Instruction descriptor: fp32 accumulator, A and B of one 16-bit type, A K-major, B K-major or
+// (transposed) MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn_major) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzled layout: rows of 128
+// bytes hold 64 elements along M or N, one row per k, 8 k's in 1024 bytes; the next 64 elements
+// lie `panel` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t panel) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// D[tmem] (+)= A[smem] x B[smem]^T, K = 16.
+__device__ __forceinline__ void tc_mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in tensor memory (two elements per 32-bit column).
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 32 consecutive 32-bit columns of this thread's lane (whole warp).
+__device__ __forceinline__ void tc_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// Register split between the warpgroups of a CTA (a multiple of 8; the sum over all threads
+// stays below what the CTA was launched with).
+template <int N>
+__device__ __forceinline__ void reg_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 2^x, relative error about 2^-22; exact zero for x = -inf, results below 2^-126 flushed to zero.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma_x2(float& x, float& y, float a0, float a1, float b, float c) {
+    asm("{\n .reg .b64 t, u, v, w;\n mov.b64 t, {%2, %3};\n mov.b64 u, {%4, %4};\n mov.b64 v, {%5, %5};\n"
+        " fma.rn.f32x2 w, t, u, v;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add_x2(float& x, float& y, float a0, float a1) {
+    asm("{\n .reg .b64 t, u, w;\n mov.b64 t, {%0, %1};\n mov.b64 u, {%2, %3};\n add.rn.f32x2 w, t, u;\n mov.b64 {%0, %1}, w;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void mul_x2(float& x, float& y, float b) {
+    asm("{\n .reg .b64 t, u, w;\n mov.b64 t, {%0, %1};\n mov.b64 u, {%2, %2};\n mul.rn.f32x2 w, t, u;\n mov.b64 {%0, %1}, w;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(b));
+}
+
+// (lo, hi) rounded to nearest even, lo in the low half.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    if (kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace moe
