@@ -5,24 +5,25 @@
 // largest t; partial results over parts of the keys are merged by their logarithms of sums.
 //
 // Work.  The G = q_heads / kv_heads rows that read one kv head are packed (b, g) and, over the
-// shared prefix, (s, b, g): a unit is up to 256 such rows, a job a unit with its run of keys (the
-// shared prefix once for the rows of all streams; every stream's own keys), cut into tiles of 128
-// keys.  The tiles of all jobs in order are dealt out evenly to one CTA per SM, so that a long
-// context is split over many CTAs and short ones are packed; a CTA's part of a job is a segment.
+// shared prefix, (s, b, g).  A job is a unit of these rows with its run of keys (the shared prefix
+// once for the rows of all streams; every stream's own keys), cut into tiles of 128 keys.  There
+// are two kinds of units.  Wide ones (where there are more than 128 rows) have 256 rows: both row
+// slots of a CTA take each tile of keys, so that it is read from memory once for 256 rows and the
+// tensor core always has a slot that is ready.  Narrow ones have up to 128 rows: the two slots of
+// a CTA work on different jobs, or parts of a job, each with a ring of its own, so that the wait
+// for memory in one is covered by the other.  The tiles of the wide jobs are dealt out evenly to
+// the CTAs (one per SM), those of the narrow ones to their 2 x CTAs slots, in order: a long run of
+// keys is split over many, short ones are packed.  What one worker does of a job is a segment.
 // A segment that is all its rows need is written straight to the output; the others leave
 // normalised partial rows and the logarithm of their sum, which a second kernel merges in a fixed
 // order.  The lengths are read on the device, so a captured graph follows the cache.
 //
-// A segment.  Two row slots of 128 rows, each with a softmax warpgroup (a thread per row), share
-// a producer warp (TMA boxes of one head's page into a ring of K and V tiles) and an MMA warp
-// (tcgen05: S = Q K^T from shared memory into tensor memory; O += P V with P, in 16 bits, from
-// tensor memory over the columns of S).  While one slot's softmax runs, the tensor core works for
-// the other.  Units of more than 128 rows use the slots for rows (each tile is used twice);
-// smaller ones use both for the same rows, with every other tile, and merge the two accumulators
-// at the end, so that a few rows over long keys, which wait for memory, keep two tiles going.
-// The reference of the exponentials follows the running maximum only when that passes it by 2^8
-// (P stays below 2^8 in any type, sums are fp32), so the accumulator is rescaled rarely, by the
-// softmax warps themselves.
+// A slot.  Producer warp: walks the worker's segments, publishes each, and copies the K and V
+// tiles (TMA boxes of one head's page) into the ring.  MMA warp: S = Q K^T from shared memory into
+// tensor memory, O += P V with P, in 16 bits, from tensor memory over the columns of S.  Softmax
+// warpgroup: a thread per row.  The reference of the exponentials follows the running maximum only
+// when that passes it by 2^8 (P stays below 2^8 in any type, sums are fp32), so the accumulator is
+// rescaled rarely, by the softmax warps themselves.
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
@@ -31,44 +32,61 @@
 namespace moe {
 
 constexpr int kKeyTile = 128;
-constexpr int kUnitRows = 256;                 // rows of a unit: two slots
-constexpr int kAttThreads = 384;               // softmax warps 0-3 (slot 0), 4-7 (slot 1), producer, MMA, 2 idle
-constexpr int kAttProducer = 8, kAttMma = 9;
+constexpr int kAttThreads = 384;               // softmax warps 0-3 (slot 0), 4-7 (slot 1), producers, MMA
+constexpr int kAttProducer = 8, kAttMma = 10;  // + slot
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // columns: S of slot x at 128 x, O at 256 + 128 x
 constexpr float kRescale = 8.0f;               // exponents that the maximum may pass the reference by
+// A segment costs about this many tiles more than its tiles (its queries, its start, its rows' way
+// out); dealt out with them, narrow jobs being short.
+constexpr int kPadWide = 1, kPadNarrow = 2;
 
 struct AttendParams {
     moe_mxfp4_attend_args a;
     const uint16_t* v_pool;
     int G;                     // query heads per kv head
-    int U;                     // units of a stream's own rows
-    int U_sh;                  // units of all streams' rows
+    int wide_sh, wide_own;     // units of 256 rows (else 128) over the shared prefix, over the own keys
+    int U, U_sh;               // units of a stream's own rows, of all streams' rows
     int R_own;                 // rows of a slot for a stream's unit, a multiple of 4
     float c;                   // |scale| log2 e
     uint32_t q_flip;           // sign flips of a pair of query elements (a negative scale)
     unsigned long long timeout_ns;
-    long long* head;           // workspace: schedule for the merge
-    long long* cum;            // first own tile of each unit (of a head)
-    float* split;              // partial rows of split jobs: 2 per CTA, kUnitRows rows each
+    long long* head;           // workspace: the schedule for the merge
+    long long* cum;            // first own place of each unit (of a head)
+    float* split_wide;         // partial rows of split jobs: 2 per worker, 256 rows each, ...
+    float* split_narrow;       // ... 128 rows each
     float* whole_sh;           // partial rows of whole jobs: shared, ...
     float* whole_own;          // ... and own
+    __host__ __device__ int rows_sh() const { return wide_sh ? 256 : 128; }
+    __host__ __device__ int rows_own() const { return wide_own ? 256 : 128; }
 };
-enum : int { kHeadShared = 0, kHeadTilesSh, kHeadTilesOwn, kHeadWords = 8 };
+enum : int { kHeadShared = 0, kHeadOwn = 1 };  // shared tokens in use, places of one head's own jobs
+
+// One worker's part of a job, for one slot.
+struct Segment {
+    float* out;                // partial rows (nullptr: straight to the output)
+    int R, out_row;            // rows of that slot, the first one here
+    int own, wide, h, s;
+    int r0, nrows;             // first packed row, rows
+    int key0, T, key_end, ctx; // first key, tiles (0: no more segments), end of the keys, first block position
+    int no;                    // segments of this slot before it
+};
 
 template <int D>
 struct AttSmem {
     static constexpr int kPanel = 128 * 128;                 // 128 rows x 64 elements
     static constexpr int kTileBytes = kPanel * (D / 64);     // a K, V or Q tile
-    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kStages = D == 128 ? 4 : 8;         // of the wide ring; half of them for each narrow one
     uint8_t q[2][kTileBytes];
     uint8_t kv[kStages][kTileBytes];
-    uint64_t full[kStages], empty[kStages], qfull, sfull[2], pfull[2], ofull[2], pair, drain;
+    uint64_t full[2][kStages], empty[2][kStages];            // [0]: wide, [1]: narrow
+    uint64_t mended[kStages];                                // wide: slot 0's MMA warp has mended the V tile
+    uint64_t segf[2][2], sege[2][2], qfull[2], sfull[2], pfull[2], ofull[2], drain[2];
+    Segment seg[2][2];
     long long scan[3][12];
-    long long first_y;
-    float ml[2][128][2];                                     // the slots' references and sums
     uint32_t tmem;
-    int first_unit, first_off;
-    int bad_value;                                           // last segment (+ 1) with a non-finite block value
+    int first_unit[2];
+    long long first_off[2];
+    int bad_value[2];                                        // last segment (+ 1) with a non-finite block value
     int abort;
 };
 
@@ -121,17 +139,41 @@ __device__ __forceinline__ OwnUnit att_unit(const CacheView& c, const AttendPara
     OwnUnit w{0, 0, 0, 0, 0};
     const int s = unit / p.U;
     if (s >= p.a.streams) return w;
-    w.r0 = (unit - s * p.U) * kUnitRows;
+    w.r0 = (unit - s * p.U) * p.rows_own();
     const int used = att_used(p, s), rows = used * p.G;
     if (w.r0 >= rows) return w;
-    w.nrows = min(kUnitRows, rows - w.r0);
+    w.nrows = min(p.rows_own(), rows - w.r0);
     w.ctx = att_ctx(c, s);
     w.end = w.ctx + (p.a.mask_dev ? used : (w.r0 + w.nrows - 1) / p.G + 1);
     w.begin = att_shares(c, p, s, shared) ? shared : 0;
     return w;
 }
 
-// Sums over the CTA of a value per thread, and the thread's exclusive prefix.
+// The jobs of one list (wide or narrow): shared ones, then own ones, each with its places in a
+// row of W: a job with n tiles has pad + n, tile i at place pad + i.
+struct JobList {
+    int pad, tiles_sh;
+    bool has_sh, has_own;
+    long long W_sh, W1, W;            // places of the shared jobs, of one head's own jobs, of all
+    long long workers;
+    __device__ long long first(long long w) const { return W * w / workers; }
+    __device__ int worker(long long place) const { return (int)min(((place + 1) * workers - 1) / W, workers - 1); }
+};
+// W1: places of one head's own jobs (with this list's padding).
+__device__ __forceinline__ JobList att_list(const CacheView& c, const AttendParams& p, bool wide, int shared, long long W1, int grid) {
+    JobList L;
+    L.pad = wide ? kPadWide : kPadNarrow;
+    L.has_sh = shared > 0 && (p.wide_sh != 0) == wide;
+    L.has_own = (p.wide_own != 0) == wide;
+    L.tiles_sh = (shared + kKeyTile - 1) / kKeyTile;
+    L.W_sh = L.has_sh ? (long long)c.Hkv * p.U_sh * (L.tiles_sh + L.pad) : 0;
+    L.W1 = L.has_own ? W1 : 0;
+    L.W = L.W_sh + (long long)c.Hkv * L.W1;
+    L.workers = min((long long)(wide ? grid : 2 * grid), L.W);   // none of them without a place
+    return L;
+}
+
+// Exclusive prefix over the CTA's threads of a value per thread, and the sum.
 template <int D>
 __device__ __forceinline__ long long att_scan(AttSmem<D>& sm, int k, long long v, long long* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -144,6 +186,7 @@ __device__ __forceinline__ long long att_scan(AttSmem<D>& sm, int k, long long v
     if (lane == 31) sm.scan[k][warp] = x;
     __syncthreads();
     long long before = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < kAttThreads / 32; ++w) {
         if (w < warp) before += sm.scan[k][w];
         all += sm.scan[k][w];
@@ -153,190 +196,233 @@ __device__ __forceinline__ long long att_scan(AttSmem<D>& sm, int k, long long v
     return before + x - v;
 }
 
-// What every warp knows of the schedule.
+// Shared tokens in use and the places of one head's own jobs; writes what the merge needs, and
+// where each slot's own jobs begin.
 struct Schedule {
-    int shared, tiles_sh;             // shared prefix in use, its tiles
-    long long W_sh, W1;               // tiles of the shared jobs, of one head's own jobs
-    long long g0, g1;                 // this CTA's tiles
+    int shared;
+    long long W1;
 };
-
 template <int D>
 __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttSmem<D>& sm) {
     Schedule sc;
-    const int units = p.a.streams * p.U, tid = threadIdx.x;
+    const int units = p.a.streams * p.U, tid = threadIdx.x, pad = p.wide_own ? kPadWide : kPadNarrow;
     const int shared = att_shared(c, p);
     long long with = 0, without = 0, sharers = 0, t;
     for (int i = tid; i < units; i += kAttThreads) {
         const OwnUnit w = att_unit(c, p, i, shared);
         if (w.nrows == 0) continue;
-        with += w.tiles();
-        without += (w.end + kKeyTile - 1) / kKeyTile;
+        with += w.tiles() + pad;
+        without += (w.end + kKeyTile - 1) / kKeyTile + pad;
         sharers += w.r0 == 0 && w.begin > 0;
     }
-    att_scan(sm, 0, sharers, &t);
-    sharers = t;
-    att_scan(sm, 1, with, &t);
-    with = t;
-    att_scan(sm, 2, without, &t);
-    without = t;
-    sc.shared = sharers > 1 ? shared : 0;      // one stream alone reads all through its own table
-    sc.tiles_sh = (sc.shared + kKeyTile - 1) / kKeyTile;
-    sc.W_sh = (long long)c.Hkv * p.U_sh * sc.tiles_sh;
-    sc.W1 = sc.shared ? with : without;
-    const long long W = sc.W_sh + (long long)c.Hkv * sc.W1;
-    // as many CTAs as there are tiles, so that none of them is without one
-    const long long n_cta = min((long long)gridDim.x, W), cta = blockIdx.x;
-    sc.g0 = cta < n_cta ? W * cta / n_cta : W;
-    sc.g1 = cta < n_cta ? W * (cta + 1) / n_cta : W;
-    // the unit and the tile of it where this CTA's own jobs begin
-    const long long y = sc.g0 > sc.W_sh ? (sc.g0 - sc.W_sh) % sc.W1 : 0;
-    if (tid == 0) {
-        sm.first_unit = 0;
-        sm.first_off = 0;
+    att_scan(sm, 0, without, &t);
+    sc.W1 = t;
+    sc.shared = 0;
+    if (shared > 0) {
+        att_scan(sm, 1, sharers, &t);
+        if (t > 1) {                           // one stream alone reads all through its own table
+            sc.shared = shared;
+            att_scan(sm, 2, with, &t);
+            sc.W1 = t;
+        }
+    }
+    // the unit, and the place in it, where each slot's own jobs begin
+    const JobList L = att_list(c, p, p.wide_own != 0, sc.shared, sc.W1, gridDim.x);
+    long long y[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const long long w = p.wide_own ? blockIdx.x : x * (long long)gridDim.x + blockIdx.x;
+        const long long at = w < L.workers ? L.first(w) : 0;
+        y[x] = at > L.W_sh ? (at - L.W_sh) % L.W1 : 0;
+    }
+    if (tid < 2) {
+        sm.first_unit[tid] = 0;
+        sm.first_off[tid] = 0;
     }
     __syncthreads();
-    if (blockIdx.x == 0 || y > 0) {
+    if (blockIdx.x == 0 || y[0] > 0 || y[1] > 0) {
         long long at = 0;
         for (int i0 = 0; i0 < units; i0 += kAttThreads) {
             const int i = i0 + tid;
-            const int n = i < units ? att_unit(c, p, i, sc.shared).tiles() : 0;
+            int n = i < units ? att_unit(c, p, i, sc.shared).tiles() : 0;
+            if (n > 0) n += pad;
             long long sum;
-            const long long x = at + att_scan(sm, 0, n, &sum);
-            if (n > 0 && x <= y && y < x + n) {
-                sm.first_unit = i;
-                sm.first_off = (int)(y - x);
-            }
-            if (blockIdx.x == 0 && i < units) p.cum[i] = x;
+            const long long x0 = at + att_scan(sm, 0, n, &sum);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (n > 0 && x0 <= y[x] && y[x] < x0 + n) {
+                    sm.first_unit[x] = i;
+                    sm.first_off[x] = y[x] - x0;
+                }
+            if (blockIdx.x == 0 && i < units) p.cum[i] = x0;
             at += sum;
         }
     }
     if (blockIdx.x == 0 && tid == 0) {
         p.head[kHeadShared] = sc.shared;
-        p.head[kHeadTilesSh] = sc.W_sh;
-        p.head[kHeadTilesOwn] = sc.W1;
+        p.head[kHeadOwn] = sc.W1;
     }
     __syncthreads();
     return sc;
 }
 
-// Where the partial rows of a segment go: first float4 of row 0 (rows run fastest, then the
-// columns in fours), and the logarithms behind them.
+// Partial rows of a part of a job: rows run fastest, then the columns in fours; the logarithms of
+// the sums are behind them.
 struct Slot {
     float* base;
-    int R;                     // rows of the slot
+    int R;
 };
 template <int D>
-__device__ __forceinline__ int64_t slot_floats(int R) { return (int64_t)R * (D + 1); }
-template <int D>
-__device__ __forceinline__ Slot att_slot(const AttendParams& p, bool own, long long job, int cta, bool whole, bool first) {
-    if (!whole) return {p.split + (2 * (int64_t)cta + (first ? 1 : 0)) * slot_floats<D>(kUnitRows), kUnitRows};
-    if (own) return {p.whole_own + job * slot_floats<D>(p.R_own), p.R_own};
-    return {p.whole_sh + job * slot_floats<D>(kUnitRows), kUnitRows};
+__device__ __forceinline__ Slot att_slot(const AttendParams& p, bool wide, bool own, long long job, int worker, bool whole, bool first) {
+    if (!whole) {                              // at most one part of a job it does not begin and one that it does
+        const int R = wide ? 256 : 128;
+        return {(wide ? p.split_wide : p.split_narrow) + (2 * (int64_t)worker + (first ? 1 : 0)) * R * (D + 1), R};
+    }
+    const int R = own ? p.R_own : p.rows_sh();
+    return {(own ? p.whole_own : p.whole_sh) + job * R * (D + 1), R};
 }
 
-struct Segment {
-    bool own;
-    bool by_keys;              // both slots hold the same rows and take every other tile
-    bool direct;               // the rows need nothing else
-    int h, s;
-    int r0, nrows;
-    int key0, T, key_end, ctx; // first key, tiles, end of the unit's keys, first block position
-    long long job;
-    bool whole, first;         // all tiles of the job; its first tile is here
-};
-
-// A warp's walk over its CTA's segments; all lanes hold the same values but `n`.
+// A producer warp's walk over the segments of one list; all lanes hold the same values but `n`.
 struct Walk {
-    long long g;
-    int h, unit, off;
+    long long v, end;          // places
+    int h, unit;
+    long long off;
     int base, n;               // tiles of the units base + lane
 };
 template <int D>
-__device__ __forceinline__ Walk att_walk(const Schedule& sc, const AttSmem<D>& sm) {
+__device__ __forceinline__ Walk att_walk(const JobList& L, const AttSmem<D>& sm, int slot, int worker) {
     Walk w;
-    w.g = sc.g0;
-    w.h = sc.g0 > sc.W_sh ? (int)((sc.g0 - sc.W_sh) / sc.W1) : 0;
-    w.unit = sm.first_unit;
-    w.off = sm.first_off;
+    w.v = worker < L.workers ? L.first(worker) : 0;
+    w.end = worker < L.workers ? L.first(worker + 1) : 0;
+    w.h = 0;
+    w.unit = 0;
+    w.off = 0;
+    if (L.has_own && w.v >= L.W_sh && w.v < w.end) {
+        w.h = (int)((w.v - L.W_sh) / L.W1);
+        w.unit = sm.first_unit[slot];
+        w.off = sm.first_off[slot];
+    }
     w.base = -1;
     w.n = 0;
     return w;
 }
-__device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedule& sc, Walk& w, Segment& sg) {
-    if (w.g >= sc.g1) return false;
-    if (w.g < sc.W_sh) {
-        sg.own = false;
-        sg.job = w.g / sc.tiles_sh;
-        const int t0 = (int)(w.g - sg.job * sc.tiles_sh);
-        sg.h = (int)(sg.job / p.U_sh);
-        sg.r0 = (int)(sg.job % p.U_sh) * kUnitRows;
-        sg.nrows = (int)min((long long)kUnitRows, (long long)p.a.streams * p.a.block * p.G - sg.r0);
-        sg.s = p.a.shared_stream;
-        sg.T = (int)min((long long)(sc.tiles_sh - t0), sc.g1 - w.g);
-        sg.key0 = t0 * kKeyTile;
-        sg.key_end = sg.ctx = sc.shared;
-        sg.first = t0 == 0;
-        sg.whole = sg.T == sc.tiles_sh;
-        sg.direct = false;
-    } else {
-        const int units = p.a.streams * p.U, lane = threadIdx.x & 31;
-        for (;;) {             // the next unit with tiles
-            if (w.unit >= units) {
-                w.unit = 0;
-                if (++w.h >= c.Hkv) return false;
+template <int D>
+__device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedule& sc, const JobList& L, bool wide, int slot,
+                         int worker, Walk& w, Segment& sg) {
+    for (;;) {
+        if (w.v >= w.end) return false;
+        int n, begin;                          // tiles of the job, first key
+        long long o0, job;                     // first place of it here
+        if (w.v < L.W_sh) {
+            job = w.v / (L.tiles_sh + L.pad);
+            o0 = w.v - job * (L.tiles_sh + L.pad);
+            n = L.tiles_sh;
+            begin = 0;
+            sg.own = 0;
+            sg.h = (int)(job / p.U_sh);
+            sg.r0 = (int)(job % p.U_sh) * p.rows_sh();
+            sg.nrows = (int)min((long long)p.rows_sh(), (long long)p.a.streams * p.a.block * p.G - sg.r0);
+            sg.s = p.a.shared_stream;
+            sg.key_end = sg.ctx = sc.shared;
+        } else {
+            const int units = p.a.streams * p.U, lane = threadIdx.x & 31;
+            for (;;) {                         // the next unit with tiles
+                if (w.unit >= units) {
+                    w.unit = 0;
+                    if (++w.h >= c.Hkv) return false;
+                }
+                const int base = w.unit & ~31;
+                if (base != w.base) {
+                    w.base = base;
+                    w.n = base + lane < units ? att_unit(c, p, base + lane, sc.shared).tiles() : 0;
+                }
+                const unsigned some = __ballot_sync(0xFFFFFFFFu, w.n > 0) >> (w.unit - base);
+                if (some) {
+                    w.unit += __ffs(some) - 1;
+                    break;
+                }
+                w.unit = base + 32;
             }
-            const int base = w.unit & ~31;
-            if (base != w.base) {
-                w.base = base;
-                w.n = base + lane < units ? att_unit(c, p, base + lane, sc.shared).tiles() : 0;
-            }
-            const unsigned some = __ballot_sync(0xFFFFFFFFu, w.n > 0) >> (w.unit - base);
-            if (some) {
-                w.unit += __ffs(some) - 1;
-                break;
-            }
-            w.unit = base + 32;
+            const OwnUnit u = att_unit(c, p, w.unit, sc.shared);
+            n = u.tiles();
+            begin = u.begin;
+            o0 = w.off;
+            job = (long long)w.h * units + w.unit;
+            sg.own = 1;
+            sg.h = w.h;
+            sg.s = w.unit / p.U;
+            sg.r0 = u.r0;
+            sg.nrows = u.nrows;
+            sg.key_end = u.end;
+            sg.ctx = u.ctx;
+            w.off = 0;
+            ++w.unit;
         }
-        const OwnUnit u = att_unit(c, p, w.unit, sc.shared);
-        const int n = u.tiles();
-        sg.own = true;
-        sg.h = w.h;
-        sg.s = w.unit / p.U;
-        sg.r0 = u.r0;
-        sg.nrows = u.nrows;
-        sg.job = (long long)w.h * units + w.unit;
-        sg.T = (int)min((long long)(n - w.off), sc.g1 - w.g);
-        sg.key0 = u.begin + w.off * kKeyTile;
-        sg.key_end = u.end;
-        sg.ctx = u.ctx;
-        sg.first = w.off == 0;
-        sg.whole = sg.T == n;
-        sg.direct = sg.whole && u.begin == 0;
-        w.off = 0;
-        ++w.unit;
+        const long long o1 = min((long long)(L.pad + n), o0 + (w.end - w.v));
+        w.v += o1 - o0;
+        const int t0 = (int)max(o0 - L.pad, 0ll), t1 = (int)max(o1 - L.pad, 0ll);
+        if (t1 <= t0) continue;                // places without a tile
+        const bool whole = t1 - t0 == n;
+        const Slot to = att_slot<D>(p, wide, sg.own, job, worker, whole, t0 == 0);
+        sg.out = whole && sg.own && begin == 0 ? nullptr : to.base;
+        sg.R = to.R;
+        sg.out_row = wide ? 128 * slot : 0;
+        sg.r0 += sg.out_row;
+        sg.nrows = min(128, sg.nrows - sg.out_row);
+        sg.wide = wide;
+        sg.key0 = begin + t0 * kKeyTile;
+        sg.T = t1 - t0;
+        return true;
     }
-    sg.by_keys = sg.nrows <= 128;
-    w.g += sg.T;
-    return true;
 }
-
-// Positions in the ring of a segment's tiles, in the order in which the MMA warp takes them:
-// by rows K0 V0 K1 V1 ..., by keys K0 K1 V0 K2 V1 K3 ...
-__device__ __forceinline__ int ring_k(const Segment& sg, int t) { return !sg.by_keys ? 2 * t : t < 2 ? t : 2 * t - 1; }
-__device__ __forceinline__ int ring_v(const Segment& sg, int t) { return !sg.by_keys ? 2 * t + 1 : t + min(sg.T, t + 2); }
 
 // ---- producer ------------------------------------------------------------------------------
 
+// The ring of a list's tiles: K and V of each tile in turn.
 template <int D>
-__device__ void att_produce(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm,
-                            const CUtensorMap* kmap, const CUtensorMap* vmap) {
+struct Ring {
+    AttSmem<D>* sm;
+    int wide, first, stages;
+    __device__ Ring(AttSmem<D>& s, bool w, int slot)
+        : sm(&s), wide(w), first(w ? 0 : slot * (AttSmem<D>::kStages / 2)), stages(w ? AttSmem<D>::kStages : AttSmem<D>::kStages / 2) {}
+    __device__ int stage(uint32_t i) const { return first + (int)(i % stages); }
+    __device__ uint32_t round(uint32_t i) const { return (i / stages) & 1; }
+    __device__ uint64_t* full(uint32_t i) const { return &sm->full[wide ? 0 : 1][stage(i)]; }
+    __device__ uint64_t* empty(uint32_t i) const { return &sm->empty[wide ? 0 : 1][stage(i)]; }
+};
+
+// Makes a segment known to the slot's other warps.
+template <int D>
+__device__ __forceinline__ bool att_publish(const AttendParams& p, AttSmem<D>& sm, int slot, const Segment& sg) {
+    const int e = sg.no & 1;
+    if (!att_warp_wait(&sm.sege[slot][e], ((sg.no >> 1) & 1) ^ 1, &sm.abort, p.timeout_ns)) return false;
+    if ((threadIdx.x & 31) == 0) {
+        sm.seg[slot][e] = sg;
+        mbar_arrive(&sm.segf[slot][e]);
+    }
+    __syncwarp();
+    return true;
+}
+
+// One list.  Returns false when a wait gave up; *n: tiles of the ring.
+template <int D>
+__device__ bool att_produce(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm, const CUtensorMap* kmap,
+                            const CUtensorMap* vmap, bool wide, int slot, Segment& sg, uint32_t& n) {
     using SM = AttSmem<D>;
     const int lane = threadIdx.x & 31, per_tile = kKeyTile >> c.page_shift;
-    Walk w = att_walk<D>(sc, sm);
-    Segment sg;
-    uint32_t n = 0;                                    // tiles issued so far
-    bool ok = true;
-    while (ok && att_next(c, p, sc, w, sg)) {
+    const JobList L = att_list(c, p, wide, sc.shared, sc.W1, gridDim.x);
+    if (L.W == 0) return true;
+    const int worker = wide ? blockIdx.x : slot * gridDim.x + blockIdx.x;
+    const bool loads = !wide || slot == 0;
+    const Ring<D> ring(sm, wide, slot);
+    Walk w = att_walk<D>(L, sm, slot, worker);
+    while (att_next<D>(c, p, sc, L, wide, slot, worker, w, sg)) {
+        if (!att_publish<D>(p, sm, slot, sg)) return false;
+        ++sg.no;
+        if (!loads) {
+            n += 2 * sg.T;
+            continue;
+        }
         const int* table = c.table(sg.s);
         const int pages = min(min(c.held()[sg.s], c.L.M), (sg.key_end + c.page - 1) >> c.page_shift);
         // the page that this lane copies of a tile; outside the pool (zeros) where there is none
@@ -345,47 +431,61 @@ __device__ void att_produce(const CacheView& c, const AttendParams& p, const Sch
             const int id = lane < per_tile && t < sg.T && i < pages ? table[i] : -1;
             return (unsigned)id < (unsigned)c.L.P ? id : c.L.P;
         };
-        int kt = 0, vt = 0;                            // next K and V tile
-        int kp = page_of(0), vp = kp;
-        for (int i = 0; ok && i < 2 * sg.T; ++i, ++n) {
-            const bool is_k = kt < sg.T && ring_k(sg, kt) == i;
-            const int id = is_k ? kp : vp;
-            const uint32_t st = n % SM::kStages;
-            if (!att_warp_wait(&sm.empty[st], ((n / SM::kStages) & 1) ^ 1, &sm.abort, p.timeout_ns)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], SM::kTileBytes);
-            __syncwarp();
-            if (lane < per_tile) {
-                const uint32_t dst = smem_u32(sm.kv[st]) + lane * c.page * 128;
+        int id = page_of(0);
+        for (int t = 0; t < sg.T; ++t) {
+            const int next = page_of(t + 1);
 #pragma unroll
-                for (int x = 0; x < D / 64; ++x)
-                    tma_load_3d(dst + x * SM::kPanel, is_k ? kmap : vmap, 64 * x, sg.h * c.page, id, &sm.full[st]);
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                if (!att_warp_wait(ring.empty(n), ring.round(n) ^ 1, &sm.abort, p.timeout_ns)) return false;
+                uint64_t* full = ring.full(n);
+                if (lane == 0) mbar_arrive_expect_tx(full, SM::kTileBytes);
+                __syncwarp();
+                if (lane < per_tile) {
+                    const uint32_t dst = smem_u32(sm.kv[ring.stage(n)]) + lane * c.page * 128;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_3d(dst + x * SM::kPanel, kv ? vmap : kmap, 64 * x, sg.h * c.page, id, full);
+                }
             }
-            if (is_k) kp = page_of(++kt);
-            else vp = page_of(++vt);
+            id = next;
         }
     }
-    // every copy has landed before the CTA leaves (already so but after an abort)
-    const uint32_t last = n > SM::kStages ? n - SM::kStages : 0;
-    if (!ok || *reinterpret_cast<volatile int*>(&sm.abort))
-        for (uint32_t i = last; i < n; ++i) {
-            const unsigned long long until = globaltimer_ns() + p.timeout_ns;
-            while (!mbar_try_wait(&sm.full[i % SM::kStages], (i / SM::kStages) & 1))
-                if (globaltimer_ns() > until) break;
-        }
+    return true;
+}
+
+template <int D>
+__device__ void att_producer(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm, const CUtensorMap* kmap,
+                             const CUtensorMap* vmap, int slot) {
+    Segment sg;
+    sg.no = 0;
+    uint32_t nw = 0, nn = 0;
+    bool ok = att_produce<D>(c, p, sc, sm, kmap, vmap, true, slot, sg, nw);
+    // the narrow rings take over the wide one's stages when all its tiles are used up
+    const Ring<D> wide(sm, true, slot), narrow(sm, false, slot);
+    for (uint32_t i = nw > (uint32_t)wide.stages ? nw - wide.stages : 0; ok && i < nw; ++i)
+        ok = att_warp_wait(wide.empty(i), wide.round(i), &sm.abort, p.timeout_ns);
+    if (ok) ok = att_produce<D>(c, p, sc, sm, kmap, vmap, false, slot, sg, nn);
+    sg.T = 0;
+    if (ok) ok = att_publish<D>(p, sm, slot, sg);
+    if (ok && !*reinterpret_cast<volatile int*>(&sm.abort)) return;
+    // after an abort: every copy has landed before the CTA leaves
+    const unsigned long long until = globaltimer_ns() + p.timeout_ns;
+    if (slot == 0)
+        for (uint32_t i = nw > (uint32_t)wide.stages ? nw - wide.stages : 0; i < nw; ++i)
+            while (!mbar_try_wait(wide.full(i), wide.round(i)) && globaltimer_ns() < until) {}
+    for (uint32_t i = nn > (uint32_t)narrow.stages ? nn - narrow.stages : 0; i < nn; ++i)
+        while (!mbar_try_wait(narrow.full(i), narrow.round(i)) && globaltimer_ns() < until) {}
 }
 
 // ---- MMA -------------------------------------------------------------------------------------
 
 // Rows of a V tile that no product may see: positions behind the unit's keys become zero, and so
 // do non-finite elements at block positions, which some rows may not see (0 x NaN is NaN); the
-// epilogue adds those to the rows that do see them.  Whole warp.
+// epilogue adds those to the rows that do see them.  Whole warp; true in every lane when there
+// were any.
 template <int D, bool kBf16>
-__device__ __forceinline__ void att_mend_v(AttSmem<D>& sm, uint8_t* tile, const Segment& sg, int key0, int seg_no) {
+__device__ __noinline__ bool att_mend_v(uint8_t* tile, int from, int end) {
     const int lane = threadIdx.x & 31;
-    const int from = min(max(sg.ctx - key0, 0), kKeyTile), end = min(max(sg.key_end - key0, 0), kKeyTile);
     constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
     bool bad = false;
     for (int i = lane; i < (kKeyTile - from) * 8; i += 32) {
@@ -409,73 +509,85 @@ __device__ __forceinline__ void att_mend_v(AttSmem<D>& sm, uint8_t* tile, const 
             bad |= hit;
         }
     }
-    if (bad) {
-        *reinterpret_cast<volatile int*>(&sm.bad_value) = seg_no + 1;
-        __threadfence_block();
-    }
     fence_proxy_async_shared();
     __syncwarp();
+    return __any_sync(0xFFFFFFFFu, bad);
 }
 
 template <int D, bool kBf16>
-__device__ void att_mma(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm, uint32_t tmem) {
+__device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, int slot) {
     using SM = AttSmem<D>;
     constexpr uint32_t idesc_s = idesc_f16(128, 128, kBf16, false), idesc_o = idesc_f16(128, D, kBf16, true);
     const int lane = threadIdx.x & 31;
-    Walk w = att_walk<D>(sc, sm);
-    Segment sg;
-    uint32_t base = 0, np[2] = {0, 0};
-    int seg_no = 0;
-    for (; att_next(c, p, sc, w, sg); ++seg_no) {
-        const int N = sg.by_keys ? sg.T : 2 * sg.T;     // steps: slot n & 1
-        const auto wait_full = [&](int pos) {
-            const uint32_t i = base + pos;
-            const bool ok = att_warp_wait(&sm.full[i % SM::kStages], (i / SM::kStages) & 1, &sm.abort, p.timeout_ns);
+    const uint32_t ts = tmem + kTmemS + 128 * slot, to = tmem + kTmemO + 128 * slot, q = smem_u32(sm.q[slot]);
+    uint32_t used[2] = {0, 0}, np = 0, mends = 0;          // tiles of each ring so far; mends: a bit per stage
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return att_warp_wait(bar, parity, &sm.abort, p.timeout_ns); };
+    for (int no = 0;; ++no) {
+        if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
+        const Segment& sg = sm.seg[slot][no & 1];
+        const int T = sg.T, wide = sg.wide, key0 = sg.key0, ctx = sg.ctx, key_end = sg.key_end;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sege[slot][no & 1]);
+        if (T == 0) return;
+        const Ring<D> ring(sm, wide, slot);
+        uint32_t n = used[wide];
+        used[wide] += 2 * T;
+        const auto scores = [&]() {                        // S of the tile whose K is tile n of the ring
+            if (!wait(ring.full(n), ring.round(n))) return false;
             tc_fence_after();
-            return ok;
-        };
-        const auto scores = [&](int n) {                // S of step n
-            const int t = sg.by_keys ? n : n >> 1, pos = ring_k(sg, t), x = n & 1;
-            if (!wait_full(pos)) return false;
             if (lane == 0) {
-                const uint32_t st = (base + pos) % SM::kStages;
-                const uint32_t q = smem_u32(sm.q[sg.by_keys ? 0 : x]), k = smem_u32(sm.kv[st]);
+                const uint32_t k = smem_u32(sm.kv[ring.stage(n)]);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t o = (i / 4) * SM::kPanel + (i % 4) * 32;
-                    tc_mma_f16_ss(tmem + kTmemS + 128 * x, smem_desc_sw128(q + o), smem_desc_sw128(k + o), idesc_s, i > 0);
+                    tc_mma_f16_ss(ts, smem_desc_sw128(q + o), smem_desc_sw128(k + o), idesc_s, i > 0);
                 }
-                tc_commit(&sm.sfull[x]);
-                if (sg.by_keys || x == 1) tc_commit(&sm.empty[st]);
+                tc_commit(&sm.sfull[slot]);
+                tc_commit(ring.empty(n));
             }
             __syncwarp();
             return true;
         };
-        if (!att_warp_wait(&sm.qfull, seg_no & 1, &sm.abort, p.timeout_ns)) return;
-        tc_fence_after();
-        for (int n = 0; n < min(N, 2); ++n)
-            if (!scores(n)) return;
-        for (int n = 0; n < N; ++n) {
-            const int t = sg.by_keys ? n : n >> 1, pos = ring_v(sg, t), x = n & 1;
-            if (!wait_full(pos)) return;
-            const uint32_t st = (base + pos) % SM::kStages;
-            const int key0 = sg.key0 + t * kKeyTile;
-            if (key0 + kKeyTile > sg.ctx && (sg.by_keys || x == 0)) att_mend_v<D, kBf16>(sm, sm.kv[st], sg, key0, seg_no);
-            if (!att_warp_wait(&sm.pfull[x], np[x]++ & 1, &sm.abort, p.timeout_ns)) return;
+        if (!wait(&sm.qfull[slot], no & 1)) return;
+        if (!scores()) return;
+        for (int t = 0; t < T; ++t, ++n) {
+            ++n;                                           // V of tile t
+            if (!wait(ring.full(n), ring.round(n))) return;
+            const int st = ring.stage(n), j0 = key0 + t * kKeyTile;
+            if (j0 + kKeyTile > ctx) {                     // block positions, or the end of the keys
+                if (!wide || slot == 0) {
+                    const bool bad = att_mend_v<D, kBf16>(sm.kv[st], min(max(ctx - j0, 0), kKeyTile), min(max(key_end - j0, 0), kKeyTile));
+                    if (lane == 0) {
+                        if (bad) {
+                            *reinterpret_cast<volatile int*>(&sm.bad_value[slot]) = no + 1;
+                            if (wide) *reinterpret_cast<volatile int*>(&sm.bad_value[1]) = no + 1;
+                            __threadfence_block();
+                        }
+                        if (wide) mbar_arrive(&sm.mended[st]);
+                    }
+                    __syncwarp();
+                } else {
+                    if (!wait(&sm.mended[st], mends >> st & 1)) return;
+                    mends ^= 1u << st;
+                }
+            }
+            if (!wait(&sm.pfull[slot], np++ & 1)) return;
             tc_fence_after();
             if (lane == 0) {
                 const uint32_t v = smem_u32(sm.kv[st]);
 #pragma unroll
                 for (int i = 0; i < kKeyTile / 16; ++i)
-                    tc_mma_f16_ts(tmem + kTmemO + 128 * x, tmem + kTmemS + 128 * x + 8 * i,
-                                  smem_desc_mn_sw128(v + i * 2048, SM::kPanel), idesc_o, n > 1 || i > 0);
-                if (sg.by_keys || x == 1) tc_commit(&sm.empty[st]);
-                if (n + 2 >= N) tc_commit(&sm.ofull[x]);
+                    tc_mma_f16_ts(to, ts + 8 * i, smem_desc_mn_sw128(v + i * 2048, SM::kPanel), idesc_o, t > 0 || i > 0);
+                tc_commit(ring.empty(n));
+                if (t + 1 == T) tc_commit(&sm.ofull[slot]);
             }
             __syncwarp();
-            if (n + 2 < N && !scores(n + 2)) return;
+            if (t + 1 < T) {
+                ++n;
+                if (!scores()) return;
+                --n;
+            }
         }
-        base += 2 * sg.T;
     }
 }
 
@@ -484,60 +596,55 @@ __device__ void att_mma(const CacheView& c, const AttendParams& p, const Schedul
 // A row of a segment: its token (stream * block + position) and query head.
 struct Row {
     int64_t tok;
-    int s, b, head;
+    int b, head;
     bool valid;
 };
-__device__ __forceinline__ Row att_row(const CacheView& c, const AttendParams& p, const Schedule& sc, const Segment& sg, int r) {
+__device__ __forceinline__ Row att_row(const CacheView& c, const AttendParams& p, int shared, const Segment& sg, int r) {
     Row x;
     const int i = sg.r0 + r, q = i / p.G;
     x.head = sg.h * p.G + (i - q * p.G);
     x.valid = r < sg.nrows;
+    x.b = q;
+    x.tok = q;
     if (sg.own) {
-        x.s = sg.s;
-        x.b = q;
-        x.tok = (int64_t)sg.s * p.a.block + q;
-    } else {
-        x.s = q / p.a.block;
-        x.b = q - x.s * p.a.block;
-        x.tok = q;
-        if (x.valid) x.valid = x.b < att_used(p, x.s) && att_shares(c, p, x.s, sc.shared);
+        x.tok += (int64_t)sg.s * p.a.block;
+    } else if (x.valid) {
+        const int s = q / p.a.block;
+        x.b = q - s * p.a.block;
+        x.valid = x.b < att_used(p, s) && att_shares(c, p, s, shared);
     }
     return x;
 }
 
-// Query rows r .. r + n - 1 of a segment into a Q tile (128-byte swizzle), zeros behind the unit.
-// 128 threads; 16-byte chunks of a row on neighbouring lanes.
+// The query rows of a segment into its Q tile (128-byte swizzle), zeros behind them.  128 threads;
+// 16-byte chunks of a row on neighbouring lanes.
 template <int D>
-__device__ __forceinline__ void att_load_q(const AttendParams& p, const Segment& sg, uint8_t* tile, int from_row, int tile_row,
-                                           int n) {
+__device__ __forceinline__ void att_load_q(const AttendParams& p, const Segment& sg, uint8_t* tile) {
     constexpr int kChunks = D / 8;
-    const int tid = threadIdx.x & 127;
-    const uint16_t* q = static_cast<const uint16_t*>(p.a.q_dev);
-#pragma unroll 8
-    for (int i = tid; i < n * kChunks; i += 128) {
-        const int row = i / kChunks, x = i % kChunks, r = sg.r0 + from_row + row;
+    const int tid = threadIdx.x & 127, x = tid % kChunks;
+    const uint16_t* q = static_cast<const uint16_t*>(p.a.q_dev) + x * 8;
+    const int64_t tok0 = sg.own ? (int64_t)sg.s * p.a.block : 0;
+    const int nrows = sg.nrows, r0 = sg.r0, h0 = sg.h * p.G;
+#pragma unroll
+    for (int row = tid / kChunks; row < 128; row += 128 / kChunks) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (from_row + row < sg.nrows) {
-            const int t = r / p.G;
-            const int64_t tok = sg.own ? (int64_t)sg.s * p.a.block + t : t;
-            v = *reinterpret_cast<const uint4*>(q + tok * p.a.q_stride + (int64_t)(sg.h * p.G + r - t * p.G) * D + x * 8);
+        if (row < nrows) {
+            const int r = r0 + row, t = r / p.G;
+            v = *reinterpret_cast<const uint4*>(q + (tok0 + t) * p.a.q_stride + (int64_t)(h0 + r - t * p.G) * D);
             v.x ^= p.q_flip; v.y ^= p.q_flip; v.z ^= p.q_flip; v.w ^= p.q_flip;
         }
-        const int tr = tile_row + row;
-        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + tr * 128 + (((x & 7) ^ (tr & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v;
     }
 }
 
 // Bit i: the row sees key j0 + i.
-__device__ __forceinline__ void att_visible(const AttendParams& p, const Segment& sg, const Row& row, uint64_t bits, int j0,
-                                            uint32_t (&vis)[4]) {
-    const int lim = !sg.own ? sg.key_end : p.a.mask_dev ? sg.ctx : sg.ctx + row.b + 1;   // keys below it are seen
-    const int n = min(max(lim - j0, 0), kKeyTile);
+__device__ __forceinline__ void att_visible(bool masked, int ctx, int key_end, int lim, uint64_t bits, int j0, uint32_t (&vis)[4]) {
+    const int n = min(max(lim - j0, 0), kKeyTile);                                       // keys below lim are seen
     uint64_t lo = n >= 64 ? ~0ull : (1ull << n) - 1, hi = n >= 128 ? ~0ull : n > 64 ? (1ull << (n - 64)) - 1 : 0ull;
-    if (sg.own && p.a.mask_dev) {
-        const int len = sg.key_end - sg.ctx;                                             // block positions, at most 64
+    if (masked) {
+        const int len = key_end - ctx;                                                   // block positions, at most 64
         bits &= len >= 64 ? ~0ull : (1ull << len) - 1;
-        const int at = sg.ctx - j0;                                                      // of block position 0 in the tile
+        const int at = ctx - j0;                                                         // of block position 0 in the tile
         if (at <= -64 || at >= kKeyTile) bits = 0;
         else if (at < 0) lo |= bits >> -at;
         else if (at < 64) { lo |= bits << at; if (at) hi |= bits >> (64 - at); }
@@ -546,193 +653,160 @@ __device__ __forceinline__ void att_visible(const AttendParams& p, const Segment
     vis[0] = (uint32_t)lo; vis[1] = (uint32_t)(lo >> 32); vis[2] = (uint32_t)hi; vis[3] = (uint32_t)(hi >> 32);
 }
 
-// Non-finite values at block positions that this row sees, added to columns col .. col + 31 of o.
+// Sum over the block positions that this row sees of the non-finite values of one column, else 0.
 template <int D, bool kBf16>
-__device__ __noinline__ void att_add_bad(const CacheView& c, const AttendParams& p, const Segment& sg, const Row& row,
-                                         uint64_t bits, int col, float (&o)[32]) {
+__device__ __noinline__ float att_bad_sum(const CacheView& c, const AttendParams& p, const Segment& sg, int b, uint64_t bits, int col) {
     const int from = max(sg.ctx, sg.key0), end = min(sg.key_end, sg.key0 + sg.T * kKeyTile);
     const int held = min(c.held()[sg.s], c.L.M);
     constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+    float sum = 0.0f;
     for (int j = from; j < end; ++j) {
         const int i = j - sg.ctx;
-        if (p.a.mask_dev ? !(bits >> i & 1) : i > row.b) continue;
+        if (p.a.mask_dev ? !(bits >> i & 1) : i > b) continue;
         const int pi = j >> c.page_shift, page = pi < held ? c.table(sg.s)[pi] : -1;
         if ((unsigned)page >= (unsigned)c.L.P) continue;
-        const uint16_t* v = p.v_pool + page * c.page_stride + ((int64_t)sg.h * c.page + (j & (c.page - 1))) * D + col;
-        for (int k = 0; k < 32; ++k)
-            if ((v[k] & kExp) == kExp)
-                o[k] += kBf16 ? __uint_as_float((uint32_t)v[k] << 16) : __half2float(__ushort_as_half(v[k]));
+        const uint16_t v = p.v_pool[page * c.page_stride + ((int64_t)sg.h * c.page + (j & (c.page - 1))) * D + col];
+        if ((v & kExp) == kExp) sum += kBf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
     }
+    return sum;
 }
 
 template <int D, bool kBf16>
-__device__ void att_softmax(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm, uint32_t tmem) {
-    const int slot = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = threadIdx.x & 31;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;          // this warp's quarter of the tensor memory
+__device__ void att_softmax(const CacheView& c, const AttendParams& p, int shared, AttSmem<D>& sm, uint32_t tmem) {
+    const int slot = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(tid & ~31) << 16;          // this warp's quarter of the tensor memory
     const uint32_t ts = tmem + kTmemS + 128 * slot + lanes, to = tmem + kTmemO + 128 * slot + lanes;
-    Walk w = att_walk<D>(sc, sm);
-    Segment sg;
-    uint32_t ns = 0, no[2] = {0, 0}, np = 0;
-    int seg_no = 0;
-    bool ok = true;
-    const auto both_here = [&] {              // a bounded barrier of the two warpgroups
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.pair);
-        const bool here = att_warp_wait(&sm.pair, np++ & 1, &sm.abort, p.timeout_ns);
-        tc_fence_after();
-        return here;
-    };
-    for (; ok && att_next(c, p, sc, w, sg); ++seg_no) {
+    uint32_t ns = 0;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return att_warp_wait(bar, parity, &sm.abort, p.timeout_ns); };
+    for (int no = 0;; ++no) {
+        if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
+        const Segment& sg = sm.seg[slot][no & 1];
+        const int T = sg.T;
+        if (T == 0) return;
         // the query rows; the products that read the last ones have completed (ofull, below)
-        if (sg.by_keys) att_load_q<D>(p, sg, sm.q[0], 64 * slot, 64 * slot, 64);
-        else att_load_q<D>(p, sg, sm.q[slot], 128 * slot, 0, 128);
+        att_load_q<D>(p, sg, sm.q[slot]);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.qfull);
-        const int r = sg.by_keys ? tid : 128 * slot + tid;
-        const Row row = att_row(c, p, sc, sg, r);
+        if (lane == 0) mbar_arrive(&sm.qfull[slot]);
+        const Row row = att_row(c, p, shared, sg, tid);
         const bool busy = __any_sync(0xFFFFFFFFu, row.valid);
-        const uint64_t bits = sg.own && p.a.mask_dev && row.valid ? p.a.mask_dev[row.tok] : 0;
-        const int steps = sg.by_keys ? (sg.T + 1 - slot) / 2 : sg.T;
+        const bool masked = sg.own && p.a.mask_dev;
+        const uint64_t bits = masked && row.valid ? p.a.mask_dev[row.tok] : 0;
+        const int lim = !sg.own ? sg.key_end : masked ? sg.ctx : sg.ctx + row.b + 1;
         float m = -INFINITY, l = 0.0f;
-        for (int i = 0; i < steps; ++i) {
-            const int t = sg.by_keys ? 2 * i + slot : i, j0 = sg.key0 + t * kKeyTile;
-            if (!att_warp_wait(&sm.sfull[slot], ns++ & 1, &sm.abort, p.timeout_ns)) { ok = false; break; }
+        int j0 = sg.key0;
+        const int tail = sg.ctx - kKeyTile;                      // tiles from behind here on have hidden keys
+        for (int t = 0; t < T; ++t, j0 += kKeyTile) {
+            if (!wait(&sm.sfull[slot], ns++ & 1)) return;
             tc_fence_after();
             if (busy) {
                 uint32_t x[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tc_ld_x32(ts + 32 * k, x[k]);
                 tc_wait_ld();
-                if (j0 + kKeyTile > sg.ctx) {
+                if (j0 > tail) {
                     uint32_t vis[4];
-                    att_visible(p, sg, row, bits, j0, vis);
+                    att_visible(masked, sg.ctx, sg.key_end, lim, bits, j0, vis);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!(vis[k] >> e & 1)) x[k][e] = 0xFF800000u;
                 }
-                float mx[4];
+                float mx[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    mx[k] = __uint_as_float(x[k][0]);
+                for (int k = 0; k < 8; ++k) {
+                    mx[k] = __uint_as_float(x[k / 2][16 * (k & 1)]);
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(x[k][e]));
+                    for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(x[k / 2][16 * (k & 1) + e]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.c;
                 const bool passed = m != -INFINITY && top > m + kRescale;
                 if (__any_sync(0xFFFFFFFFu, passed)) {
                     const float f = passed ? exp2_approx(m - top) : 1.0f;
                     l *= f;
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t o[32];
-                        tc_ld_x32(to + 32 * k, o);
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t o[16];
+                        tc_ld_x16(to + 16 * k, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_st_x32(to + 32 * k, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc_st_x16(to + 16 * k, o);
                     }
                 }
                 if (passed || m == -INFINITY) m = top;
                 const float ref = m == -INFINITY ? 0.0f : m;
-                float sum[2][2] = {};
+                float sum[4][2] = {};
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    uint32_t pk[32];
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
+                    for (int e = 0; e < 32; e += 2) {
                         float a, b;
-                        fma_x2(a, b, __uint_as_float(x[k + e / 32][e % 32]), __uint_as_float(x[k + e / 32][e % 32 + 1]), p.c,
-                               -ref);
+                        fma_x2(a, b, __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]), p.c, -ref);
                         a = exp2_approx(a);
                         b = exp2_approx(b);
-                        add_x2(sum[(e / 2) & 1][0], sum[(e / 2) & 1][1], a, b);
+                        add_x2(sum[(e / 2) & 3][0], sum[(e / 2) & 3][1], a, b);
                         pk[e / 2] = pack_f16<kBf16>(a, b);
                     }
-                    tc_st_x32(ts + 16 * k, pk);
+                    tc_st_x16(ts + 16 * k, pk);
                 }
-                l += (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
+                l += ((sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1])) + ((sum[2][0] + sum[2][1]) + (sum[3][0] + sum[3][1]));
                 tc_wait_st();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.pfull[slot]);
         }
-        // the rows: out of tensor memory, by keys merged from both slots (half of the columns each)
-        const bool both = sg.by_keys && sg.T > 1;
-        if (ok && (both || !sg.by_keys || slot == 0)) {
-            if (both || slot == 0) ok = att_warp_wait(&sm.ofull[0], no[0] & 1, &sm.abort, p.timeout_ns);
-            if (ok && (both || (!sg.by_keys && slot == 1))) ok = att_warp_wait(&sm.ofull[1], no[1] & 1, &sm.abort, p.timeout_ns);
-        } else if (ok) {       // slot 1 without a tile: the products that read the queries have completed
-            ok = att_warp_wait(&sm.ofull[0], no[0] & 1, &sm.abort, p.timeout_ns);
-        }
-        ++no[0];
-        if (!sg.by_keys || sg.T > 1) ++no[1];
-        if (!ok) break;
+        // the rows, out of tensor memory
+        if (!wait(&sm.ofull[slot], no & 1)) return;
         tc_fence_after();
-        float f[2] = {1.0f, 0.0f};
-        if (both) {
-            sm.ml[slot][tid][0] = m;
-            sm.ml[slot][tid][1] = l;
-            if (!both_here()) { ok = false; break; }
-            const float m2 = sm.ml[slot ^ 1][tid][0], l2 = sm.ml[slot ^ 1][tid][1];
-            // in the order of the slots, so that both compute the same
-            const float ma = slot ? m2 : m, mb = slot ? m : m2, la = slot ? l2 : l, lb = slot ? l : l2;
-            const float mm = fmaxf(ma, mb);
-            f[0] = ma == -INFINITY ? 0.0f : exp2_approx(ma - mm);
-            f[1] = mb == -INFINITY ? 0.0f : exp2_approx(mb - mm);
-            if (ma != ma || mb != mb) f[0] = f[1] = NAN;
-            m = mm;
-            l = la * f[0] + lb * f[1];
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-        const bool mend = *reinterpret_cast<volatile int*>(&sm.bad_value) == seg_no + 1;
-        const bool writes = busy && (both || !sg.by_keys || slot == 0);
-        const int col0 = both ? slot * (D / 2) : 0, cols = both ? D / 2 : D;
-        const Slot out = att_slot<D>(p, sg.own, sg.job, blockIdx.x, sg.whole, sg.first);
-        if (writes) {
-            for (int col = col0; col < col0 + cols; col += 32) {
-                float o[32];
+        if (busy) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+            const bool mend = sg.own && *reinterpret_cast<volatile int*>(&sm.bad_value[slot]) == no + 1;
+            float* const out = sg.out;
+            const int R = sg.R, r = sg.out_row + tid;
+            const int64_t at = row.tok * p.a.q_heads + row.head;
+#pragma unroll
+            for (int col = 0; col < D; col += 32) {
                 uint32_t y[32];
-                if (both) {
-                    uint32_t z[32];
-                    tc_ld_x32(tmem + kTmemO + lanes + col, y);
-                    tc_ld_x32(tmem + kTmemO + 128 + lanes + col, z);
-                    tc_wait_ld();
+                tc_ld_x32(to + col, y);
+                tc_wait_ld();
+                if (mend && row.valid)
+                    for (int e = 0; e < 32; ++e) {               // (rare: the loop is not unrolled)
+                        const float bad = att_bad_sum<D, kBf16>(c, p, sg, row.b, bits, col + e);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]) * f[0] + __uint_as_float(z[e]) * f[1];
-                } else {
-                    tc_ld_x32(to + col, y);
-                    tc_wait_ld();
+                        for (int i = 0; i < 32; ++i)
+                            if (i == e) y[i] = __float_as_uint(__uint_as_float(y[i]) + bad);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(y[e]);
-                }
-                if (mend && row.valid) att_add_bad<D, kBf16>(c, p, sg, row, bits, col, o);
-                if (row.valid && sg.direct) {
-                    uint16_t* to_row = static_cast<uint16_t*>(p.a.out_dev) + (row.tok * p.a.q_heads + row.head) * D + col;
+                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * inv);
+                const auto f = [&](int e) { return __uint_as_float(y[e]); };
+                if (row.valid && !out) {
+                    uint16_t* to_row = static_cast<uint16_t*>(p.a.out_dev) + at * D + col;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         *reinterpret_cast<uint4*>(to_row + e) =
-                            make_uint4(pack_f16<kBf16>(o[e] * inv, o[e + 1] * inv), pack_f16<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
-                                       pack_f16<kBf16>(o[e + 4] * inv, o[e + 5] * inv), pack_f16<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+                            make_uint4(pack_f16<kBf16>(f(e), f(e + 1)), pack_f16<kBf16>(f(e + 2), f(e + 3)),
+                                       pack_f16<kBf16>(f(e + 4), f(e + 5)), pack_f16<kBf16>(f(e + 6), f(e + 7)));
                 } else if (row.valid) {
-                    float4* to_slot = reinterpret_cast<float4*>(out.base) + (int64_t)(col / 4) * out.R + r;
+                    float4* to_slot = reinterpret_cast<float4*>(out) + (int64_t)(col / 4) * R + r;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        to_slot[(int64_t)(e / 4) * out.R] = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+                        to_slot[(int64_t)(e / 4) * R] = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
                 }
                 __syncwarp();
             }
-            if (col0 == 0 && row.valid) {
-                if (!sg.direct) out.base[(int64_t)out.R * D + r] = lse2;
-                else if (p.a.lse_dev) p.a.lse_dev[row.tok * p.a.q_heads + row.head] = lse2 * 0.693147180559945309f;
+            if (row.valid) {
+                if (out) out[(int64_t)R * D + r] = lse2;
+                else if (p.a.lse_dev) p.a.lse_dev[at] = lse2 * 0.693147180559945309f;
             }
         }
-        if (both && !both_here()) { ok = false; break; }      // both have read both accumulators
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sege[slot][no & 1]);
     }
 }
 
@@ -745,19 +819,25 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < AttSmem<D>::kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.full[0][i], 1);
+            mbar_init(&sm.full[1][i], 1);
+            mbar_init(&sm.empty[0][i], 2);                 // both slots' MMA warps
+            mbar_init(&sm.empty[1][i], 1);
+            mbar_init(&sm.mended[i], 1);
         }
-        mbar_init(&sm.qfull, 8);
         for (int x = 0; x < 2; ++x) {
+            for (int e = 0; e < 2; ++e) {
+                mbar_init(&sm.segf[x][e], 1);
+                mbar_init(&sm.sege[x][e], 5);              // MMA warp, softmax warps
+            }
+            mbar_init(&sm.qfull[x], 4);
             mbar_init(&sm.sfull[x], 1);
             mbar_init(&sm.pfull[x], 4);
             mbar_init(&sm.ofull[x], 1);
+            mbar_init(&sm.drain[x], 1);
+            sm.bad_value[x] = 0;
         }
-        mbar_init(&sm.pair, 8);
-        mbar_init(&sm.drain, 1);
         sm.abort = 0;
-        sm.bad_value = 0;
         fence_barrier_init();
     }
     if (warp == kAttMma) {
@@ -765,28 +845,28 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
         tmem_relinquish();
     }
     tc_fence_before();
-    const Schedule sc = att_schedule<D>(c, p, sm);      // ends with a CTA barrier
+    const Schedule sc = att_schedule<D>(c, p, sm);         // ends with a CTA barrier
     tc_fence_after();
     grid_dependency_launch();
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
-        reg_grow<208>();
-        att_softmax<D, kBf16>(c, p, sc, sm, tmem);
+        reg_grow<216>();
+        att_softmax<D, kBf16>(c, p, sc.shared, sm, tmem);
     } else {
-        reg_shrink<80>();
-        if (warp == kAttProducer) {
+        reg_shrink<72>();
+        if (warp < kAttMma) {
             if (lane == 0) {
                 prefetch_tensormap(&kmap);
                 prefetch_tensormap(&vmap);
             }
-            att_produce<D>(c, p, sc, sm, &kmap, &vmap);
-        } else if (warp == kAttMma) {
-            att_mma<D, kBf16>(c, p, sc, sm, tmem);
-            if (lane == 0) {                            // every product has completed before the memory is freed
-                tc_commit(&sm.drain);
+            att_producer<D>(c, p, sc, sm, &kmap, &vmap, warp - kAttProducer);
+        } else {
+            const int slot = warp - kAttMma;
+            att_mma<D, kBf16>(p, sm, tmem, slot);
+            if (lane == 0) {                               // every product has completed before the memory is freed
+                tc_commit(&sm.drain[slot]);
                 const unsigned long long until = globaltimer_ns() + p.timeout_ns;
-                while (!mbar_try_wait(&sm.drain, 0))
-                    if (globaltimer_ns() > until) break;
+                while (!mbar_try_wait(&sm.drain[slot], 0) && globaltimer_ns() < until) {}
             }
         }
     }
@@ -800,102 +880,129 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
 
 // ---- merge -----------------------------------------------------------------------------------
 
-// The parts of a job: tiles x0 .. x0 + n of all W, over `grid` CTAs.
-struct Parts {
-    long long job;
-    int c0, c1;
-    bool own;
-};
-__device__ __forceinline__ Parts att_parts(bool own, long long job, long long x0, long long n, long long W, int grid) {
-    Parts q;
-    q.own = own;
-    q.job = job;
-    const long long n_cta = min((long long)grid, W);
-    q.c0 = (int)min(((x0 + 1) * n_cta - 1) / W, n_cta - 1);
-    q.c1 = (int)min(((x0 + n) * n_cta - 1) / W, n_cta - 1);
-    return q;
-}
-template <int D>
-__device__ __forceinline__ Slot att_part(const AttendParams& p, const Parts& q, int cta) {
-    return att_slot<D>(p, q.own, q.job, cta, q.c0 == q.c1, cta == q.c0);
-}
+constexpr int kMergeThreads = 256;
+constexpr int kMergeParts = 1024;              // at most 2 x 152 parts of each of three jobs, on any grid up to 340 CTAs
 
-constexpr int kMergeRows = 32;
-
-// A CTA per (head, unit of a stream, 32 rows): out = sum of w_i part_i, w_i = 2^(lse_i - lse).
+// A CTA per (head, unit of a stream, `rows` rows): out = sum of w_i part_i, w_i = 2^(lse_i - lse),
+// over the parts of the rows' own job and, where the stream shares the prefix, of the shared job
+// (two of them when the rows lie in two units).  The list of parts goes to shared memory, a warp
+// per row finds the weights' base, then every four columns of a row have a thread, or several that
+// take parts in turn where there are few rows.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int groups) {
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int rows, int groups) {
+    constexpr int kChunks = D / 4;
+    __shared__ Slot s_part[kMergeParts];
+    __shared__ float s_m[16], s_inv[16];
+    __shared__ float4 s_acc[kMergeThreads];
+    __shared__ uint2 s_out[16][kChunks + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, units = p.a.streams * p.U;
+    long long blk = blockIdx.x;
+    const int group = (int)(blk % groups); blk /= groups;
+    const int unit = (int)(blk % units), h = (int)(blk / units);
     grid_dependency_wait();
-    __shared__ float s_m[kMergeRows], s_inv[kMergeRows];
-    __shared__ uint2 s_out[kMergeRows][D / 4 + 1];
     const int shared = (int)p.head[kHeadShared];
-    const long long W_sh = p.head[kHeadTilesSh], W1 = p.head[kHeadTilesOwn], W = W_sh + (long long)c.Hkv * W1;
-    const int units = p.a.streams * p.U;
-    long long b = blockIdx.x;
-    const int group = (int)(b % groups); b /= groups;
-    const int unit = (int)(b % units), h = (int)(b / units);
     const OwnUnit u = att_unit(c, p, unit, shared);
-    const int row0 = group * kMergeRows, n = min(kMergeRows, u.nrows - row0);
+    const int row0 = group * rows, n = min(rows, u.nrows - row0);
     if (n <= 0) return;
-    const Parts own = att_parts(true, (long long)h * units + unit, W_sh + (long long)h * W1 + p.cum[unit], u.tiles(), W, grid);
+    const long long W1 = p.head[kHeadOwn];
     const bool shares = u.begin > 0;
-    if (!shares && own.c0 == own.c1) return;            // written by its only segment
-    const int s = unit / p.U, tiles_sh = (shared + kKeyTile - 1) / kKeyTile;
-    // rows of this stream among the packed rows of all: they may cross from one shared unit to the next
+    const int s = unit / p.U;
+    // rows of this stream among the packed rows of all: they may lie in two shared units
     const long long packed = (long long)s * p.a.block * p.G + u.r0 + row0;
-    const auto shared_parts = [&](int row) {
-        const long long job = (long long)h * p.U_sh + (packed + row) / kUnitRows;
-        return att_parts(false, job, job * tiles_sh, tiles_sh, W, grid);
-    };
-    const auto each = [&](int row, auto f) {
-        for (int i = own.c0; i <= own.c1; ++i) f(att_part<D>(p, own, i), u.r0 % kUnitRows + row0 + row);
-        if (!shares) return;
-        const Parts q = shared_parts(row);
-        for (int i = q.c0; i <= q.c1; ++i) f(att_part<D>(p, q, i), (int)((packed + row) % kUnitRows));
-    };
-    const int64_t first_tok = (int64_t)s * p.a.block;
-    if (threadIdx.x < n) {
-        const int row = threadIdx.x;
-        float m = -INFINITY, z = 0.0f;
-        bool nan = false;
-        each(row, [&](const Slot& sl, int r) {
-            const float x = sl.base[(int64_t)sl.R * D + r];
-            m = fmaxf(m, x);
-            nan |= x != x;
-        });
-        const float ref = m == -INFINITY ? 0.0f : m;
-        each(row, [&](const Slot& sl, int r) { z += exp2_approx(sl.base[(int64_t)sl.R * D + r] - ref); });
-        if (nan) z = NAN;
-        s_m[row] = ref;
-        s_inv[row] = z == 0.0f ? 0.0f : 1.0f / z;
-        if (p.a.lse_dev) {
-            const int i = u.r0 + row0 + row, t = i / p.G;
-            p.a.lse_dev[(first_tok + t) * p.a.q_heads + h * p.G + (i - t * p.G)] =
-                z == 0.0f ? -INFINITY : (ref + log2f(z)) * 0.693147180559945309f;
+    const long long unit_a = packed / p.rows_sh(), unit_b = (packed + n - 1) / p.rows_sh();
+    // parts of job j: first list entry, count, workers
+    int count[3] = {0, 0, 0};
+    {
+        const JobList L = att_list(c, p, p.wide_own != 0, shared, W1, grid);
+        const long long x = L.W_sh + (long long)h * L.W1 + p.cum[unit] + L.pad, job = (long long)h * units + unit;
+        const int c0 = L.worker(x), c1 = L.worker(x + u.tiles() - 1);
+        if (!shares && c0 == c1) return;       // written by its only segment
+        count[0] = c1 - c0 + 1;
+        for (int i = tid; i < count[0]; i += kMergeThreads)
+            s_part[i] = att_slot<D>(p, p.wide_own, true, job, c0 + i, c0 == c1, i == 0);
+    }
+    if (shares) {
+        const JobList L = att_list(c, p, p.wide_sh != 0, shared, W1, grid);
+        for (int k = 0; k <= (int)(unit_b - unit_a); ++k) {
+            const long long job = (long long)h * p.U_sh + unit_a + k, x = job * (L.tiles_sh + L.pad) + L.pad;
+            const int c0 = L.worker(x), c1 = L.worker(x + L.tiles_sh - 1), at = count[0] + count[1];
+            count[1 + k] = c1 - c0 + 1;
+            for (int i = tid; i < count[1 + k]; i += kMergeThreads)
+                s_part[at + i] = att_slot<D>(p, p.wide_sh, false, job, c0 + i, c0 == c1, i == 0);
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
-        const int row = e % n, x = e / n;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float ref = s_m[row], inv = s_inv[row];
-        each(row, [&](const Slot& sl, int r) {
-            const float w = exp2_approx(sl.base[(int64_t)sl.R * D + r] - ref) * inv;
-            const float4 v = reinterpret_cast<const float4*>(sl.base)[(int64_t)x * sl.R + r];
-            if (w != 0.0f) {                             // a part that saw nothing may hold nothing
-                acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-                acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-            }
-        });
-        s_out[row][x] = make_uint2(pack_f16<kBf16>(acc.x, acc.y), pack_f16<kBf16>(acc.z, acc.w));
+    const int cut = (int)((unit_a + 1) * p.rows_sh() - packed);   // rows from here on are in the second shared unit
+    // a row's parts: its own job's, and one shared job's; part i of them, and the row in its slot
+    const auto parts_of = [&](int row) { return count[0] + (row < cut ? count[1] : count[2]); };
+    const auto part = [&](int row, int i) { return s_part[i < count[0] || row < cut ? i : i + count[1]]; };
+    const auto slot_row = [&](int row, int i) { return i < count[0] ? row0 + row : (int)((packed + row) % p.rows_sh()); };
+    const auto lse_of = [&](int row, int i) {
+        const Slot sl = part(row, i);
+        return sl.base[(int64_t)sl.R * D + slot_row(row, i)];
+    };
+    const auto place = [&](int row) {          // of a row in the output
+        const int i = u.r0 + row0 + row, t = i / p.G;
+        return ((int64_t)s * p.a.block + t) * p.a.q_heads + h * p.G + (i - t * p.G);
+    };
+    for (int row = warp; row < n; row += kMergeThreads / 32) {
+        const int np = parts_of(row);
+        float m = -INFINITY, z = 0.0f;
+        bool nan = false;
+        for (int i = lane; i < np; i += 32) {
+            const float x = lse_of(row, i);
+            m = fmaxf(m, x);
+            nan |= x != x;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float ref = m == -INFINITY ? 0.0f : m;
+        for (int i = lane; i < np; i += 32) z += exp2_approx(lse_of(row, i) - ref);
+        z = warp_sum(z);
+        if (__any_sync(0xFFFFFFFFu, nan)) z = NAN;
+        if (lane == 0) {
+            s_m[row] = ref;
+            s_inv[row] = z == 0.0f ? 0.0f : 1.0f / z;
+            if (p.a.lse_dev) p.a.lse_dev[place(row)] = z == 0.0f ? -INFINITY : (ref + log2f(z)) * 0.693147180559945309f;
+        }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < n * (D / 4); e += 256) {
-        const int row = e / (D / 4), x = e % (D / 4);
-        const int i = u.r0 + row0 + row, t = i / p.G;
-        uint16_t* out = static_cast<uint16_t*>(p.a.out_dev) +
-                        ((first_tok + t) * p.a.q_heads + h * p.G + (i - t * p.G)) * (int64_t)D;
-        reinterpret_cast<uint2*>(out)[x] = s_out[row][x];
+    const int e_all = n * kChunks;
+    const int turns = max(1, kMergeThreads / e_all);              // threads that share a row's four columns
+    for (int e0 = 0; e0 < e_all; e0 += kMergeThreads) {
+        const int e = turns > 1 ? tid % e_all : e0 + tid, turn = turns > 1 ? tid / e_all : 0;
+        const int row = e % n, x = e / n;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (e < e_all && turn < turns) {
+            const int np = parts_of(row);
+            const float ref = s_m[row], inv = s_inv[row];
+#pragma unroll 4
+            for (int i = turn; i < np; i += turns) {
+                const Slot sl = part(row, i);
+                const int r = slot_row(row, i);
+                const float w = exp2_approx(sl.base[(int64_t)sl.R * D + r] - ref) * inv;
+                const float4 v = reinterpret_cast<const float4*>(sl.base)[(int64_t)x * sl.R + r];
+                if (w != 0.0f) {                                  // a part that saw nothing adds nothing
+                    acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+                    acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
+                }
+            }
+        }
+        if (turns > 1) {
+            s_acc[tid] = acc;
+            __syncthreads();
+            if (tid < e_all)
+                for (int k = 1; k < turns; ++k) {
+                    const float4 v = s_acc[tid + k * e_all];
+                    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+                }
+        }
+        if (e < e_all && turn == 0) s_out[row][x] = make_uint2(pack_f16<kBf16>(acc.x, acc.y), pack_f16<kBf16>(acc.z, acc.w));
+    }
+    __syncthreads();
+    for (int e = tid; e < e_all; e += kMergeThreads) {
+        const int row = e / kChunks, x = e % kChunks;
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out_dev) + place(row) * D)[x] = s_out[row][x];
     }
 }
 
@@ -913,23 +1020,28 @@ int check_shape(const moe_mxfp4_cache* c, int32_t streams, int32_t block, int32_
     return MOE_OK;
 }
 
-// Sections of the workspace.
+// Sections of the workspace, and the units.
 struct AttendLayout {
-    int G, U, U_sh, R_own;
-    size_t cum, split, whole_sh, whole_own, total;
+    int G, wide_sh, wide_own, U, U_sh, R_own;
+    size_t cum, split_wide, split_narrow, whole_sh, whole_own, total;
 };
 AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int q_heads) {
     AttendLayout L;
     L.G = q_heads / c->cfg.kv_heads;
-    const int64_t rows = (int64_t)block * L.G;
-    L.U = (int)((rows + moe::kUnitRows - 1) / moe::kUnitRows);
-    L.U_sh = (int)((streams * rows + moe::kUnitRows - 1) / moe::kUnitRows);
-    L.R_own = (int)(rows < moe::kUnitRows ? (rows + 3) / 4 * 4 : moe::kUnitRows);   // slots are whole float4s
+    const int64_t rows = (int64_t)block * L.G, all = streams * rows;
+    L.wide_own = rows > 128;
+    L.wide_sh = all > 128;
+    const int ro = L.wide_own ? 256 : 128, rs = L.wide_sh ? 256 : 128;
+    L.U = (int)((rows + ro - 1) / ro);
+    L.U_sh = (int)((all + rs - 1) / rs);
+    L.R_own = (int)(rows < ro ? (rows + 3) / 4 * 4 : ro);   // slots are whole float4s
     const size_t row = (size_t)(c->cfg.head_dim + 1) * 4, jobs = (size_t)c->cfg.kv_heads;
+    const size_t split = up256(4 * (size_t)c->sm_count * 128 * row);
     L.cum = 256;
-    L.split = L.cum + up256((size_t)streams * L.U * 8);
-    L.whole_sh = L.split + up256(2 * (size_t)c->sm_count * moe::kUnitRows * row);
-    L.whole_own = L.whole_sh + up256(jobs * L.U_sh * moe::kUnitRows * row);
+    L.split_wide = L.cum + up256((size_t)streams * L.U * 8);
+    L.split_narrow = L.split_wide + split;
+    L.whole_sh = L.split_narrow + split;
+    L.whole_own = L.whole_sh + up256(jobs * L.U_sh * rs * row);
     L.total = L.whole_own + up256(jobs * streams * L.U * L.R_own * row);
     return L;
 }
@@ -938,14 +1050,16 @@ template <int D, bool kBf16>
 int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, const moe::AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(moe::AttSmem<D>);
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
-    auto* kern = moe::attend_kernel<D, kBf16>;
-    const int groups = (p.R_own + moe::kMergeRows - 1) / moe::kMergeRows;
-    const int64_t merge = (int64_t)c->cfg.kv_heads * p.a.streams * p.U * groups;
-    if (merge > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-    kern<<<c->sm_count, moe::kAttThreads, smem, st>>>(v, p, c->maps[2 * layer], c->maps[2 * layer + 1]);
+    // rows of a merging CTA: as many as leave two CTAs for every SM, at most 16
+    const int64_t jobs = (int64_t)c->cfg.kv_heads * p.a.streams * p.U;
+    int rows = 16;
+    while (rows > 2 && jobs * ((p.R_own + rows - 1) / rows) < 2 * c->sm_count) rows /= 2;
+    const int groups = (p.R_own + rows - 1) / rows;
+    if (jobs * groups > 0x7FFFFFFF || 6 * c->sm_count > moe::kMergeParts) return MOE_ERR_UNSUPPORTED;
+    moe::attend_kernel<D, kBf16><<<c->sm_count, moe::kAttThreads, smem, st>>>(v, p, c->maps[2 * layer], c->maps[2 * layer + 1]);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3((unsigned)merge), dim3(256), 0, st, v, p, c->sm_count,
-                                 groups) == cudaSuccess
+    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3((unsigned)(jobs * groups)), dim3(moe::kMergeThreads), 0,
+                                 st, v, p, c->sm_count, rows, groups) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -994,6 +1108,8 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     char* ws = static_cast<char*>(workspace_dev);
     p.v_pool = static_cast<const uint16_t*>(c->layers[layer].v_dev);
     p.G = L.G;
+    p.wide_sh = L.wide_sh;
+    p.wide_own = L.wide_own;
     p.U = L.U;
     p.U_sh = L.U_sh;
     p.R_own = L.R_own;
@@ -1006,7 +1122,8 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     p.timeout_ns = (unsigned long long)c->cfg.timeout_us * 1000ull;
     p.head = reinterpret_cast<long long*>(ws);
     p.cum = reinterpret_cast<long long*>(ws + L.cum);
-    p.split = reinterpret_cast<float*>(ws + L.split);
+    p.split_wide = reinterpret_cast<float*>(ws + L.split_wide);
+    p.split_narrow = reinterpret_cast<float*>(ws + L.split_narrow);
     p.whole_sh = reinterpret_cast<float*>(ws + L.whole_sh);
     p.whole_own = reinterpret_cast<float*>(ws + L.whole_own);
     const moe::CacheView v = moe::cache_view(c, state_dev);
