@@ -44,18 +44,20 @@ struct AttendParams {
     moe_mxfp4_attend_args a;
     const uint16_t* v_pool;
     int G;                     // query heads per kv head
+    uint32_t g_mul;            // ceil(2^32 / G): x / G = high word of x g_mul for x < 2^16 (G = 1 apart)
     int wide_sh, wide_own;     // units of 256 rows (else 128) over the shared prefix, over the own keys
     int U, U_sh;               // units of a stream's own rows, of all streams' rows
     int R_own;                 // rows of a slot for a stream's unit, a multiple of 4
     float c;                   // |scale| log2 e
     uint32_t q_flip;           // sign flips of a pair of query elements (a negative scale)
     unsigned long long timeout_ns;
-    long long* head;           // workspace: the schedule for the merge
-    long long* cum;            // first own place of each unit (of a head)
+    int* head;                 // workspace: the schedule for the merge
+    int* cum;                  // first own place of each unit (of a head)
     float* split_wide;         // partial rows of split jobs: 2 per worker, 256 rows each, ...
     float* split_narrow;       // ... 128 rows each
     float* whole_sh;           // partial rows of whole jobs: shared, ...
     float* whole_own;          // ... and own
+    __device__ __forceinline__ int div_g(int x) const { return G == 1 ? x : (int)__umulhi((uint32_t)x, g_mul); }
     __host__ __device__ int rows_sh() const { return wide_sh ? 256 : 128; }
     __host__ __device__ int rows_own() const { return wide_own ? 256 : 128; }
 };
@@ -80,12 +82,12 @@ struct AttSmem {
     uint8_t kv[kStages][kTileBytes];
     uint64_t full[2][kStages], empty[2][kStages];            // [0]: wide, [1]: narrow
     uint64_t mended[kStages];                                // wide: slot 0's MMA warp has mended the V tile
-    uint64_t segf[2][2], sege[2][2], qfull[2], sfull[2], pfull[2], ofull[2], drain[2];
+    uint64_t turn[2];                                        // wide: the slot's turn on the tensor core
+    uint64_t segf[2][2], sege[2][2], qfull[2], sfull[2], phalf[2], pfull[2], ofull[2], drain[2];
     Segment seg[2][2];
-    long long scan[3][12];
+    int scan[3][12];
     uint32_t tmem;
-    int first_unit[2];
-    long long first_off[2];
+    int first_unit[2], first_off[2];
     int bad_value[2];                                        // last segment (+ 1) with a non-finite block value
     int abort;
 };
@@ -122,12 +124,14 @@ __device__ __forceinline__ int att_used(const AttendParams& p, int s) {
 __device__ __forceinline__ bool att_shares(const CacheView& c, const AttendParams& p, int s, int shared) {
     if (shared <= 0) return false;
     const int i = (shared >> c.page_shift) - 1;
-    return c.length()[s] >= shared && c.held()[s] > i && c.table(s)[i] == c.table(p.a.shared_stream)[i];
+    const int len = c.length()[s], held = c.held()[s], mine = c.table(s)[i], theirs = c.table(p.a.shared_stream)[i];
+    return (len >= shared) & (held > i) & (mine == theirs);
 }
 __device__ __forceinline__ int att_shared(const CacheView& c, const AttendParams& p) {
     const int n = p.a.shared_tokens;
     if (n <= 0) return 0;
-    return c.length()[p.a.shared_stream] >= n && c.held()[p.a.shared_stream] >= (n >> c.page_shift) ? n : 0;
+    const int len = c.length()[p.a.shared_stream], held = c.held()[p.a.shared_stream];
+    return (len >= n) & (held >= (n >> c.page_shift)) ? n : 0;
 }
 
 // A unit of a stream's own rows: its keys [begin, end) and rows.
@@ -140,52 +144,59 @@ __device__ __forceinline__ OwnUnit att_unit(const CacheView& c, const AttendPara
     const int s = unit / p.U;
     if (s >= p.a.streams) return w;
     w.r0 = (unit - s * p.U) * p.rows_own();
-    const int used = att_used(p, s), rows = used * p.G;
+    const int ctx = att_ctx(c, s), used = att_used(p, s), rows = used * p.G;   // (loads side by side)
+    const bool shares = att_shares(c, p, s, shared);
     if (w.r0 >= rows) return w;
     w.nrows = min(p.rows_own(), rows - w.r0);
-    w.ctx = att_ctx(c, s);
-    w.end = w.ctx + (p.a.mask_dev ? used : (w.r0 + w.nrows - 1) / p.G + 1);
-    w.begin = att_shares(c, p, s, shared) ? shared : 0;
+    w.ctx = ctx;
+    w.end = ctx + (p.a.mask_dev ? used : (w.r0 + w.nrows - 1) / p.G + 1);
+    w.begin = shares ? shared : 0;
     return w;
 }
 
 // The jobs of one list (wide or narrow): shared ones, then own ones, each with its places in a
-// row of W: a job with n tiles has pad + n, tile i at place pad + i.
+// row of W (below 2^31: checked on the host): a job with n tiles has pad + n, tile i at place
+// pad + i.  Worker w has q places, one more when w < rem.
 struct JobList {
     int pad, tiles_sh;
     bool has_sh, has_own;
-    long long W_sh, W1, W;            // places of the shared jobs, of one head's own jobs, of all
-    long long workers;
-    __device__ long long first(long long w) const { return W * w / workers; }
-    __device__ int worker(long long place) const { return (int)min(((place + 1) * workers - 1) / W, workers - 1); }
+    int W_sh, W1, W;                  // places of the shared jobs, of one head's own jobs, of all
+    int workers, q, rem;
+    __device__ int first(int w) const { return q * w + min(w, rem); }
+    __device__ int worker(int place) const {
+        const int big = rem * (q + 1);
+        return min(place < big ? place / (q + 1) : rem + (place - big) / q, workers - 1);
+    }
 };
 // W1: places of one head's own jobs (with this list's padding).
-__device__ __forceinline__ JobList att_list(const CacheView& c, const AttendParams& p, bool wide, int shared, long long W1, int grid) {
+__device__ __forceinline__ JobList att_list(const CacheView& c, const AttendParams& p, bool wide, int shared, int W1, int grid) {
     JobList L;
     L.pad = wide ? kPadWide : kPadNarrow;
     L.has_sh = shared > 0 && (p.wide_sh != 0) == wide;
     L.has_own = (p.wide_own != 0) == wide;
     L.tiles_sh = (shared + kKeyTile - 1) / kKeyTile;
-    L.W_sh = L.has_sh ? (long long)c.Hkv * p.U_sh * (L.tiles_sh + L.pad) : 0;
+    L.W_sh = L.has_sh ? c.Hkv * p.U_sh * (L.tiles_sh + L.pad) : 0;
     L.W1 = L.has_own ? W1 : 0;
-    L.W = L.W_sh + (long long)c.Hkv * L.W1;
-    L.workers = min((long long)(wide ? grid : 2 * grid), L.W);   // none of them without a place
+    L.W = L.W_sh + c.Hkv * L.W1;
+    L.workers = min(wide ? grid : 2 * grid, L.W);                // none of them without a place
+    L.q = L.workers ? L.W / L.workers : 0;
+    L.rem = L.W - L.q * L.workers;
     return L;
 }
 
 // Exclusive prefix over the CTA's threads of a value per thread, and the sum.
 template <int D>
-__device__ __forceinline__ long long att_scan(AttSmem<D>& sm, int k, long long v, long long* total) {
+__device__ __forceinline__ int att_scan(AttSmem<D>& sm, int k, int v, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) sm.scan[k][warp] = x;
     __syncthreads();
-    long long before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kAttThreads / 32; ++w) {
         if (w < warp) before += sm.scan[k][w];
@@ -199,15 +210,14 @@ __device__ __forceinline__ long long att_scan(AttSmem<D>& sm, int k, long long v
 // Shared tokens in use and the places of one head's own jobs; writes what the merge needs, and
 // where each slot's own jobs begin.
 struct Schedule {
-    int shared;
-    long long W1;
+    int shared, W1;
 };
 template <int D>
 __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttSmem<D>& sm) {
     Schedule sc;
     const int units = p.a.streams * p.U, tid = threadIdx.x, pad = p.wide_own ? kPadWide : kPadNarrow;
     const int shared = att_shared(c, p);
-    long long with = 0, without = 0, sharers = 0, t;
+    int with = 0, without = 0, sharers = 0, t;
     for (int i = tid; i < units; i += kAttThreads) {
         const OwnUnit w = att_unit(c, p, i, shared);
         if (w.nrows == 0) continue;
@@ -228,11 +238,10 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     }
     // the unit, and the place in it, where each slot's own jobs begin
     const JobList L = att_list(c, p, p.wide_own != 0, sc.shared, sc.W1, gridDim.x);
-    long long y[2];
+    int y[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const long long w = p.wide_own ? blockIdx.x : x * (long long)gridDim.x + blockIdx.x;
-        const long long at = w < L.workers ? L.first(w) : 0;
+        const int w = p.wide_own ? blockIdx.x : x * gridDim.x + blockIdx.x, at = w < L.workers ? L.first(w) : 0;
         y[x] = at > L.W_sh ? (at - L.W_sh) % L.W1 : 0;
     }
     if (tid < 2) {
@@ -241,13 +250,13 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     }
     __syncthreads();
     if (blockIdx.x == 0 || y[0] > 0 || y[1] > 0) {
-        long long at = 0;
+        int at = 0;
         for (int i0 = 0; i0 < units; i0 += kAttThreads) {
             const int i = i0 + tid;
             int n = i < units ? att_unit(c, p, i, sc.shared).tiles() : 0;
             if (n > 0) n += pad;
-            long long sum;
-            const long long x0 = at + att_scan(sm, 0, n, &sum);
+            int sum;
+            const int x0 = at + att_scan(sm, 0, n, &sum);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (n > 0 && x0 <= y[x] && y[x] < x0 + n) {
@@ -273,20 +282,19 @@ struct Slot {
     int R;
 };
 template <int D>
-__device__ __forceinline__ Slot att_slot(const AttendParams& p, bool wide, bool own, long long job, int worker, bool whole, bool first) {
+__device__ __forceinline__ Slot att_slot(const AttendParams& p, bool wide, bool own, int job, int worker, bool whole, bool first) {
     if (!whole) {                              // at most one part of a job it does not begin and one that it does
         const int R = wide ? 256 : 128;
         return {(wide ? p.split_wide : p.split_narrow) + (2 * (int64_t)worker + (first ? 1 : 0)) * R * (D + 1), R};
     }
     const int R = own ? p.R_own : p.rows_sh();
-    return {(own ? p.whole_own : p.whole_sh) + job * R * (D + 1), R};
+    return {(own ? p.whole_own : p.whole_sh) + (int64_t)job * R * (D + 1), R};
 }
 
 // A producer warp's walk over the segments of one list; all lanes hold the same values but `n`.
 struct Walk {
-    long long v, end;          // places
-    int h, unit;
-    long long off;
+    int v, end;                // places
+    int h, unit, off;
     int base, n;               // tiles of the units base + lane
 };
 template <int D>
@@ -298,7 +306,7 @@ __device__ __forceinline__ Walk att_walk(const JobList& L, const AttSmem<D>& sm,
     w.unit = 0;
     w.off = 0;
     if (L.has_own && w.v >= L.W_sh && w.v < w.end) {
-        w.h = (int)((w.v - L.W_sh) / L.W1);
+        w.h = (w.v - L.W_sh) / L.W1;
         w.unit = sm.first_unit[slot];
         w.off = sm.first_off[slot];
     }
@@ -311,17 +319,16 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
                          int worker, Walk& w, Segment& sg) {
     for (;;) {
         if (w.v >= w.end) return false;
-        int n, begin;                          // tiles of the job, first key
-        long long o0, job;                     // first place of it here
+        int n, begin, o0, job;                 // tiles of the job, first key; first place of it here
         if (w.v < L.W_sh) {
             job = w.v / (L.tiles_sh + L.pad);
             o0 = w.v - job * (L.tiles_sh + L.pad);
             n = L.tiles_sh;
             begin = 0;
             sg.own = 0;
-            sg.h = (int)(job / p.U_sh);
-            sg.r0 = (int)(job % p.U_sh) * p.rows_sh();
-            sg.nrows = (int)min((long long)p.rows_sh(), (long long)p.a.streams * p.a.block * p.G - sg.r0);
+            sg.h = job / p.U_sh;
+            sg.r0 = (job - sg.h * p.U_sh) * p.rows_sh();
+            sg.nrows = min(p.rows_sh(), p.a.streams * p.a.block * p.G - sg.r0);
             sg.s = p.a.shared_stream;
             sg.key_end = sg.ctx = sc.shared;
         } else {
@@ -347,7 +354,7 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
             n = u.tiles();
             begin = u.begin;
             o0 = w.off;
-            job = (long long)w.h * units + w.unit;
+            job = w.h * units + w.unit;
             sg.own = 1;
             sg.h = w.h;
             sg.s = w.unit / p.U;
@@ -358,9 +365,9 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
             w.off = 0;
             ++w.unit;
         }
-        const long long o1 = min((long long)(L.pad + n), o0 + (w.end - w.v));
+        const int o1 = min(L.pad + n, o0 + (w.end - w.v));
         w.v += o1 - o0;
-        const int t0 = (int)max(o0 - L.pad, 0ll), t1 = (int)max(o1 - L.pad, 0ll);
+        const int t0 = max(o0 - L.pad, 0), t1 = max(o1 - L.pad, 0);
         if (t1 <= t0) continue;                // places without a tile
         const bool whole = t1 - t0 == n;
         const Slot to = att_slot<D>(p, wide, sg.own, job, worker, whole, t0 == 0);
@@ -382,11 +389,12 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
 template <int D>
 struct Ring {
     AttSmem<D>* sm;
-    int wide, first, stages;
+    int wide, first, stages, log;                            // stages = 2^log
     __device__ Ring(AttSmem<D>& s, bool w, int slot)
-        : sm(&s), wide(w), first(w ? 0 : slot * (AttSmem<D>::kStages / 2)), stages(w ? AttSmem<D>::kStages : AttSmem<D>::kStages / 2) {}
-    __device__ int stage(uint32_t i) const { return first + (int)(i % stages); }
-    __device__ uint32_t round(uint32_t i) const { return (i / stages) & 1; }
+        : sm(&s), wide(w), first(w ? 0 : slot * (AttSmem<D>::kStages / 2)), stages(w ? AttSmem<D>::kStages : AttSmem<D>::kStages / 2),
+          log((AttSmem<D>::kStages == 4 ? 2 : 3) - (w ? 0 : 1)) {}
+    __device__ int stage(uint32_t i) const { return first + (int)(i & (stages - 1)); }
+    __device__ uint32_t round(uint32_t i) const { return (i >> log) & 1; }
     __device__ uint64_t* full(uint32_t i) const { return &sm->full[wide ? 0 : 1][stage(i)]; }
     __device__ uint64_t* empty(uint32_t i) const { return &sm->empty[wide ? 0 : 1][stage(i)]; }
 };
@@ -518,24 +526,25 @@ template <int D, bool kBf16>
 __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, int slot) {
     using SM = AttSmem<D>;
     constexpr uint32_t idesc_s = idesc_f16(128, 128, kBf16, false), idesc_o = idesc_f16(128, D, kBf16, true);
-    const int lane = threadIdx.x & 31;
+    const bool issues = elect_one();
     const uint32_t ts = tmem + kTmemS + 128 * slot, to = tmem + kTmemO + 128 * slot, q = smem_u32(sm.q[slot]);
-    uint32_t used[2] = {0, 0}, np = 0, mends = 0;          // tiles of each ring so far; mends: a bit per stage
+    uint32_t used_wide = 0, used_narrow = 0, np = 0, turns = 0, mends = 0;   // mends: a bit per stage
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return att_warp_wait(bar, parity, &sm.abort, p.timeout_ns); };
     for (int no = 0;; ++no) {
         if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
         const Segment& sg = sm.seg[slot][no & 1];
-        const int T = sg.T, wide = sg.wide, key0 = sg.key0, ctx = sg.ctx, key_end = sg.key_end;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sege[slot][no & 1]);
+        const int T = uniform(sg.T), wide = uniform(sg.wide), key0 = uniform(sg.key0), ctx = uniform(sg.ctx);
+        const int key_end = uniform(sg.key_end);
+        if (issues) mbar_arrive(&sm.sege[slot][no & 1]);
         if (T == 0) return;
         const Ring<D> ring(sm, wide, slot);
-        uint32_t n = used[wide];
-        used[wide] += 2 * T;
+        uint32_t n = wide ? used_wide : used_narrow;       // (next tile of the ring)
+        if (wide) used_wide += 2 * T;
+        else used_narrow += 2 * T;
         const auto scores = [&]() {                        // S of the tile whose K is tile n of the ring
             if (!wait(ring.full(n), ring.round(n))) return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (issues) {
                 const uint32_t k = smem_u32(sm.kv[ring.stage(n)]);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -548,8 +557,18 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
             __syncwarp();
             return true;
         };
+        // Wide units: the slots take turns, each with the products of a step in one go, so that one
+        // slot's scores are ready while the other's products run (interleaved, both would wait for all).
+        const auto begin_turn = [&]() { return !wide || wait(&sm.turn[slot], (turns & 1) ^ (slot == 0)); };
+        const auto end_turn = [&]() {
+            if (!wide) return;
+            ++turns;
+            if (issues) mbar_arrive(&sm.turn[slot ^ 1]);
+            __syncwarp();
+        };
         if (!wait(&sm.qfull[slot], no & 1)) return;
-        if (!scores()) return;
+        if (!begin_turn() || !scores()) return;
+        end_turn();
         for (int t = 0; t < T; ++t, ++n) {
             ++n;                                           // V of tile t
             if (!wait(ring.full(n), ring.round(n))) return;
@@ -557,7 +576,7 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
             if (j0 + kKeyTile > ctx) {                     // block positions, or the end of the keys
                 if (!wide || slot == 0) {
                     const bool bad = att_mend_v<D, kBf16>(sm.kv[st], min(max(ctx - j0, 0), kKeyTile), min(max(key_end - j0, 0), kKeyTile));
-                    if (lane == 0) {
+                    if (issues) {
                         if (bad) {
                             *reinterpret_cast<volatile int*>(&sm.bad_value[slot]) = no + 1;
                             if (wide) *reinterpret_cast<volatile int*>(&sm.bad_value[1]) = no + 1;
@@ -571,13 +590,21 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
                     mends ^= 1u << st;
                 }
             }
+            const uint32_t v = smem_u32(sm.kv[st]);
+            if (!wait(&sm.phalf[slot], np & 1) || !begin_turn()) return;
+            tc_fence_after();
+            if (issues) {
+#pragma unroll
+                for (int i = 0; i < kKeyTile / 32; ++i)
+                    tc_mma_f16_ts(to, ts + 8 * i, smem_desc_mn_sw128(v + i * 2048, SM::kPanel), idesc_o, t > 0 || i > 0);
+            }
+            __syncwarp();
             if (!wait(&sm.pfull[slot], np++ & 1)) return;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t v = smem_u32(sm.kv[st]);
+            if (issues) {
 #pragma unroll
-                for (int i = 0; i < kKeyTile / 16; ++i)
-                    tc_mma_f16_ts(to, ts + 8 * i, smem_desc_mn_sw128(v + i * 2048, SM::kPanel), idesc_o, t > 0 || i > 0);
+                for (int i = kKeyTile / 32; i < kKeyTile / 16; ++i)
+                    tc_mma_f16_ts(to, ts + 8 * i, smem_desc_mn_sw128(v + i * 2048, SM::kPanel), idesc_o, 1);
                 tc_commit(ring.empty(n));
                 if (t + 1 == T) tc_commit(&sm.ofull[slot]);
             }
@@ -587,6 +614,7 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
                 if (!scores()) return;
                 --n;
             }
+            end_turn();
         }
     }
 }
@@ -624,16 +652,24 @@ __device__ __forceinline__ void att_load_q(const AttendParams& p, const Segment&
     const int tid = threadIdx.x & 127, x = tid % kChunks;
     const uint16_t* q = static_cast<const uint16_t*>(p.a.q_dev) + x * 8;
     const int64_t tok0 = sg.own ? (int64_t)sg.s * p.a.block : 0;
-    const int nrows = sg.nrows, r0 = sg.r0, h0 = sg.h * p.G;
+    const int nrows = sg.nrows, t0 = sg.r0 / p.G, g0 = sg.r0 - t0 * p.G;     // first row's token and head
+    q += (tok0 + t0) * p.a.q_stride + (int64_t)sg.h * p.G * D;
+    // all loads go out before the first store
+    uint4 v[kChunks];
 #pragma unroll
-    for (int row = tid / kChunks; row < 128; row += 128 / kChunks) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kChunks; ++i) {
+        const int row = tid / kChunks + i * (128 / kChunks);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < nrows) {
-            const int r = r0 + row, t = r / p.G;
-            v = *reinterpret_cast<const uint4*>(q + (tok0 + t) * p.a.q_stride + (int64_t)(h0 + r - t * p.G) * D);
-            v.x ^= p.q_flip; v.y ^= p.q_flip; v.z ^= p.q_flip; v.w ^= p.q_flip;
+            const int g = g0 + row, t = p.div_g(g);
+            v[i] = __ldg(reinterpret_cast<const uint4*>(q + t * p.a.q_stride + (g - t * p.G) * D));
         }
-        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int row = tid / kChunks + i * (128 / kChunks);
+        v[i].x ^= p.q_flip; v[i].y ^= p.q_flip; v[i].z ^= p.q_flip; v[i].w ^= p.q_flip;
+        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v[i];
     }
 }
 
@@ -700,28 +736,24 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
             if (!wait(&sm.sfull[slot], ns++ & 1)) return;
             tc_fence_after();
             if (busy) {
-                uint32_t x[4][32];
+                uint32_t x[4][32], vis[4];
+                const bool hidden = j0 > tail;
+                if (hidden) att_visible(masked, sg.ctx, sg.key_end, lim, bits, j0, vis);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tc_ld_x32(ts, x[0]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_ld_x32(ts + 32 * k, x[k]);
-                tc_wait_ld();
-                if (j0 > tail) {
-                    uint32_t vis[4];
-                    att_visible(masked, sg.ctx, sg.key_end, lim, bits, j0, vis);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {                    // the next 32 keys load while these are looked over
+                    tc_wait_ld(x[k]);
+                    if (k < 3) tc_ld_x32(ts + 32 * (k + 1), x[k < 3 ? k + 1 : 3]);
+                    if (hidden)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!(vis[k] >> e & 1)) x[k][e] = 0xFF800000u;
-                }
-                float mx[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mx[k] = __uint_as_float(x[k / 2][16 * (k & 1)]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(x[k / 2][16 * (k & 1) + e]));
+                    for (int e = 0; e < 32; e += 2)
+                        mx[(e / 2) & 3] = max3(mx[(e / 2) & 3], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
                 }
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.c;
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.c;
                 const bool passed = m != -INFINITY && top > m + kRescale;
                 if (__any_sync(0xFFFFFFFFu, passed)) {
                     const float f = passed ? exp2_approx(m - top) : 1.0f;
@@ -730,7 +762,7 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
                     for (int k = 0; k < D / 16; ++k) {
                         uint32_t o[16];
                         tc_ld_x16(to + 16 * k, o);
-                        tc_wait_ld();
+                        tc_wait_ld(o);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                         tc_st_x16(to + 16 * k, o);
@@ -752,9 +784,17 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
                         pk[e / 2] = pack_f16<kBf16>(a, b);
                     }
                     tc_st_x16(ts + 16 * k, pk);
+                    if (k == 1) {                                // the first half of the keys can go
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.phalf[slot]);
+                    }
                 }
                 l += ((sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1])) + ((sum[2][0] + sum[2][1]) + (sum[3][0] + sum[3][1]));
                 tc_wait_st();
+            } else if (lane == 0) {
+                mbar_arrive(&sm.phalf[slot]);
             }
             tc_fence_before();
             __syncwarp();
@@ -774,7 +814,7 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
             for (int col = 0; col < D; col += 32) {
                 uint32_t y[32];
                 tc_ld_x32(to + col, y);
-                tc_wait_ld();
+                tc_wait_ld(y);
                 if (mend && row.valid)
                     for (int e = 0; e < 32; ++e) {               // (rare: the loop is not unrolled)
                         const float bad = att_bad_sum<D, kBf16>(c, p, sg, row.b, bits, col + e);
@@ -816,7 +856,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
                                                                 const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) uint8_t raw[];       // the only shared memory: its tiles are 1024-byte aligned
     AttSmem<D>& sm = *reinterpret_cast<AttSmem<D>*>(raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < AttSmem<D>::kStages; ++i) {
             mbar_init(&sm.full[0][i], 1);
@@ -830,8 +870,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
                 mbar_init(&sm.segf[x][e], 1);
                 mbar_init(&sm.sege[x][e], 5);              // MMA warp, softmax warps
             }
+            mbar_init(&sm.turn[x], 1);
             mbar_init(&sm.qfull[x], 4);
             mbar_init(&sm.sfull[x], 1);
+            mbar_init(&sm.phalf[x], 4);
             mbar_init(&sm.pfull[x], 4);
             mbar_init(&sm.ofull[x], 1);
             mbar_init(&sm.drain[x], 1);
@@ -848,7 +890,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
     const Schedule sc = att_schedule<D>(c, p, sm);         // ends with a CTA barrier
     tc_fence_after();
     grid_dependency_launch();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = uniform(sm.tmem);
     if (warp < 8) {
         reg_grow<216>();
         att_softmax<D, kBf16>(c, p, sc.shared, sm, tmem);
@@ -863,7 +905,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
         } else {
             const int slot = warp - kAttMma;
             att_mma<D, kBf16>(p, sm, tmem, slot);
-            if (lane == 0) {                               // every product has completed before the memory is freed
+            if (elect_one()) {                             // every product has completed before the memory is freed
                 tc_commit(&sm.drain[slot]);
                 const unsigned long long until = globaltimer_ns() + p.timeout_ns;
                 while (!mbar_try_wait(&sm.drain[slot], 0) && globaltimer_ns() < until) {}
@@ -883,38 +925,35 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
 constexpr int kMergeThreads = 256;
 constexpr int kMergeParts = 1024;              // at most 2 x 152 parts of each of three jobs, on any grid up to 340 CTAs
 
-// A CTA per (head, unit of a stream, `rows` rows): out = sum of w_i part_i, w_i = 2^(lse_i - lse),
+// A CTA per (unit of a stream, `rows` rows, head): out = sum of w_i part_i, w_i = 2^(lse_i - lse),
 // over the parts of the rows' own job and, where the stream shares the prefix, of the shared job
 // (two of them when the rows lie in two units).  The list of parts goes to shared memory, a warp
 // per row finds the weights' base, then every four columns of a row have a thread, or several that
 // take parts in turn where there are few rows.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int rows, int groups) {
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int rows) {
     constexpr int kChunks = D / 4;
     __shared__ Slot s_part[kMergeParts];
     __shared__ float s_m[16], s_inv[16];
     __shared__ float4 s_acc[kMergeThreads];
     __shared__ uint2 s_out[16][kChunks + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, units = p.a.streams * p.U;
-    long long blk = blockIdx.x;
-    const int group = (int)(blk % groups); blk /= groups;
-    const int unit = (int)(blk % units), h = (int)(blk / units);
+    const int unit = blockIdx.x, h = blockIdx.z, row0 = blockIdx.y * rows;
     grid_dependency_wait();
-    const int shared = (int)p.head[kHeadShared];
+    const int shared = p.head[kHeadShared], W1 = p.head[kHeadOwn], first = p.cum[unit];
     const OwnUnit u = att_unit(c, p, unit, shared);
-    const int row0 = group * rows, n = min(rows, u.nrows - row0);
+    const int n = min(rows, u.nrows - row0);
     if (n <= 0) return;
-    const long long W1 = p.head[kHeadOwn];
     const bool shares = u.begin > 0;
     const int s = unit / p.U;
     // rows of this stream among the packed rows of all: they may lie in two shared units
-    const long long packed = (long long)s * p.a.block * p.G + u.r0 + row0;
-    const long long unit_a = packed / p.rows_sh(), unit_b = (packed + n - 1) / p.rows_sh();
+    const int packed = s * p.a.block * p.G + u.r0 + row0, in_unit = p.rows_sh() - 1;   // (256 or 128) - 1
+    const int unit_a = packed / p.rows_sh(), unit_b = (packed + n - 1) / p.rows_sh();
     // parts of job j: first list entry, count, workers
     int count[3] = {0, 0, 0};
     {
         const JobList L = att_list(c, p, p.wide_own != 0, shared, W1, grid);
-        const long long x = L.W_sh + (long long)h * L.W1 + p.cum[unit] + L.pad, job = (long long)h * units + unit;
+        const int x = L.W_sh + h * L.W1 + first + L.pad, job = h * units + unit;
         const int c0 = L.worker(x), c1 = L.worker(x + u.tiles() - 1);
         if (!shares && c0 == c1) return;       // written by its only segment
         count[0] = c1 - c0 + 1;
@@ -923,8 +962,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Cache
     }
     if (shares) {
         const JobList L = att_list(c, p, p.wide_sh != 0, shared, W1, grid);
-        for (int k = 0; k <= (int)(unit_b - unit_a); ++k) {
-            const long long job = (long long)h * p.U_sh + unit_a + k, x = job * (L.tiles_sh + L.pad) + L.pad;
+        for (int k = 0; k <= unit_b - unit_a; ++k) {
+            const int job = h * p.U_sh + unit_a + k, x = job * (L.tiles_sh + L.pad) + L.pad;
             const int c0 = L.worker(x), c1 = L.worker(x + L.tiles_sh - 1), at = count[0] + count[1];
             count[1 + k] = c1 - c0 + 1;
             for (int i = tid; i < count[1 + k]; i += kMergeThreads)
@@ -932,11 +971,11 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Cache
         }
     }
     __syncthreads();
-    const int cut = (int)((unit_a + 1) * p.rows_sh() - packed);   // rows from here on are in the second shared unit
+    const int cut = (unit_a + 1) * p.rows_sh() - packed;   // rows from here on are in the second shared unit
     // a row's parts: its own job's, and one shared job's; part i of them, and the row in its slot
     const auto parts_of = [&](int row) { return count[0] + (row < cut ? count[1] : count[2]); };
     const auto part = [&](int row, int i) { return s_part[i < count[0] || row < cut ? i : i + count[1]]; };
-    const auto slot_row = [&](int row, int i) { return i < count[0] ? row0 + row : (int)((packed + row) % p.rows_sh()); };
+    const auto slot_row = [&](int row, int i) { return i < count[0] ? row0 + row : (packed + row) & in_unit; };
     const auto lse_of = [&](int row, int i) {
         const Slot sl = part(row, i);
         return sl.base[(int64_t)sl.R * D + slot_row(row, i)];
@@ -1038,7 +1077,7 @@ AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int
     const size_t row = (size_t)(c->cfg.head_dim + 1) * 4, jobs = (size_t)c->cfg.kv_heads;
     const size_t split = up256(4 * (size_t)c->sm_count * 128 * row);
     L.cum = 256;
-    L.split_wide = L.cum + up256((size_t)streams * L.U * 8);
+    L.split_wide = L.cum + up256((size_t)streams * L.U * 4);
     L.split_narrow = L.split_wide + split;
     L.whole_sh = L.split_narrow + split;
     L.whole_own = L.whole_sh + up256(jobs * L.U_sh * rs * row);
@@ -1055,11 +1094,11 @@ int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, 
     int rows = 16;
     while (rows > 2 && jobs * ((p.R_own + rows - 1) / rows) < 2 * c->sm_count) rows /= 2;
     const int groups = (p.R_own + rows - 1) / rows;
-    if (jobs * groups > 0x7FFFFFFF || 6 * c->sm_count > moe::kMergeParts) return MOE_ERR_UNSUPPORTED;
+    if (6 * c->sm_count > moe::kMergeParts) return MOE_ERR_UNSUPPORTED;
     moe::attend_kernel<D, kBf16><<<c->sm_count, moe::kAttThreads, smem, st>>>(v, p, c->maps[2 * layer], c->maps[2 * layer + 1]);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3((unsigned)(jobs * groups)), dim3(moe::kMergeThreads), 0,
-                                 st, v, p, c->sm_count, rows, groups) == cudaSuccess
+    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3(p.a.streams * p.U, groups, c->cfg.kv_heads),
+                                 dim3(moe::kMergeThreads), 0, st, v, p, c->sm_count, rows) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -1103,11 +1142,15 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     if (!a.q_dev || !a.out_dev || !aligned(a.q_dev, 16) || !aligned(a.out_dev, 16)) return MOE_ERR_INVALID_ARG;
     const AttendLayout L = attend_layout(c, a.streams, a.block, a.q_heads);
     if (!workspace_dev || !aligned(workspace_dev, 256) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+    // places of the schedule, with every stream as long as its table
+    const double tiles = ((double)c->cfg.max_pages * c->cfg.page_tokens + a.block) / moe::kKeyTile + 2 + moe::kPadNarrow;
+    if (c->cfg.kv_heads * ((double)L.U_sh + (double)a.streams * L.U) * tiles >= 2147483647.0) return MOE_ERR_UNSUPPORTED;
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
     char* ws = static_cast<char*>(workspace_dev);
     p.v_pool = static_cast<const uint16_t*>(c->layers[layer].v_dev);
     p.G = L.G;
+    p.g_mul = 0xFFFFFFFFu / (uint32_t)L.G + 1;
     p.wide_sh = L.wide_sh;
     p.wide_own = L.wide_own;
     p.U = L.U;
@@ -1120,8 +1163,8 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     if (p.c < 0x1p-100f) p.c = 0x1p-100f;
     p.q_flip = a.scale < 0.0f ? 0x80008000u : 0u;
     p.timeout_ns = (unsigned long long)c->cfg.timeout_us * 1000ull;
-    p.head = reinterpret_cast<long long*>(ws);
-    p.cum = reinterpret_cast<long long*>(ws + L.cum);
+    p.head = reinterpret_cast<int*>(ws);
+    p.cum = reinterpret_cast<int*>(ws + L.cum);
     p.split_wide = reinterpret_cast<float*>(ws + L.split_wide);
     p.split_narrow = reinterpret_cast<float*>(ws + L.split_narrow);
     p.whole_sh = reinterpret_cast<float*>(ws + L.whole_sh);
