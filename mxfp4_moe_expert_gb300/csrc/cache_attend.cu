@@ -52,7 +52,7 @@ struct AttendParams {
     uint32_t q_flip;           // sign flips of a pair of query elements (a negative scale)
     unsigned long long timeout_ns;
     int* head;                 // workspace: the schedule for the merge
-    int* cum;                  // first own place of each unit (of a head)
+    int4* units;               // each unit: first own place (of a head), rows, tiles, whether it shares the prefix
     float* split_wide;         // partial rows of split jobs: 2 per worker, 256 rows each, ...
     float* split_narrow;       // ... 128 rows each
     float* whole_sh;           // partial rows of whole jobs: shared, ...
@@ -253,8 +253,8 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
         int at = 0;
         for (int i0 = 0; i0 < units; i0 += kAttThreads) {
             const int i = i0 + tid;
-            int n = i < units ? att_unit(c, p, i, sc.shared).tiles() : 0;
-            if (n > 0) n += pad;
+            const OwnUnit u = i < units ? att_unit(c, p, i, sc.shared) : OwnUnit{0, 0, 0, 0, 0};
+            const int n = u.nrows > 0 ? u.tiles() + pad : 0;
             int sum;
             const int x0 = at + att_scan(sm, 0, n, &sum);
 #pragma unroll
@@ -263,7 +263,7 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
                     sm.first_unit[x] = i;
                     sm.first_off[x] = y[x] - x0;
                 }
-            if (blockIdx.x == 0 && i < units) p.cum[i] = x0;
+            if (blockIdx.x == 0 && i < units) p.units[i] = make_int4(x0, u.nrows, n - pad, u.begin > 0);
             at += sum;
         }
     }
@@ -654,22 +654,17 @@ __device__ __forceinline__ void att_load_q(const AttendParams& p, const Segment&
     const int64_t tok0 = sg.own ? (int64_t)sg.s * p.a.block : 0;
     const int nrows = sg.nrows, t0 = sg.r0 / p.G, g0 = sg.r0 - t0 * p.G;     // first row's token and head
     q += (tok0 + t0) * p.a.q_stride + (int64_t)sg.h * p.G * D;
-    // all loads go out before the first store
     uint4 v[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int row = tid / kChunks + i * (128 / kChunks);
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < nrows) {
-            const int g = g0 + row, t = p.div_g(g);
-            v[i] = __ldg(reinterpret_cast<const uint4*>(q + t * p.a.q_stride + (g - t * p.G) * D));
-        }
+        const int row = tid / kChunks + i * (128 / kChunks), g = g0 + row, t = p.div_g(g);
+        v[i] = load_or_zero(q + t * p.a.q_stride + (g - t * p.G) * D, row < nrows);
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int row = tid / kChunks + i * (128 / kChunks);
-        v[i].x ^= p.q_flip; v[i].y ^= p.q_flip; v[i].z ^= p.q_flip; v[i].w ^= p.q_flip;
-        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v[i];
+        *reinterpret_cast<uint4*>(tile + (x / 8) * AttSmem<D>::kPanel + row * 128 + (((x & 7) ^ (row & 7)) << 4)) =
+            make_uint4(v[i].x ^ p.q_flip, v[i].y ^ p.q_flip, v[i].z ^ p.q_flip, v[i].w ^ p.q_flip);
     }
 }
 
@@ -689,22 +684,29 @@ __device__ __forceinline__ void att_visible(bool masked, int ctx, int key_end, i
     vis[0] = (uint32_t)lo; vis[1] = (uint32_t)(lo >> 32); vis[2] = (uint32_t)hi; vis[3] = (uint32_t)(hi >> 32);
 }
 
-// Sum over the block positions that this row sees of the non-finite values of one column, else 0.
+// Columns of a row whose values at the block positions that it sees are not all finite, which the
+// products left out: any sum with one is not finite either, and is the sum of those alone.
 template <int D, bool kBf16>
-__device__ __noinline__ float att_bad_sum(const CacheView& c, const AttendParams& p, const Segment& sg, int b, uint64_t bits, int col) {
+__device__ __noinline__ void att_put_bad(const CacheView& c, const AttendParams& p, const Segment& sg, int b, uint64_t bits, int64_t at,
+                                         int r, float inv) {
     const int from = max(sg.ctx, sg.key0), end = min(sg.key_end, sg.key0 + sg.T * kKeyTile);
     const int held = min(c.held()[sg.s], c.L.M);
     constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
-    float sum = 0.0f;
-    for (int j = from; j < end; ++j) {
-        const int i = j - sg.ctx;
-        if (p.a.mask_dev ? !(bits >> i & 1) : i > b) continue;
-        const int pi = j >> c.page_shift, page = pi < held ? c.table(sg.s)[pi] : -1;
-        if ((unsigned)page >= (unsigned)c.L.P) continue;
-        const uint16_t v = p.v_pool[page * c.page_stride + ((int64_t)sg.h * c.page + (j & (c.page - 1))) * D + col];
-        if ((v & kExp) == kExp) sum += kBf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+    for (int col = 0; col < D; ++col) {
+        float sum = 0.0f;
+        for (int j = from; j < end; ++j) {
+            const int i = j - sg.ctx;
+            if (p.a.mask_dev ? !(bits >> i & 1) : i > b) continue;
+            const int pi = j >> c.page_shift, page = pi < held ? c.table(sg.s)[pi] : -1;
+            if ((unsigned)page >= (unsigned)c.L.P) continue;
+            const uint16_t v = p.v_pool[page * c.page_stride + ((int64_t)sg.h * c.page + (j & (c.page - 1))) * D + col];
+            if ((v & kExp) == kExp) sum += kBf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+        }
+        if (sum == 0.0f) continue;
+        sum *= inv;
+        if (sg.out) sg.out[((col / 4) * sg.R + r) * 4 + col % 4] = sum;
+        else static_cast<uint16_t*>(p.a.out_dev)[at * D + col] = (uint16_t)pack_f16<kBf16>(sum, 0.0f);
     }
-    return sum;
 }
 
 template <int D, bool kBf16>
@@ -811,35 +813,27 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
             const int R = sg.R, r = sg.out_row + tid;
             const int64_t at = row.tok * p.a.q_heads + row.head;
 #pragma unroll
-            for (int col = 0; col < D; col += 32) {
-                uint32_t y[32];
-                tc_ld_x32(to + col, y);
-                tc_wait_ld(y);
-                if (mend && row.valid)
-                    for (int e = 0; e < 32; ++e) {               // (rare: the loop is not unrolled)
-                        const float bad = att_bad_sum<D, kBf16>(c, p, sg, row.b, bits, col + e);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i == e) y[i] = __float_as_uint(__uint_as_float(y[i]) + bad);
-                    }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * inv);
-                const auto f = [&](int e) { return __uint_as_float(y[e]); };
+            for (int col = 0; col < D; col += 64) {
+                uint32_t y[2][32];
+                tc_ld_x32(to + col, y[0]);
+                tc_ld_x32(to + col + 32, y[1]);
+                tc_wait_ld(y[0]);
+                tc_wait_ld(y[1]);
+                const auto f = [&](int e) { return __uint_as_float(y[e / 32][e % 32]) * inv; };
                 if (row.valid && !out) {
-                    uint16_t* to_row = static_cast<uint16_t*>(p.a.out_dev) + at * D + col;
+                    uint4* to_row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out_dev) + at * D + col);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(to_row + e) =
-                            make_uint4(pack_f16<kBf16>(f(e), f(e + 1)), pack_f16<kBf16>(f(e + 2), f(e + 3)),
-                                       pack_f16<kBf16>(f(e + 4), f(e + 5)), pack_f16<kBf16>(f(e + 6), f(e + 7)));
+                    for (int e = 0; e < 64; e += 8)
+                        to_row[e / 8] = make_uint4(pack_f16<kBf16>(f(e), f(e + 1)), pack_f16<kBf16>(f(e + 2), f(e + 3)),
+                                                   pack_f16<kBf16>(f(e + 4), f(e + 5)), pack_f16<kBf16>(f(e + 6), f(e + 7)));
                 } else if (row.valid) {
-                    float4* to_slot = reinterpret_cast<float4*>(out) + (int64_t)(col / 4) * R + r;
+                    float4* to_slot = reinterpret_cast<float4*>(out) + (col / 4) * R + r;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        to_slot[(int64_t)(e / 4) * R] = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
+                    for (int e = 0; e < 64; e += 4) to_slot[(e / 4) * R] = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
                 }
                 __syncwarp();
             }
+            if (mend && row.valid) att_put_bad<D, kBf16>(c, p, sg, row.b, bits, at, r, inv);
             if (row.valid) {
                 if (out) out[(int64_t)R * D + r] = lse2;
                 else if (p.a.lse_dev) p.a.lse_dev[at] = lse2 * 0.693147180559945309f;
@@ -923,126 +917,106 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
 // ---- merge -----------------------------------------------------------------------------------
 
 constexpr int kMergeThreads = 256;
-constexpr int kMergeParts = 1024;              // at most 2 x 152 parts of each of three jobs, on any grid up to 340 CTAs
+constexpr int kMergeCols = 16;                 // columns of a thread
 
-// A CTA per (unit of a stream, `rows` rows, head): out = sum of w_i part_i, w_i = 2^(lse_i - lse),
-// over the parts of the rows' own job and, where the stream shares the prefix, of the shared job
-// (two of them when the rows lie in two units).  The list of parts goes to shared memory, a warp
-// per row finds the weights' base, then every four columns of a row have a thread, or several that
-// take parts in turn where there are few rows.
+// One job's parts, in order: part i is worker c0 + i's.
+struct Parts {
+    float* base;               // of the first part
+    int64_t step;              // floats from part 1 to part 2 and so on ...
+    int64_t gap;               // ... and from part 0 to part 1
+    int n, R;
+};
+template <int D>
+__device__ __forceinline__ Parts att_parts(const AttendParams& p, const JobList& L, bool wide, bool own, int job, int first, int tiles) {
+    const int c0 = L.worker(first), c1 = L.worker(first + tiles - 1);
+    const Slot s = att_slot<D>(p, wide, own, job, c0, c0 == c1, true);
+    const int64_t row = (int64_t)s.R * (D + 1);
+    return {s.base, 2 * row, row, c1 - c0 + 1, s.R};           // (the first part begins the job: slot 2 c0 + 1)
+}
+
+// out = sum of w_i part_i / sum of w_i, w_i = 2^lse_i, over the parts of a row's own job and, where
+// its stream shares the prefix, of the shared job.  A CTA per (unit of a stream, `rows` rows,
+// head); a thread has 16 columns of a row (rows on neighbouring lanes, as the parts store them);
+// where there are few rows, several threads take the parts in turn, each with the running maximum
+// and sum of a softmax, and are merged in order.  Bound by reading the parts (from L2).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int rows) {
-    constexpr int kChunks = D / 4;
-    __shared__ Slot s_part[kMergeParts];
-    __shared__ float s_m[16], s_inv[16];
-    __shared__ float4 s_acc[kMergeThreads];
-    __shared__ uint2 s_out[16][kChunks + 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, units = p.a.streams * p.U;
-    const int unit = blockIdx.x, h = blockIdx.z, row0 = blockIdx.y * rows;
+    constexpr int kGroups = D / kMergeCols;
+    __shared__ float s_acc[kMergeThreads][kMergeCols + 3];     // sums, maximum, weight (odd stride: no bank twice)
+    const int tid = threadIdx.x, units = p.a.streams * p.U, unit = blockIdx.x, h = blockIdx.z, row0 = blockIdx.y * rows;
+    const int row = tid % rows, group = tid / rows % kGroups, turn = tid / (rows * kGroups), turns = kMergeThreads / (rows * kGroups);
     grid_dependency_wait();
-    const int shared = p.head[kHeadShared], W1 = p.head[kHeadOwn], first = p.cum[unit];
-    const OwnUnit u = att_unit(c, p, unit, shared);
-    const int n = min(rows, u.nrows - row0);
-    if (n <= 0) return;
-    const bool shares = u.begin > 0;
-    const int s = unit / p.U;
-    // rows of this stream among the packed rows of all: they may lie in two shared units
-    const int packed = s * p.a.block * p.G + u.r0 + row0, in_unit = p.rows_sh() - 1;   // (256 or 128) - 1
-    const int unit_a = packed / p.rows_sh(), unit_b = (packed + n - 1) / p.rows_sh();
-    // parts of job j: first list entry, count, workers
-    int count[3] = {0, 0, 0};
+    const int shared = p.head[kHeadShared], W1 = p.head[kHeadOwn];
+    const int4 u = p.units[unit];                              // first place, rows, tiles, shares
+    if (row0 >= u.y) return;
+    Parts own, sh = {nullptr, 0, 0, 0, 0};
     {
         const JobList L = att_list(c, p, p.wide_own != 0, shared, W1, grid);
-        const int x = L.W_sh + h * L.W1 + first + L.pad, job = h * units + unit;
-        const int c0 = L.worker(x), c1 = L.worker(x + u.tiles() - 1);
-        if (!shares && c0 == c1) return;       // written by its only segment
-        count[0] = c1 - c0 + 1;
-        for (int i = tid; i < count[0]; i += kMergeThreads)
-            s_part[i] = att_slot<D>(p, p.wide_own, true, job, c0 + i, c0 == c1, i == 0);
+        own = att_parts<D>(p, L, p.wide_own, true, h * units + unit, L.W_sh + h * L.W1 + u.x + L.pad, u.z);
     }
-    if (shares) {
+    if (!u.w && own.n == 1) return;                            // written by its only segment
+    const int s = unit / p.U, u0 = (unit - s * p.U) * p.rows_own();
+    const int r = u0 + row0 + row, packed = s * p.a.block * p.G + r;
+    if (u.w) {                                                 // the shared unit that this row lies in
         const JobList L = att_list(c, p, p.wide_sh != 0, shared, W1, grid);
-        for (int k = 0; k <= unit_b - unit_a; ++k) {
-            const int job = h * p.U_sh + unit_a + k, x = job * (L.tiles_sh + L.pad) + L.pad;
-            const int c0 = L.worker(x), c1 = L.worker(x + L.tiles_sh - 1), at = count[0] + count[1];
-            count[1 + k] = c1 - c0 + 1;
-            for (int i = tid; i < count[1 + k]; i += kMergeThreads)
-                s_part[at + i] = att_slot<D>(p, p.wide_sh, false, job, c0 + i, c0 == c1, i == 0);
-        }
+        const int job = h * p.U_sh + packed / p.rows_sh();
+        sh = att_parts<D>(p, L, p.wide_sh, false, job, job * (L.tiles_sh + L.pad) + L.pad, L.tiles_sh);
     }
-    __syncthreads();
-    const int cut = (unit_a + 1) * p.rows_sh() - packed;   // rows from here on are in the second shared unit
-    // a row's parts: its own job's, and one shared job's; part i of them, and the row in its slot
-    const auto parts_of = [&](int row) { return count[0] + (row < cut ? count[1] : count[2]); };
-    const auto part = [&](int row, int i) { return s_part[i < count[0] || row < cut ? i : i + count[1]]; };
-    const auto slot_row = [&](int row, int i) { return i < count[0] ? row0 + row : (packed + row) & in_unit; };
-    const auto lse_of = [&](int row, int i) {
-        const Slot sl = part(row, i);
-        return sl.base[(int64_t)sl.R * D + slot_row(row, i)];
-    };
-    const auto place = [&](int row) {          // of a row in the output
-        const int i = u.r0 + row0 + row, t = i / p.G;
-        return ((int64_t)s * p.a.block + t) * p.a.q_heads + h * p.G + (i - t * p.G);
-    };
-    for (int row = warp; row < n; row += kMergeThreads / 32) {
-        const int np = parts_of(row);
-        float m = -INFINITY, z = 0.0f;
-        bool nan = false;
-        for (int i = lane; i < np; i += 32) {
-            const float x = lse_of(row, i);
-            m = fmaxf(m, x);
-            nan |= x != x;
-        }
+    const bool valid = row0 + row < u.y;
+    float m = -INFINITY, z = 0.0f, acc[kMergeCols] = {};
+    if (valid) {
+        const int n = own.n + sh.n, r_sh = packed & (p.rows_sh() - 1);
+#pragma unroll 2
+        for (int i = turn; i < n; i += turns) {
+            const bool mine = i < own.n;
+            const int k = mine ? i : i - own.n, R = mine ? own.R : sh.R, at = mine ? row0 + row : r_sh;
+            const float* part = (mine ? own.base : sh.base) + (k ? (mine ? own.gap : sh.gap) + (k - 1) * (mine ? own.step : sh.step) : 0);
+            const float lse = __ldcg(part + R * D + at);
+            float4 v[kMergeCols / 4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float ref = m == -INFINITY ? 0.0f : m;
-        for (int i = lane; i < np; i += 32) z += exp2_approx(lse_of(row, i) - ref);
-        z = warp_sum(z);
-        if (__any_sync(0xFFFFFFFFu, nan)) z = NAN;
-        if (lane == 0) {
-            s_m[row] = ref;
-            s_inv[row] = z == 0.0f ? 0.0f : 1.0f / z;
-            if (p.a.lse_dev) p.a.lse_dev[place(row)] = z == 0.0f ? -INFINITY : (ref + log2f(z)) * 0.693147180559945309f;
-        }
-    }
-    __syncthreads();
-    const int e_all = n * kChunks;
-    const int turns = max(1, kMergeThreads / e_all);              // threads that share a row's four columns
-    for (int e0 = 0; e0 < e_all; e0 += kMergeThreads) {
-        const int e = turns > 1 ? tid % e_all : e0 + tid, turn = turns > 1 ? tid / e_all : 0;
-        const int row = e % n, x = e / n;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (e < e_all && turn < turns) {
-            const int np = parts_of(row);
-            const float ref = s_m[row], inv = s_inv[row];
-#pragma unroll 4
-            for (int i = turn; i < np; i += turns) {
-                const Slot sl = part(row, i);
-                const int r = slot_row(row, i);
-                const float w = exp2_approx(sl.base[(int64_t)sl.R * D + r] - ref) * inv;
-                const float4 v = reinterpret_cast<const float4*>(sl.base)[(int64_t)x * sl.R + r];
-                if (w != 0.0f) {                                  // a part that saw nothing adds nothing
-                    acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-                    acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-                }
+            for (int x = 0; x < kMergeCols / 4; ++x)
+                v[x] = __ldcg(reinterpret_cast<const float4*>(part) + (group * (kMergeCols / 4) + x) * R + at);
+            if (lse == -INFINITY) continue;                    // a part that saw nothing
+            const float top = fmaxf(m, lse), f = exp2_approx(m - top), w = exp2_approx(lse - top);
+            m = top;
+            z = z * f + w;
+#pragma unroll
+            for (int x = 0; x < kMergeCols / 4; ++x) {
+                acc[4 * x] = fmaf(w, v[x].x, acc[4 * x] * f);
+                acc[4 * x + 1] = fmaf(w, v[x].y, acc[4 * x + 1] * f);
+                acc[4 * x + 2] = fmaf(w, v[x].z, acc[4 * x + 2] * f);
+                acc[4 * x + 3] = fmaf(w, v[x].w, acc[4 * x + 3] * f);
             }
         }
-        if (turns > 1) {
-            s_acc[tid] = acc;
-            __syncthreads();
-            if (tid < e_all)
-                for (int k = 1; k < turns; ++k) {
-                    const float4 v = s_acc[tid + k * e_all];
-                    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-                }
+    }
+    if (turns > 1) {
+#pragma unroll
+        for (int x = 0; x < kMergeCols; ++x) s_acc[tid][x] = acc[x];
+        s_acc[tid][kMergeCols] = m;
+        s_acc[tid][kMergeCols + 1] = z;
+        __syncthreads();
+        if (turn > 0) return;
+        for (int k = 1; k < turns; ++k) {
+            const float* o = s_acc[tid + k * rows * kGroups];
+            const float mk = o[kMergeCols];
+            if (o[kMergeCols + 1] == 0.0f) continue;
+            const float top = fmaxf(m, mk), f = exp2_approx(m - top), w = exp2_approx(mk - top);
+            m = top;
+            z = z * f + o[kMergeCols + 1] * w;
+#pragma unroll
+            for (int x = 0; x < kMergeCols; ++x) acc[x] = fmaf(w, o[x], acc[x] * f);
         }
-        if (e < e_all && turn == 0) s_out[row][x] = make_uint2(pack_f16<kBf16>(acc.x, acc.y), pack_f16<kBf16>(acc.z, acc.w));
     }
-    __syncthreads();
-    for (int e = tid; e < e_all; e += kMergeThreads) {
-        const int row = e / kChunks, x = e % kChunks;
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out_dev) + place(row) * D)[x] = s_out[row][x];
-    }
+    if (!valid || turn > 0) return;
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    const int t = r / p.G;
+    const int64_t at = ((int64_t)s * p.a.block + t) * p.a.q_heads + h * p.G + (r - t * p.G);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out_dev) + at * D + group * kMergeCols);
+#pragma unroll
+    for (int x = 0; x < kMergeCols / 8; ++x)
+        out[x] = make_uint4(pack_f16<kBf16>(acc[8 * x] * inv, acc[8 * x + 1] * inv), pack_f16<kBf16>(acc[8 * x + 2] * inv, acc[8 * x + 3] * inv),
+                            pack_f16<kBf16>(acc[8 * x + 4] * inv, acc[8 * x + 5] * inv), pack_f16<kBf16>(acc[8 * x + 6] * inv, acc[8 * x + 7] * inv));
+    if (p.a.lse_dev && group == 0) p.a.lse_dev[at] = z == 0.0f ? -INFINITY : (m + log2f(z)) * 0.693147180559945309f;
 }
 
 }  // namespace moe
@@ -1062,7 +1036,7 @@ int check_shape(const moe_mxfp4_cache* c, int32_t streams, int32_t block, int32_
 // Sections of the workspace, and the units.
 struct AttendLayout {
     int G, wide_sh, wide_own, U, U_sh, R_own;
-    size_t cum, split_wide, split_narrow, whole_sh, whole_own, total;
+    size_t units, split_wide, split_narrow, whole_sh, whole_own, total;
 };
 AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int q_heads) {
     AttendLayout L;
@@ -1076,8 +1050,8 @@ AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int
     L.R_own = (int)(rows < ro ? (rows + 3) / 4 * 4 : ro);   // slots are whole float4s
     const size_t row = (size_t)(c->cfg.head_dim + 1) * 4, jobs = (size_t)c->cfg.kv_heads;
     const size_t split = up256(4 * (size_t)c->sm_count * 128 * row);
-    L.cum = 256;
-    L.split_wide = L.cum + up256((size_t)streams * L.U * 4);
+    L.units = 256;
+    L.split_wide = L.units + up256((size_t)streams * L.U * 16);
     L.split_narrow = L.split_wide + split;
     L.whole_sh = L.split_narrow + split;
     L.whole_own = L.whole_sh + up256(jobs * L.U_sh * rs * row);
@@ -1089,12 +1063,11 @@ template <int D, bool kBf16>
 int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, const moe::AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(moe::AttSmem<D>);
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
-    // rows of a merging CTA: as many as leave two CTAs for every SM, at most 16
+    // rows of a merging CTA: as many as leave two CTAs for every SM, at most 32
     const int64_t jobs = (int64_t)c->cfg.kv_heads * p.a.streams * p.U;
-    int rows = 16;
+    int rows = 32;
     while (rows > 2 && jobs * ((p.R_own + rows - 1) / rows) < 2 * c->sm_count) rows /= 2;
     const int groups = (p.R_own + rows - 1) / rows;
-    if (6 * c->sm_count > moe::kMergeParts) return MOE_ERR_UNSUPPORTED;
     moe::attend_kernel<D, kBf16><<<c->sm_count, moe::kAttThreads, smem, st>>>(v, p, c->maps[2 * layer], c->maps[2 * layer + 1]);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3(p.a.streams * p.U, groups, c->cfg.kv_heads),
@@ -1164,7 +1137,7 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     p.q_flip = a.scale < 0.0f ? 0x80008000u : 0u;
     p.timeout_ns = (unsigned long long)c->cfg.timeout_us * 1000ull;
     p.head = reinterpret_cast<int*>(ws);
-    p.cum = reinterpret_cast<int*>(ws + L.cum);
+    p.units = reinterpret_cast<int4*>(ws + L.units);
     p.split_wide = reinterpret_cast<float*>(ws + L.split_wide);
     p.split_narrow = reinterpret_cast<float*>(ws + L.split_narrow);
     p.whole_sh = reinterpret_cast<float*>(ws + L.whole_sh);

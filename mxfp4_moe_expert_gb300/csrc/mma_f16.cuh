@@ -91,6 +91,19 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// 16 bytes of read-only global memory, or zeros; issued in program order, so that a run of them is
+// in flight together.
+__device__ __forceinline__ uint4 load_or_zero(const void* p, bool there) {
+    uint4 v;
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+        " @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p), "r"((int)there)
+        : "memory");
+    return v;
+}
+
 // True in one lane of the (converged) warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
