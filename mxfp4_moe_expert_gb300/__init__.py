@@ -535,7 +535,7 @@ class KvCache:
                     or pool.stride()[1:] != (tokens * dim, dim, 1) or (pages > 1 and pool.stride(0) != k0.stride(0))):
                 raise ValueError("the pools of a cache have one shape, type, device and page stride")
         self._keep = layers
-        self.device, self.dtype = k0.device, k0.dtype
+        self.device, self.dtype = k0.device, k0.dtype      # (a tensor's device has its index)
         self.num_layers, self.num_streams, self.max_pages = len(layers), num_streams, max_pages
         self.num_pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, tokens, dim
         cfg = moe_mxfp4_cache_config(len(layers), num_streams, max_pages, pages, tokens, heads, dim,
@@ -555,8 +555,11 @@ class KvCache:
         self.page_table, at = self.state[at:at + S * max_pages].view(S, max_pages), at + S * max_pages
         self.refcount = self.state[at:at + pages]
         self._lib = load_library()
-        self._args = moe_mxfp4_attend_args()
         self._ws, self._ws_bytes, self._ws_kept = None, {}, []
+        self._layouts = {}        # shapes and strides seen so far -> how a call lays them out
+        self._i32, self._f32, self._mask_types = torch.int32, torch.float32, (torch.int64, torch.uint64)
+        # the raw handle of the current stream (torch.cuda.current_stream() builds a Stream object around it)
+        self._current_stream = torch._C._cuda_getCurrentRawStream
 
     # -- the books
 
@@ -568,8 +571,9 @@ class KvCache:
             add, n = None, tokens
         else:
             add, n = self._books("tokens", tokens, self.num_streams), 0
-        _check(self._lib.moe_mxfp4_cache_reserve(self.handle, self._state_ptr, add, n, self._stream(stream)),
-               "moe_mxfp4_cache_reserve")
+        st = self._lib.moe_mxfp4_cache_reserve(self.handle, self._state_ptr, add, n, self._stream(stream))
+        if st:
+            _check(st, "moe_mxfp4_cache_reserve")
 
     def commit(self, accepted, stream=None):
         """length += accepted (int32 [num_streams]; accept()'s output); the pages behind are given back."""
@@ -605,16 +609,16 @@ class KvCache:
     def append(self, layer, k, v, lengths=None, stream=None):
         """k, v: [streams, block, kv_heads, head_dim], contiguous or rows of one wider tensor (a fused projection's
         output); lengths: int32 [streams], tokens in use of each block."""
-        S, B, H, D = self._rows("k", k)
-        if (H, D) != (self.kv_heads, self.head_dim) or v.shape != k.shape:
+        S, B, H, D, row = self._rows("k", k)
+        if H != self.kv_heads or D != self.head_dim or self._rows("v", v)[:4] != (S, B, H, D):
             raise ValueError("k and v are [streams, block, kv_heads, head_dim]")
-        self._rows("v", v)
-        if S * B > 1 and self._row_stride(v) != self._row_stride(k):
+        if S * B > 1 and self._rows("v", v)[4] != row:
             raise ValueError("k and v have one stride between tokens")
-        _check(self._lib.moe_mxfp4_cache_append(self.handle, self._state_ptr, layer, k.data_ptr(), v.data_ptr(),
-                                                self._row_stride(k), S, B,
-                                                None if lengths is None else self._books("lengths", lengths, S),
-                                                self._stream(stream)), "moe_mxfp4_cache_append")
+        st = self._lib.moe_mxfp4_cache_append(self.handle, self._state_ptr, layer, k.data_ptr(), v.data_ptr(), row, S, B,
+                                              None if lengths is None else self._books("lengths", lengths, S),
+                                              self._stream(stream))
+        if st:
+            _check(st, "moe_mxfp4_cache_append")
 
     def attend(self, layer, q, lengths=None, mask=None, shared_stream=0, shared_tokens=0, scale=None, out=None, lse=None,
                workspace=None, stream=None):
@@ -622,35 +626,32 @@ class KvCache:
         int64 [streams, block], bit i = sees block position i (default: causal); scale: default 1 / sqrt(head_dim).
         Returns (out, lse): out like q, contiguous; lse fp32 [streams, block, q_heads].  Rows that `lengths` leaves
         out are zero in an out (lse) that is made here and unchanged in one that is given."""
-        import torch
-        S, B, H, D = self._rows("q", q)
+        S, B, H, D, row = self._rows("q", q)
         if D != self.head_dim:
             raise ValueError("q is [streams, block, q_heads, head_dim]")
-        make = torch.empty if lengths is None else torch.zeros
-        if out is None:
-            out = make((S, B, H, D), dtype=self.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+        if out is None or lse is None:
+            import torch
+            make = torch.empty if lengths is None else torch.zeros
+            if out is None:
+                out = make((S, B, H, D), dtype=self.dtype, device=self.device)
+            if lse is None:
+                lse = make((S, B, H), dtype=torch.float32, device=self.device)
+        if out.shape != (S, B, H, D) or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
             raise ValueError("out: contiguous, of q's shape and type")
-        if lse is None:
-            lse = make((S, B, H), dtype=torch.float32, device=self.device)
-        elif (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != self.device
-              or not lse.is_contiguous()):
+        if lse.shape != (S, B, H) or lse.dtype != self._f32 or lse.device != self.device or not lse.is_contiguous():
             raise ValueError("lse: contiguous fp32 [streams, block, q_heads]")
-        if mask is not None and (mask.shape != q.shape[:2] or mask.dtype not in (torch.int64, torch.uint64)
+        if mask is not None and (mask.shape != (S, B) or mask.dtype not in self._mask_types
                                  or mask.device != self.device or not mask.is_contiguous()):
             raise ValueError("mask: contiguous int64 [streams, block]")
-        a = self._args
-        a.q_dev, a.q_stride, a.out_dev, a.lse_dev = q.data_ptr(), self._row_stride(q), out.data_ptr(), lse.data_ptr()
-        a.lengths_dev = None if lengths is None else self._books("lengths", lengths, S)
-        a.mask_dev = None if mask is None else mask.data_ptr()
-        a.streams, a.block, a.q_heads = S, B, H
-        a.shared_stream, a.shared_tokens = shared_stream, shared_tokens
-        a.scale = self.head_dim ** -0.5 if scale is None else scale
-        st = self._stream(stream)
         ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else \
             self._workspace(S, B, H)
-        _check(self._lib.moe_mxfp4_cache_attend(self.handle, self._state_ptr, layer, ctypes.byref(a), ws, n, st),
-               "moe_mxfp4_cache_attend")
+        a = moe_mxfp4_attend_args(q.data_ptr(), row, out.data_ptr(), lse.data_ptr(),
+                                  None if lengths is None else self._books("lengths", lengths, S),
+                                  None if mask is None else mask.data_ptr(), S, B, H, shared_stream, shared_tokens,
+                                  self.head_dim ** -0.5 if scale is None else scale)
+        st = self._lib.moe_mxfp4_cache_attend(self.handle, self._state_ptr, layer, a, ws, n, self._stream(stream))
+        if st:
+            _check(st, "moe_mxfp4_cache_attend")
         return out, lse
 
     def attend_bytes(self, streams, block, q_heads) -> int:
@@ -661,32 +662,29 @@ class KvCache:
     # -- arguments
 
     def _stream(self, stream):
-        if stream is not None:
-            return stream
-        import torch
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return self._current_stream(self.device.index) if stream is None else stream
 
     def _books(self, name, t, n):
-        import torch
-        if t.dtype != torch.int32 or t.device != self.device or t.numel() != n or not t.is_contiguous():
+        if t.dtype != self._i32 or t.device != self.device or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name}: {n} contiguous int32 values on {self.device}")
         return t.data_ptr()
 
     def _rows(self, name, t):
-        if t.dim() != 4 or t.dtype != self.dtype or t.device != self.device:
+        """(streams, block, heads, head_dim, elements between tokens) of a tensor of rows."""
+        if t.dtype != self.dtype or t.device != self.device:
             raise ValueError(f"{name}: a 4-dimensional {self.dtype} tensor on {self.device}")
-        S, B, H, D = t.shape
-        st = t.stride()
-        if t.numel() and ((D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (S > 1 and B > 1 and st[0] != B * st[1])):
-            raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
-        return t.shape
-
-    @staticmethod
-    def _row_stride(t):
-        S, B, H, D = t.shape
-        if B > 1:
-            return t.stride(1)
-        return t.stride(0) if S > 1 else H * D
+        key = (t.shape, t.stride())
+        rows = self._layouts.get(key)
+        if rows is None:
+            if t.dim() != 4:
+                raise ValueError(f"{name}: a 4-dimensional {self.dtype} tensor on {self.device}")
+            (S, B, H, D), st = key
+            if t.numel() and ((D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (S > 1 and B > 1 and st[0] != B * st[1])):
+                raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
+            if len(self._layouts) >= 1024:
+                self._layouts.clear()
+            rows = self._layouts[key] = (S, B, H, D, st[1] if B > 1 else st[0] if S > 1 else H * D)
+        return rows
 
     def _workspace(self, S, B, H):
         """The cache's own workspace, grown when a call needs more; earlier ones are kept, since captured graphs may

@@ -881,6 +881,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
         tmem_relinquish();
     }
     tc_fence_before();
+    grid_dependency_wait();
     const Schedule sc = att_schedule<D>(c, p, sm);         // ends with a CTA barrier
     tc_fence_after();
     grid_dependency_launch();
@@ -1068,8 +1069,9 @@ int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, 
     int rows = 32;
     while (rows > 2 && jobs * ((p.R_own + rows - 1) / rows) < 2 * c->sm_count) rows /= 2;
     const int groups = (p.R_own + rows - 1) / rows;
-    moe::attend_kernel<D, kBf16><<<c->sm_count, moe::kAttThreads, smem, st>>>(v, p, c->maps[2 * layer], c->maps[2 * layer + 1]);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (moe::launch_dependent(moe::attend_kernel<D, kBf16>, dim3(c->sm_count), dim3(moe::kAttThreads), smem, st, v, p,
+                              c->maps[2 * layer], c->maps[2 * layer + 1]) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3(p.a.streams * p.U, groups, c->cfg.kv_heads),
                                  dim3(moe::kMergeThreads), 0, st, v, p, c->sm_count, rows) == cudaSuccess
                ? MOE_OK

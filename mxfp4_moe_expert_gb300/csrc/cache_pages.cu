@@ -15,14 +15,14 @@
 
 namespace moe {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // at most; plan_threads() below
 constexpr int kNoStream = 0x7FFFFFFF;
 
 __device__ __forceinline__ void cache_error(const CacheView& c, int code, int detail) {
     raise_status(c.state + kCacheStatus, code, detail);
 }
 
-// Exclusive prefix sum over the CTA's kPlanThreads threads; *total: the CTA's sum.
+// Exclusive prefix sum over the CTA's threads; *total: the CTA's sum.
 __device__ __forceinline__ long long block_scan(long long v, long long* total) {
     __shared__ long long sums[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -35,7 +35,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* total) {
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        long long t = sums[lane];
+        long long t = lane < (int)(blockDim.x >> 5) ? sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, t, o);
@@ -56,7 +56,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* total) {
 // as many free pages, lowest first; and, when there are enough, the books.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c, const int* __restrict__ add, int add_all) {
     __shared__ int s_bad;
-    const int tid = threadIdx.x, S = c.L.S, P = c.L.P;
+    const int tid = threadIdx.x, threads = blockDim.x, S = c.L.S, P = c.L.P;
     int* const writers = c.state + c.L.writers;
     int* const first = c.state + c.L.first;
     int* const ref = c.refcount();
@@ -66,8 +66,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c
     int* const off = c.state + c.L.off;
     int* const mv_src = c.state + c.L.move_src;
     if (tid == 0) s_bad = kNoStream;
+    grid_dependency_wait();
     __syncthreads();
-    for (int s = tid; s < S; s += kPlanThreads) {
+    for (int s = tid; s < S; s += threads) {
         const int len = c.length()[s], held = c.held()[s], n = add ? add[s] : add_all;
         int want = held, page = -1;
         if (n > 0) {
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c
     // they are its only holders.  Pages and copies are summed in the order of the streams.
     long long total = 0;
     int moves = 0;
-    for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
+    for (int s0 = 0; s0 < S; s0 += threads) {
         const int s = s0 + tid;
         int want = 0, copy = 0;
         if (s < S) {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c
     bool ok = s_bad == kNoStream;
     long long found = 0;
     if (ok && total <= P) {
-        for (int p0 = 0; p0 < P && found < total; p0 += 4 * kPlanThreads) {
+        for (int p0 = 0; p0 < P && found < total; p0 += 4 * threads) {
             const int p = p0 + 4 * tid;
             bool r[4];
             int n = 0;
@@ -151,13 +152,13 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c
     }
     ok = ok && found >= total;
     __syncthreads();
-    for (int s = tid; s < S; s += kPlanThreads)
+    for (int s = tid; s < S; s += threads)
         if (last[s] >= 0) {                       // the marks back to rest
             writers[last[s] >> 1] = 0;
             first[last[s] >> 1] = 0;
         }
     if (!ok) return;
-    for (int m = tid; m < moves; m += kPlanThreads) {
+    for (int m = tid; m < moves; m += threads) {
         const int s = mv_src[m], len = c.length()[s], old = last[s] >> 1, to = fl[off[s]];
         mv_src[m] = old;
         c.state[c.L.move_dst + m] = to;
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheView c
         c.table(s)[len >> c.page_shift] = to;
         atomicSub(ref + old, 1);
     }
-    for (int i = tid; i < (int)total; i += kPlanThreads) ref[fl[i]] = 1;
+    for (int i = tid; i < (int)total; i += threads) ref[fl[i]] = 1;
     const int lane = tid & 31;
-    for (int s = tid >> 5; s < S; s += kPlanThreads / 32) {   // a warp per stream
+    for (int s = tid >> 5; s < S; s += threads / 32) {   // a warp per stream
         const int held = c.held()[s], n = need[s];
         const int* from = fl + off[s] + (last[s] >= 0 ? last[s] & 1 : 0);
         for (int i = held + lane; i < n; i += 32) c.table(s)[i] = from[i - held];
@@ -187,21 +188,23 @@ constexpr int kCopyThreads = 512;
 constexpr int kPiece = 4096;      // bytes a warp copies at a time: 8 independent 16-byte loads per lane
 
 // move_src[m] -> move_dst[m] in every pool of the list, the first move_used[m] tokens of
-// every head.  A warp takes pieces of one head's page.
-__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, __grid_constant__ const PoolList pools, int n_pools) {
+// every head (a warp takes pieces of one head's page); with `remap`, the tables after a
+// compact too: entries at U or above have moved.  Bound by HBM: it reads and writes each
+// byte once, 64 KB in flight per SM.
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, const __grid_constant__ PoolList pools, int n_pools, int remap) {
     grid_dependency_wait();
     const int moves = c.state[kCacheMoves];
     const int row = c.D * 2, head = c.page * row;            // bytes of a token, of a head's page
     const int pieces = (head + kPiece - 1) / kPiece;
+    const int lane = threadIdx.x & 31, warp0 = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+    const int warps = gridDim.x * (kCopyThreads / 32);
     const long long n = (long long)moves * n_pools * c.Hkv * pieces;
-    const int lane = threadIdx.x & 31;
-    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
-    for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < n; u += warps) {
-        long long w = u;
-        const int piece = (int)(w % pieces); w /= pieces;
-        const int h = (int)(w % c.Hkv); w /= c.Hkv;
-        const int pool = (int)(w % n_pools);
-        const int m = (int)(w / n_pools);
+    for (long long u = warp0; u < n; u += warps) {
+        const int m = (int)(u / (n_pools * c.Hkv * pieces));
+        int w = (int)(u - (long long)m * (n_pools * c.Hkv * pieces));
+        const int pool = w / (c.Hkv * pieces);
+        w -= pool * (c.Hkv * pieces);
+        const int h = w / pieces, piece = w - h * pieces;
         const int bytes = c.state[c.L.move_used + m] * row;
         char* const base = static_cast<char*>(pools.base[pool]);
         const int64_t at = (int64_t)h * head + (int64_t)piece * kPiece;
@@ -216,34 +219,63 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, _
         for (int i = 0; i < 8; ++i)
             if (i * 32 + lane < left) __stcs(dst + i * 32 + lane, v[i]);
     }
+    if (!remap) return;
+    const int U = c.state[kCacheLive];
+    const int* to = c.state + c.L.free_list;
+    for (int s = warp0; s < c.L.S; s += warps) {
+        const int held = min(c.held()[s], c.L.M);
+        for (int i = lane; i < held; i += 32) {
+            const int p = c.table(s)[i];
+            if (p >= U && p < c.L.P) c.table(s)[i] = to[p];
+            else if ((unsigned)p >= (unsigned)c.L.P) cache_error(c, MOE_ERR_CACHE_STATE, s);
+        }
+    }
 }
 
 // ---- append --------------------------------------------------------------------------
 
-// A thread per 16 bytes of a token's keys (y = 0) or values (y = 1).
+// A warp has 32 16-byte words, at the same place, of kTok consecutive tokens of a stream, keys
+// and values: 2 kTok loads are in flight per lane while the pages are looked up (a lane per
+// token).  Bound by HBM for long blocks, by the launch and that look-up for short ones.
+template <int kTok>
 __global__ void __launch_bounds__(256) cache_append_kernel(CacheView c, const char* __restrict__ k, const char* __restrict__ v,
                                                            int64_t row_bytes, char* __restrict__ kp, char* __restrict__ vp,
-                                                           int streams, int block, const int* __restrict__ lengths) {
-    const int per_head = c.D / 8, per_token = c.Hkv * per_head;
-    const int64_t n = (int64_t)streams * block * per_token;
-    const char* src = blockIdx.y ? v : k;
-    char* const dst = blockIdx.y ? vp : kp;
-    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < n; u += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t tok = u / per_token;
-        const int w = (int)(u - tok * per_token), h = w / per_head, x = w - h * per_head;
-        const int s = (int)(tok / block), i = (int)(tok - (int64_t)s * block);
-        if (lengths && i >= lengths[s]) continue;
-        const int len = c.length()[s];
-        const int64_t pos = (int64_t)len + i, at = pos >> c.page_shift;
+                                                           int streams, int block, int groups, const int* __restrict__ lengths) {
+    const int lane = threadIdx.x & 31, log_head = c.D == 128 ? 4 : 3;        // words of a head: 16 or 8
+    const int words = c.Hkv << log_head, parts = (words + 31) / 32;
+    const int n = streams * groups * parts;
+    grid_dependency_wait();
+    for (int u = blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += gridDim.x * 8) {
+        const int g = u / parts, w = (u - g * parts) * 32 + lane;
+        const int s = g / groups, i0 = (g - s * groups) * kTok;
+        const int used = lengths ? min(lengths[s], block) : block;
+        const int64_t tok = (int64_t)s * block + i0;
+        uint4 a[2][kTok];
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+            if (w < words && i0 + t < used) {
+                a[0][t] = __ldcs(reinterpret_cast<const uint4*>(k + (tok + t) * row_bytes) + w);
+                a[1][t] = __ldcs(reinterpret_cast<const uint4*>(v + (tok + t) * row_bytes) + w);
+            }
+        const int len = c.length()[s], held = min(c.held()[s], c.L.M);
         int page = -1;
-        if (len >= 0 && at < c.held()[s] && at < c.L.M) page = c.table(s)[at];
-        if ((unsigned)page >= (unsigned)c.L.P || c.refcount()[page] > 1) {
-            if (w == 0) cache_error(c, MOE_ERR_CACHE_STATE, s);
-            continue;
+        if (lane < kTok && i0 + lane < used) {
+            const int at = (int)(((unsigned)len + i0 + lane) >> c.page_shift);   // (a sum beyond 2^31 is beyond any table)
+            if (len >= 0 && at < held) page = c.table(s)[at];
+            if ((unsigned)page >= (unsigned)c.L.P || c.refcount()[page] > 1) {
+                page = -1;
+                if (w == lane) cache_error(c, MOE_ERR_CACHE_STATE, s);
+            }
         }
-        const uint4 val = __ldg(reinterpret_cast<const uint4*>(src + tok * row_bytes + (int64_t)w * 16));
-        const int64_t e = page * c.page_stride + ((int64_t)h * c.page + (pos & (c.page - 1))) * c.D + x * 8;
-        *reinterpret_cast<uint4*>(dst + e * 2) = val;
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            const int to = __shfl_sync(0xFFFFFFFFu, page, t);
+            if (w >= words || i0 + t >= used || to < 0) continue;
+            const int64_t e = to * c.page_stride + ((int64_t)(w >> log_head) * c.page + ((len + i0 + t) & (c.page - 1))) * c.D +
+                              (w & ((1 << log_head) - 1)) * 8;
+            *reinterpret_cast<uint4*>(kp + e * 2) = a[0][t];
+            *reinterpret_cast<uint4*>(vp + e * 2) = a[1][t];
+        }
     }
 }
 
@@ -252,6 +284,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(CacheView c, const ch
 // A warp per stream: gives back the pages behind its new length.
 __global__ void __launch_bounds__(256) cache_truncate_kernel(CacheView c, const int* __restrict__ value, int relative) {
     const int s = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    grid_dependency_wait();
     if (s >= c.L.S || value[s] < 0) return;
     const int len = c.length()[s], held = c.held()[s];
     const long long to = (long long)value[s] + (relative ? len : 0);
@@ -284,6 +317,7 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(CacheView c, const int*
     const int tid = threadIdx.x, S = c.L.S;
     for (int i = tid; i < (S + 31) / 32; i += 256) taken[i] = 0;
     if (tid == 0) s_bad = kNoStream;
+    grid_dependency_wait();
     __syncthreads();
     for (int i = tid; i < n; i += 256) {
         const int a = src[i], b = dst[i];
@@ -334,18 +368,19 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(CacheView c, const int*
 // One CTA.  U = pages in use; the i-th used page at U or above goes to the i-th free one
 // below U (there are as many of one as of the other).
 __global__ void __launch_bounds__(kPlanThreads) cache_compact_kernel(CacheView c) {
-    const int tid = threadIdx.x, P = c.L.P;
+    const int tid = threadIdx.x, threads = blockDim.x, P = c.L.P;
     int* const ref = c.refcount();
     int* const to = c.state + c.L.free_list;     // old page -> new page, for the pages that move
     int* const src = c.state + c.L.move_src;
     int* const dst = c.state + c.L.move_dst;
     long long sum;
     int mine = 0;
-    for (int p = tid; p < P; p += kPlanThreads) mine += ref[p] != 0;
+    grid_dependency_wait();
+    for (int p = tid; p < P; p += threads) mine += ref[p] != 0;
     block_scan(mine, &sum);
     const int U = (int)sum;
     int n_src = 0, n_dst = 0;
-    for (int p0 = 0; p0 < P; p0 += kPlanThreads) {
+    for (int p0 = 0; p0 < P; p0 += threads) {
         const int p = p0 + tid;
         const bool used = p < P && ref[p] != 0;
         const bool up = used && p >= U, hole = p < U && !used;
@@ -356,7 +391,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_kernel(CacheView c
         n_dst += (int)(sum & 0xFFFFFFFF);
     }
     __syncthreads();
-    for (int m = tid; m < n_src; m += kPlanThreads) {
+    for (int m = tid; m < n_src; m += threads) {
         const int a = src[m], b = dst[m];
         to[a] = b;
         c.state[c.L.move_used + m] = c.page;
@@ -366,21 +401,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_kernel(CacheView c
     if (tid == 0) {
         c.state[kCacheMoves] = n_src;
         c.state[kCacheLive] = U;
-    }
-}
-
-// The tables after a compact: entries at U or above have moved.
-__global__ void __launch_bounds__(256) cache_remap_kernel(CacheView c) {
-    grid_dependency_wait();
-    const int U = c.state[kCacheLive];
-    const int* to = c.state + c.L.free_list;
-    for (int s = blockIdx.x; s < c.L.S; s += gridDim.x) {
-        const int held = min(c.held()[s], c.L.M);
-        for (int i = threadIdx.x; i < held; i += 256) {
-            const int p = c.table(s)[i];
-            if (p >= U && p < c.L.P) c.table(s)[i] = to[p];
-            else if ((unsigned)p >= (unsigned)c.L.P) cache_error(c, MOE_ERR_CACHE_STATE, s);
-        }
     }
 }
 
@@ -423,10 +443,15 @@ bool encode_pool(CUtensorMap* m, const void* base, const moe_mxfp4_cache_config&
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+int status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// Copies the pages of the move list in every pool, kMaxPools pools a launch.
-int launch_copies(const moe_mxfp4_cache* c, const moe::CacheView& v, cudaStream_t st) {
+// Threads of a planning CTA: a barrier of fewer warps is cheaper, and few streams and pages
+// need no more (a pass over the pages takes four per thread).
+int plan_threads(const moe_mxfp4_cache* c) { return c->cfg.num_streams <= 256 && c->cfg.num_pages <= 2048 ? 256 : moe::kPlanThreads; }
+
+// Copies the pages of the move list (at most `moves` of them) in every pool, kMaxPools pools a
+// launch; the last launch also rewrites the tables, with `remap`.
+int launch_copies(const moe_mxfp4_cache* c, const moe::CacheView& v, int64_t moves, int remap, cudaStream_t st) {
     for (int l0 = 0; l0 < c->cfg.num_layers; l0 += moe::kMaxPools / 2) {
         moe::PoolList pools = {};
         int n = 0;
@@ -434,8 +459,12 @@ int launch_copies(const moe_mxfp4_cache* c, const moe::CacheView& v, cudaStream_
             pools.base[n++] = c->layers[l].k_dev;
             pools.base[n++] = c->layers[l].v_dev;
         }
-        if (moe::launch_dependent(moe::cache_copy_kernel, dim3(4 * c->sm_count), dim3(moe::kCopyThreads), 0, st, v, pools,
-                                  n) != cudaSuccess)
+        const int64_t head = (int64_t)c->cfg.page_tokens * c->cfg.head_dim * 2;
+        int64_t warps = moves * n * c->cfg.kv_heads * ((head + moe::kPiece - 1) / moe::kPiece);
+        if (remap && warps < c->cfg.num_streams) warps = c->cfg.num_streams;
+        const int64_t per_cta = moe::kCopyThreads / 32, want = (warps + per_cta - 1) / per_cta, most = 4 * c->sm_count;
+        if (moe::launch_dependent(moe::cache_copy_kernel, dim3((unsigned)(want < most ? want : most)), dim3(moe::kCopyThreads), 0, st,
+                                  v, pools, n, remap && l0 + moe::kMaxPools / 2 >= c->cfg.num_layers) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     return MOE_OK;
@@ -507,9 +536,9 @@ int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* 
     if (!on.ok()) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const moe::CacheView v = moe::cache_view(c, state_dev);
-    moe::cache_reserve_kernel<<<1, moe::kPlanThreads, 0, st>>>(v, add_dev, add);
-    if (const int r = launch_copies(c, v, st)) return r;
-    return launched();
+    if (moe::launch_dependent(moe::cache_reserve_kernel, dim3(1), dim3(plan_threads(c)), 0, st, v, add_dev, add) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch_copies(c, v, c->cfg.num_streams, 0, st);
 }
 
 int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const void* k_dev, const void* v_dev,
@@ -523,21 +552,25 @@ int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, c
     if (!k_dev || !v_dev || !aligned16(k_dev) || !aligned16(v_dev)) return MOE_ERR_INVALID_ARG;
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
-    const int64_t n = (int64_t)streams * block * (row / 8);
-    const int64_t want = (n + 255) / 256, most = 32 * (int64_t)c->sm_count;
-    moe::cache_append_kernel<<<dim3((unsigned)(want < most ? want : most), 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        moe::cache_view(c, state_dev), static_cast<const char*>(k_dev), static_cast<const char*>(v_dev), row_stride * 2,
-        static_cast<char*>(c->layers[layer].k_dev), static_cast<char*>(c->layers[layer].v_dev), streams, block, lengths_dev);
-    return launched();
+    // four tokens a warp where that still leaves 16 warps for every SM, else one
+    const int parts = (int)((row / 8 + 31) / 32);
+    const auto warps = [&](int tok) { return (int64_t)streams * ((block + tok - 1) / tok) * parts; };
+    const int tok = warps(4) >= 16 * (int64_t)c->sm_count ? 4 : 1;
+    if (warps(tok) > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    const int64_t want = (warps(tok) + 7) / 8, most = 64 * (int64_t)c->sm_count;
+    return status_of(moe::launch_dependent(
+        tok == 4 ? moe::cache_append_kernel<4> : moe::cache_append_kernel<1>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
+        static_cast<cudaStream_t>(stream), moe::cache_view(c, state_dev), static_cast<const char*>(k_dev), static_cast<const char*>(v_dev),
+        row_stride * 2, static_cast<char*>(c->layers[layer].k_dev), static_cast<char*>(c->layers[layer].v_dev), streams, block,
+        (block + tok - 1) / tok, lengths_dev));
 }
 
 static int cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* value, int relative, void* stream) {
     if (!good_state(c, state_dev) || !value || !aligned4(value)) return MOE_ERR_INVALID_ARG;
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
-    moe::cache_truncate_kernel<<<(c->cfg.num_streams + 7) / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        moe::cache_view(c, state_dev), value, relative);
-    return launched();
+    return status_of(moe::launch_dependent(moe::cache_truncate_kernel, dim3((c->cfg.num_streams + 7) / 8), dim3(256), 0,
+                                           static_cast<cudaStream_t>(stream), moe::cache_view(c, state_dev), value, relative));
 }
 
 int moe_mxfp4_cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* new_length_dev, void* stream) {
@@ -556,9 +589,8 @@ int moe_mxfp4_cache_fork(moe_mxfp4_cache* c, void* state_dev, const int32_t* src
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
     const size_t smem = (size_t)((c->cfg.num_streams + 31) / 32) * 4;
-    moe::cache_fork_kernel<<<n, 256, smem, static_cast<cudaStream_t>(stream)>>>(moe::cache_view(c, state_dev), src_dev,
-                                                                              dst_dev, n);
-    return launched();
+    return status_of(moe::launch_dependent(moe::cache_fork_kernel, dim3(n), dim3(256), smem, static_cast<cudaStream_t>(stream),
+                                           moe::cache_view(c, state_dev), src_dev, dst_dev, n));
 }
 
 int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream) {
@@ -567,12 +599,8 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream) {
     if (!on.ok()) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const moe::CacheView v = moe::cache_view(c, state_dev);
-    moe::cache_compact_kernel<<<1, moe::kPlanThreads, 0, st>>>(v);
-    if (const int r = launch_copies(c, v, st)) return r;
-    const int S = c->cfg.num_streams;
-    if (moe::launch_dependent(moe::cache_remap_kernel, dim3(S < 4096 ? S : 4096), dim3(256), 0, st, v) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return launched();
+    if (moe::launch_dependent(moe::cache_compact_kernel, dim3(1), dim3(plan_threads(c)), 0, st, v) != cudaSuccess) return MOE_ERR_CUDA;
+    return launch_copies(c, v, c->cfg.num_pages / 2, 1, st);
 }
 
 int moe_mxfp4_cache_check(moe_mxfp4_cache* c, void* state_dev, void* stream) {
