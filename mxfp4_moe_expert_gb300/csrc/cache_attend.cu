@@ -70,7 +70,7 @@ struct Segment {
     int own, wide, h, s;
     int r0, nrows;             // first packed row, rows
     int key0, T, key_end, ctx; // first key, tiles (0: no more segments), end of the keys, first block position
-    int no;                    // segments of this slot before it
+    int no, wide_no;           // segments, and wide ones, of this slot before it
 };
 
 template <int D>
@@ -83,12 +83,13 @@ struct AttSmem {
     uint64_t full[2][kStages], empty[2][kStages];            // [0]: wide, [1]: narrow
     uint64_t mended[kStages];                                // wide: slot 0's MMA warp has mended the V tile
     uint64_t turn[2];                                        // wide: the slot's turn on the tensor core
+    uint64_t handover;                                       // slot 1's narrow tiles are used up
     uint64_t segf[2][2], sege[2][2], qfull[2], sfull[2], phalf[2], pfull[2], ofull[2], drain[2];
     Segment seg[2][2];
     int scan[3][12];
     uint32_t tmem;
     int first_unit[2], first_off[2];
-    int bad_value[2];                                        // last segment (+ 1) with a non-finite block value
+    int bad_value[2], bad_wide;                              // last narrow (wide) segment (+ 1) with a non-finite block value
     int abort;
 };
 
@@ -427,6 +428,7 @@ __device__ bool att_produce(const CacheView& c, const AttendParams& p, const Sch
     while (att_next<D>(c, p, sc, L, wide, slot, worker, w, sg)) {
         if (!att_publish<D>(p, sm, slot, sg)) return false;
         ++sg.no;
+        sg.wide_no += wide;
         if (!loads) {
             n += 2 * sg.T;
             continue;
@@ -465,14 +467,32 @@ template <int D>
 __device__ void att_producer(const CacheView& c, const AttendParams& p, const Schedule& sc, AttSmem<D>& sm, const CUtensorMap* kmap,
                              const CUtensorMap* vmap, int slot) {
     Segment sg;
-    sg.no = 0;
+    sg.no = sg.wide_no = 0;
     uint32_t nw = 0, nn = 0;
-    bool ok = att_produce<D>(c, p, sc, sm, kmap, vmap, true, slot, sg, nw);
-    // the narrow rings take over the wide one's stages when all its tiles are used up
     const Ring<D> wide(sm, true, slot), narrow(sm, false, slot);
-    for (uint32_t i = nw > (uint32_t)wide.stages ? nw - wide.stages : 0; ok && i < nw; ++i)
-        ok = att_warp_wait(wide.empty(i), wide.round(i), &sm.abort, p.timeout_ns);
-    if (ok) ok = att_produce<D>(c, p, sc, sm, kmap, vmap, false, slot, sg, nn);
+    const auto used_up = [&](const Ring<D>& ring, uint32_t n) {   // all tiles of a ring
+        for (uint32_t i = n > (uint32_t)ring.stages ? n - ring.stages : 0; i < n; ++i)
+            if (!att_warp_wait(ring.empty(i), ring.round(i), &sm.abort, p.timeout_ns)) return false;
+        return true;
+    };
+    // Wide jobs keep the tensor core busy, narrow ones the memory: half of the CTAs begin with one
+    // kind and half with the other.  The rings share their stages, so one kind's tiles are all used
+    // up before the other's are copied.
+    bool ok = true;
+    for (int phase = 0; phase < 2 && ok; ++phase) {
+        const bool is_wide = (phase ^ blockIdx.x & 1) == 0;
+        uint32_t& n = is_wide ? nw : nn;
+        ok = att_produce<D>(c, p, sc, sm, kmap, vmap, is_wide, slot, sg, n);
+        if (phase == 1 || !ok) break;
+        ok = used_up(is_wide ? wide : narrow, n);
+        if (is_wide) continue;
+        if (slot == 0) {                       // slot 0 copies the wide tiles, into both narrow rings' stages
+            ok = ok && att_warp_wait(&sm.handover, 0, &sm.abort, p.timeout_ns);
+        } else if (ok) {
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.handover);
+            __syncwarp();
+        }
+    }
     sg.T = 0;
     if (ok) ok = att_publish<D>(p, sm, slot, sg);
     if (ok && !*reinterpret_cast<volatile int*>(&sm.abort)) return;
@@ -534,7 +554,7 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
         if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
         const Segment& sg = sm.seg[slot][no & 1];
         const int T = uniform(sg.T), wide = uniform(sg.wide), key0 = uniform(sg.key0), ctx = uniform(sg.ctx);
-        const int key_end = uniform(sg.key_end);
+        const int key_end = uniform(sg.key_end), wide_no = uniform(sg.wide_no);
         if (issues) mbar_arrive(&sm.sege[slot][no & 1]);
         if (T == 0) return;
         const Ring<D> ring(sm, wide, slot);
@@ -578,8 +598,7 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
                     const bool bad = att_mend_v<D, kBf16>(sm.kv[st], min(max(ctx - j0, 0), kKeyTile), min(max(key_end - j0, 0), kKeyTile));
                     if (issues) {
                         if (bad) {
-                            *reinterpret_cast<volatile int*>(&sm.bad_value[slot]) = no + 1;
-                            if (wide) *reinterpret_cast<volatile int*>(&sm.bad_value[1]) = no + 1;
+                            *reinterpret_cast<volatile int*>(wide ? &sm.bad_wide : &sm.bad_value[slot]) = (wide ? wide_no : no) + 1;
                             __threadfence_block();
                         }
                         if (wide) mbar_arrive(&sm.mended[st]);
@@ -808,7 +827,8 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
         if (busy) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-            const bool mend = sg.own && *reinterpret_cast<volatile int*>(&sm.bad_value[slot]) == no + 1;
+            const bool mend = sg.own && *reinterpret_cast<volatile int*>(sg.wide ? &sm.bad_wide : &sm.bad_value[slot]) ==
+                                            (sg.wide ? sg.wide_no : no) + 1;
             float* const out = sg.out;
             const int R = sg.R, r = sg.out_row + tid;
             const int64_t at = row.tok * p.a.q_heads + row.head;
@@ -873,6 +893,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
             mbar_init(&sm.drain[x], 1);
             sm.bad_value[x] = 0;
         }
+        mbar_init(&sm.handover, 1);
+        sm.bad_wide = 0;
         sm.abort = 0;
         fence_barrier_init();
     }
