@@ -38,7 +38,7 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // columns: S of slot x at 128 x,
 constexpr float kRescale = 8.0f;               // exponents that the maximum may pass the reference by
 // A segment costs about this many tiles more than its tiles (its queries, its start, its rows' way
 // out); dealt out with them, narrow jobs being short.
-constexpr int kPadWide = 1, kPadNarrow = 2;
+constexpr int kPadWide = 1, kPadNarrow = 3;
 
 struct AttendParams {
     moe_mxfp4_attend_args a;
@@ -83,10 +83,10 @@ struct AttSmem {
     uint64_t full[2][kStages], empty[2][kStages];            // [0]: wide, [1]: narrow
     uint64_t mended[kStages];                                // wide: slot 0's MMA warp has mended the V tile
     uint64_t turn[2];                                        // wide: the slot's turn on the tensor core
-    uint64_t handover;                                       // slot 1's narrow tiles are used up
+    uint64_t handover;                                       // the first kind's tiles are used up (att_producer)
     uint64_t segf[2][2], sege[2][2], qfull[2], sfull[2], phalf[2], pfull[2], ofull[2], drain[2];
     Segment seg[2][2];
-    int scan[3][12];
+    int sums[4][kAttThreads / 32];
     uint32_t tmem;
     int first_unit[2], first_off[2];
     int bad_value[2], bad_wide;                              // last narrow (wide) segment (+ 1) with a non-finite block value
@@ -187,7 +187,7 @@ __device__ __forceinline__ JobList att_list(const CacheView& c, const AttendPara
 
 // Exclusive prefix over the CTA's threads of a value per thread, and the sum.
 template <int D>
-__device__ __forceinline__ int att_scan(AttSmem<D>& sm, int k, int v, int* total) {
+__device__ __forceinline__ int att_scan(AttSmem<D>& sm, int v, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -195,13 +195,13 @@ __device__ __forceinline__ int att_scan(AttSmem<D>& sm, int k, int v, int* total
         const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) sm.scan[k][warp] = x;
+    if (lane == 31) sm.sums[3][warp] = x;
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kAttThreads / 32; ++w) {
-        if (w < warp) before += sm.scan[k][w];
-        all += sm.scan[k][w];
+        if (w < warp) before += sm.sums[3][w];
+        all += sm.sums[3][w];
     }
     *total = all;
     __syncthreads();
@@ -218,25 +218,40 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     Schedule sc;
     const int units = p.a.streams * p.U, tid = threadIdx.x, pad = p.wide_own ? kPadWide : kPadNarrow;
     const int shared = att_shared(c, p);
-    int with = 0, without = 0, sharers = 0, t;
+    // places of one head's own jobs with and without the shared pass, and the streams that share
+    int sum[3] = {0, 0, 0}, mine[2] = {0, 0}, rows = 0, begin = 0;   // (mine: of unit `tid`)
     for (int i = tid; i < units; i += kAttThreads) {
         const OwnUnit w = att_unit(c, p, i, shared);
         if (w.nrows == 0) continue;
-        with += w.tiles() + pad;
-        without += (w.end + kKeyTile - 1) / kKeyTile + pad;
-        sharers += w.r0 == 0 && w.begin > 0;
-    }
-    att_scan(sm, 0, without, &t);
-    sc.W1 = t;
-    sc.shared = 0;
-    if (shared > 0) {
-        att_scan(sm, 1, sharers, &t);
-        if (t > 1) {                           // one stream alone reads all through its own table
-            sc.shared = shared;
-            att_scan(sm, 2, with, &t);
-            sc.W1 = t;
+        const int with = w.tiles() + pad, without = (w.end + kKeyTile - 1) / kKeyTile + pad;
+        sum[0] += with;
+        sum[1] += without;
+        sum[2] += w.r0 == 0 && w.begin > 0;
+        if (i == tid) {
+            mine[0] = with;
+            mine[1] = without;
+            rows = w.nrows;
+            begin = w.begin;
         }
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int x = __reduce_add_sync(0xFFFFFFFFu, sum[k]);
+        if ((tid & 31) == 0) sm.sums[k][tid >> 5] = x;
+        sum[k] = 0;
+    }
+    if (tid < 2) {
+        sm.first_unit[tid] = 0;
+        sm.first_off[tid] = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttThreads / 32; ++w)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum[k] += sm.sums[k][w];
+    const bool share = sum[2] > 1;             // one stream alone reads all through its own table
+    sc.shared = share ? shared : 0;
+    sc.W1 = share ? sum[0] : sum[1];
     // the unit, and the place in it, where each slot's own jobs begin
     const JobList L = att_list(c, p, p.wide_own != 0, sc.shared, sc.W1, gridDim.x);
     int y[2];
@@ -245,27 +260,27 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
         const int w = p.wide_own ? blockIdx.x : x * gridDim.x + blockIdx.x, at = w < L.workers ? L.first(w) : 0;
         y[x] = at > L.W_sh ? (at - L.W_sh) % L.W1 : 0;
     }
-    if (tid < 2) {
-        sm.first_unit[tid] = 0;
-        sm.first_off[tid] = 0;
-    }
-    __syncthreads();
     if (blockIdx.x == 0 || y[0] > 0 || y[1] > 0) {
         int at = 0;
         for (int i0 = 0; i0 < units; i0 += kAttThreads) {
             const int i = i0 + tid;
-            const OwnUnit u = i < units ? att_unit(c, p, i, sc.shared) : OwnUnit{0, 0, 0, 0, 0};
-            const int n = u.nrows > 0 ? u.tiles() + pad : 0;
-            int sum;
-            const int x0 = at + att_scan(sm, 0, n, &sum);
+            int n = mine[share ? 0 : 1];
+            if (i0 > 0) {                      // (units behind the first pass are read again)
+                const OwnUnit u = i < units ? att_unit(c, p, i, sc.shared) : OwnUnit{0, 0, 0, 0, 0};
+                n = u.nrows > 0 ? u.tiles() + pad : 0;
+                rows = u.nrows;
+                begin = u.begin;
+            }
+            int all;
+            const int x0 = at + att_scan(sm, n, &all);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (n > 0 && x0 <= y[x] && y[x] < x0 + n) {
                     sm.first_unit[x] = i;
                     sm.first_off[x] = y[x] - x0;
                 }
-            if (blockIdx.x == 0 && i < units) p.units[i] = make_int4(x0, u.nrows, n - pad, u.begin > 0);
-            at += sum;
+            if (blockIdx.x == 0 && i < units) p.units[i] = make_int4(x0, rows, n - pad, share && begin > 0);
+            at += all;
         }
     }
     if (blockIdx.x == 0 && tid == 0) {
@@ -484,13 +499,15 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
         uint32_t& n = is_wide ? nw : nn;
         ok = att_produce<D>(c, p, sc, sm, kmap, vmap, is_wide, slot, sg, n);
         if (phase == 1 || !ok) break;
-        ok = used_up(is_wide ? wide : narrow, n);
-        if (is_wide) continue;
-        if (slot == 0) {                       // slot 0 copies the wide tiles, into both narrow rings' stages
-            ok = ok && att_warp_wait(&sm.handover, 0, &sm.abort, p.timeout_ns);
-        } else if (ok) {
-            if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.handover);
+        // The warp that copied the last tiles waits for their ring (the other one has not followed its
+        // phases) and tells the other: slot 0 after the wide jobs; after the narrow ones slot 1 tells
+        // slot 0, which then copies into both.
+        if (!is_wide || slot == 0) ok = used_up(is_wide ? wide : narrow, n);
+        if (slot == (is_wide ? 0 : 1)) {
+            if (ok && (threadIdx.x & 31) == 0) mbar_arrive(&sm.handover);
             __syncwarp();
+        } else {
+            ok = ok && att_warp_wait(&sm.handover, 0, &sm.abort, p.timeout_ns);
         }
     }
     sg.T = 0;

@@ -114,6 +114,20 @@ def test_long_and_many(S, prefix, lo, hi):
     c.check(out, lse, streams=sorted({0, S - 1, S // 2, S // 3}))
 
 
+@pytest.mark.parametrize("S,Hq,D,prefix,hi", [(32, 56, 128, 8192, 1500), (24, 64, 64, 6000, 3000), (64, 64, 128, 12288, 100)])
+def test_many_tiles_for_every_cta(S, Hq, D, prefix, hi):
+    """Enough tiles of the shared prefix and of the streams' own keys that every ring goes round many times, and
+    passes from one kind of work to the other; every row of some streams, and all rows twice."""
+    rng = random.Random(S)
+    c = Case([prefix + rng.randint(1, hi) for _ in range(S)], 8, Hq, 8, D=D, page=16 if D == 64 else 64, prefix=prefix, seed=S)
+    out, lse = c.attend()
+    c.check(out, lse, streams=sorted(rng.sample(range(S), 4)))
+    alone, alse = c.attend(shared_tokens=0)
+    assert (lse - alse).abs().max() <= 2e-5
+    again, again_lse = c.attend()
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
 def test_padded_positions_are_left_alone():
     used = [0, 5, 8, 1, 0, 7]
     c = Case([100, 640, 641, 0, 3000, 700], 8, 8, 2, prefix=640, seed=3)
