@@ -384,7 +384,8 @@ typedef struct {
     int32_t dtype;        /* MOE_DTYPE_*: of the pools, the queries and the outputs */
     int64_t page_stride;  /* elements between pages of a pool, a multiple of 8, at least
                            * kv_heads * page_tokens * head_dim; 0 = exactly that */
-    int32_t timeout_us;   /* bound of every device-side wait in microseconds; 0 = default (200000) */
+    int32_t timeout_us;   /* bound of every device-side wait in microseconds, and 10 more for each tile of
+                           * keys that the wait stands for; 0 = default (200000) */
 } moe_mxfp4_cache_config;
 
 typedef struct {
@@ -416,7 +417,7 @@ int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* 
  * k_dev, v_dev: [streams, block, kv_heads, head_dim], 16-byte aligned, `row_stride`
  * elements between tokens (a multiple of 8; 0 = kv_heads * head_dim).  length is not
  * changed.  A position that is not reserved, or whose page other streams hold too, is
- * skipped, with MOE_ERR_CACHE_STATE (detail: the stream). */
+ * skipped, with MOE_ERR_CACHE_STATE (detail: a stream with such a position). */
 int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const void* k_dev, const void* v_dev,
                            int64_t row_stride, int32_t streams, int32_t block, const int32_t* lengths_dev,
                            void* stream);
@@ -448,14 +449,17 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
  * out = sum_j softmax_j(scale * q.k_j) v_j over the keys it sees, lse = ln sum_j
  * exp(scale * q.k_j); a row that sees nothing has out = 0, lse = -inf.  Rows of positions
  * n_s and behind are left as they were.  Keys that a row does not see have no part in
- * it, whatever their bits (NaN and infinities among them).
+ * it, whatever their bits (NaN and infinities among them).  Positions that the stream holds
+ * no page for read as zeros.
  * shared_tokens (a multiple of page_tokens, 0 = none): the first tokens of stream slot
  * shared_stream, read once for all the streams that hold the same pages (forked from it,
  * directly or not); a stream with other pages there, or with fewer tokens, reads its own.
  * Arithmetic: products of q and k are exact and summed in fp32, as are the statistics of
  * the softmax; its terms are rounded to the cache's type for their product with v, which
  * is summed in fp32.
- * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents. */
+ * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents.
+ * MOE_ERR_UNSUPPORTED when the rows and the keys that max_pages allows make 2^31 tiles or
+ * more (256 rows x 128 keys). */
 typedef struct {
     const void* q_dev;           /* [streams, block, q_heads, head_dim], 16-byte aligned */
     int64_t q_stride;            /* elements between tokens, a multiple of 8; 0 = q_heads * head_dim */

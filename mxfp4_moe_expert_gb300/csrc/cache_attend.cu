@@ -415,11 +415,14 @@ struct Ring {
     __device__ uint64_t* empty(uint32_t i) const { return &sm->empty[wide ? 0 : 1][stage(i)]; }
 };
 
+// Limit of a wait for work on `tiles` tiles (of K or V) that are under way.
+__device__ __forceinline__ unsigned long long att_limit(const AttendParams& p, uint32_t tiles) { return p.timeout_ns + 10000ull * tiles; }
+
 // Makes a segment known to the slot's other warps.
 template <int D>
-__device__ __forceinline__ bool att_publish(const AttendParams& p, AttSmem<D>& sm, int slot, const Segment& sg) {
+__device__ __forceinline__ bool att_publish(const AttendParams& p, AttSmem<D>& sm, int slot, const Segment& sg, uint32_t tiles) {
     const int e = sg.no & 1;
-    if (!att_warp_wait(&sm.sege[slot][e], ((sg.no >> 1) & 1) ^ 1, &sm.abort, p.timeout_ns)) return false;
+    if (!att_warp_wait(&sm.sege[slot][e], ((sg.no >> 1) & 1) ^ 1, &sm.abort, att_limit(p, tiles))) return false;
     if ((threadIdx.x & 31) == 0) {
         sm.seg[slot][e] = sg;
         mbar_arrive(&sm.segf[slot][e]);
@@ -441,7 +444,7 @@ __device__ bool att_produce(const CacheView& c, const AttendParams& p, const Sch
     const Ring<D> ring(sm, wide, slot);
     Walk w = att_walk<D>(L, sm, slot, worker);
     while (att_next<D>(c, p, sc, L, wide, slot, worker, w, sg)) {
-        if (!att_publish<D>(p, sm, slot, sg)) return false;
+        if (!att_publish<D>(p, sm, slot, sg, n)) return false;
         ++sg.no;
         sg.wide_no += wide;
         if (!loads) {
@@ -507,11 +510,11 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
             if (ok && (threadIdx.x & 31) == 0) mbar_arrive(&sm.handover);
             __syncwarp();
         } else {
-            ok = ok && att_warp_wait(&sm.handover, 0, &sm.abort, p.timeout_ns);
+            ok = ok && att_warp_wait(&sm.handover, 0, &sm.abort, att_limit(p, n));
         }
     }
     sg.T = 0;
-    if (ok) ok = att_publish<D>(p, sm, slot, sg);
+    if (ok) ok = att_publish<D>(p, sm, slot, sg, nw + nn);
     if (ok && !*reinterpret_cast<volatile int*>(&sm.abort)) return;
     // after an abort: every copy has landed before the CTA leaves
     const unsigned long long until = globaltimer_ns() + p.timeout_ns;
@@ -567,9 +570,11 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
     const uint32_t ts = tmem + kTmemS + 128 * slot, to = tmem + kTmemO + 128 * slot, q = smem_u32(sm.q[slot]);
     uint32_t used_wide = 0, used_narrow = 0, np = 0, turns = 0, mends = 0;   // mends: a bit per stage
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return att_warp_wait(bar, parity, &sm.abort, p.timeout_ns); };
+    uint32_t tiles = 0;                                    // so far
     for (int no = 0;; ++no) {
-        if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
+        if (!att_warp_wait(&sm.segf[slot][no & 1], (no >> 1) & 1, &sm.abort, att_limit(p, tiles))) return;
         const Segment& sg = sm.seg[slot][no & 1];
+        tiles += 2 * sg.T;
         const int T = uniform(sg.T), wide = uniform(sg.wide), key0 = uniform(sg.key0), ctx = uniform(sg.ctx);
         const int key_end = uniform(sg.key_end), wide_no = uniform(sg.wide_no);
         if (issues) mbar_arrive(&sm.sege[slot][no & 1]);
@@ -752,11 +757,13 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
     const uint32_t ts = tmem + kTmemS + 128 * slot + lanes, to = tmem + kTmemO + 128 * slot + lanes;
     uint32_t ns = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return att_warp_wait(bar, parity, &sm.abort, p.timeout_ns); };
+    uint32_t tiles = 0;                                          // so far
     for (int no = 0;; ++no) {
-        if (!wait(&sm.segf[slot][no & 1], (no >> 1) & 1)) return;
+        if (!att_warp_wait(&sm.segf[slot][no & 1], (no >> 1) & 1, &sm.abort, att_limit(p, tiles))) return;
         const Segment& sg = sm.seg[slot][no & 1];
         const int T = sg.T;
         if (T == 0) return;
+        tiles += 2 * T;
         // the query rows; the products that read the last ones have completed (ofull, below)
         att_load_q<D>(p, sg, sm.q[slot]);
         fence_proxy_async_shared();

@@ -128,6 +128,34 @@ def test_many_tiles_for_every_cta(S, Hq, D, prefix, hi):
     assert torch.equal(again, out) and torch.equal(again_lse, lse)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,prefix", [(1, 256, 1, 0), (3, 255, 1, 256), (2, 512, 2, 128), (1, 129, 1, 64)])
+def test_many_heads_on_one(B, Hq, Hkv, prefix):
+    c = Case([prefix + n for n in (0, 1, 130, 500)], B, Hq, Hkv, prefix=prefix, seed=Hq)
+    c.check(*c.attend())
+
+
+def test_the_shared_stream_may_be_one_of_the_batch():
+    """Streams forked from stream 0, which goes on itself; stream 2 was cut back into the prefix and has new pages."""
+    S, page, D, Hkv = 5, 32, 64, 2
+    mem = torch.randn((2, 120, Hkv, page, D), device="cuda").bfloat16()
+    cache = pkg.KvCache(layers=[(mem[0], mem[1])], num_streams=S, max_pages=20)
+    books = Books(S, 20, 120, page)
+    for c in (cache, books):
+        arg = (lambda x: x) if c is books else i32
+        c.reserve(arg([330, 0, 0, 0, 0]))
+        c.truncate(arg([330, -1, -1, -1, -1]))
+        c.fork(arg([0, 0, 0]), arg([1, 2, 4]))
+        c.truncate(arg([-1, -1, 70, -1, -1]))
+        c.reserve(arg([0, 0, 300, 0, 0]))
+        c.truncate(arg([-1, -1, 360, -1, -1]))
+        c.reserve(arg([6, 6, 6, 6, 6]))
+    cache.check()
+    q = torch.randn((S, 6, 12, D), device="cuda").bfloat16()
+    out, lse = cache.attend(0, q, shared_stream=0, shared_tokens=320)
+    cache.check()
+    assert_attention(out, lse, q, mem[0], mem[1], books, [6] * S, D ** -0.5)
+
+
 def test_padded_positions_are_left_alone():
     used = [0, 5, 8, 1, 0, 7]
     c = Case([100, 640, 641, 0, 3000, 700], 8, 8, 2, prefix=640, seed=3)
