@@ -51,7 +51,7 @@ struct AttendParams {
     float c;                   // |scale| log2 e
     uint32_t q_flip;           // sign flips of a pair of query elements (a negative scale)
     unsigned long long timeout_ns;
-    int* head;                 // workspace: the schedule for the merge
+    struct JobList* head;      // workspace: the lists (narrow, wide) for the merge
     int4* units;               // each unit: first own place (of a head), rows, tiles, whether it shares the prefix
     float* split_wide;         // partial rows of split jobs: 2 per worker, 256 rows each, ...
     float* split_narrow;       // ... 128 rows each
@@ -61,8 +61,6 @@ struct AttendParams {
     __host__ __device__ int rows_sh() const { return wide_sh ? 256 : 128; }
     __host__ __device__ int rows_own() const { return wide_own ? 256 : 128; }
 };
-enum : int { kHeadShared = 0, kHeadOwn = 1 };  // shared tokens in use, places of one head's own jobs
-
 // One worker's part of a job, for one slot.
 struct Segment {
     float* out;                // partial rows (nullptr: straight to the output)
@@ -73,6 +71,19 @@ struct Segment {
     int no, wide_no;           // segments, and wide ones, of this slot before it
 };
 
+// The jobs of one list (wide or narrow): shared ones, then own ones, each with its places in a
+// row of W (below 2^31: checked on the host): a job with n tiles has pad + n, tile i at place
+// pad + i.  Worker w has q places, one more when w < rem.
+struct JobList {
+    int pad, tiles_sh, has_own;
+    int W_sh, W1, W;                  // places of the shared jobs, of one head's own jobs, of all
+    int workers, q, rem;
+    __device__ int first(int w) const { return q * w + min(w, rem); }
+    __device__ int worker(int place) const {
+        const int big = rem * (q + 1);
+        return min(place < big ? place / (q + 1) : rem + (place - big) / q, workers - 1);
+    }
+};
 template <int D>
 struct AttSmem {
     static constexpr int kPanel = 128 * 128;                 // 128 rows x 64 elements
@@ -88,7 +99,8 @@ struct AttSmem {
     Segment seg[2][2];
     int sums[4][kAttThreads / 32];
     uint32_t tmem;
-    int first_unit[2], first_off[2];
+    JobList list[2];                                         // narrow, wide
+    int first_h[2], first_unit[2], first_off[2];             // where each slot's own jobs begin
     int bad_value[2], bad_wide;                              // last narrow (wide) segment (+ 1) with a non-finite block value
     int abort;
 };
@@ -155,28 +167,13 @@ __device__ __forceinline__ OwnUnit att_unit(const CacheView& c, const AttendPara
     return w;
 }
 
-// The jobs of one list (wide or narrow): shared ones, then own ones, each with its places in a
-// row of W (below 2^31: checked on the host): a job with n tiles has pad + n, tile i at place
-// pad + i.  Worker w has q places, one more when w < rem.
-struct JobList {
-    int pad, tiles_sh;
-    bool has_sh, has_own;
-    int W_sh, W1, W;                  // places of the shared jobs, of one head's own jobs, of all
-    int workers, q, rem;
-    __device__ int first(int w) const { return q * w + min(w, rem); }
-    __device__ int worker(int place) const {
-        const int big = rem * (q + 1);
-        return min(place < big ? place / (q + 1) : rem + (place - big) / q, workers - 1);
-    }
-};
 // W1: places of one head's own jobs (with this list's padding).
 __device__ __forceinline__ JobList att_list(const CacheView& c, const AttendParams& p, bool wide, int shared, int W1, int grid) {
     JobList L;
     L.pad = wide ? kPadWide : kPadNarrow;
-    L.has_sh = shared > 0 && (p.wide_sh != 0) == wide;
     L.has_own = (p.wide_own != 0) == wide;
     L.tiles_sh = (shared + kKeyTile - 1) / kKeyTile;
-    L.W_sh = L.has_sh ? c.Hkv * p.U_sh * (L.tiles_sh + L.pad) : 0;
+    L.W_sh = shared > 0 && (p.wide_sh != 0) == wide ? c.Hkv * p.U_sh * (L.tiles_sh + L.pad) : 0;
     L.W1 = L.has_own ? W1 : 0;
     L.W = L.W_sh + c.Hkv * L.W1;
     L.workers = min(wide ? grid : 2 * grid, L.W);                // none of them without a place
@@ -254,11 +251,17 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     sc.W1 = share ? sum[0] : sum[1];
     // the unit, and the place in it, where each slot's own jobs begin
     const JobList L = att_list(c, p, p.wide_own != 0, sc.shared, sc.W1, gridDim.x);
+    if (tid == 0) {
+        sm.list[p.wide_own] = L;
+        sm.list[p.wide_own ^ 1] = att_list(c, p, !p.wide_own, sc.shared, sc.W1, gridDim.x);
+    }
     int y[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int w = p.wide_own ? blockIdx.x : x * gridDim.x + blockIdx.x, at = w < L.workers ? L.first(w) : 0;
-        y[x] = at > L.W_sh ? (at - L.W_sh) % L.W1 : 0;
+        const int h = at > L.W_sh ? (at - L.W_sh) / L.W1 : 0;
+        y[x] = at > L.W_sh ? at - L.W_sh - h * L.W1 : 0;
+        if (tid == 0) sm.first_h[x] = h;
     }
     if (blockIdx.x == 0 || y[0] > 0 || y[1] > 0) {
         int at = 0;
@@ -283,11 +286,8 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
             at += all;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) {
-        p.head[kHeadShared] = sc.shared;
-        p.head[kHeadOwn] = sc.W1;
-    }
     __syncthreads();
+    if (blockIdx.x == 0 && tid < 2) p.head[tid] = sm.list[tid];
     return sc;
 }
 
@@ -322,7 +322,7 @@ __device__ __forceinline__ Walk att_walk(const JobList& L, const AttSmem<D>& sm,
     w.unit = 0;
     w.off = 0;
     if (L.has_own && w.v >= L.W_sh && w.v < w.end) {
-        w.h = (w.v - L.W_sh) / L.W1;
+        w.h = sm.first_h[slot];
         w.unit = sm.first_unit[slot];
         w.off = sm.first_off[slot];
     }
@@ -437,8 +437,7 @@ __device__ bool att_produce(const CacheView& c, const AttendParams& p, const Sch
                             const CUtensorMap* vmap, bool wide, int slot, Segment& sg, uint32_t& n) {
     using SM = AttSmem<D>;
     const int lane = threadIdx.x & 31, per_tile = kKeyTile >> c.page_shift;
-    const JobList L = att_list(c, p, wide, sc.shared, sc.W1, gridDim.x);
-    if (L.W == 0) return true;
+    const JobList L = sm.list[wide];
     const int worker = wide ? blockIdx.x : slot * gridDim.x + blockIdx.x;
     const bool loads = !wide || slot == 0;
     const Ring<D> ring(sm, wide, slot);
@@ -499,6 +498,7 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
     bool ok = true;
     for (int phase = 0; phase < 2 && ok; ++phase) {
         const bool is_wide = (phase ^ blockIdx.x & 1) == 0;
+        if (sm.list[is_wide].W == 0) continue;
         uint32_t& n = is_wide ? nw : nn;
         ok = att_produce<D>(c, p, sc, sm, kmap, vmap, is_wide, slot, sg, n);
         if (phase == 1 || !ok) break;
@@ -987,33 +987,30 @@ __device__ __forceinline__ Parts att_parts(const AttendParams& p, const JobList&
 // where there are few rows, several threads take the parts in turn, each with the running maximum
 // and sum of a softmax, and are merged in order.  Bound by reading the parts (from L2).
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const CacheView c, const AttendParams p, int grid, int rows) {
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const AttendParams p, int log_rows) {
     constexpr int kGroups = D / kMergeCols;
     __shared__ float s_acc[kMergeThreads][kMergeCols + 3];     // sums, maximum, weight (odd stride: no bank twice)
-    const int tid = threadIdx.x, units = p.a.streams * p.U, unit = blockIdx.x, h = blockIdx.z, row0 = blockIdx.y * rows;
-    const int row = tid % rows, group = tid / rows % kGroups, turn = tid / (rows * kGroups), turns = kMergeThreads / (rows * kGroups);
+    const int tid = threadIdx.x, units = p.a.streams * p.U, unit = blockIdx.x, h = blockIdx.z, row0 = blockIdx.y << log_rows;
+    const int rows = 1 << log_rows, row = tid & (rows - 1), group = (tid >> log_rows) & (kGroups - 1);
+    const int turn = (tid >> log_rows) / kGroups, turns = (kMergeThreads >> log_rows) / kGroups;
     grid_dependency_wait();
-    const int shared = p.head[kHeadShared], W1 = p.head[kHeadOwn];
     const int4 u = p.units[unit];                              // first place, rows, tiles, shares
+    const JobList Lo = p.head[p.wide_own], Ls = p.head[p.wide_sh];
     if (row0 >= u.y) return;
-    Parts own, sh = {nullptr, 0, 0, 0, 0};
-    {
-        const JobList L = att_list(c, p, p.wide_own != 0, shared, W1, grid);
-        own = att_parts<D>(p, L, p.wide_own, true, h * units + unit, L.W_sh + h * L.W1 + u.x + L.pad, u.z);
-    }
+    Parts sh = {nullptr, 0, 0, 0, 0};
+    const Parts own = att_parts<D>(p, Lo, p.wide_own, true, h * units + unit, Lo.W_sh + h * Lo.W1 + u.x + Lo.pad, u.z);
     if (!u.w && own.n == 1) return;                            // written by its only segment
-    const int s = unit / p.U, u0 = (unit - s * p.U) * p.rows_own();
+    const int s = p.U == 1 ? unit : unit / p.U, u0 = (unit - s * p.U) * p.rows_own();
     const int r = u0 + row0 + row, packed = s * p.a.block * p.G + r;
     if (u.w) {                                                 // the shared unit that this row lies in
-        const JobList L = att_list(c, p, p.wide_sh != 0, shared, W1, grid);
-        const int job = h * p.U_sh + packed / p.rows_sh();
-        sh = att_parts<D>(p, L, p.wide_sh, false, job, job * (L.tiles_sh + L.pad) + L.pad, L.tiles_sh);
+        const int job = h * p.U_sh + (packed >> (p.wide_sh ? 8 : 7));
+        sh = att_parts<D>(p, Ls, p.wide_sh, false, job, job * (Ls.tiles_sh + Ls.pad) + Ls.pad, Ls.tiles_sh);
     }
     const bool valid = row0 + row < u.y;
     float m = -INFINITY, z = 0.0f, acc[kMergeCols] = {};
     if (valid) {
         const int n = own.n + sh.n, r_sh = packed & (p.rows_sh() - 1);
-#pragma unroll 2
+#pragma unroll 4
         for (int i = turn; i < n; i += turns) {
             const bool mine = i < own.n;
             const int k = mine ? i : i - own.n, R = mine ? own.R : sh.R, at = mine ? row0 + row : r_sh;
@@ -1036,23 +1033,26 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Cache
             }
         }
     }
-    if (turns > 1) {
+    for (int half = turns / 2; half > 0; half /= 2) {          // the upper half of the turns joins the lower
+        if (turn >= half && turn < 2 * half) {
 #pragma unroll
-        for (int x = 0; x < kMergeCols; ++x) s_acc[tid][x] = acc[x];
-        s_acc[tid][kMergeCols] = m;
-        s_acc[tid][kMergeCols + 1] = z;
-        __syncthreads();
-        if (turn > 0) return;
-        for (int k = 1; k < turns; ++k) {
-            const float* o = s_acc[tid + k * rows * kGroups];
-            const float mk = o[kMergeCols];
-            if (o[kMergeCols + 1] == 0.0f) continue;
-            const float top = fmaxf(m, mk), f = exp2_approx(m - top), w = exp2_approx(mk - top);
-            m = top;
-            z = z * f + o[kMergeCols + 1] * w;
-#pragma unroll
-            for (int x = 0; x < kMergeCols; ++x) acc[x] = fmaf(w, o[x], acc[x] * f);
+            for (int x = 0; x < kMergeCols; ++x) s_acc[tid][x] = acc[x];
+            s_acc[tid][kMergeCols] = m;
+            s_acc[tid][kMergeCols + 1] = z;
         }
+        __syncthreads();
+        if (turn < half) {
+            const float* o = s_acc[tid + half * rows * kGroups];
+            const float mk = o[kMergeCols], zk = o[kMergeCols + 1];
+            if (zk != 0.0f) {
+                const float top = fmaxf(m, mk), f = exp2_approx(m - top), w = exp2_approx(mk - top);
+                m = top;
+                z = z * f + zk * w;
+#pragma unroll
+                for (int x = 0; x < kMergeCols; ++x) acc[x] = fmaf(w, o[x], acc[x] * f);
+            }
+        }
+        __syncthreads();
     }
     if (!valid || turn > 0) return;
     const float inv = z == 0.0f ? 0.0f : 1.0f / z;
@@ -1110,16 +1110,19 @@ template <int D, bool kBf16>
 int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, const moe::AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(moe::AttSmem<D>);
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
-    // rows of a merging CTA: as many as leave two CTAs for every SM, at most 32
+    // Rows of a merging CTA (a power of two): with few rows, as many as leave two CTAs for every SM;
+    // with many, 16 rather than 32 (two threads to take a row's parts) up to eight CTAs.
     const int64_t jobs = (int64_t)c->cfg.kv_heads * p.a.streams * p.U;
-    int rows = 32;
-    while (rows > 2 && jobs * ((p.R_own + rows - 1) / rows) < 2 * c->sm_count) rows /= 2;
-    const int groups = (p.R_own + rows - 1) / rows;
+    const auto ctas = [&](int log) { return jobs * ((p.R_own + (1 << log) - 1) >> log); };
+    int log_rows = 5;
+    while (log_rows > 1 && (1 << (log_rows - 1) >= p.R_own || ctas(log_rows) < 2 * c->sm_count)) --log_rows;
+    if (log_rows == 5 && ctas(log_rows) < 8 * c->sm_count) --log_rows;
     if (moe::launch_dependent(moe::attend_kernel<D, kBf16>, dim3(c->sm_count), dim3(moe::kAttThreads), smem, st, v, p,
                               c->maps[2 * layer], c->maps[2 * layer + 1]) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>, dim3(p.a.streams * p.U, groups, c->cfg.kv_heads),
-                                 dim3(moe::kMergeThreads), 0, st, v, p, c->sm_count, rows) == cudaSuccess
+    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>,
+                                 dim3(p.a.streams * p.U, (p.R_own + (1 << log_rows) - 1) >> log_rows, c->cfg.kv_heads),
+                                 dim3(moe::kMergeThreads), 0, st, p, log_rows) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -1184,7 +1187,7 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     if (p.c < 0x1p-100f) p.c = 0x1p-100f;
     p.q_flip = a.scale < 0.0f ? 0x80008000u : 0u;
     p.timeout_ns = (unsigned long long)c->cfg.timeout_us * 1000ull;
-    p.head = reinterpret_cast<int*>(ws);
+    p.head = reinterpret_cast<moe::JobList*>(ws);
     p.units = reinterpret_cast<int4*>(ws + L.units);
     p.split_wide = reinterpret_cast<float*>(ws + L.split_wide);
     p.split_narrow = reinterpret_cast<float*>(ws + L.split_narrow);
