@@ -1082,18 +1082,19 @@ int check_shape(const moe_mxfp4_cache* c, int32_t streams, int32_t block, int32_
 
 // Sections of the workspace, and the units.
 struct AttendLayout {
-    int G, wide_sh, wide_own, U, U_sh, R_own;
+    int G, wide_own, U, U_wide, R_own;
     size_t units, split_wide, split_narrow, whole_sh, whole_own, total;
 };
 AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int q_heads) {
     AttendLayout L;
     L.G = q_heads / c->cfg.kv_heads;
     const int64_t rows = (int64_t)block * L.G, all = streams * rows;
+    // A stream's own rows in wide units wherever one of 128 rows would not do (32 streams over
+    // 3500 keys: 136 rows 101 us against 158 in narrow units, 256 rows 111 against 167).
     L.wide_own = rows > 128;
-    L.wide_sh = all > 128;
-    const int ro = L.wide_own ? 256 : 128, rs = L.wide_sh ? 256 : 128;
+    const int ro = L.wide_own ? 256 : 128;
     L.U = (int)((rows + ro - 1) / ro);
-    L.U_sh = (int)((all + rs - 1) / rs);
+    L.U_wide = (int)((all + 255) / 256);
     L.R_own = (int)(rows < ro ? (rows + 3) / 4 * 4 : ro);   // slots are whole float4s
     const size_t row = (size_t)(c->cfg.head_dim + 1) * 4, jobs = (size_t)c->cfg.kv_heads;
     const size_t split = up256(4 * (size_t)c->sm_count * 128 * row);
@@ -1101,7 +1102,7 @@ AttendLayout attend_layout(const moe_mxfp4_cache* c, int streams, int block, int
     L.split_wide = L.units + up256((size_t)streams * L.U * 16);
     L.split_narrow = L.split_wide + split;
     L.whole_sh = L.split_narrow + split;
-    L.whole_own = L.whole_sh + up256(jobs * L.U_sh * rs * row);
+    L.whole_own = L.whole_sh + up256(jobs * L.U_wide * 256 * row);   // (units of 128 rows need no more)
     L.total = L.whole_own + up256(jobs * streams * L.U * L.R_own * row);
     return L;
 }
@@ -1110,13 +1111,12 @@ template <int D, bool kBf16>
 int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, const moe::AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(moe::AttSmem<D>);
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
-    // Rows of a merging CTA (a power of two): with few rows, as many as leave two CTAs for every SM;
-    // with many, 16 rather than 32 (two threads to take a row's parts) up to eight CTAs.
+    // Rows of a merging CTA (a power of two): as many as leave two CTAs for every SM, at most 32 (with 16
+    // the same rows take two waves of CTAs: 84.4 instead of 82.1 us for 32 streams behind 8192 keys).
     const int64_t jobs = (int64_t)c->cfg.kv_heads * p.a.streams * p.U;
     const auto ctas = [&](int log) { return jobs * ((p.R_own + (1 << log) - 1) >> log); };
     int log_rows = 5;
     while (log_rows > 1 && (1 << (log_rows - 1) >= p.R_own || ctas(log_rows) < 2 * c->sm_count)) --log_rows;
-    if (log_rows == 5 && ctas(log_rows) < 8 * c->sm_count) --log_rows;
     if (moe::launch_dependent(moe::attend_kernel<D, kBf16>, dim3(c->sm_count), dim3(moe::kAttThreads), smem, st, v, p,
                               c->maps[2 * layer], c->maps[2 * layer + 1]) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -1168,17 +1168,22 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     if (!workspace_dev || !aligned(workspace_dev, 256) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
     // places of the schedule, with every stream as long as its table
     const double tiles = ((double)c->cfg.max_pages * c->cfg.page_tokens + a.block) / moe::kKeyTile + 2 + moe::kPadNarrow;
-    if (c->cfg.kv_heads * ((double)L.U_sh + (double)a.streams * L.U) * tiles >= 2147483647.0) return MOE_ERR_UNSUPPORTED;
+    if (c->cfg.kv_heads * (2.0 * L.U_wide + (double)a.streams * L.U) * tiles >= 2147483647.0) return MOE_ERR_UNSUPPORTED;
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
     char* ws = static_cast<char*>(workspace_dev);
     p.v_pool = static_cast<const uint16_t*>(c->layers[layer].v_dev);
     p.G = L.G;
     p.g_mul = 0xFFFFFFFFu / (uint32_t)L.G + 1;
-    p.wide_sh = L.wide_sh;
+    // The shared prefix in wide units where that makes 20 tiles or more for every CTA: a wide tile
+    // costs less than two narrow ones (64 streams behind 32768 keys, 216 tiles: 395 us against 499;
+    // 32 behind 8192, 24 tiles: 82.3 against 84.8), but few of them leave slots without work (16
+    // behind 8192, 13 tiles: 54.1 against 48.6; 4, 3 tiles: 32.0 against 24.8).
+    const int64_t rows = (int64_t)a.streams * a.block * L.G;
+    p.wide_sh = rows > 128 && (int64_t)c->cfg.kv_heads * L.U_wide * (a.shared_tokens / moe::kKeyTile) >= 20 * (int64_t)c->sm_count;
     p.wide_own = L.wide_own;
     p.U = L.U;
-    p.U_sh = L.U_sh;
+    p.U_sh = p.wide_sh ? L.U_wide : (int)((rows + 127) / 128);
     p.R_own = L.R_own;
     // a negative scale turns the queries' signs; a scale of zero is one below any score's last bit,
     // which keeps hidden keys (-inf) hidden

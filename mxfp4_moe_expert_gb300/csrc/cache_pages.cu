@@ -15,7 +15,7 @@
 
 namespace moe {
 
-constexpr int kPlanThreads = 1024;   // at most; plan_threads() below
+constexpr int kPlanThreads = 1024;   // of a planning CTA, at most
 constexpr int kNoStream = 0x7FFFFFFF;
 
 __device__ __forceinline__ void cache_error(const CacheView& c, int code, int detail) {
@@ -234,48 +234,40 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, c
 
 // ---- append --------------------------------------------------------------------------
 
-// A warp has 32 16-byte words, at the same place, of kTok consecutive tokens of a stream, keys
-// and values: 2 kTok loads are in flight per lane while the pages are looked up (a lane per
-// token).  Bound by HBM for long blocks, by the launch and that look-up for short ones.
-template <int kTok>
+// A warp has 32 16-byte words of a token's keys and of its values, which are under way while the
+// page is looked up.  Bound by HBM for long blocks (24 x 1999 tokens of 4 heads of 64, 98 MB read
+// and written: 16.7 us, 5.9 TB/s), by the launch and that look-up for short ones (8 tokens of 8
+// heads of 128: 1.4 us in a graph).  Warps with four tokens at a time measured 17.0 and 1.9 us.
 __global__ void __launch_bounds__(256) cache_append_kernel(CacheView c, const char* __restrict__ k, const char* __restrict__ v,
                                                            int64_t row_bytes, char* __restrict__ kp, char* __restrict__ vp,
-                                                           int streams, int block, int groups, const int* __restrict__ lengths) {
+                                                           int streams, int block, const int* __restrict__ lengths) {
     const int lane = threadIdx.x & 31, log_head = c.D == 128 ? 4 : 3;        // words of a head: 16 or 8
     const int words = c.Hkv << log_head, parts = (words + 31) / 32;
-    const int n = streams * groups * parts;
+    const int n = streams * block * parts;
     grid_dependency_wait();
     for (int u = blockIdx.x * 8 + (threadIdx.x >> 5); u < n; u += gridDim.x * 8) {
-        const int g = u / parts, w = (u - g * parts) * 32 + lane;
-        const int s = g / groups, i0 = (g - s * groups) * kTok;
-        const int used = lengths ? min(lengths[s], block) : block;
-        const int64_t tok = (int64_t)s * block + i0;
-        uint4 a[2][kTok];
-#pragma unroll
-        for (int t = 0; t < kTok; ++t)
-            if (w < words && i0 + t < used) {
-                a[0][t] = __ldcs(reinterpret_cast<const uint4*>(k + (tok + t) * row_bytes) + w);
-                a[1][t] = __ldcs(reinterpret_cast<const uint4*>(v + (tok + t) * row_bytes) + w);
-            }
+        const int tok = u / parts, w = (u - tok * parts) * 32 + lane;
+        const int s = tok / block, i = tok - s * block;
+        if (lengths && i >= lengths[s]) continue;
+        const bool mine = w < words;
+        uint4 a, b;
+        if (mine) {
+            a = __ldcs(reinterpret_cast<const uint4*>(k + tok * row_bytes) + w);
+            b = __ldcs(reinterpret_cast<const uint4*>(v + tok * row_bytes) + w);
+        }
         const int len = c.length()[s], held = min(c.held()[s], c.L.M);
+        const int64_t pos = (int64_t)len + i;
         int page = -1;
-        if (lane < kTok && i0 + lane < used) {
-            const int at = (int)(((unsigned)len + i0 + lane) >> c.page_shift);   // (a sum beyond 2^31 is beyond any table)
-            if (len >= 0 && at < held) page = c.table(s)[at];
-            if ((unsigned)page >= (unsigned)c.L.P || c.refcount()[page] > 1) {
-                page = -1;
-                if (w == lane) cache_error(c, MOE_ERR_CACHE_STATE, s);
-            }
+        if (len >= 0 && (pos >> c.page_shift) < held) page = c.table(s)[pos >> c.page_shift];
+        if ((unsigned)page >= (unsigned)c.L.P || c.refcount()[page] > 1) {
+            if (w == 0) cache_error(c, MOE_ERR_CACHE_STATE, s);
+            continue;
         }
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const int to = __shfl_sync(0xFFFFFFFFu, page, t);
-            if (w >= words || i0 + t >= used || to < 0) continue;
-            const int64_t e = to * c.page_stride + ((int64_t)(w >> log_head) * c.page + ((len + i0 + t) & (c.page - 1))) * c.D +
-                              (w & ((1 << log_head) - 1)) * 8;
-            *reinterpret_cast<uint4*>(kp + e * 2) = a[0][t];
-            *reinterpret_cast<uint4*>(vp + e * 2) = a[1][t];
-        }
+        if (!mine) continue;
+        const int64_t e = page * c.page_stride + ((int64_t)(w >> log_head) * c.page + (pos & (c.page - 1))) * c.D +
+                          (w & ((1 << log_head) - 1)) * 8;
+        *reinterpret_cast<uint4*>(kp + e * 2) = a;
+        *reinterpret_cast<uint4*>(vp + e * 2) = b;
     }
 }
 
@@ -445,9 +437,12 @@ bool encode_pool(CUtensorMap* m, const void* base, const moe_mxfp4_cache_config&
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// Threads of a planning CTA: a barrier of fewer warps is cheaper, and few streams and pages
-// need no more (a pass over the pages takes four per thread).
-int plan_threads(const moe_mxfp4_cache* c) { return c->cfg.num_streams <= 256 && c->cfg.num_pages <= 2048 ? 256 : moe::kPlanThreads; }
+// Threads of a planning CTA.  A barrier of 8 warps is cheaper than one of 32, and few streams and
+// pages need no more: reserving for 32 streams of 521 pages takes 5.8 us with 256 threads and 6.4
+// with 1024, for 256 streams 10.1 and 8.5; compacting 10 pages 3.1 and 3.5, 521 pages 4.0 and 3.4
+// (with the copying kernel that follows, in a graph).
+int reserve_threads(const moe_mxfp4_cache* c) { return c->cfg.num_streams <= 64 && c->cfg.num_pages <= 1024 ? 256 : moe::kPlanThreads; }
+int compact_threads(const moe_mxfp4_cache* c) { return c->cfg.num_pages <= 256 ? 256 : moe::kPlanThreads; }
 
 // Copies the pages of the move list (at most `moves` of them) in every pool, kMaxPools pools a
 // launch; the last launch also rewrites the tables, with `remap`.
@@ -536,7 +531,7 @@ int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* 
     if (!on.ok()) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const moe::CacheView v = moe::cache_view(c, state_dev);
-    if (moe::launch_dependent(moe::cache_reserve_kernel, dim3(1), dim3(plan_threads(c)), 0, st, v, add_dev, add) != cudaSuccess)
+    if (moe::launch_dependent(moe::cache_reserve_kernel, dim3(1), dim3(reserve_threads(c)), 0, st, v, add_dev, add) != cudaSuccess)
         return MOE_ERR_CUDA;
     return launch_copies(c, v, c->cfg.num_streams, 0, st);
 }
@@ -552,17 +547,13 @@ int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, c
     if (!k_dev || !v_dev || !aligned16(k_dev) || !aligned16(v_dev)) return MOE_ERR_INVALID_ARG;
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
-    // four tokens a warp where that still leaves 16 warps for every SM, else one
-    const int parts = (int)((row / 8 + 31) / 32);
-    const auto warps = [&](int tok) { return (int64_t)streams * ((block + tok - 1) / tok) * parts; };
-    const int tok = warps(4) >= 16 * (int64_t)c->sm_count ? 4 : 1;
-    if (warps(tok) > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-    const int64_t want = (warps(tok) + 7) / 8, most = 64 * (int64_t)c->sm_count;
+    const int64_t warps = (int64_t)streams * block * ((row / 8 + 31) / 32);
+    if (warps > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    const int64_t want = (warps + 7) / 8, most = 64 * (int64_t)c->sm_count;
     return status_of(moe::launch_dependent(
-        tok == 4 ? moe::cache_append_kernel<4> : moe::cache_append_kernel<1>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
-        static_cast<cudaStream_t>(stream), moe::cache_view(c, state_dev), static_cast<const char*>(k_dev), static_cast<const char*>(v_dev),
-        row_stride * 2, static_cast<char*>(c->layers[layer].k_dev), static_cast<char*>(c->layers[layer].v_dev), streams, block,
-        (block + tok - 1) / tok, lengths_dev));
+        moe::cache_append_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, static_cast<cudaStream_t>(stream),
+        moe::cache_view(c, state_dev), static_cast<const char*>(k_dev), static_cast<const char*>(v_dev), row_stride * 2,
+        static_cast<char*>(c->layers[layer].k_dev), static_cast<char*>(c->layers[layer].v_dev), streams, block, lengths_dev));
 }
 
 static int cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* value, int relative, void* stream) {
@@ -599,7 +590,7 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream) {
     if (!on.ok()) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const moe::CacheView v = moe::cache_view(c, state_dev);
-    if (moe::launch_dependent(moe::cache_compact_kernel, dim3(1), dim3(plan_threads(c)), 0, st, v) != cudaSuccess) return MOE_ERR_CUDA;
+    if (moe::launch_dependent(moe::cache_compact_kernel, dim3(1), dim3(compact_threads(c)), 0, st, v) != cudaSuccess) return MOE_ERR_CUDA;
     return launch_copies(c, v, c->cfg.num_pages / 2, 1, st);
 }
 

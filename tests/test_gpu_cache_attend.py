@@ -114,7 +114,8 @@ def test_long_and_many(S, prefix, lo, hi):
     c.check(out, lse, streams=sorted({0, S - 1, S // 2, S // 3}))
 
 
-@pytest.mark.parametrize("S,Hq,D,prefix,hi", [(32, 56, 128, 8192, 1500), (24, 64, 64, 6000, 3000), (64, 64, 128, 12288, 100)])
+@pytest.mark.parametrize("S,Hq,D,prefix,hi", [(32, 56, 128, 8192, 1500), (24, 64, 64, 12288, 3000),
+                                                (64, 64, 128, 12288, 100), (24, 64, 64, 6000, 900)])
 def test_many_tiles_for_every_cta(S, Hq, D, prefix, hi):
     """Enough tiles of the shared prefix and of the streams' own keys that every ring goes round many times, and
     passes from one kind of work to the other; every row of some streams, and all rows twice."""
@@ -221,6 +222,34 @@ def test_keys_that_a_row_does_not_see_have_no_part(bad):
     out, lse = c.attend()
     assert torch.equal(out[:, :3], want[:, :3]) and torch.equal(lse[:, :3], wlse[:, :3])
     assert out[:, 3:].isnan().all() and lse[:, 3:].isnan().all()
+
+
+@pytest.mark.parametrize("D,prefix", [(128, 0), (64, 128)])
+def test_bad_values_in_blocks_of_many_rows(D, prefix):
+    """Blocks whose rows fill both halves of a CTA, and several CTAs."""
+    B, used = 90, [90, 33, 0, 77]
+    c = Case([prefix, prefix + 100, prefix + 3, prefix + 259], B, 8, 2, D=D, page=32, prefix=prefix, seed=D)
+    lengths = i32(used)
+    want, wlse = c.attend(lengths=lengths)
+    c.check(want, wlse, used=used)
+    for s in range(c.S):
+        for pos, col in ((20, 3), (76, 7), (89, 11)):
+            i, off = divmod(c.books.length[s] + pos, c.page)
+            c.v[c.books.table[s][i], :, off, col] = float("nan")
+            c.k[c.books.table[s][i], :, off, col] = float("inf") if pos == 89 else 0.5
+    base = c.v.clone()
+    clean = torch.where(base.isnan(), torch.zeros_like(base), base)
+    c.v.copy_(clean)
+    want, wlse = c.attend(lengths=lengths)
+    c.v.copy_(base)
+    out, lse = c.attend(lengths=lengths)
+    for s, n in enumerate(used):
+        assert torch.equal(lse[s, :min(n, 89)], wlse[s, :min(n, 89)])
+        for b in range(min(n, 89)):
+            bad = [col for pos, col in ((20, 3), (76, 7)) if pos <= b]
+            keep = [d for d in range(D) if d not in bad]
+            assert torch.equal(out[s, b][:, keep], want[s, b][:, keep]), (s, b)
+            assert out[s, b][:, bad].isnan().all(), (s, b)
 
 
 def test_masks_of_one_row_leave_the_others_alone():
