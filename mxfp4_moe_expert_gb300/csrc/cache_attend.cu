@@ -7,11 +7,11 @@
 // Work.  The G = q_heads / kv_heads rows that read one kv head are packed (b, g) and, over the
 // shared prefix, (s, b, g).  A job is a unit of these rows with its run of keys (the shared prefix
 // once for the rows of all streams; every stream's own keys), cut into tiles of 128 keys.  There
-// are two kinds of units.  Wide ones (where there are more than 128 rows) have 256 rows: both row
-// slots of a CTA take each tile of keys, so that it is read from memory once for 256 rows and the
-// tensor core always has a slot that is ready.  Narrow ones have up to 128 rows: the two slots of
-// a CTA work on different jobs, or parts of a job, each with a ring of its own, so that the wait
-// for memory in one is covered by the other.  The tiles of the wide jobs are dealt out evenly to
+// are two kinds of units (the rules between them are beside attend_layout and in the entry point).
+// Wide ones have 256 rows: both row slots of a CTA take each tile of keys, so that it is read from
+// memory once for 256 rows.  Narrow ones have up to 128 rows: the two slots of a CTA work on
+// different jobs, or parts of a job, each with a ring of its own, so that the wait for memory in
+// one is covered by the other.  The tiles of the wide jobs are dealt out evenly to
 // the CTAs (one per SM), those of the narrow ones to their 2 x CTAs slots, in order: a long run of
 // keys is split over many, short ones are packed.  What one worker does of a job is a segment.
 // A segment that is all its rows need is written straight to the output; the others leave
@@ -24,6 +24,15 @@
 // warpgroup: a thread per row.  The reference of the exponentials follows the running maximum only
 // when that passes it by 2^8 (P stays below 2^8 in any type, sums are fp32), so the accumulator is
 // rescaled rarely, by the softmax warps themselves.
+//
+// What bounds it, on 152 SMs.  Reading keys where there are few rows: 96 streams that decode one
+// position over 700..6000 keys (1.32 GB) take 203 us, 6.5 TB/s, 0.96 of the copy rate.  The tensor
+// core's chain where a long prefix is shared: 64 streams x 8 positions x 64 heads behind 32768 keys
+// (0.57 PFLOP) take 431 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
+// keys) takes about 2950 cycles for 2048 of products: scores -> softmax (1500) -> P V and the next
+// scores (1024) follow one another in each slot, and shared memory is read at its full 128 bytes a
+// cycle while Q K^T runs.  The launches, the schedule and the merge where there is little work: one
+// stream of 8 positions over 4093 keys takes 18 us, of which its tiles are 3.
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
@@ -37,7 +46,8 @@ constexpr int kAttProducer = 8, kAttMma = 10;  // + slot
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // columns: S of slot x at 128 x, O at 256 + 128 x
 constexpr float kRescale = 8.0f;               // exponents that the maximum may pass the reference by
 // A segment costs about this many tiles more than its tiles (its queries, its start, its rows' way
-// out); dealt out with them, narrow jobs being short.
+// out); dealt out with them.  3 for narrow ones rather than 2: 96 streams decode in 205.7 us
+// instead of 209.0, other cases do not change.
 constexpr int kPadWide = 1, kPadNarrow = 3;
 
 struct AttendParams {
@@ -493,7 +503,7 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
         return true;
     };
     // Wide jobs keep the tensor core busy, narrow ones the memory: half of the CTAs begin with one
-    // kind and half with the other.  The rings share their stages, so one kind's tiles are all used
+    // kind and half with the other (64 streams behind 32768 keys: 445 -> 410 us).  The rings share their stages, so one kind's tiles are all used
     // up before the other's are copied.
     bool ok = true;
     for (int phase = 0; phase < 2 && ok; ++phase) {
@@ -600,7 +610,8 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
             return true;
         };
         // Wide units: the slots take turns, each with the products of a step in one go, so that one
-        // slot's scores are ready while the other's products run (interleaved, both would wait for all).
+        // slot's scores are ready while the other's products run (interleaved, both would wait for all:
+        // 473 us instead of 450 for 64 streams behind 32768 keys).
         const auto begin_turn = [&]() { return !wide || wait(&sm.turn[slot], (turns & 1) ^ (slot == 0)); };
         const auto end_turn = [&]() {
             if (!wide) return;
@@ -985,7 +996,9 @@ __device__ __forceinline__ Parts att_parts(const AttendParams& p, const JobList&
 // its stream shares the prefix, of the shared job.  A CTA per (unit of a stream, `rows` rows,
 // head); a thread has 16 columns of a row (rows on neighbouring lanes, as the parts store them);
 // where there are few rows, several threads take the parts in turn, each with the running maximum
-// and sum of a softmax, and are merged in order.  Bound by reading the parts (from L2).
+// and sum of a softmax, and are joined pairwise in a fixed order.  Bound by latency (the schedule,
+// then the parts, from L2): 7 us after the attention for one stream, about 10 for 14336 rows with
+// 5.7 parts each (42 MB).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const AttendParams p, int log_rows) {
     constexpr int kGroups = D / kMergeCols;
