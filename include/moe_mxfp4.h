@@ -364,8 +364,9 @@ int moe_mxfp4_accept(const float* logits_dev, const int32_t* tokens_dev, int32_t
  * outside the pool) is recorded in the status words (the first error is kept until
  * moe_mxfp4_cache_check) and nothing outside the pools and the state is touched.  Results
  * do not depend on the timing of threads: two runs of the same calls give the same bits.
- * A cache (state and workspace) may be used by one stream at a time, captured graphs
- * included.  Calls run on the handle's device, whichever device is current.  No call
+ * A cache may be used by one stream at a time, captured graphs included; calls of
+ * moe_mxfp4_cache_attend, which only read it, may overlap one another when they have
+ * workspaces of their own.  Calls run on the handle's device, whichever device is current.  No call
  * allocates device memory or synchronises, but moe_mxfp4_cache_check. */
 
 #define MOE_DTYPE_BF16 0
@@ -412,7 +413,8 @@ int moe_mxfp4_cache_state_bytes(const moe_mxfp4_cache* c, size_t* bytes);
  * whose table is out of the pool) is recorded, and no stream gets a page. */
 int moe_mxfp4_cache_reserve(moe_mxfp4_cache* c, void* state_dev, const int32_t* add_dev, int32_t add, void* stream);
 
-/* Writes a block's keys and values of one layer: token i < n_s of stream s < streams goes
+/* Writes a block's keys and values of one layer (MOE_ERR_UNSUPPORTED beyond 2^30 times 512
+ * bytes of either): token i < n_s of stream s < streams goes
  * to position length[s] + i, n_s = lengths_dev ? min(lengths_dev[s], block) : block.
  * k_dev, v_dev: [streams, block, kv_heads, head_dim], 16-byte aligned, `row_stride`
  * elements between tokens (a multiple of 8; 0 = kv_heads * head_dim).  length is not
@@ -457,6 +459,7 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
  * Arithmetic: products of q and k are exact and summed in fp32, as are the statistics of
  * the softmax; its terms are rounded to the cache's type for their product with v, which
  * is summed in fp32.
+ * out and lse overlap no input.
  * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents.
  * MOE_ERR_UNSUPPORTED when the rows and the keys that max_pages allows make 2^31 tiles or
  * more (256 rows x 128 keys). */

@@ -625,7 +625,8 @@ class KvCache:
         """Attention of a block (moe_mxfp4_cache_attend).  q: [streams, block, q_heads, head_dim], as k in append; mask:
         int64 [streams, block], bit i = sees block position i (default: causal); scale: default 1 / sqrt(head_dim).
         Returns (out, lse): out like q, contiguous; lse fp32 [streams, block, q_heads].  Rows that `lengths` leaves
-        out are zero in an out (lse) that is made here and unchanged in one that is given."""
+        out are zero in an out (lse) that is made here and unchanged in one that is given.  Calls that may overlap on
+        the GPU (on two streams) are given a `workspace` each (uint8, attend_bytes long, 256-byte aligned)."""
         S, B, H, D, row = self._rows("q", q)
         if D != self.head_dim:
             raise ValueError("q is [streams, block, q_heads, head_dim]")

@@ -88,8 +88,8 @@ inline CacheView cache_view(const moe_mxfp4_cache* c, void* state) {
     return v;
 }
 
-// Allows the attention's kernels their shared memory on the current device.
-bool attend_prepare();
+// Allows the attention's kernels their shared memory on the current device, once for each.
+bool attend_prepare(int device);
 
 // The handle's device for the duration of a call.
 class DeviceScope {

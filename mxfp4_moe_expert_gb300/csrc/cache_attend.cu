@@ -35,6 +35,8 @@
 // stream of 8 positions over 4093 keys takes 18 us, of which its tiles are 3.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "cache.cuh"
 #include "mma_f16.cuh"
 
@@ -503,8 +505,8 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
         return true;
     };
     // Wide jobs keep the tensor core busy, narrow ones the memory: half of the CTAs begin with one
-    // kind and half with the other (64 streams behind 32768 keys: 445 -> 410 us).  The rings share their stages, so one kind's tiles are all used
-    // up before the other's are copied.
+    // kind and half with the other (64 streams behind 32768 keys: 445 -> 410 us).  The rings share
+    // their stages, so one kind's tiles are all used up before the other's are copied.
     bool ok = true;
     for (int phase = 0; phase < 2 && ok; ++phase) {
         const bool is_wide = (phase ^ blockIdx.x & 1) == 0;
@@ -1142,12 +1144,18 @@ int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, 
 
 }  // namespace
 
-bool moe::attend_prepare() {
+bool moe::attend_prepare(int device) {
+    static std::atomic<uint64_t> done{0};          // a bit per device (more than 64: set every time)
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done.load() & bit) return true;
     const auto set = [](auto* kern, size_t smem) {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
     };
-    return set(attend_kernel<128, true>, sizeof(AttSmem<128>)) && set(attend_kernel<128, false>, sizeof(AttSmem<128>)) &&
-           set(attend_kernel<64, true>, sizeof(AttSmem<64>)) && set(attend_kernel<64, false>, sizeof(AttSmem<64>));
+    if (!set(attend_kernel<128, true>, sizeof(AttSmem<128>)) || !set(attend_kernel<128, false>, sizeof(AttSmem<128>)) ||
+        !set(attend_kernel<64, true>, sizeof(AttSmem<64>)) || !set(attend_kernel<64, false>, sizeof(AttSmem<64>)))
+        return false;
+    done.fetch_or(bit);
+    return true;
 }
 
 extern "C" int moe_mxfp4_cache_attend_bytes(const moe_mxfp4_cache* c, int32_t streams, int32_t block, int32_t q_heads,

@@ -498,7 +498,7 @@ int moe_mxfp4_cache_create(const moe_mxfp4_cache_config* cfg, const moe_mxfp4_ca
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     for (int l = 0; l < c.num_layers; ++l)
         if (!device_memory(layers[l].k_dev, dev) || !device_memory(layers[l].v_dev, dev)) return MOE_ERR_INVALID_ARG;
-    if (!moe::attend_prepare()) return MOE_ERR_CUDA;
+    if (!moe::attend_prepare(dev)) return MOE_ERR_CUDA;
     try {
         moe_mxfp4_cache* h = new moe_mxfp4_cache();
         h->cfg = c;
@@ -549,7 +549,7 @@ int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, c
     const moe::DeviceScope on(c->device);
     if (!on.ok()) return MOE_ERR_CUDA;
     const int64_t warps = (int64_t)streams * block * ((row / 8 + 31) / 32);
-    if (warps > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    if (warps > 1 << 30) return MOE_ERR_UNSUPPORTED;
     const int64_t want = (warps + 7) / 8, most = 64 * (int64_t)c->sm_count;
     return status_of(moe::launch_dependent(
         moe::cache_append_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, static_cast<cudaStream_t>(stream),

@@ -357,6 +357,28 @@ def test_graph_replay_follows_the_books_and_repeats_bit_for_bit():
     c.check(gout, glse)
 
 
+def test_calls_that_overlap_on_two_streams():
+    c = Case([700, 3000, 1200, 90], 8, 16, 2, prefix=64, seed=16)
+    c2 = Case([500, 64, 2000], 5, 8, 4, prefix=64, seed=17)
+    want = [x.clone() for case in (c, c2) for x in case.attend()]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    q2 = c.q.flip(0).contiguous()
+    flipped = [x.clone() for x in c.cache.attend(0, q2, shared_stream=c.S, shared_tokens=64)]
+    ws = [torch.empty(c.cache.attend_bytes(c.S, c.B, c.Hq), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for k, q in ((0, c.q), (1, q2)):
+            with torch.cuda.stream(streams[k]):
+                got.append((k, c.cache.attend(0, q, shared_stream=c.S, shared_tokens=64, workspace=ws[k])))
+        with torch.cuda.stream(streams[1]):
+            got.append((2, c2.cache.attend(0, c2.q, shared_stream=c2.S, shared_tokens=64)))
+    torch.cuda.synchronize()
+    for k, (out, lse) in got:
+        ref = (want[0], want[1]) if k == 0 else tuple(flipped) if k == 1 else (want[2], want[3])
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1]), k
+
+
 def test_a_verify_forward_from_reserve_to_commit():
     """The calls as a user makes them: streams fork from a prompt, and blocks are reserved, appended, attended, judged
     by accept() and committed; the attention then equals that over contiguous keys."""
