@@ -555,8 +555,9 @@ class KvCache:
         self.page_table, at = self.state[at:at + S * max_pages].view(S, max_pages), at + S * max_pages
         self.refcount = self.state[at:at + pages]
         self._lib = load_library()
+        self._index, self._append = k0.get_device(), self._lib.moe_mxfp4_cache_append
         self._ws, self._ws_bytes, self._ws_kept = None, {}, []
-        self._layouts = {}        # shapes and strides seen so far -> how a call lays them out
+        self._layouts, self._pairs = {}, {}     # shapes and strides seen so far -> how a call lays them out
         self._i32, self._f32, self._mask_types = torch.int32, torch.float32, (torch.int64, torch.uint64)
         # the raw handle of the current stream (torch.cuda.current_stream() builds a Stream object around it)
         self._current_stream = torch._C._cuda_getCurrentRawStream
@@ -565,7 +566,8 @@ class KvCache:
 
     def reserve(self, tokens, stream=None):
         """Room for `tokens` more tokens: an int (in every stream) or an int32 tensor [num_streams]."""
-        if isinstance(tokens, int):
+        if type(tokens) is int or not hasattr(tokens, "data_ptr"):
+            tokens = int(tokens)
             if not -(1 << 31) <= tokens < 1 << 31:
                 raise ValueError("tokens: a 32-bit count")
             add, n = None, tokens
@@ -609,14 +611,14 @@ class KvCache:
     def append(self, layer, k, v, lengths=None, stream=None):
         """k, v: [streams, block, kv_heads, head_dim], contiguous or rows of one wider tensor (a fused projection's
         output); lengths: int32 [streams], tokens in use of each block."""
-        S, B, H, D, row = self._rows("k", k)
-        if H != self.kv_heads or D != self.head_dim or self._rows("v", v)[:4] != (S, B, H, D):
-            raise ValueError("k and v are [streams, block, kv_heads, head_dim]")
-        if S * B > 1 and self._rows("v", v)[4] != row:
-            raise ValueError("k and v have one stride between tokens")
-        st = self._lib.moe_mxfp4_cache_append(self.handle, self._state_ptr, layer, k.data_ptr(), v.data_ptr(), row, S, B,
-                                              None if lengths is None else self._books("lengths", lengths, S),
-                                              self._stream(stream))
+        layout = self._pairs.get((k.shape, k.stride(), v.shape, v.stride()))
+        if (layout is None or k.dtype is not self.dtype or v.dtype is not self.dtype or k.get_device() != self._index
+                or v.get_device() != self._index):
+            layout = self._pair(k, v)
+        S, B, row = layout
+        st = self._append(self.handle, self._state_ptr, layer, k.data_ptr(), v.data_ptr(), row, S, B,
+                          None if lengths is None else self._books("lengths", lengths, S),
+                          self._current_stream(self._index) if stream is None else stream)
         if st:
             _check(st, "moe_mxfp4_cache_append")
 
@@ -637,12 +639,14 @@ class KvCache:
                 out = make((S, B, H, D), dtype=self.dtype, device=self.device)
             if lse is None:
                 lse = make((S, B, H), dtype=torch.float32, device=self.device)
-        if out.shape != (S, B, H, D) or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+        if (out.shape != (S, B, H, D) or out.dtype is not self.dtype or out.get_device() != self._index
+                or not out.is_contiguous()):
             raise ValueError("out: contiguous, of q's shape and type")
-        if lse.shape != (S, B, H) or lse.dtype != self._f32 or lse.device != self.device or not lse.is_contiguous():
+        if (lse.shape != (S, B, H) or lse.dtype is not self._f32 or lse.get_device() != self._index
+                or not lse.is_contiguous()):
             raise ValueError("lse: contiguous fp32 [streams, block, q_heads]")
         if mask is not None and (mask.shape != (S, B) or mask.dtype not in self._mask_types
-                                 or mask.device != self.device or not mask.is_contiguous()):
+                                 or mask.get_device() != self._index or not mask.is_contiguous()):
             raise ValueError("mask: contiguous int64 [streams, block]")
         ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else \
             self._workspace(S, B, H)
@@ -663,16 +667,28 @@ class KvCache:
     # -- arguments
 
     def _stream(self, stream):
-        return self._current_stream(self.device.index) if stream is None else stream
+        return self._current_stream(self._index) if stream is None else stream
 
     def _books(self, name, t, n):
-        if t.dtype != self._i32 or t.device != self.device or t.numel() != n or not t.is_contiguous():
+        if t.dtype is not self._i32 or t.get_device() != self._index or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name}: {n} contiguous int32 values on {self.device}")
         return t.data_ptr()
 
+    def _pair(self, k, v):
+        """(streams, block, elements between tokens) of new keys and values; remembered by shape and stride."""
+        S, B, H, D, row = self._rows("k", k)
+        if (H, D) != (self.kv_heads, self.head_dim) or self._rows("v", v)[:4] != (S, B, H, D):
+            raise ValueError("k and v are [streams, block, kv_heads, head_dim]")
+        if S * B > 1 and self._rows("v", v)[4] != row:
+            raise ValueError("k and v have one stride between tokens")
+        if len(self._pairs) >= 1024:
+            self._pairs.clear()
+        layout = self._pairs[(k.shape, k.stride(), v.shape, v.stride())] = (S, B, row)
+        return layout
+
     def _rows(self, name, t):
         """(streams, block, heads, head_dim, elements between tokens) of a tensor of rows."""
-        if t.dtype != self.dtype or t.device != self.device:
+        if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name}: a 4-dimensional {self.dtype} tensor on {self.device}")
         key = (t.shape, t.stride())
         rows = self._layouts.get(key)

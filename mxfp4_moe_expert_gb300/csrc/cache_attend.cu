@@ -1001,7 +1001,9 @@ __device__ __forceinline__ Parts att_parts(const AttendParams& p, const JobList&
 // and sum of a softmax, and are joined pairwise in a fixed order.  Bound by latency (the schedule,
 // then the parts, from L2): 7 us after the attention for one stream, about 10 for 14336 rows with
 // 5.7 parts each (42 MB).
-template <int D, bool kBf16>
+// kDeep parts are under way together: 4 where one wave of CTAs holds all rows (one stream: 16.5 us
+// against 17.3 with 2), 2 where the registers would cost CTAs (96 streams: 201.4 against 202.9).
+template <int D, bool kBf16, int kDeep>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const AttendParams p, int log_rows) {
     constexpr int kGroups = D / kMergeCols;
     __shared__ float s_acc[kMergeThreads][kMergeCols + 3];     // sums, maximum, weight (odd stride: no bank twice)
@@ -1025,26 +1027,33 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Atten
     float m = -INFINITY, z = 0.0f, acc[kMergeCols] = {};
     if (valid) {
         const int n = own.n + sh.n, r_sh = packed & (p.rows_sh() - 1);
-#pragma unroll 4
-        for (int i = turn; i < n; i += turns) {
-            const bool mine = i < own.n;
-            const int k = mine ? i : i - own.n, R = mine ? own.R : sh.R, at = mine ? row0 + row : r_sh;
-            const float* part = (mine ? own.base : sh.base) + (k ? (mine ? own.gap : sh.gap) + (k - 1) * (mine ? own.step : sh.step) : 0);
-            const float lse = __ldcg(part + R * D + at);
-            float4 v[kMergeCols / 4];
+        for (int i0 = turn; i0 < n; i0 += kDeep * turns) {
+            float lse[kDeep];
+            float4 v[kDeep][kMergeCols / 4];
 #pragma unroll
-            for (int x = 0; x < kMergeCols / 4; ++x)
-                v[x] = __ldcg(reinterpret_cast<const float4*>(part) + (group * (kMergeCols / 4) + x) * R + at);
-            if (lse == -INFINITY) continue;                    // a part that saw nothing
-            const float top = fmaxf(m, lse), f = exp2_approx(m - top), w = exp2_approx(lse - top);
-            m = top;
-            z = z * f + w;
+            for (int d = 0; d < kDeep; ++d) {
+                const int i = i0 + d * turns;
+                const bool there = i < n, mine = i < own.n;
+                const int k = mine ? i : i - own.n, R = mine ? own.R : sh.R, at = mine ? row0 + row : r_sh;
+                const float* part = (mine ? own.base : sh.base) + (k ? (mine ? own.gap : sh.gap) + (k - 1) * (mine ? own.step : sh.step) : 0);
+                lse[d] = load_cg_or(part + R * D + at, there, -INFINITY);
 #pragma unroll
-            for (int x = 0; x < kMergeCols / 4; ++x) {
-                acc[4 * x] = fmaf(w, v[x].x, acc[4 * x] * f);
-                acc[4 * x + 1] = fmaf(w, v[x].y, acc[4 * x + 1] * f);
-                acc[4 * x + 2] = fmaf(w, v[x].z, acc[4 * x + 2] * f);
-                acc[4 * x + 3] = fmaf(w, v[x].w, acc[4 * x + 3] * f);
+                for (int x = 0; x < kMergeCols / 4; ++x)
+                    v[d][x] = load_cg_or_zero(reinterpret_cast<const float4*>(part) + (group * (kMergeCols / 4) + x) * R + at, there);
+            }
+#pragma unroll
+            for (int d = 0; d < kDeep; ++d) {
+                if (lse[d] == -INFINITY) continue;             // a part that saw nothing, or none
+                const float top = fmaxf(m, lse[d]), f = exp2_approx(m - top), w = exp2_approx(lse[d] - top);
+                m = top;
+                z = z * f + w;
+#pragma unroll
+                for (int x = 0; x < kMergeCols / 4; ++x) {
+                    acc[4 * x] = fmaf(w, v[d][x].x, acc[4 * x] * f);
+                    acc[4 * x + 1] = fmaf(w, v[d][x].y, acc[4 * x + 1] * f);
+                    acc[4 * x + 2] = fmaf(w, v[d][x].z, acc[4 * x + 2] * f);
+                    acc[4 * x + 3] = fmaf(w, v[d][x].w, acc[4 * x + 3] * f);
+                }
             }
         }
     }
@@ -1126,16 +1135,17 @@ template <int D, bool kBf16>
 int launch_attend(const moe_mxfp4_cache* c, int layer, const moe::CacheView& v, const moe::AttendParams& p, cudaStream_t st) {
     constexpr size_t smem = sizeof(moe::AttSmem<D>);
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
-    // Rows of a merging CTA (a power of two): as many as leave two CTAs for every SM, at most 32 (with 16
-    // the same rows take two waves of CTAs: 84.4 instead of 82.1 us for 32 streams behind 8192 keys).
+    // Rows of a merging CTA (a power of two): as few as keep all rows in two CTAs for every SM, else 32
+    // (with 16 they take two waves of CTAs: 84.4 instead of 82.1 us for 32 streams behind 8192 keys).
     const int64_t jobs = (int64_t)c->cfg.kv_heads * p.a.streams * p.U;
     const auto ctas = [&](int log) { return jobs * ((p.R_own + (1 << log) - 1) >> log); };
     int log_rows = 5;
-    while (log_rows > 1 && (1 << (log_rows - 1) >= p.R_own || ctas(log_rows) < 2 * c->sm_count)) --log_rows;
+    while (log_rows > 1 && (1 << (log_rows - 1) >= p.R_own || ctas(log_rows - 1) <= 2 * c->sm_count)) --log_rows;
     if (moe::launch_dependent(moe::attend_kernel<D, kBf16>, dim3(c->sm_count), dim3(moe::kAttThreads), smem, st, v, p,
                               c->maps[2 * layer], c->maps[2 * layer + 1]) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return moe::launch_dependent(moe::attend_merge_kernel<D, kBf16>,
+    const bool one_wave = ctas(log_rows) <= 2 * c->sm_count;
+    return moe::launch_dependent(one_wave ? moe::attend_merge_kernel<D, kBf16, 4> : moe::attend_merge_kernel<D, kBf16, 2>,
                                  dim3(p.a.streams * p.U, (p.R_own + (1 << log_rows) - 1) >> log_rows, c->cfg.kv_heads),
                                  dim3(moe::kMergeThreads), 0, st, p, log_rows) == cudaSuccess
                ? MOE_OK

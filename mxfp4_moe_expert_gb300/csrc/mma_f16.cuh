@@ -104,6 +104,26 @@ __device__ __forceinline__ uint4 load_or_zero(const void* p, bool there) {
     return v;
 }
 
+// The same for floats that another kernel has just written (from L2).
+__device__ __forceinline__ float4 load_cg_or_zero(const float4* p, bool there) {
+    float4 v;
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+        " @q ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "l"(p), "r"((int)there)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_cg_or(const float* p, bool there, float other) {
+    float v;
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, %3;\n @q ld.global.cg.f32 %0, [%1];\n}"
+                 : "=&f"(v)
+                 : "l"(p), "r"((int)there), "f"(other)
+                 : "memory");
+    return v;
+}
+
 // True in one lane of the (converged) warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
