@@ -96,6 +96,11 @@ struct JobList {
         return min(place < big ? place / (q + 1) : rem + (place - big) / q, workers - 1);
     }
 };
+// A unit of a stream's own rows: its keys [begin, end) and rows.
+struct OwnUnit {
+    int r0, nrows, ctx, begin, end;
+    __device__ int tiles() const { return (end - begin + kKeyTile - 1) / kKeyTile; }
+};
 template <int D>
 struct AttSmem {
     static constexpr int kPanel = 128 * 128;                 // 128 rows x 64 elements
@@ -112,7 +117,8 @@ struct AttSmem {
     int sums[4][kAttThreads / 32];
     uint32_t tmem;
     JobList list[2];                                         // narrow, wide
-    int first_h[2], first_unit[2], first_off[2];             // where each slot's own jobs begin
+    int first_h[2], first_unit[2], first_off[2];             // where each slot's own jobs begin,
+    OwnUnit first_own[2];                                    // and that unit (no rows: not looked up)
     int bad_value[2], bad_wide;                              // last narrow (wide) segment (+ 1) with a non-finite block value
     int abort;
 };
@@ -159,11 +165,6 @@ __device__ __forceinline__ int att_shared(const CacheView& c, const AttendParams
     return (len >= n) & (held >= (n >> c.page_shift)) ? n : 0;
 }
 
-// A unit of a stream's own rows: its keys [begin, end) and rows.
-struct OwnUnit {
-    int r0, nrows, ctx, begin, end;
-    __device__ int tiles() const { return (end - begin + kKeyTile - 1) / kKeyTile; }
-};
 __device__ __forceinline__ OwnUnit att_unit(const CacheView& c, const AttendParams& p, int unit, int shared) {
     OwnUnit w{0, 0, 0, 0, 0};
     const int s = unit / p.U;
@@ -228,7 +229,8 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     const int units = p.a.streams * p.U, tid = threadIdx.x, pad = p.wide_own ? kPadWide : kPadNarrow;
     const int shared = att_shared(c, p);
     // places of one head's own jobs with and without the shared pass, and the streams that share
-    int sum[3] = {0, 0, 0}, mine[2] = {0, 0}, rows = 0, begin = 0;   // (mine: of unit `tid`)
+    int sum[3] = {0, 0, 0}, mine[2] = {0, 0};
+    OwnUnit u{0, 0, 0, 0, 0};                  // (u, mine: of unit `tid`)
     for (int i = tid; i < units; i += kAttThreads) {
         const OwnUnit w = att_unit(c, p, i, shared);
         if (w.nrows == 0) continue;
@@ -239,8 +241,7 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
         if (i == tid) {
             mine[0] = with;
             mine[1] = without;
-            rows = w.nrows;
-            begin = w.begin;
+            u = w;
         }
     }
 #pragma unroll
@@ -252,6 +253,7 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
     if (tid < 2) {
         sm.first_unit[tid] = 0;
         sm.first_off[tid] = 0;
+        sm.first_own[tid].nrows = 0;
     }
     __syncthreads();
 #pragma unroll
@@ -281,11 +283,10 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
             const int i = i0 + tid;
             int n = mine[share ? 0 : 1];
             if (i0 > 0) {                      // (units behind the first pass are read again)
-                const OwnUnit u = i < units ? att_unit(c, p, i, sc.shared) : OwnUnit{0, 0, 0, 0, 0};
+                u = i < units ? att_unit(c, p, i, sc.shared) : OwnUnit{0, 0, 0, 0, 0};
                 n = u.nrows > 0 ? u.tiles() + pad : 0;
-                rows = u.nrows;
-                begin = u.begin;
             }
+            if (!share) u.begin = 0;
             int all;
             const int x0 = at + att_scan(sm, n, &all);
 #pragma unroll
@@ -293,8 +294,9 @@ __device__ Schedule att_schedule(const CacheView& c, const AttendParams& p, AttS
                 if (n > 0 && x0 <= y[x] && y[x] < x0 + n) {
                     sm.first_unit[x] = i;
                     sm.first_off[x] = y[x] - x0;
+                    sm.first_own[x] = u;
                 }
-            if (blockIdx.x == 0 && i < units) p.units[i] = make_int4(x0, rows, n - pad, share && begin > 0);
+            if (blockIdx.x == 0 && i < units) p.units[i] = make_int4(x0, u.nrows, n - pad, u.begin > 0);
             at += all;
         }
     }
@@ -324,6 +326,7 @@ struct Walk {
     int v, end;                // places
     int h, unit, off;
     int base, n;               // tiles of the units base + lane
+    bool known;                // the first unit has been looked up
 };
 template <int D>
 __device__ __forceinline__ Walk att_walk(const JobList& L, const AttSmem<D>& sm, int slot, int worker) {
@@ -333,18 +336,20 @@ __device__ __forceinline__ Walk att_walk(const JobList& L, const AttSmem<D>& sm,
     w.h = 0;
     w.unit = 0;
     w.off = 0;
+    w.known = false;
     if (L.has_own && w.v >= L.W_sh && w.v < w.end) {
         w.h = sm.first_h[slot];
         w.unit = sm.first_unit[slot];
         w.off = sm.first_off[slot];
+        w.known = sm.first_own[slot].nrows > 0;
     }
     w.base = -1;
     w.n = 0;
     return w;
 }
 template <int D>
-__device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedule& sc, const JobList& L, bool wide, int slot,
-                         int worker, Walk& w, Segment& sg) {
+__device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedule& sc, const JobList& L, const AttSmem<D>& sm,
+                         bool wide, int slot, int worker, Walk& w, Segment& sg) {
     for (;;) {
         if (w.v >= w.end) return false;
         int n, begin, o0, job;                 // tiles of the job, first key; first place of it here
@@ -361,7 +366,7 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
             sg.key_end = sg.ctx = sc.shared;
         } else {
             const int units = p.a.streams * p.U, lane = threadIdx.x & 31;
-            for (;;) {                         // the next unit with tiles
+            while (!w.known) {                 // the next unit with tiles
                 if (w.unit >= units) {
                     w.unit = 0;
                     if (++w.h >= c.Hkv) return false;
@@ -378,7 +383,8 @@ __device__ bool att_next(const CacheView& c, const AttendParams& p, const Schedu
                 }
                 w.unit = base + 32;
             }
-            const OwnUnit u = att_unit(c, p, w.unit, sc.shared);
+            const OwnUnit u = w.known ? sm.first_own[slot] : att_unit(c, p, w.unit, sc.shared);
+            w.known = false;
             n = u.tiles();
             begin = u.begin;
             o0 = w.off;
@@ -454,14 +460,7 @@ __device__ bool att_produce(const CacheView& c, const AttendParams& p, const Sch
     const bool loads = !wide || slot == 0;
     const Ring<D> ring(sm, wide, slot);
     Walk w = att_walk<D>(L, sm, slot, worker);
-    while (att_next<D>(c, p, sc, L, wide, slot, worker, w, sg)) {
-        if (!att_publish<D>(p, sm, slot, sg, n)) return false;
-        ++sg.no;
-        sg.wide_no += wide;
-        if (!loads) {
-            n += 2 * sg.T;
-            continue;
-        }
+    while (att_next<D>(c, p, sc, L, sm, wide, slot, worker, w, sg)) {
         const int* table = c.table(sg.s);
         const int pages = min(min(c.held()[sg.s], c.L.M), (sg.key_end + c.page - 1) >> c.page_shift);
         // the page that this lane copies of a tile; outside the pool (zeros) where there is none
@@ -471,6 +470,13 @@ __device__ bool att_produce(const CacheView& c, const AttendParams& p, const Sch
             return (unsigned)id < (unsigned)c.L.P ? id : c.L.P;
         };
         int id = page_of(0);
+        if (!att_publish<D>(p, sm, slot, sg, n)) return false;
+        ++sg.no;
+        sg.wide_no += wide;
+        if (!loads) {
+            n += 2 * sg.T;
+            continue;
+        }
         for (int t = 0; t < sg.T; ++t) {
             const int next = page_of(t + 1);
 #pragma unroll
