@@ -26,13 +26,13 @@
 // rescaled rarely, by the softmax warps themselves.
 //
 // What bounds it, on 152 SMs.  Reading keys where there are few rows: 96 streams that decode one
-// position over 700..6000 keys (1.32 GB) take 203 us, 6.5 TB/s, 0.96 of the copy rate.  The tensor
+// position over 700..6000 keys (1.32 GB) take 200 us, 6.6 TB/s, 0.97 of the copy rate.  The tensor
 // core's chain where a long prefix is shared: 64 streams x 8 positions x 64 heads behind 32768 keys
 // (0.57 PFLOP) take 431 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
 // keys) takes about 2950 cycles for 2048 of products: scores -> softmax (1500) -> P V and the next
 // scores (1024) follow one another in each slot, and shared memory is read at its full 128 bytes a
 // cycle while Q K^T runs.  The launches, the schedule and the merge where there is little work: one
-// stream of 8 positions over 4093 keys takes 18 us, of which its tiles are 3.
+// stream of 8 positions over 4093 keys takes 16 us, of which its tiles are 3.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -1005,7 +1005,7 @@ __device__ __forceinline__ Parts att_parts(const AttendParams& p, const JobList&
 // head); a thread has 16 columns of a row (rows on neighbouring lanes, as the parts store them);
 // where there are few rows, several threads take the parts in turn, each with the running maximum
 // and sum of a softmax, and are joined pairwise in a fixed order.  Bound by latency (the schedule,
-// then the parts, from L2): 7 us after the attention for one stream, about 10 for 14336 rows with
+// then the parts, from L2): 5 us after the attention for one stream, about 10 for 14336 rows with
 // 5.7 parts each (42 MB).
 // kDeep parts are under way together: 4 where one wave of CTAs holds all rows (one stream: 16.5 us
 // against 17.3 with 2), 2 where the registers would cost CTAs (96 streams: 201.4 against 202.9).
