@@ -90,6 +90,39 @@ def test_any_sequence_of_calls_keeps_the_books(kw, seed):
     c.close()
 
 
+@pytest.mark.parametrize("S,P,seed", [(1100, 5000, 1), (2100, 9000, 2)])
+def test_books_of_more_streams_and_pages_than_one_pass(S, P, seed):
+    """More streams than a planning CTA has threads, and more pages than it looks at in one pass; copies included."""
+    c, mem, b = make(L=1, S=S, M=6, P=P, Hkv=1, page=16, D=64, seed=seed)
+    rng = random.Random(seed)
+    for step in range(14):
+        add = [rng.choice([0, 0, 3, 16, 40]) for _ in range(S)]
+        ok = b.reserve(add)
+        c.reserve(i32(add))
+        assert status(c) == (pkg.MOE_OK if ok else status_of_refusal(b, add)), step
+        if ok:
+            acc = [rng.randint(0, n) for n in add]
+            c.commit(i32(acc))
+            b.truncate([b.length[s] + acc[s] for s in range(S)])
+        new = [rng.choice([-1, -1, 0, b.length[s] // 2, b.length[s]]) for s in range(S)]
+        c.truncate(i32(new))
+        b.truncate(new)
+        empty = [s for s in range(S) if not b.held[s]]
+        full = [s for s in range(S) if b.held[s]]
+        if full and empty:
+            dst = rng.sample(empty, rng.randint(1, len(empty)))
+            src = [rng.choice(full[:20]) for _ in dst]       # many holders of a page, many writers of it next
+            c.fork(i32(src), i32(dst))
+            b.fork(src, dst)
+        if step % 4 == 3:
+            c.compact()
+            b.compact()
+        assert status(c) == pkg.MOE_OK
+        b.consistent()
+        assert_books(c, b)
+    assert torch.equal(mem.cpu().view(torch.int16), b.pool.view(torch.int16))
+
+
 def status_of_refusal(b, add):
     over = any(n > 0 and b.length[s] + n > b.M * b.page for s, n in enumerate(add))
     return pkg.MOE_ERR_CACHE_STATE if over else pkg.MOE_ERR_CACHE_FULL

@@ -286,6 +286,21 @@ def test_extreme_scores():
     c.check(*c.attend(scale=1.0), scale=1.0)
 
 
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16)])
+def test_the_maximum_climbs_along_a_shared_prefix(D, dtype):
+    """Scores that grow by some tens along the prefix for half of the rows and fall for the others, in units that fill
+    both halves of a CTA: the accumulators are rescaled many times."""
+    S, prefix = 24, 12288
+    c = Case([prefix + n for n in range(1, 25)], 8, 64, 8, D=D, dtype=dtype, page=64, prefix=prefix, seed=18)
+    ids = torch.tensor(c.books.table[S][:prefix // c.page], device="cuda")
+    ramp = torch.linspace(-20, 20, len(ids), device="cuda")[:, None, None, None]
+    c.k[ids] = (c.k[ids].float() * 0.5 + ramp).to(dtype)
+    out, lse = c.attend()
+    c.check(out, lse, streams=[0, 11, 23])
+    again, _ = c.attend()
+    assert torch.equal(again, out)
+
+
 def test_rows_of_a_fused_projection_and_bad_tables():
     c = Case([100, 259], 4, 4, 2, seed=12)
     want, wlse = c.attend()
