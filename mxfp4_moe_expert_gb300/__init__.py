@@ -515,7 +515,7 @@ class KvCache:
     """The paged key/value cache of a verify forward (moe_mxfp4.h, "paged key/value cache").
 
     layers: a list of (k, v) pool tensors [num_pages, kv_heads, page_tokens, head_dim], bf16 or fp16 on one CUDA
-    device, contiguous within a page (all with the same stride between pages); kept alive here.  The books are views of
+    device, contiguous within a page (all with the same stride between pages, which share no memory); kept alive here.  The books are views of
     one int32 tensor: length [S], held [S], page_table [S, max_pages], refcount [num_pages].  Every call runs on
     `stream` (a cudaStream_t as int; default: torch's current stream on the cache's device); device-side errors are
     raised by check().
@@ -534,6 +534,8 @@ class KvCache:
             if (pool.shape != k0.shape or pool.dtype != k0.dtype or pool.device != k0.device
                     or pool.stride()[1:] != (tokens * dim, dim, 1) or (pages > 1 and pool.stride(0) != k0.stride(0))):
                 raise ValueError("the pools of a cache have one shape, type, device and page stride")
+        if pages > 1 and k0.stride(0) < heads * tokens * dim:
+            raise ValueError("the pages of a pool do not share memory")
         self._keep = layers
         self.device, self.dtype = k0.device, k0.dtype      # (a tensor's device has its index)
         self.num_layers, self.num_streams, self.max_pages = len(layers), num_streams, max_pages
@@ -610,7 +612,7 @@ class KvCache:
 
     def append(self, layer, k, v, lengths=None, stream=None):
         """k, v: [streams, block, kv_heads, head_dim], contiguous or rows of one wider tensor (a fused projection's
-        output); lengths: int32 [streams], tokens in use of each block."""
+        output), each token in memory of its own (an expanded tensor is refused); lengths: int32 [streams], tokens in use of each block."""
         layout = self._pairs.get((k.shape, k.stride(), v.shape, v.stride()))
         if (layout is None or k.dtype is not self.dtype or v.dtype is not self.dtype or k.get_device() != self._index
                 or v.get_device() != self._index):
@@ -698,9 +700,12 @@ class KvCache:
             (S, B, H, D), st = key
             if t.numel() and ((D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (S > 1 and B > 1 and st[0] != B * st[1])):
                 raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
+            row = st[1] if B > 1 else st[0] if S > 1 else H * D
+            if t.numel() and row < H * D:      # (expanded ones have 0, which the library takes for contiguous rows)
+                raise ValueError(f"{name}: tokens do not share memory")
             if len(self._layouts) >= 1024:
                 self._layouts.clear()
-            rows = self._layouts[key] = (S, B, H, D, st[1] if B > 1 else st[0] if S > 1 else H * D)
+            rows = self._layouts[key] = (S, B, H, D, row)
         return rows
 
     def _workspace(self, S, B, H):

@@ -1,0 +1,61 @@
+"""The binding's checks of the paged cache without a GPU: layouts of tensors on the CPU, in a cache that has no handle."""
+import pytest
+import torch
+
+import mxfp4_moe_expert_gb300 as pkg
+
+
+def bare(kv_heads=2, head_dim=64, num_streams=8):
+    """A KvCache whose tensors are on the CPU and that makes no library call by itself."""
+    c = pkg.KvCache.__new__(pkg.KvCache)
+    c.handle, c.device, c._index, c.dtype = None, torch.device("cpu"), -1, torch.bfloat16
+    c.kv_heads, c.head_dim, c.num_streams = kv_heads, head_dim, num_streams
+    c._layouts, c._pairs, c._ws, c._ws_bytes, c._ws_kept = {}, {}, None, {}, []
+    c._i32, c._f32, c._mask_types = torch.int32, torch.float32, (torch.int64, torch.uint64)
+    return c
+
+
+def rows(S, B, H=2, D=64):
+    return torch.zeros((S, B, H, D), dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("S,B", [(4, 1), (1, 5), (4, 3)])
+def test_tokens_that_share_memory_are_refused(S, B):
+    """A token broadcast over streams or positions has a stride of zero, which the library takes for contiguous rows."""
+    c, whole = bare(), rows(S, B)
+    wide = rows(1, 1).expand(S, B, 2, 64)
+    near = torch.zeros(4096, dtype=torch.bfloat16).as_strided((S, B, 2, 64), (B * 64, 64, 64, 1))   # rows that overlap
+    for t in (wide, near):
+        with pytest.raises(ValueError, match="tokens"):
+            c._rows("q", t)
+        with pytest.raises(ValueError, match="tokens"):
+            c._pair(t, t)
+        with pytest.raises(ValueError, match="tokens|stride"):
+            c._pair(whole, t)
+    assert not c._pairs and c._rows("q", whole) == (S, B, 2, 64, 128)
+
+
+def test_a_single_token_may_have_any_stride():
+    c = bare()
+    assert c._rows("q", rows(1, 1).expand(1, 1, 2, 64)) == (1, 1, 2, 64, 128)
+    assert c._pair(rows(1, 1), rows(4, 4)[:1, :1]) == (1, 1, 128)
+    assert c._rows("q", rows(3, 4)[:0])[:2] == (0, 4) and c._rows("q", rows(3, 4)[:, :0])[:2] == (3, 0)
+
+
+class OnGpu:
+    """A CPU tensor that says that it is on a GPU."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_pools_whose_pages_share_memory_are_refused():
+    one = torch.zeros((1, 2, 16, 64), dtype=torch.bfloat16)
+    page = 2 * 16 * 64
+    for t in (one.expand(5, 2, 16, 64), torch.zeros(5 * page, dtype=one.dtype).as_strided((5, 2, 16, 64), (page // 2, 1024, 64, 1))):
+        with pytest.raises(ValueError, match="pages"):
+            pkg.KvCache(layers=[(OnGpu(t), OnGpu(t))], num_streams=1, max_pages=1)
