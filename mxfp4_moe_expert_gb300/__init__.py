@@ -515,10 +515,11 @@ class KvCache:
     """The paged key/value cache of a verify forward (moe_mxfp4.h, "paged key/value cache").
 
     layers: a list of (k, v) pool tensors [num_pages, kv_heads, page_tokens, head_dim], bf16 or fp16 on one CUDA
-    device, contiguous within a page (all with the same stride between pages, which share no memory); kept alive here.  The books are views of
-    one int32 tensor: length [S], held [S], page_table [S, max_pages], refcount [num_pages].  Every call runs on
-    `stream` (a cudaStream_t as int; default: torch's current stream on the cache's device); device-side errors are
-    raised by check().
+    device, contiguous within a page (all with the same stride between pages, which share no memory); kept alive here.
+    The books are views of one int32 tensor: length [S], held [S], page_table [S, max_pages], refcount [num_pages]; they
+    are zeroed on the stream that is current when the cache is made.  Every call runs on `stream` (a cudaStream_t as int;
+    default: torch's current stream on the cache's device), and what it makes belongs to that stream; device-side errors
+    are raised by check().
     """
 
     def __init__(self, *, layers, num_streams, max_pages, timeout_us=0):
@@ -560,7 +561,7 @@ class KvCache:
         self._index, self._append = k0.get_device(), self._lib.moe_mxfp4_cache_append
         self._ws, self._ws_bytes, self._ws_kept = None, {}, []
         self._layouts, self._pairs = {}, {}     # shapes and strides seen so far -> how a call lays them out
-        self._i32, self._f32, self._mask_types = torch.int32, torch.float32, (torch.int64, torch.uint64)
+        self._i32, self._f32, self._u8, self._mask_types = torch.int32, torch.float32, torch.uint8, (torch.int64, torch.uint64)
         # the raw handle of the current stream (torch.cuda.current_stream() builds a Stream object around it)
         self._current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -634,13 +635,12 @@ class KvCache:
         S, B, H, D, row = self._rows("q", q)
         if D != self.head_dim:
             raise ValueError("q is [streams, block, q_heads, head_dim]")
-        if out is None or lse is None:
-            import torch
-            make = torch.empty if lengths is None else torch.zeros
-            if out is None:
-                out = make((S, B, H, D), dtype=self.dtype, device=self.device)
-            if lse is None:
-                lse = make((S, B, H), dtype=torch.float32, device=self.device)
+        if stream is None:
+            stream = self._current_stream(self._index)
+        if out is None:
+            out = self._new((S, B, H, D), self.dtype, stream, zero=lengths is not None)
+        if lse is None:
+            lse = self._new((S, B, H), self._f32, stream, zero=lengths is not None)
         if (out.shape != (S, B, H, D) or out.dtype is not self.dtype or out.get_device() != self._index
                 or not out.is_contiguous()):
             raise ValueError("out: contiguous, of q's shape and type")
@@ -651,12 +651,12 @@ class KvCache:
                                  or mask.get_device() != self._index or not mask.is_contiguous()):
             raise ValueError("mask: contiguous int64 [streams, block]")
         ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else \
-            self._workspace(S, B, H)
+            self._workspace(S, B, H, stream)
         a = moe_mxfp4_attend_args(q.data_ptr(), row, out.data_ptr(), lse.data_ptr(),
                                   None if lengths is None else self._books("lengths", lengths, S),
                                   None if mask is None else mask.data_ptr(), S, B, H, shared_stream, shared_tokens,
                                   self.head_dim ** -0.5 if scale is None else scale)
-        st = self._lib.moe_mxfp4_cache_attend(self.handle, self._state_ptr, layer, a, ws, n, self._stream(stream))
+        st = self._lib.moe_mxfp4_cache_attend(self.handle, self._state_ptr, layer, a, ws, n, stream)
         if st:
             _check(st, "moe_mxfp4_cache_attend")
         return out, lse
@@ -708,7 +708,17 @@ class KvCache:
             rows = self._layouts[key] = (S, B, H, D, row)
         return rows
 
-    def _workspace(self, S, B, H):
+    def _new(self, shape, dtype, stream, zero=False):
+        """A tensor made on a call's stream: its fill is ordered with the call, and so is what still uses its memory."""
+        import torch
+        make = torch.zeros if zero else torch.empty
+        if stream == self._current_stream(self._index):
+            return make(shape, dtype=dtype, device=self.device)
+        on = torch.cuda.ExternalStream(stream, self.device) if stream else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(on):
+            return make(shape, dtype=dtype, device=self.device)
+
+    def _workspace(self, S, B, H, stream):
         """The cache's own workspace, grown when a call needs more; earlier ones are kept, since captured graphs may
         hold their addresses."""
         key = (S, B, H)
@@ -717,8 +727,7 @@ class KvCache:
             n = self._ws_bytes[key] = self.attend_bytes(S, B, H)
         ws = self._ws
         if ws is None or ws.numel() < n:
-            import torch
-            raw = torch.empty(n + 256, dtype=torch.uint8, device=self.device)
+            raw = self._new(n + 256, self._u8, stream)
             off = (-raw.data_ptr()) % 256
             ws = self._ws = raw[off:off + n]
             self._ws_kept.append(ws)

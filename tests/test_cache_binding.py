@@ -1,4 +1,6 @@
-"""The binding's checks of the paged cache without a GPU: layouts of tensors on the CPU, in a cache that has no handle."""
+"""The binding of the paged cache without a GPU: tensors on the CPU, in a cache that has no handle."""
+import contextlib
+
 import pytest
 import torch
 
@@ -11,7 +13,7 @@ def bare(kv_heads=2, head_dim=64, num_streams=8):
     c.handle, c.device, c._index, c.dtype = None, torch.device("cpu"), -1, torch.bfloat16
     c.kv_heads, c.head_dim, c.num_streams = kv_heads, head_dim, num_streams
     c._layouts, c._pairs, c._ws, c._ws_bytes, c._ws_kept = {}, {}, None, {}, []
-    c._i32, c._f32, c._mask_types = torch.int32, torch.float32, (torch.int64, torch.uint64)
+    c._i32, c._f32, c._u8, c._mask_types = torch.int32, torch.float32, torch.uint8, (torch.int64, torch.uint64)
     return c
 
 
@@ -59,3 +61,49 @@ def test_pools_whose_pages_share_memory_are_refused():
     for t in (one.expand(5, 2, 16, 64), torch.zeros(5 * page, dtype=one.dtype).as_strided((5, 2, 16, 64), (page // 2, 1024, 64, 1))):
         with pytest.raises(ValueError, match="pages"):
             pkg.KvCache(layers=[(OnGpu(t), OnGpu(t))], num_streams=1, max_pages=1)
+
+
+class FakeLibrary:
+    def __init__(self):
+        self.attends = []
+
+    def moe_mxfp4_cache_attend(self, handle, state, layer, args, ws, n, stream):
+        self.attends.append((stream, ws, n))
+        return 0
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The stream that torch has as current (7 at first), and the one that each new tensor was made on."""
+    now, made = [7], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        now.append(stream)
+        yield
+        now.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: ptr)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    for name in ("empty", "zeros"):
+        plain = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, plain=plain, **kw: (made.append(now[-1]), plain(*a, **kw))[1])
+    return now, made
+
+
+@pytest.mark.parametrize("stream", [None, 7, 99, 0])
+@pytest.mark.parametrize("lengths", [False, True])
+def test_what_attend_makes_is_made_on_the_stream_of_the_call(stream, lengths, streams):
+    """A fill on another stream may land after the kernels, and memory of another stream may still be in use there."""
+    now, made = streams
+    c = bare()
+    c._lib, c._state_ptr = FakeLibrary(), 16
+    c._current_stream = lambda index: now[-1]
+    c.attend_bytes = lambda S, B, H: 1000
+    q = rows(3, 2)
+    made.clear()
+    c.attend(0, q, lengths=torch.ones(3, dtype=torch.int32) if lengths else None, stream=stream)
+    on = 7 if stream is None else stream
+    assert made == [on] * 3 and now == [7]            # out, lse, the workspace
+    assert c._lib.attends[0][0] == on

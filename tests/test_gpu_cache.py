@@ -321,6 +321,37 @@ def test_two_streams_a_graph_and_its_replay():
     assert torch.equal(mem.cpu(), b.pool) and status(c) == pkg.MOE_OK
 
 
+def test_every_call_on_a_stream_of_its_own():
+    """stream= of each call, while another stream is current (and busy)."""
+    c, mem, b = make(S=4, M=6, P=24, L=2, seed=3)
+    k, v = torch.randn((2, 4, 20, 2, 64)).bfloat16()
+    gk, gv, side = k.cuda(), v.cuda(), torch.cuda.Stream()
+    n, dst, src, acc, cut = i32([20, 20, 20, 0]), i32([3]), i32([1]), i32([20, 9, 0, 0]), i32([-1, -1, -1, 4])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    on = dict(stream=side.cuda_stream)
+    c.reserve(n, **on)
+    for layer in range(2):
+        c.append(layer, gk, gv, lengths=n, **on)
+    c.commit(acc, **on)
+    c.fork(src, dst, **on)
+    c.truncate(cut, **on)
+    c.reserve(1, **on)
+    c.compact(**on)
+    c.check(**on)
+    b.reserve([20, 20, 20, 0])
+    for layer in range(2):
+        b.append(k, v, layer, [20, 20, 20, 0])
+    b.truncate([20, 9, 0, -1])
+    b.fork([1], [3])
+    b.truncate([-1, -1, -1, 4])
+    b.reserve([1] * 4)
+    b.compact()
+    torch.cuda.synchronize()
+    assert_books(c, b)
+    assert torch.equal(mem.cpu(), b.pool)
+
+
 def test_argument_checks_of_the_binding():
     c, mem, b = make()
     k = torch.zeros((6, 2, 2, 64), dtype=torch.bfloat16, device="cuda")

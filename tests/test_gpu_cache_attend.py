@@ -394,6 +394,29 @@ def test_calls_that_overlap_on_two_streams():
         assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1]), k
 
 
+def test_outputs_belong_to_the_stream_of_the_call():
+    """attend(stream=...) while torch's current stream is busy: the fills of the outputs do not wait for that one, and
+    no later fill reaches them."""
+    c = Case([700, 90, 0, 300], 8, 16, 2, prefix=64, seed=19)
+    used = i32([8, 3, 0, 8])
+    want, wlse = c.attend(lengths=used)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)              # some 10 ms on the current stream
+        got = [c.cache.attend(0, c.q, lengths=used, shared_stream=c.S, shared_tokens=64, stream=side.cuda_stream),
+               c.cache.attend(0, c.q, lengths=used, shared_stream=c.S, shared_tokens=64, stream=side.cuda_stream)]
+        side.synchronize()
+        early = [(out.cpu(), lse.cpu()) for out, lse in got]
+        torch.cuda.synchronize()
+        for (out, lse), (e, el) in zip(got, early):
+            assert torch.equal(out, want) and torch.equal(lse, wlse)
+            assert torch.equal(e, want.cpu()) and torch.equal(el, wlse.cpu())
+    out, lse = c.cache.attend(0, c.q, lengths=used, shared_stream=c.S, shared_tokens=64, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_a_verify_forward_from_reserve_to_commit():
     """The calls as a user makes them: streams fork from a prompt, and blocks are reserved, appended, attended, judged
     by accept() and committed; the attention then equals that over contiguous keys."""
