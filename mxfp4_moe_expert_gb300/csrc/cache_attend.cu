@@ -51,6 +51,10 @@ constexpr float kRescale = 8.0f;               // exponents that the maximum may
 // out); dealt out with them.  3 for narrow ones rather than 2: 96 streams decode in 205.7 us
 // instead of 209.0, other cases do not change.
 constexpr int kPadWide = 1, kPadNarrow = 3;
+// Marks of wide segments, in turn.  Slot 0's MMA warp may mark the next segment while slot 1's softmax
+// warps have yet to read the mark of this one, but not the one after it: its turn there follows slot
+// 1's products of the next segment, whose queries those warps load after they have read.
+constexpr int kWideMarks = 2;
 
 struct AttendParams {
     moe_mxfp4_attend_args a;
@@ -119,7 +123,7 @@ struct AttSmem {
     JobList list[2];                                         // narrow, wide
     int first_h[2], first_unit[2], first_off[2];             // where each slot's own jobs begin,
     OwnUnit first_own[2];                                    // and that unit (no rows: not looked up)
-    int bad_value[2], bad_wide;                              // last narrow (wide) segment (+ 1) with a non-finite block value
+    int bad_value[2], bad_wide[kWideMarks];                  // last narrow (wide) segment (+ 1) with a non-finite block value
     int abort;
 };
 
@@ -639,7 +643,8 @@ __device__ void att_mma(const AttendParams& p, AttSmem<D>& sm, uint32_t tmem, in
                     const bool bad = att_mend_v<D, kBf16>(sm.kv[st], min(max(ctx - j0, 0), kKeyTile), min(max(key_end - j0, 0), kKeyTile));
                     if (issues) {
                         if (bad) {
-                            *reinterpret_cast<volatile int*>(wide ? &sm.bad_wide : &sm.bad_value[slot]) = (wide ? wide_no : no) + 1;
+                            *reinterpret_cast<volatile int*>(wide ? &sm.bad_wide[wide_no % kWideMarks] : &sm.bad_value[slot]) =
+                                (wide ? wide_no : no) + 1;
                             __threadfence_block();
                         }
                         if (wide) mbar_arrive(&sm.mended[st]);
@@ -870,7 +875,8 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
         if (busy) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-            const bool mend = sg.own && *reinterpret_cast<volatile int*>(sg.wide ? &sm.bad_wide : &sm.bad_value[slot]) ==
+            const bool mend = sg.own && *reinterpret_cast<volatile int*>(sg.wide ? &sm.bad_wide[sg.wide_no % kWideMarks]
+                                                                                 : &sm.bad_value[slot]) ==
                                             (sg.wide ? sg.wide_no : no) + 1;
             float* const out = sg.out;
             const int R = sg.R, r = sg.out_row + tid;
@@ -937,7 +943,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
             sm.bad_value[x] = 0;
         }
         mbar_init(&sm.handover, 1);
-        sm.bad_wide = 0;
+        for (int i = 0; i < kWideMarks; ++i) sm.bad_wide[i] = 0;
         sm.abort = 0;
         fence_barrier_init();
     }

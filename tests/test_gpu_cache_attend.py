@@ -252,6 +252,26 @@ def test_bad_values_in_blocks_of_many_rows(D, prefix):
             assert out[s, b][:, bad].isnan().all(), (s, b)
 
 
+def test_bad_values_in_many_short_blocks_that_follow_one_another():
+    """Several units of more than 128 rows for every CTA, each a tile long, with a bad value in its block: each
+    unit's rows get their own, in both halves, every time."""
+    S, B, D, Hkv = 300, 20, 64, 2
+    c = Case([(37 * s) % 90 for s in range(S)], B, 16, Hkv, D=D, page=32, seed=20)
+    want, wlse = c.attend()
+    at = torch.tensor([(7 * s) % B for s in range(S)], device="cuda")
+    col = torch.tensor([(11 * s) % D for s in range(S)], device="cuda")
+    for s in range(S):
+        i, off = divmod(c.books.length[s] + int(at[s]), c.page)
+        c.v[c.books.table[s][i], :, off, int(col[s])] = float("inf") if s % 3 else float("nan")
+    sees = torch.arange(B, device="cuda")[None, :] >= at[:, None]
+    bad = sees[:, :, None, None] & (torch.arange(D, device="cuda") == col[:, None])[:, None, None, :]
+    for _ in range(20):
+        out, lse = c.attend()
+        assert torch.equal(lse, wlse)
+        assert torch.equal(~out.isfinite(), bad.expand_as(out))
+        assert torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, want))
+
+
 def test_masks_of_one_row_leave_the_others_alone():
     """The same with a mask: a bad value is seen by the rows whose bit is set, and by no other."""
     B = 5
