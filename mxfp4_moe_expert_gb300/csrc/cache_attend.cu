@@ -145,6 +145,13 @@ __device__ __forceinline__ bool att_wait(uint64_t* bar, uint32_t parity, int* ab
 __device__ __forceinline__ bool att_warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned long long timeout_ns) {
     return __all_sync(0xFFFFFFFFu, att_wait(bar, parity, abort, timeout_ns));
 }
+// Copies and products that are under way end by themselves, whatever the other warps do: a CTA that
+// gives up still waits for them, with a limit of its own that does not follow the caller's (two
+// seconds, some 10^5 times what they take).
+__device__ __forceinline__ void att_drain(uint64_t* bar, uint32_t parity) {
+    const unsigned long long until = globaltimer_ns() + 2000000000ull;
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() < until) {}
+}
 
 // ---- the schedule ------------------------------------------------------------------------
 
@@ -536,15 +543,11 @@ __device__ void att_producer(const CacheView& c, const AttendParams& p, const Sc
         }
     }
     sg.T = 0;
-    if (ok) ok = att_publish<D>(p, sm, slot, sg, nw + nn);
-    if (ok && !*reinterpret_cast<volatile int*>(&sm.abort)) return;
-    // after an abort: every copy has landed before the CTA leaves
-    const unsigned long long until = globaltimer_ns() + p.timeout_ns;
+    if (ok) att_publish<D>(p, sm, slot, sg, nw + nn);
+    // Every copy has landed before the CTA leaves, also where another warp gives up after this one is done.
     if (slot == 0)
-        for (uint32_t i = nw > (uint32_t)wide.stages ? nw - wide.stages : 0; i < nw; ++i)
-            while (!mbar_try_wait(wide.full(i), wide.round(i)) && globaltimer_ns() < until) {}
-    for (uint32_t i = nn > (uint32_t)narrow.stages ? nn - narrow.stages : 0; i < nn; ++i)
-        while (!mbar_try_wait(narrow.full(i), narrow.round(i)) && globaltimer_ns() < until) {}
+        for (uint32_t i = nw > (uint32_t)wide.stages ? nw - wide.stages : 0; i < nw; ++i) att_drain(wide.full(i), wide.round(i));
+    for (uint32_t i = nn > (uint32_t)narrow.stages ? nn - narrow.stages : 0; i < nn; ++i) att_drain(narrow.full(i), narrow.round(i));
 }
 
 // ---- MMA -------------------------------------------------------------------------------------
@@ -973,8 +976,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const CacheView 
             att_mma<D, kBf16>(p, sm, tmem, slot);
             if (elect_one()) {                             // every product has completed before the memory is freed
                 tc_commit(&sm.drain[slot]);
-                const unsigned long long until = globaltimer_ns() + p.timeout_ns;
-                while (!mbar_try_wait(&sm.drain[slot], 0) && globaltimer_ns() < until) {}
+                att_drain(&sm.drain[slot], 0);
             }
         }
     }

@@ -272,6 +272,41 @@ def test_bad_values_in_many_short_blocks_that_follow_one_another():
         assert torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, want))
 
 
+def bad_prompt(B, Hkv, D=128, every=64):
+    """A prompt of B positions with a NaN at every 64th, whose rows are slow to write out; what its rows should be."""
+    c = Case([0], B, Hkv, Hkv, D=D, page=128, seed=21)
+    want, wlse = c.attend()
+    ids = torch.tensor(c.books.table[0][:c.books.held[0]], device="cuda")
+    for at in range(every // 2, B, every):
+        c.v[ids[at // c.page], :, at % c.page, at // every % D] = float("nan")
+    b = torch.arange(B, device="cuda")[:, None]
+    last = (b + every // 2) // every - 1                     # number of the last bad value that the row sees
+    bad = torch.arange(D, device="cuda")[None, :] <= last
+    return c, want, wlse, bad[None, :, None, :]
+
+
+def assert_bad_prompt(out, lse, want, wlse, bad):
+    assert torch.equal(lse, wlse)
+    assert torch.equal(out.isnan(), bad.expand_as(out))
+    assert torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, want))
+
+
+def test_a_wait_that_runs_out_is_an_error_that_the_host_reads():
+    """A limit of 1 us is below what a warp waits for rows with bad values to be written out: the call ends, check()
+    says why, and the next call, on a handle with the usual limit, is right."""
+    c, want, wlse, bad = bad_prompt(2048, 64)
+    hasty = pkg.KvCache(layers=[(c.k, c.v)], num_streams=2, max_pages=c.books.M, timeout_us=1)
+    write_books(hasty, c.books)
+    for _ in range(3):
+        hasty.attend(0, c.q)
+        with pytest.raises(pkg.MoeError) as e:
+            hasty.check()
+        assert e.value.status == pkg.MOE_ERR_TIMEOUT
+        hasty.check()
+        out, lse = c.attend()
+        assert_bad_prompt(out, lse, want, wlse, bad)
+
+
 def test_masks_of_one_row_leave_the_others_alone():
     """The same with a mask: a bad value is seen by the rows whose bit is set, and by no other."""
     B = 5
