@@ -291,6 +291,45 @@ def assert_bad_prompt(out, lse, want, wlse, bad):
     assert torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, want))
 
 
+def test_bad_values_of_a_long_prompt_are_no_reason_to_give_up():
+    """Writing out rows with bad values is quick enough for the waits of the other warps, at 16384 positions too."""
+    c, want, wlse, bad = bad_prompt(16384, 8)
+    out, lse = c.attend()
+    assert_bad_prompt(out, lse, want, wlse, bad)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.float16), (64, torch.bfloat16)])
+def test_infinities_of_both_signs_and_nan(D, dtype):
+    """Every kind of bad value at random block positions and columns, under random masks: a column is what the sum of
+    the bad values that the row sees is."""
+    rng = random.Random(D)
+    B, Hkv = 40, 2
+    c = Case([0, 3, 100, 250], B, 8, Hkv, D=D, dtype=dtype, page=16, seed=22)
+    rows = [[rng.getrandbits(B) | 1 << b for b in range(B)] for _ in range(c.S)]
+    mask = torch.tensor(rows, dtype=torch.int64, device="cuda")
+    want, wlse = c.attend(mask=mask)
+    kinds = [float("inf"), -float("inf"), float("nan")]
+    seen = [[[[] for _ in range(D)] for _ in range(Hkv)] for _ in range(c.S)]
+    for s in range(c.S):
+        for _ in range(25):
+            pos, h, col, x = rng.randrange(B), rng.randrange(Hkv), rng.randrange(D), kinds[rng.choice([0, 0, 1, 1, 2])]
+            i, off = divmod(c.books.length[s] + pos, c.page)
+            if c.v[c.books.table[s][i], h, off, col].isfinite():
+                c.v[c.books.table[s][i], h, off, col] = x
+                seen[s][h][col].append((pos, x))
+    out, lse = c.attend(mask=mask)
+    assert torch.equal(lse, wlse)
+    ref = want.cpu().clone()
+    for s in range(c.S):
+        for h in range(Hkv):
+            for col in range(D):
+                for b in range(B):
+                    xs = [x for pos, x in seen[s][h][col] if rows[s][b] >> pos & 1]
+                    if xs:
+                        ref[s, b, 4 * h:4 * h + 4, col] = sum(xs)
+    assert torch.equal(out.cpu().nan_to_num(nan=12345.0), ref.nan_to_num(nan=12345.0))
+
+
 def test_a_wait_that_runs_out_is_an_error_that_the_host_reads():
     """A limit of 1 us is below what a warp waits for rows with bad values to be written out: the call ends, check()
     says why, and the next call, on a handle with the usual limit, is right."""
