@@ -650,8 +650,12 @@ class KvCache:
         if mask is not None and (mask.shape != (S, B) or mask.dtype not in self._mask_types
                                  or mask.get_device() != self._index or not mask.is_contiguous()):
             raise ValueError("mask: contiguous int64 [streams, block]")
-        ws, n = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else \
-            self._workspace(S, B, H, stream)
+        if workspace is None:
+            ws, n = self._workspace(S, B, H, stream)
+        elif workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous, on {self.device}")
+        else:
+            ws, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         a = moe_mxfp4_attend_args(q.data_ptr(), row, out.data_ptr(), lse.data_ptr(),
                                   None if lengths is None else self._books("lengths", lengths, S),
                                   None if mask is None else mask.data_ptr(), S, B, H, shared_stream, shared_tokens,

@@ -107,3 +107,16 @@ def test_what_attend_makes_is_made_on_the_stream_of_the_call(stream, lengths, st
     on = 7 if stream is None else stream
     assert made == [on] * 3 and now == [7]            # out, lse, the workspace
     assert c._lib.attends[0][0] == on
+
+
+def test_a_workspace_elsewhere_or_in_pieces_is_refused():
+    c = bare()
+    c._lib, c._state_ptr, c._current_stream = FakeLibrary(), 16, lambda index: 7
+    q, other = rows(3, 2), OnGpu(torch.zeros(1024, dtype=torch.uint8))
+    other.get_device = lambda: 0                     # (the cache's own device here is -1, the CPU)
+    for ws in (other, torch.zeros(2048, dtype=torch.uint8)[::2], torch.zeros((4, 512), dtype=torch.uint8).T):
+        with pytest.raises(ValueError, match="workspace"):
+            c.attend(0, q, workspace=ws)
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    c.attend(0, q, workspace=ws)
+    assert c._lib.attends == [(7, ws.data_ptr(), 1024)]
