@@ -723,14 +723,15 @@ class KvCache:
             return make(shape, dtype=dtype, device=self.device)
 
     def _workspace(self, S, B, H, stream):
-        """The cache's own workspace, grown when a call needs more; earlier ones are kept, since captured graphs may
-        hold their addresses."""
+        """The cache's own workspace, at least doubled when a call needs more; earlier ones are kept, since captured
+        graphs may hold their addresses (all together, at most four times what the largest call needs)."""
         key = (S, B, H)
         n = self._ws_bytes.get(key)
         if n is None:
             n = self._ws_bytes[key] = self.attend_bytes(S, B, H)
         ws = self._ws
         if ws is None or ws.numel() < n:
+            n = max(n, 2 * ws.numel() if ws is not None else 0)
             raw = self._new(n + 256, self._u8, stream)
             off = (-raw.data_ptr()) % 256
             ws = self._ws = raw[off:off + n]

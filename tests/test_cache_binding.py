@@ -120,3 +120,18 @@ def test_a_workspace_elsewhere_or_in_pieces_is_refused():
     ws = torch.zeros(1024, dtype=torch.uint8)
     c.attend(0, q, workspace=ws)
     assert c._lib.attends == [(7, ws.data_ptr(), 1024)]
+
+
+def test_kept_workspaces_stay_a_small_multiple_of_what_is_needed():
+    """Captured graphs may hold a workspace's address, so none is given back: a batch that grows stream by stream must
+    not leave one behind for every size."""
+    c = bare()
+    c._lib, c._state_ptr, c._current_stream = FakeLibrary(), 16, lambda index: 7
+    c.attend_bytes = lambda S, B, H: 1000 + 100 * S
+    for S in range(1, 101):
+        c.attend(0, rows(S, 1))
+    need = c.attend_bytes(100, 1, 2)
+    assert all(n >= c.attend_bytes(S + 1, 1, 2) and ws % 256 == 0 for S, (_, ws, n) in enumerate(c._lib.attends))
+    assert sum(ws.numel() for ws in c._ws_kept) <= 4 * need
+    held = {ws.data_ptr() for ws in c._ws_kept}
+    assert {ws for _, ws, _ in c._lib.attends} <= held
