@@ -537,7 +537,7 @@ class KvCache:
                 raise ValueError("the pools of a cache have one shape, type, device and page stride")
         if pages > 1 and k0.stride(0) < heads * tokens * dim:
             raise ValueError("the pages of a pool do not share memory")
-        self._keep = layers
+        self._keep = [tuple(kv) for kv in layers]
         self.device, self.dtype = k0.device, k0.dtype      # (a tensor's device has its index)
         self.num_layers, self.num_streams, self.max_pages = len(layers), num_streams, max_pages
         self.num_pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, tokens, dim

@@ -1,5 +1,7 @@
 """The binding of the paged cache without a GPU: tensors on the CPU, in a cache that has no handle."""
 import contextlib
+import gc
+import weakref
 
 import pytest
 import torch
@@ -135,3 +137,18 @@ def test_kept_workspaces_stay_a_small_multiple_of_what_is_needed():
     assert sum(ws.numel() for ws in c._ws_kept) <= 4 * need
     held = {ws.data_ptr() for ws in c._ws_kept}
     assert {ws for _, ws, _ in c._lib.attends} <= held
+
+
+def test_pools_stay_alive_whatever_becomes_of_the_list(monkeypatch):
+    monkeypatch.setattr(pkg, "moe_mxfp4_cache_create", lambda cfg, layers: (0, 1))
+    monkeypatch.setattr(pkg, "moe_mxfp4_cache_state_bytes", lambda cache: (0, 4096))
+    monkeypatch.setattr(pkg, "moe_mxfp4_cache_destroy", lambda cache: None)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    layers = [[OnGpu(torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)) for _ in range(2)] for _ in range(2)]
+    refs = [weakref.ref(t) for kv in layers for t in kv]
+    c = pkg.KvCache(layers=layers, num_streams=2, max_pages=3)
+    layers[1].pop()
+    layers.clear()
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    c.close()
