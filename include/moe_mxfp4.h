@@ -458,7 +458,7 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
  * directly or not); a stream with other pages there, or with fewer tokens, reads its own.
  * Arithmetic: products of q and k are exact and summed in fp32, as are the statistics of
  * the softmax; its terms are rounded to the cache's type for their product with v, which
- * is summed in fp32.
+ * is summed in fp32 (fp16: half a step, for terms below 2^-26 of the row's largest 2^-37 of it).
  * out and lse overlap no input.
  * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents.
  * MOE_ERR_UNSUPPORTED when the rows and the keys that max_pages allows make 2^31 tiles or

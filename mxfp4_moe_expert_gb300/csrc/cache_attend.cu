@@ -22,8 +22,8 @@
 // tiles (TMA boxes of one head's page) into the ring.  MMA warp: S = Q K^T from shared memory into
 // tensor memory, O += P V with P, in 16 bits, from tensor memory over the columns of S.  Softmax
 // warpgroup: a thread per row.  The reference of the exponentials follows the running maximum only
-// when that passes it by 2^8 (P stays below 2^8 in any type, sums are fp32), so the accumulator is
-// rescaled rarely, by the softmax warps themselves.
+// when that passes it by some exponents (kRescale; P stays below 2^8 in bf16 and 2^15 in fp16, sums
+// are fp32), so the accumulator is rescaled rarely, by the softmax warps themselves.
 //
 // What bounds it, on 152 SMs.  Reading keys where there are few rows: 96 streams that decode one
 // position over 700..6000 keys (1.32 GB) take 200 us, 6.6 TB/s, 0.97 of the copy rate.  The tensor
@@ -46,7 +46,15 @@ constexpr int kKeyTile = 128;
 constexpr int kAttThreads = 384;               // softmax warps 0-3 (slot 0), 4-7 (slot 1), producers, MMA
 constexpr int kAttProducer = 8, kAttMma = 10;  // + slot
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // columns: S of slot x at 128 x, O at 256 + 128 x
-constexpr float kRescale = 8.0f;               // exponents that the maximum may pass the reference by
+// The reference of a row's exponentials is this many exponents below its maximum when it was set
+// (att_below), and follows when the maximum passes that by kRescale.  bf16 terms have fp32's range.
+// An fp16 term is exact to half a step down to 2^-14 and at most 2^-25 off below: with terms of up to
+// 2^15 that is 2^-26 and 2^-37 of the maximum, so that a tail of many small terms keeps its weight
+// (with a reference at the maximum, 65536 terms of 2^-26 of it were lost, 0.07 % of the sum).
+// Exponents beyond 2^22 have steps of half and more, and terms no room for them below fp16's largest.
+template <bool kBf16>
+__device__ __forceinline__ float att_below(float m) { return !kBf16 && fabsf(m) < 0x1p22f ? 12.0f : 0.0f; }
+template <bool kBf16> constexpr float kRescale = kBf16 ? 8.0f : 3.0f;
 // A segment costs about this many tiles more than its tiles (its queries, its start, its rows' way
 // out); dealt out with them.  3 for narrow ones rather than 2: 96 streams decode in 205.7 us
 // instead of 209.0, other cases do not change.
@@ -865,9 +873,9 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
                         mx[(e / 2) & 3] = max3(mx[(e / 2) & 3], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
                 }
                 const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.c;
-                const bool passed = m != -INFINITY && top > m + kRescale;
+                const bool passed = m != -INFINITY && top > m + (att_below<kBf16>(m) + kRescale<kBf16>);
                 if (__any_sync(0xFFFFFFFFu, passed)) {
-                    const float f = passed ? exp2_approx(m - top) : 1.0f;
+                    const float f = passed ? exp2_approx(m - (top - att_below<kBf16>(top))) : 1.0f;
                     l *= f;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
@@ -879,7 +887,7 @@ __device__ void att_softmax(const CacheView& c, const AttendParams& p, int share
                         tc_st_x16(to + 16 * k, o);
                     }
                 }
-                if (passed || m == -INFINITY) m = top;
+                if (passed || m == -INFINITY) m = top - att_below<kBf16>(top);
                 const float ref = m == -INFINITY ? 0.0f : m;
                 float sum[4][2] = {};
 #pragma unroll

@@ -380,6 +380,65 @@ def test_extreme_scores():
     c.check(*c.attend(scale=1.0), scale=1.0)
 
 
+@pytest.mark.parametrize("together", [False, True])
+@pytest.mark.parametrize("k0,bits", [(-2.875, 16), (-4.59375, 26), (-5.0, 28)])
+def test_long_tails_of_small_terms(k0, bits, together):
+    """fp16: one key at the top and 65535 whose terms are 2^-16 .. 2^-28 of its own, in parts of some hundred tiles; the
+    values of all but the first are one, so that the output is the tail's weight.  Terms and output are rounded to the
+    type (2^-11 relative each); a term has no more than 2^-37 of the largest as its own last half step."""
+    S, n, Hkv, D, page = 40, 65536, 8, 64, 128
+    mem = torch.zeros((2, n // page + S, Hkv, page, D), dtype=torch.float16, device="cuda")
+    cache = pkg.KvCache(layers=[(mem[0], mem[1])], num_streams=S, max_pages=n // page + 1)
+    b = Books(S, n // page + 1, n // page + S, page)
+    for s in range(S):                               # all hold the same pages, and one more for the block
+        b.table[s] = list(range(n // page)) + [n // page + s]
+        b.held[s], b.length[s] = n // page + 1, n - 1
+    write_books(cache, b)
+    mem[0, :, :, :, 0] = k0
+    mem[0, 0, :, 0] = 0
+    mem[1] = 1
+    mem[1, 0, :, 0] = 0
+    q = torch.zeros((S, 4, Hkv, D), dtype=torch.float16, device="cuda")
+    q[..., 0] = 4
+    out, lse = cache.attend(0, q, shared_stream=0, shared_tokens=(n - page) if together else 0, scale=1.0)
+    cache.check()
+    term = math.exp(4 * k0)
+    assert 2 ** -(bits + 1) < term < 2 ** -bits
+    for i in range(4):
+        tail = (n - 1 + i) * term
+        want, u = tail / (1 + tail), 2.0 ** -11
+        tol = 2.02 * u * want + (n + 3) * 2.0 ** -37 + 2.0 ** -25
+        assert (out[:, i].double() - want).abs().max() <= tol, (want, float(out[:, i].min()), float(out[:, i].max()))
+        # a sum in 32 bits of up to 512 tiles, each addition off by half a step of the sum: 512 * 2^-24; and the rest
+        assert (lse[:, i].double() - math.log1p(tail)).abs().max() <= 2.0 ** -15 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("size", [1024, 1400, 2048, 4096, 8192])
+def test_fp16_scores_in_the_millions(size):
+    """Equal scores of 2^20 to 2^26, and their negatives: all terms are equal, and finite, however coarse the steps of
+    the exponents are."""
+    c = Case([500, 0, 129], 3, 4, 2, D=64, dtype=torch.float16, seed=24)
+    c.k.fill_(0)
+    c.k[..., 0] = size * 1.28125
+    c.q.fill_(0)
+    c.q[..., 0] = size
+    c.q[2] *= -1
+    out, lse = c.attend(scale=1.0)
+    assert out.isfinite().all()
+    x = size * c.k[0, 0, 0, 0].double() * torch.tensor([1.0, 1.0, -1.0], device="cuda")
+    assert ((lse - x[:, None, None]).abs() <= x[0] * 2.0 ** -20 + 8).all()
+    for s in range(3):
+        n = c.books.length[s] + 3
+        v = gather(c.v, c.books.table[s], c.books.held[s], c.page).double()[:, :n]
+        # Weights of parts that are merged carry the steps of their lse, of half and more here, so a row is held to its
+        # values' range; a row of one part has equal weights.  Its terms are rounded alike (2^-11), and the output (2^-11).
+        slack = 2.0 ** -9 * v.abs().max()
+        got = out[s, 2].double().view(2, 2, c.D)
+        assert (got <= v.amax(1)[:, None] + slack).all() and (got >= v.amin(1)[:, None] - slack).all()
+        if n <= 128:
+            assert (got - v.mean(1)[:, None]).abs().max() <= slack
+
+
 @pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16)])
 def test_the_maximum_climbs_along_a_shared_prefix(D, dtype):
     """Scores that grow by some tens along the prefix for half of the rows and fall for the others, in units that fill
