@@ -1277,11 +1277,11 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     p.U = L.U;
     p.U_sh = p.wide_sh ? L.U_wide : (int)((rows + 127) / 128);
     p.R_own = L.R_own;
-    // a negative scale turns the queries' signs; a scale of zero is one below any score's last bit,
-    // which keeps hidden keys (-inf) hidden
+    // a negative scale turns the queries' signs; a scale of zero is the smallest above it, which keeps
+    // hidden keys (-inf) hidden and takes the largest score (2^128) to 2^-21
     const float s = a.scale < 0.0f ? -a.scale : a.scale;
     p.c = s * 1.44269504088896341f;
-    if (p.c < 0x1p-100f) p.c = 0x1p-100f;
+    if (p.c < 0x1p-149f) p.c = 0x1p-149f;
     p.q_flip = a.scale < 0.0f ? 0x80008000u : 0u;
     p.timeout_ns = (unsigned long long)c->cfg.timeout_us * 1000ull;
     p.head = reinterpret_cast<moe::JobList*>(ws);

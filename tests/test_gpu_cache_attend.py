@@ -439,6 +439,14 @@ def test_fp16_scores_in_the_millions(size):
             assert (got - v.mean(1)[:, None]).abs().max() <= slack
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -1e-38, 1e-36])
+def test_tiny_scales_of_huge_scores(scale):
+    c = Case([700, 129, 0], 4, 4, 2, seed=23)
+    c.q *= 2.0 ** 54
+    c.k *= 2.0 ** 54
+    c.check(*c.attend(scale=scale), scale=scale)
+
+
 @pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16)])
 def test_the_maximum_climbs_along_a_shared_prefix(D, dtype):
     """Scores that grow by some tens along the prefix for half of the rows and fall for the others, in units that fill
