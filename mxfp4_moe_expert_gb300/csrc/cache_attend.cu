@@ -28,7 +28,7 @@
 // What bounds it, on 152 SMs.  Reading keys where there are few rows: 96 streams that decode one
 // position over 700..6000 keys (1.32 GB) take 200 us, 6.6 TB/s, 0.97 of the copy rate.  The tensor
 // core's chain where a long prefix is shared: 64 streams x 8 positions x 64 heads behind 32768 keys
-// (0.57 PFLOP) take 431 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
+// (0.57 TFLOP) take 431 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
 // keys) takes about 2950 cycles for 2048 of products: scores -> softmax (1500) -> P V and the next
 // scores (1024) follow one another in each slot, and shared memory is read at its full 128 bytes a
 // cycle while Q K^T runs.  The launches, the schedule and the merge where there is little work: one
