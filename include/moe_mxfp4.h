@@ -363,7 +363,8 @@ int moe_mxfp4_accept(const float* logits_dev, const int32_t* tokens_dev, int32_t
  * alone.  What a call finds wrong on the device (too few free pages, a table entry
  * outside the pool) is recorded in the status words (the first error is kept until
  * moe_mxfp4_cache_check) and nothing outside the pools and the state is touched.  Results
- * do not depend on the timing of threads: two runs of the same calls give the same bits.
+ * do not depend on the timing of threads: two runs of the same calls give the same bits (but
+ * where several streams of a call are at fault, its detail may name any of them).
  * A cache may be used by one stream at a time, captured graphs included; calls of
  * moe_mxfp4_cache_attend, which only read it, may overlap one another when they have
  * workspaces of their own.  Calls run on the handle's device, whichever device is current.  No call
@@ -427,7 +428,8 @@ int moe_mxfp4_cache_append(moe_mxfp4_cache* c, void* state_dev, int32_t layer, c
 /* Sets length[s] to new_length[s] (int32 [S]; negative: the stream is left alone) and
  * gives back the pages behind it.  A length beyond the pages held is refused for that
  * stream, with MOE_ERR_CACHE_STATE.  commit is the same with length[s] + accepted[s]
- * (moe_mxfp4_accept's output; 0 drops the whole block, negative: left alone). */
+ * (moe_mxfp4_accept's output for the streams of the batch, and a value for every other slot of
+ * the cache; 0 drops the whole block, negative: left alone). */
 int moe_mxfp4_cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t* new_length_dev, void* stream);
 int moe_mxfp4_cache_commit(moe_mxfp4_cache* c, void* state_dev, const int32_t* accepted_dev, void* stream);
 
@@ -459,7 +461,7 @@ int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
  * Arithmetic: products of q and k are exact and summed in fp32, as are the statistics of
  * the softmax; its terms are rounded to the cache's type for their product with v, which
  * is summed in fp32 (fp16: half a step, for terms below 2^-26 of the row's largest 2^-37 of it).
- * out and lse overlap no input.
+ * out and lse overlap no input.  After MOE_ERR_TIMEOUT the call's out and lse hold no results.
  * workspace_dev: 256-byte aligned, moe_mxfp4_cache_attend_bytes long, any contents.
  * MOE_ERR_UNSUPPORTED when the rows and the keys that max_pages allows make 2^31 tiles or
  * more (256 rows x 128 keys). */

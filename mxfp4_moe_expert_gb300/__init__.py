@@ -581,7 +581,9 @@ class KvCache:
             _check(st, "moe_mxfp4_cache_reserve")
 
     def commit(self, accepted, stream=None):
-        """length += accepted (int32 [num_streams]; accept()'s output); the pages behind are given back."""
+        """length += accepted (int32 [num_streams]); the pages behind are given back.  accept()'s output has a value for
+        each stream of the batch: slots that are not in it need one too (0: what was reserved there is given back,
+        negative: left alone)."""
         _check(self._lib.moe_mxfp4_cache_commit(self.handle, self._state_ptr,
                                                 self._books("accepted", accepted, self.num_streams), self._stream(stream)),
                "moe_mxfp4_cache_commit")

@@ -9,6 +9,8 @@ import torch
 
 import mxfp4_moe_expert_gb300 as pkg
 from cache_util import Books, assert_attention, ceil_div, gather, write_books
+from mxfp4_moe_expert_gb300.synth import Workload
+from mxfp4_moe_expert_gb300.workload import device_layers
 
 pytestmark = pytest.mark.gpu
 
@@ -627,6 +629,59 @@ def test_a_verify_forward_from_reserve_to_commit():
         n = allk[s].shape[0]
         assert c.length[s].item() == n
         assert torch.equal(gather(mem[1, 0], c.page_table[s].tolist(), c.held[s].item(), page)[:, :n], allk[s].transpose(0, 1))
+
+
+def test_the_loop_around_a_moe_layer_eager_and_captured():
+    """A whole step (reserve, append, attend, the MoE layer, accept, commit) with one slot for each stream of the batch,
+    whose prefix the first one holds: three steps one by one, and as replays of one graph, with the same bits."""
+    torch.manual_seed(3)
+    S, B, Hq, Hkv, D, page, V = 4, 4, 8, 2, 64, 16, 64
+    wl = Workload("loop", T=S * B, H=512, I=512, E=8, k=2, seed=0x5EED0400)
+    _, layers = device_layers(wl)
+    moe = pkg.MoeLayers(hidden=wl.H, inter=wl.I, num_experts=wl.E, top_k=wl.k, max_tokens=wl.T, layers=layers)
+    wq, wk, wv = (0.1 * torch.randn((wl.H, n * D), device="cuda").bfloat16() for n in (Hq, Hkv, Hkv))
+    wo, head = 0.1 * torch.randn((Hq * D, wl.H), device="cuda").bfloat16(), torch.randn((wl.H, V), device="cuda")
+    prompt = torch.randn((1, 40, wl.H), device="cuda").bfloat16()
+    xs = torch.randn((3, S, B, wl.H), device="cuda").bfloat16()
+    tokens = torch.randint(0, 3, (3, S, B), device="cuda").int()       # (few drafts are right)
+
+    def begin():
+        mem = torch.zeros((1, 2, 60, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+        c = pkg.KvCache(layers=[(mem[0, 0], mem[0, 1])], num_streams=S, max_pages=12)
+        c.reserve(i32([40] + [0] * (S - 1)))
+        c.append(0, (prompt @ wk).view(1, 40, Hkv, D), (prompt @ wv).view(1, 40, Hkv, D))
+        c.commit(i32([40] + [0] * (S - 1)))
+        c.fork(i32([0] * (S - 1)), i32(list(range(1, S))))
+        return mem, c
+
+    def step(c, x, drafts):
+        c.reserve(B)
+        c.append(0, (x @ wk).view(S, B, Hkv, D), (x @ wv).view(S, B, Hkv, D))
+        out, lse = c.attend(0, (x @ wq).view(S, B, Hq, D), shared_stream=0, shared_tokens=32)
+        h = x + (out.view(S, B, Hq * D) @ wo)
+        logits = (h.float() + moe.forward(h.view(S * B, wl.H)).view(S, B, wl.H)) @ head
+        target, accepted, next_token = pkg.accept(logits, drafts)
+        c.commit(accepted)
+        return out, lse, logits, target, accepted
+
+    mem, c = begin()
+    want = [[t.clone() for t in step(c, x, d)] + [c.length.clone()] for x, d in zip(xs, tokens)]
+    c.check()
+    assert c.length.tolist() == [40 + sum(int(w[4][s]) for w in want) for s in range(S)]
+    mem2, c2 = begin()
+    x, d, side, g = xs[0].clone(), tokens[0].clone(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    step(begin()[1], x, d)                            # workspaces and libraries are set up outside the capture
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        got = step(c2, x, d)
+    for i in range(3):
+        x.copy_(xs[i])
+        d.copy_(tokens[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([*got, c2.length], want[i])), i
+    c2.check()
+    assert torch.equal(mem, mem2)
 
 
 def test_refusals():
