@@ -28,7 +28,7 @@
 // What bounds it, on 152 SMs.  Reading keys where there are few rows: 96 streams that decode one
 // position over 700..6000 keys (1.32 GB) take 200 us, 6.6 TB/s, 0.97 of the copy rate.  The tensor
 // core's chain where a long prefix is shared: 64 streams x 8 positions x 64 heads behind 32768 keys
-// (0.57 TFLOP) take 431 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
+// (0.57 TFLOP) take 430 us, 1.32 PFLOP/s, 0.68 of the cuBLAS rate.  A wide tile (256 rows x 128
 // keys) takes about 2950 cycles for 2048 of products: scores -> softmax (1500) -> P V and the next
 // scores (1024) follow one another in each slot, and shared memory is read at its full 128 bytes a
 // cycle while Q K^T runs.  The launches, the schedule and the merge where there is little work: one
@@ -1270,7 +1270,7 @@ extern "C" int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32
     // The shared prefix in wide units where that makes 20 tiles or more for every CTA: a wide tile
     // costs less than two narrow ones (64 streams behind 32768 keys, 216 tiles: 395 us against 499;
     // 32 behind 8192, 24 tiles: 82.3 against 84.8), but few of them leave slots without work (16
-    // behind 8192, 13 tiles: 54.1 against 48.6; 4, 3 tiles: 32.0 against 24.8).
+    // behind 8192, 13 tiles: 54.1 against 48.6; 4, 3 tiles: 32.0 against 24.8; all with 8 heads of 128).
     const int64_t rows = (int64_t)a.streams * a.block * L.G;
     p.wide_sh = rows > 128 && (int64_t)c->cfg.kv_heads * L.U_wide * (a.shared_tokens / moe::kKeyTile) >= 20 * (int64_t)c->sm_count;
     p.wide_own = L.wide_own;
