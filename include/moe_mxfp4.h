@@ -387,7 +387,8 @@ typedef struct {
     int64_t page_stride;  /* elements between pages of a pool, a multiple of 8, at least
                            * kv_heads * page_tokens * head_dim; 0 = exactly that */
     int32_t timeout_us;   /* bound of every device-side wait in microseconds, and 10 more for each tile of
-                           * keys that the wait stands for; 0 = default (200000) */
+                           * keys that the wait stands for; 0 = default (200000).  Copies and products under
+                           * way end by themselves and are waited for in any case (for 2 s at most) */
 } moe_mxfp4_cache_config;
 
 typedef struct {

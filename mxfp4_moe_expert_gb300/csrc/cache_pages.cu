@@ -190,7 +190,7 @@ constexpr int kPiece = 4096;      // bytes a warp copies at a time: 8 independen
 // move_src[m] -> move_dst[m] in every pool of the list, the first move_used[m] tokens of
 // every head (a warp takes pieces of one head's page); with `remap`, the tables after a
 // compact too: entries at U or above have moved.  Bound by HBM: it reads and writes each
-// byte once (2.24 GB of a compact in 343 to 365 us from box to box, with its plan and two copies of
+// byte once (2.24 GB of a compact in 343 to 365 us from GPU to GPU, with its plan and two copies of
 // books: 6.2 to 6.5 TB/s, 0.91 to 0.97 of the copy rate).  Where these took 343, 2 KB pieces took
 // 372, 8 KB ones and fewer CTAs the same.
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, const __grid_constant__ PoolList pools, int n_pools, int remap) {

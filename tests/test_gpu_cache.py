@@ -239,6 +239,21 @@ def test_compact_of_an_empty_a_full_and_a_packed_pool():
     assert torch.equal(mem.cpu(), b.pool) and status(c) == pkg.MOE_OK
 
 
+def test_a_pool_of_one_page():
+    c, mem, b = make(L=1, S=2, M=1, P=1, page=16)
+    for call in (lambda x, a: x.reserve(a([0, 16])), lambda x, a: x.truncate(a([-1, 7])), lambda x, a: x.compact(),
+                 lambda x, a: x.fork(a([1]), a([0])), lambda x, a: x.truncate(a([-1, 0])), lambda x, a: x.reserve(a([9, 0])),
+                 lambda x, a: x.compact(), lambda x, a: x.truncate(a([0, 0])), lambda x, a: x.compact()):
+        call(c, i32)
+        call(b, lambda x: x)
+        assert status(c) == pkg.MOE_OK
+        assert_books(c, b)
+    c.reserve(1)                                   # two pages wanted, one there
+    assert status(c) == pkg.MOE_ERR_CACHE_FULL
+    assert_books(c, b)
+    assert torch.equal(mem.cpu(), b.pool)
+
+
 def test_more_pools_than_one_launch_copies():
     """130 layers: the copies go out in two launches."""
     c, mem, b = make(L=130, S=3, M=2, P=5, page=16, Hkv=1, D=64)

@@ -131,6 +131,27 @@ def test_many_tiles_for_every_cta(S, Hq, D, prefix, hi):
     assert torch.equal(again, out) and torch.equal(again_lse, lse)
 
 
+@pytest.mark.parametrize("prefix,B,Hq,Hkv", [(0, 3, 4, 2), (48, 3, 4, 2), (48, 20, 16, 1)])
+def test_more_units_than_one_pass_of_the_schedule(prefix, B, Hq, Hkv):
+    """900 streams, narrow and wide units, some of them without rows; streams of the first, the second and the third
+    pass, and all rows twice."""
+    S = 900
+    c = Case([prefix + (53 * s) % 200 for s in range(S)], B, Hq, Hkv, D=64, page=16, prefix=prefix, alone=(7, 500), seed=25)
+    used = [(s * 7) % (B + 1) for s in range(S)]
+    out, lse = c.attend(lengths=i32(used))
+    c.check(out, lse, used=used, streams=[0, 7, 8, 383, 384, 385, 500, 767, 768, 769, 898, 899])
+    again, again_lse = c.attend(lengths=i32(used))
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    alone, alse = c.attend(lengths=i32(used), shared_tokens=0)
+    seen = lse.isfinite()
+    assert torch.equal(seen, alse.isfinite()) and (lse[seen] - alse[seen]).abs().max() <= 2e-5
+
+
+def test_as_many_kv_heads_as_there_may_be():
+    c = Case([0, 65, 300], 2, 512, 256, D=64, page=16, seed=26)
+    c.check(*c.attend())
+
+
 @pytest.mark.parametrize("B,Hq,Hkv,prefix", [(1, 256, 1, 0), (3, 255, 1, 256), (2, 512, 2, 128), (1, 129, 1, 64)])
 def test_many_heads_on_one(B, Hq, Hkv, prefix):
     c = Case([prefix + n for n in (0, 1, 130, 500)], B, Hq, Hkv, prefix=prefix, seed=Hq)
