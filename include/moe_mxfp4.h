@@ -372,6 +372,7 @@ int moe_mxfp4_accept(const float* logits_dev, const int32_t* tokens_dev, int32_t
 
 #define MOE_DTYPE_BF16 0
 #define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2  /* logits only */
 
 typedef struct moe_mxfp4_cache moe_mxfp4_cache; /* opaque, host-side */
 
@@ -446,6 +447,25 @@ int moe_mxfp4_cache_fork(moe_mxfp4_cache* c, void* state_dev, const int32_t* src
  * pages in use are 0..U-1.  At most one copy of each page. */
 int moe_mxfp4_cache_compact(moe_mxfp4_cache* c, void* state_dev, void* stream);
 
+/* The same for drafted trees: the accepted nodes of a block (moe_mxfp4_accept_edited's path, ascending
+ * block positions) are moved together before the lengths grow.  For i < n = accepted[s] of stream
+ * s < streams, the keys and values at position length[s] + path[s, i] go to position length[s] + i, in
+ * every layer, and, with history_dev, history[s, length[s] + i] = tokens[s, path[s, i]]; then length[s]
+ * += n and the pages behind are given back, as in moe_mxfp4_cache_commit (streams >= `streams` have a
+ * value in accepted too, and no path).  path_dev NULL: path[s, i] = i.  A stream whose path does not
+ * ascend within the block, with n > block, with positions that are not reserved or whose pages other
+ * streams hold too, or that would pass history_stride is left alone, with MOE_ERR_CACHE_STATE (detail:
+ * the stream). */
+typedef struct {
+    const int32_t* accepted_dev;  /* [num_streams]; negative: the stream is left alone */
+    const int32_t* path_dev;      /* [streams, block] or NULL */
+    const int32_t* tokens_dev;    /* [streams, block]; read with history_dev */
+    int32_t* history_dev;         /* [streams, history_stride] or NULL */
+    int64_t history_stride;       /* tokens between the histories of two streams */
+    int32_t streams, block;       /* streams <= num_streams; block >= 1 where streams > 0 */
+} moe_mxfp4_commit_args;
+int moe_mxfp4_cache_commit_path(moe_mxfp4_cache* c, void* state_dev, const moe_mxfp4_commit_args* args, void* stream);
+
 /* Attention of a block, one layer.  Query row (s, b, h) of stream s < streams, position
  * b < n_s (as in append; the block's keys were appended, length is not yet committed),
  * head h reads kv head h / (q_heads / kv_heads) and sees the key at position j
@@ -487,6 +507,146 @@ int moe_mxfp4_cache_attend(moe_mxfp4_cache* c, void* state_dev, int32_t layer, c
 /* Synchronises the stream, returns the first error recorded in the status words since
  * they were last read (MOE_OK: none) and clears it. */
 int moe_mxfp4_cache_check(moe_mxfp4_cache* c, void* state_dev, void* stream);
+
+/* ---- norms and rotation of queries and keys -------------------------------------------
+ * Each head x [head_dim] of a query or key at position p:
+ *   x <- x * w / sqrt(mean(x^2) + eps)             with MOE_ROTARY_NORM (w NULL: ones)
+ *   (a, b) <- gain * (a cos - b sin, a sin + b cos), angle = p * f_i, for the pairs i < rotary_dim / 2:
+ *     (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1]) with MOE_ROTARY_INTERLEAVED;
+ *     elements rotary_dim and behind do not turn (and have no gain).
+ * Arithmetic: fp32, rounded once.  turns_dev[i] is f_i as a fraction of a turn per position, in units of
+ * 2^-64: position times it, modulo 2^64, is the angle's exact fraction of a turn, so far positions turn
+ * as exactly as near ones (the frequency's own rounding apart, 2^-65 of a turn a position). */
+
+#define MOE_ROTARY_INTERLEAVED (1u << 0) /* pairs side by side */
+#define MOE_ROTARY_NORM        (1u << 1) /* norms of each head before the rotation */
+
+typedef struct {
+    const uint64_t* turns_dev;  /* [rotary_dim / 2], 8-byte aligned; may be NULL when rotary_dim is 0 */
+    const void* q_norm_dev;     /* [head_dim] of dtype, 16-byte aligned, or NULL = ones; read with MOE_ROTARY_NORM */
+    const void* k_norm_dev;
+    int32_t head_dim;           /* 64 or 128 */
+    int32_t rotary_dim;         /* even, 0..head_dim */
+    int32_t dtype;              /* MOE_DTYPE_BF16 or MOE_DTYPE_FP16: of heads and weights */
+    uint32_t flags;             /* MOE_ROTARY_* */
+    float eps;                  /* >= 0 */
+    float gain;                 /* 1: a plain rotation */
+} moe_mxfp4_rotary;
+
+/* Frequencies of the common position encodings, as turns (host memory, rotary_dim / 2 values, to be
+ * copied to the device): f_i = base^(-2 i / rotary_dim), changed for contexts longer than the trained ones:
+ *   MOE_ROTARY_NONE    not at all
+ *   MOE_ROTARY_LINEAR  f_i / factor
+ *   MOE_ROTARY_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in base's place (rotary_dim > 2)
+ *   MOE_ROTARY_PARTS   g f_i + (1 - g) f_i / factor, g = clamp((original f_i / 2 pi - low) / (high - low), 0, 1):
+ *                      pairs that turn at least `high` times in the original length keep their frequency
+ * moe_mxfp4_rotary_from does the same from a caller's own f_i in radians per position (n host doubles;
+ * |f_i| <= 2 pi).  MOE_ERR_INVALID_ARG for a NULL pointer, an odd or negative size, base or factor not
+ * positive and finite, original not positive, high <= low (PARTS), or a frequency that is not finite. */
+#define MOE_ROTARY_NONE   0
+#define MOE_ROTARY_LINEAR 1
+#define MOE_ROTARY_NTK    2
+#define MOE_ROTARY_PARTS  3
+typedef struct {
+    int32_t kind;
+    double factor, original, low, high;  /* read where the kind has them */
+} moe_mxfp4_rotary_scaling;
+int moe_mxfp4_rotary_turns(int32_t rotary_dim, double base, const moe_mxfp4_rotary_scaling* scaling, uint64_t* turns);
+int moe_mxfp4_rotary_from(const double* frequencies, int32_t n, uint64_t* turns);
+
+/* Queries and keys of `tokens` rows, each at positions[t].  Heads of a row are contiguous, rows `stride`
+ * elements apart (a multiple of 8; 0 = heads * head_dim); all 16-byte aligned.  An output is its input,
+ * with the same stride (in place), or overlaps no input.  k_dev and k_out_dev may be NULL with
+ * kv_heads = 0, and q_dev with q_heads = 0.  Runs on the current device. */
+typedef struct {
+    const void* q_dev;             /* [tokens, q_heads, head_dim] */
+    const void* k_dev;             /* [tokens, kv_heads, head_dim] */
+    void* q_out_dev;
+    void* k_out_dev;
+    const int32_t* positions_dev;  /* [tokens]; any value, negative ones among them */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int32_t tokens;                /* >= 0 */
+    int32_t q_heads, kv_heads;     /* 0..65536 each */
+} moe_mxfp4_rotate_args;
+int moe_mxfp4_rotate(const moe_mxfp4_rotary* r, const moe_mxfp4_rotate_args* args, void* stream);
+
+/* moe_mxfp4_cache_append for keys that are normed and rotated on the way, with the block's queries: q goes to
+ * q_out (contiguous), k and v into the pages.  Block position b of stream s is at position
+ *   length[s] + b, or, with mask_dev (a tree of drafts, as in moe_mxfp4_cache_attend; block <= 64),
+ *   length[s] + the number of block positions before b that it sees.
+ * Tokens that `lengths` leaves out are skipped, their q_out left as it was.  What append refuses is
+ * refused here, and skipped in the pages alone: the queries do not depend on them.  r's head_dim and
+ * dtype are the cache's.  q_heads may be 0 (q_dev and q_out_dev NULL): keys and values alone. */
+typedef struct {
+    const void* q_dev;           /* [streams, block, q_heads, head_dim], q_stride elements between tokens */
+    const void* k_dev;           /* [streams, block, kv_heads, head_dim], row_stride elements between tokens */
+    const void* v_dev;
+    void* q_out_dev;             /* [streams, block, q_heads, head_dim], contiguous; q_dev itself, where that is
+                                  * contiguous, or memory that overlaps no input; all 16-byte aligned */
+    int64_t q_stride, row_stride; /* multiples of 8; 0 = contiguous */
+    const int32_t* lengths_dev;  /* [streams] or NULL */
+    const uint64_t* mask_dev;    /* [streams, block] or NULL */
+    int32_t streams, block;      /* streams <= num_streams; streams * block below 2^31 */
+    int32_t q_heads;             /* 0..65536 */
+} moe_mxfp4_append_args;
+int moe_mxfp4_cache_append_rotated(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const moe_mxfp4_rotary* r,
+                                   const moe_mxfp4_append_args* args, void* stream);
+
+/* ---- edits of the logits, and acceptance with them --------------------------------------
+ * The logits of a verify block, changed by what each stream has said so far, its biases and its grammar.
+ * Position b of stream s stands behind history[s, 0 .. history_lengths[s]) and the block's own tokens that
+ * it sees: those of positions 0..b, or, with mask_dev, of the positions before b that bit i of mask[s, b]
+ * names and its own (the cache's history: position 0 holds the last committed token, which is not stored
+ * yet).  The first prompt_lengths[s] of the history are the prompt.  With c the count of token v in the
+ * rest of the history and the tokens seen of the block,
+ *   z <- z > 0 ? z / repetition[s] : z * repetition[s]   where c > 0 or the prompt has v
+ *   z <- z - frequency[s] * c - presence[s] * [c > 0]
+ *   z <- z + the bias of v                               (of a token given twice, the last one counts)
+ *   z <- -inf                                            where bit v of allowed[s, b] is 0
+ * in fp32.  Tokens outside [0, vocab) (padding) count nowhere.  Positions lengths[s] and behind are not
+ * read, and left as they were in the output. */
+typedef struct {
+    const void* logits_dev;               /* [streams, block, vocab], row_stride elements between positions */
+    int64_t row_stride;                   /* 0 = vocab; at least vocab */
+    int32_t dtype;                        /* MOE_DTYPE_*: of the logits, which are aligned to it */
+    int32_t streams, block;               /* block 1..1024, at most 64 with mask_dev; streams * block below 2^31 */
+    int64_t vocab;                        /* 1..2^31 - 1 */
+    const int32_t* tokens_dev;            /* [streams, block] or NULL: the block's tokens count nowhere */
+    const uint64_t* mask_dev;             /* [streams, block] or NULL */
+    const int32_t* lengths_dev;           /* [streams] or NULL: all of the block */
+    const int32_t* history_dev;           /* [streams, history_stride] or NULL */
+    int64_t history_stride;               /* tokens between the histories of two streams */
+    int64_t history_room;                 /* tokens of each that may be read, 0..history_stride: longer lengths are cut */
+    const int32_t* history_lengths_dev;   /* [streams], with history_dev */
+    const int32_t* prompt_lengths_dev;    /* [streams] or NULL: no prompt */
+    const float* repetition_dev;          /* [streams], above 0, or NULL = 1 */
+    const float* frequency_dev;           /* [streams] or NULL = 0 */
+    const float* presence_dev;            /* [streams] or NULL = 0 */
+    const int32_t* bias_begin_dev;        /* [streams + 1]: stream s has entries begin[s] .. begin[s + 1], or NULL */
+    const int32_t* bias_ids_dev;          /* tokens, ... */
+    const float* bias_dev;                /* ... and what is added to their logits */
+    int64_t bias_entries;                 /* entries in all, 0..2^31 - 1: what bias_begin names beyond them is not read */
+    const uint32_t* allowed_dev;          /* [streams, block, allowed_stride] or NULL: bit v % 32 of word v / 32 */
+    int64_t allowed_stride;               /* words between positions; 0 = (vocab + 31) / 32 */
+} moe_mxfp4_edit_args;
+
+/* Writes the edited logits to out_dev (out_stride elements between positions, 0 = vocab): the logits themselves,
+ * with the same stride (in place), or memory that overlaps no input.  Runs on the current device. */
+int moe_mxfp4_edit_logits(const moe_mxfp4_edit_args* args, void* out_dev, int64_t out_stride, void* stream);
+
+/* moe_mxfp4_accept on the edited logits, without writing them, for chains and trees of drafts (tokens_dev is
+ * required):
+ *   target[s, b]  = the token with the largest edited logit (lowest index among equal ones; NaN ranks as -inf)
+ *                   of those the grammar allows; -1 where it allows none, and for positions lengths[s] and behind
+ *   parent(b)     = b - 1, or, with mask_dev, the last position before b that b sees (none: b is never accepted)
+ *   path          = 0, then of each node the first child whose token is the node's target, as far as that goes
+ *   accepted[s]   = nodes on the path; next_token[s] = target[s, last node]
+ * path_dev [streams, block] (-1 behind the path) and next_token_dev may be NULL.  A stream with lengths[s] <= 0 has
+ * accepted 0 and next_token -1.  workspace_dev: 8-byte aligned, moe_mxfp4_accept_edited_bytes long, any contents. */
+int moe_mxfp4_accept_edited_bytes(int32_t streams, int32_t block, int64_t vocab, size_t* bytes);
+int moe_mxfp4_accept_edited(const moe_mxfp4_edit_args* args, int32_t* target_dev, int32_t* accepted_dev,
+                            int32_t* next_token_dev, int32_t* path_dev, void* workspace_dev, size_t workspace_bytes,
+                            void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,7 @@ call does, and raises if the built library is missing (there is no fallback).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +34,14 @@ MOE_FLAG_TRACE = 1 << 5
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
+
+MOE_ROTARY_INTERLEAVED = 1 << 0
+MOE_ROTARY_NORM = 1 << 1
+MOE_ROTARY_NONE = 0
+MOE_ROTARY_LINEAR = 1
+MOE_ROTARY_NTK = 2
+MOE_ROTARY_PARTS = 3
 
 EXPORTED = (
     "moe_mxfp4_create",
@@ -55,11 +64,19 @@ EXPORTED = (
     "moe_mxfp4_cache_append",
     "moe_mxfp4_cache_truncate",
     "moe_mxfp4_cache_commit",
+    "moe_mxfp4_cache_commit_path",
     "moe_mxfp4_cache_fork",
     "moe_mxfp4_cache_compact",
     "moe_mxfp4_cache_attend_bytes",
     "moe_mxfp4_cache_attend",
     "moe_mxfp4_cache_check",
+    "moe_mxfp4_rotary_turns",
+    "moe_mxfp4_rotary_from",
+    "moe_mxfp4_rotate",
+    "moe_mxfp4_cache_append_rotated",
+    "moe_mxfp4_edit_logits",
+    "moe_mxfp4_accept_edited_bytes",
+    "moe_mxfp4_accept_edited",
 )
 
 MOE_MXFP4_STATIC_WORKSPACE_BYTES = 16 << 20
@@ -143,6 +160,103 @@ class moe_mxfp4_attend_args(ctypes.Structure):
     ]
 
 
+class moe_mxfp4_commit_args(ctypes.Structure):
+    _fields_ = [
+        ("accepted_dev", ctypes.c_void_p),
+        ("path_dev", ctypes.c_void_p),
+        ("tokens_dev", ctypes.c_void_p),
+        ("history_dev", ctypes.c_void_p),
+        ("history_stride", ctypes.c_int64),
+        ("streams", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+    ]
+
+
+class moe_mxfp4_rotary(ctypes.Structure):
+    _fields_ = [
+        ("turns_dev", ctypes.c_void_p),
+        ("q_norm_dev", ctypes.c_void_p),
+        ("k_norm_dev", ctypes.c_void_p),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("gain", ctypes.c_float),
+    ]
+
+
+class moe_mxfp4_rotary_scaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("original", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
+class moe_mxfp4_rotate_args(ctypes.Structure):
+    _fields_ = [
+        ("q_dev", ctypes.c_void_p),
+        ("k_dev", ctypes.c_void_p),
+        ("q_out_dev", ctypes.c_void_p),
+        ("k_out_dev", ctypes.c_void_p),
+        ("positions_dev", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64),
+        ("tokens", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+    ]
+
+
+class moe_mxfp4_append_args(ctypes.Structure):
+    _fields_ = [
+        ("q_dev", ctypes.c_void_p),
+        ("k_dev", ctypes.c_void_p),
+        ("v_dev", ctypes.c_void_p),
+        ("q_out_dev", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("lengths_dev", ctypes.c_void_p),
+        ("mask_dev", ctypes.c_void_p),
+        ("streams", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+    ]
+
+
+class moe_mxfp4_edit_args(ctypes.Structure):
+    _fields_ = [
+        ("logits_dev", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("streams", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("vocab", ctypes.c_int64),
+        ("tokens_dev", ctypes.c_void_p),
+        ("mask_dev", ctypes.c_void_p),
+        ("lengths_dev", ctypes.c_void_p),
+        ("history_dev", ctypes.c_void_p),
+        ("history_stride", ctypes.c_int64),
+        ("history_room", ctypes.c_int64),
+        ("history_lengths_dev", ctypes.c_void_p),
+        ("prompt_lengths_dev", ctypes.c_void_p),
+        ("repetition_dev", ctypes.c_void_p),
+        ("frequency_dev", ctypes.c_void_p),
+        ("presence_dev", ctypes.c_void_p),
+        ("bias_begin_dev", ctypes.c_void_p),
+        ("bias_ids_dev", ctypes.c_void_p),
+        ("bias_dev", ctypes.c_void_p),
+        ("bias_entries", ctypes.c_int64),
+        ("allowed_dev", ctypes.c_void_p),
+        ("allowed_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -194,15 +308,27 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             ("append", [P, P, I32, P, P, I64, I32, I32, P, P]),
             ("truncate", [P, P, P, P]),
             ("commit", [P, P, P, P]),
+            ("commit_path", [P, P, ctypes.POINTER(moe_mxfp4_commit_args), P]),
             ("fork", [P, P, P, P, I32, P]),
             ("compact", [P, P, P]),
             ("attend_bytes", [P, I32, I32, I32, SIZE]),
             ("attend", [P, P, I32, ctypes.POINTER(moe_mxfp4_attend_args), P, ctypes.c_size_t, P]),
+            ("append_rotated", [P, P, I32, ctypes.POINTER(moe_mxfp4_rotary), ctypes.POINTER(moe_mxfp4_append_args), P]),
             ("check", [P, P, P])):
         fn = getattr(lib, "moe_mxfp4_cache_" + name)
         fn.argtypes, fn.restype = args, ctypes.c_int
     lib.moe_mxfp4_cache_destroy.argtypes = [P]
     lib.moe_mxfp4_cache_destroy.restype = None
+    EDIT = ctypes.POINTER(moe_mxfp4_edit_args)
+    for name, args in (
+            ("rotary_turns", [I32, ctypes.c_double, ctypes.POINTER(moe_mxfp4_rotary_scaling), P]),
+            ("rotary_from", [P, I32, P]),
+            ("rotate", [ctypes.POINTER(moe_mxfp4_rotary), ctypes.POINTER(moe_mxfp4_rotate_args), P]),
+            ("edit_logits", [EDIT, P, I64, P]),
+            ("accept_edited_bytes", [I32, I32, I64, SIZE]),
+            ("accept_edited", [EDIT, P, P, P, P, P, ctypes.c_size_t, P])):
+        fn = getattr(lib, "moe_mxfp4_" + name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
     _lib = lib
     return lib
 
@@ -343,7 +469,311 @@ def moe_mxfp4_cache_check(cache, state_ptr, stream_ptr) -> int:
     return load_library().moe_mxfp4_cache_check(cache, state_ptr, stream_ptr)
 
 
+def moe_mxfp4_cache_commit_path(cache, state_ptr, args: moe_mxfp4_commit_args, stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_commit_path(cache, state_ptr, ctypes.byref(args), stream_ptr)
+
+
+def moe_mxfp4_rotary_turns(rotary_dim, base, scaling: moe_mxfp4_rotary_scaling | None, turns_ptr) -> int:
+    return load_library().moe_mxfp4_rotary_turns(rotary_dim, base, ctypes.byref(scaling) if scaling is not None else None,
+                                                 turns_ptr)
+
+
+def moe_mxfp4_rotary_from(frequencies_ptr, n, turns_ptr) -> int:
+    return load_library().moe_mxfp4_rotary_from(frequencies_ptr, n, turns_ptr)
+
+
+def moe_mxfp4_rotate(rotary: moe_mxfp4_rotary, args: moe_mxfp4_rotate_args, stream_ptr) -> int:
+    return load_library().moe_mxfp4_rotate(ctypes.byref(rotary), ctypes.byref(args), stream_ptr)
+
+
+def moe_mxfp4_cache_append_rotated(cache, state_ptr, layer, rotary: moe_mxfp4_rotary, args: moe_mxfp4_append_args,
+                                   stream_ptr) -> int:
+    return load_library().moe_mxfp4_cache_append_rotated(cache, state_ptr, layer, ctypes.byref(rotary), ctypes.byref(args),
+                                                         stream_ptr)
+
+
+def moe_mxfp4_edit_logits(args: moe_mxfp4_edit_args, out_ptr, out_stride, stream_ptr) -> int:
+    return load_library().moe_mxfp4_edit_logits(ctypes.byref(args), out_ptr, out_stride, stream_ptr)
+
+
+def moe_mxfp4_accept_edited_bytes(streams, block, vocab) -> tuple[int, int]:
+    n = ctypes.c_size_t()
+    st = load_library().moe_mxfp4_accept_edited_bytes(streams, block, vocab, ctypes.byref(n))
+    return st, n.value
+
+
+def moe_mxfp4_accept_edited(args: moe_mxfp4_edit_args, target_ptr, accepted_ptr, next_token_ptr, path_ptr, ws_ptr, ws_bytes,
+                            stream_ptr) -> int:
+    return load_library().moe_mxfp4_accept_edited(ctypes.byref(args), target_ptr, accepted_ptr, next_token_ptr, path_ptr,
+                                                  ws_ptr, ws_bytes, stream_ptr)
+
+
 # ----------------------------------------------------------------------------- torch convenience
+
+
+class _OnDevice:
+    """Makes tensors on a call's stream, and has the stream's device current for the calls that have no handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device, self.index = device, device.index
+        self.now = torch._C._cuda_getCurrentRawStream(self.index)
+        self.stream = self.now if stream is None else stream
+        self.other = torch.cuda.current_device() != self.index
+
+    def new(self, shape, dtype, zero=False):
+        """Its fill is ordered with the call, and so is what still uses its memory."""
+        import torch
+        make = torch.zeros if zero else torch.empty
+        if self.stream == self.now:
+            return make(shape, dtype=dtype, device=self.device)
+        on = torch.cuda.ExternalStream(self.stream, self.device) if self.stream else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(on):
+            return make(shape, dtype=dtype, device=self.device)
+
+    def call(self, fn, *args):
+        if not self.other:
+            return fn(*args)
+        import torch
+        with torch.cuda.device(self.device):
+            return fn(*args)
+
+
+class _Edits:
+    """The arguments that edit_logits and accept_edited share, checked and laid out."""
+
+    def __init__(self, logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency,
+                 presence, bias, allowed):
+        import torch
+        i32, f32 = torch.int32, torch.float32
+        kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, f32: MOE_DTYPE_FP32}
+        if not logits.is_cuda or logits.dim() != 3 or logits.dtype not in kinds:
+            raise ValueError("logits: a bf16, fp16 or fp32 CUDA tensor [streams, block, vocab]")
+        S, B, V = self.shape = tuple(logits.shape)
+        self.device, self.dtype = logits.device, logits.dtype
+        self.row = _logit_rows("logits", logits)
+
+        def ptr(name, t, dtype, shape):
+            if t is None:
+                return None
+            if t.dtype is not dtype and not (dtype is torch.int64 and t.dtype is torch.uint64):
+                raise ValueError(f"{name}: {dtype}")
+            if t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: contiguous {list(shape)} on {self.device}")
+            return t.data_ptr()
+
+        hist, stride, room, entries = None, 0, 0, 0
+        if history is not None:
+            if history.dim() != 2 or history.shape[0] != S or history.dtype is not i32 or history.device != self.device \
+                    or (history.shape[1] > 1 and history.stride(1) != 1):
+                raise ValueError("history: int32 [streams, tokens], tokens contiguous")
+            if history_lengths is None:
+                raise ValueError("history_lengths: int32 [streams], with history")
+            room = history.shape[1]
+            stride = room if S <= 1 else history.stride(0)
+            if stride < room:
+                raise ValueError("history: streams do not share memory")
+            hist = history.data_ptr()
+        elif history_lengths is not None or prompt_lengths is not None:
+            raise ValueError("history_lengths and prompt_lengths go with history")
+        begin = ids = values = None
+        if bias is not None:
+            begin, ids, values = bias
+            entries = ids.numel()
+            begin, ids, values = (ptr("bias begin", begin, i32, (S + 1,)), ptr("bias ids", ids, i32, (entries,)),
+                                  ptr("bias values", values, f32, (entries,)))
+        words = 0
+        if allowed is not None:
+            if allowed.dim() != 3 or tuple(allowed.shape[:2]) != (S, B) or allowed.shape[2] < (V + 31) // 32 \
+                    or allowed.dtype is not i32 or allowed.device != self.device or not allowed.is_contiguous():
+                raise ValueError("allowed: contiguous int32 [streams, block, (vocab + 31) // 32]")
+            words = allowed.shape[2]
+        self.args = moe_mxfp4_edit_args(
+            logits.data_ptr(), self.row, kinds[logits.dtype], S, B, V, ptr("tokens", tokens, i32, (S, B)),
+            ptr("mask", mask, torch.int64, (S, B)), ptr("lengths", lengths, i32, (S,)), hist, stride, room,
+            ptr("history_lengths", history_lengths, i32, (S,)), ptr("prompt_lengths", prompt_lengths, i32, (S,)),
+            ptr("repetition", repetition, f32, (S,)), ptr("frequency", frequency, f32, (S,)),
+            ptr("presence", presence, f32, (S,)), begin, ids, values, entries,
+            None if allowed is None else allowed.data_ptr(), words)
+
+
+def _logit_rows(name, t):
+    """Elements between the positions of a [streams, block, vocab] tensor whose positions lie one stride apart."""
+    (S, B, V), st = t.shape, t.stride()
+    if t.numel() and ((V > 1 and st[2] != 1) or (S > 1 and B > 1 and st[0] != B * st[1])):
+        raise ValueError(f"{name}: tokens are contiguous, positions one stride apart")
+    row = st[1] if B > 1 else st[0] if S > 1 else V
+    if t.numel() and row < V:
+        raise ValueError(f"{name}: positions do not share memory")
+    return row if t.numel() else V
+
+
+def edit_logits(logits, tokens=None, *, mask=None, lengths=None, history=None, history_lengths=None, prompt_lengths=None,
+                repetition=None, frequency=None, presence=None, bias=None, allowed=None, out=None, stream=None):
+    """Edits the logits of a verify block (moe_mxfp4_edit_logits).  logits: bf16, fp16 or fp32 CUDA [streams, block, vocab];
+    tokens: int32 [streams, block], the block's own; mask: int64 [streams, block], as in KvCache.attend; lengths: int32
+    [streams], positions in use.  history: int32 [streams, tokens], of which the first history_lengths[s] count and the first
+    prompt_lengths[s] are the prompt; repetition, frequency, presence: fp32 [streams]; bias: (begin int32 [streams + 1], ids
+    int32, values fp32), stream s having the entries begin[s] .. begin[s + 1]; allowed: int32 [streams, block, words], a bit
+    per token.  Returns out (made here: like logits, contiguous, positions that `lengths` leaves out zero; `logits` itself:
+    in place)."""
+    e = _Edits(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
+               bias, allowed)
+    on = _OnDevice(e.device, stream)
+    if out is None:
+        out, row = on.new(e.shape, e.dtype, zero=lengths is not None), e.shape[2]
+    elif out is logits:
+        row = e.row
+    else:
+        if tuple(out.shape) != e.shape or out.dtype is not e.dtype or out.device != e.device:
+            raise ValueError("out: of the logits' shape and type")
+        row = _logit_rows("out", out)
+    if out.numel():
+        _check(on.call(load_library().moe_mxfp4_edit_logits, e.args, out.data_ptr(), row, on.stream), "moe_mxfp4_edit_logits")
+    return out
+
+
+def accept_edited(logits, tokens, *, mask=None, lengths=None, history=None, history_lengths=None, prompt_lengths=None,
+                  repetition=None, frequency=None, presence=None, bias=None, allowed=None, workspace=None, stream=None):
+    """Acceptance of drafted chains and, with `mask`, trees on the edited logits (moe_mxfp4_accept_edited); arguments as in
+    edit_logits.  Returns (target [streams, block], accepted [streams], next_token [streams], path [streams, block]), int32:
+    path lists the accepted block positions, then -1 (KvCache.commit takes it).  Calls make their workspace on their stream;
+    one that is given is 8-byte aligned and moe_mxfp4_accept_edited_bytes long."""
+    import torch
+    e = _Edits(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
+               bias, allowed)
+    S, B, V = e.shape
+    on = _OnDevice(e.device, stream)
+    lib = load_library()
+    made = on.new((2 * S * B + 2 * S,), torch.int32)
+    target, path, accepted, next_token = made.split([S * B, S * B, S, S])
+    if workspace is None:
+        st, n = moe_mxfp4_accept_edited_bytes(S, B, V)
+        _check(st, "moe_mxfp4_accept_edited_bytes")
+        workspace = on.new((max(n // 8, 1),), torch.int64)
+    elif workspace.device != e.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on {e.device}")
+    _check(on.call(lib.moe_mxfp4_accept_edited, e.args, target.data_ptr(), accepted.data_ptr(), next_token.data_ptr(),
+                   path.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.stream),
+           "moe_mxfp4_accept_edited")
+    return target.view(S, B), accepted, next_token, path.view(S, B)
+
+
+class Rotary:
+    """Norms and rotation of query and key heads (moe_mxfp4.h, "norms and rotation"), for rotate() and
+    KvCache.append_rotated().
+
+    rotary_dim: elements of a head that turn (default: all); frequencies from `base` and `scaling` (None, or a dict of
+    kind = "linear", "ntk" or "parts", factor, and for "parts" original, low, high), or given: rotary_dim / 2 radians per
+    position.  q_norm, k_norm: weights [head_dim] of `dtype` on the device (kept alive here); norm: whether heads are
+    normed (default: where there is a weight; a weight that is missing then is 1).
+    """
+
+    KINDS = {"linear": MOE_ROTARY_LINEAR, "ntk": MOE_ROTARY_NTK, "parts": MOE_ROTARY_PARTS}
+
+    def __init__(self, *, head_dim, rotary_dim=None, base=10000.0, scaling=None, frequencies=None, interleaved=False, gain=1.0,
+                 q_norm=None, k_norm=None, norm=None, eps=1e-6, dtype=None, device="cuda"):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype: bf16 or fp16")
+        if head_dim not in (64, 128):
+            raise ValueError("head_dim: 64 or 128")
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if not 0 <= rotary_dim <= head_dim or rotary_dim % 2:
+            raise ValueError("rotary_dim: even, at most head_dim")
+        if not eps >= 0 or eps == float("inf") or not abs(gain) < float("inf"):
+            raise ValueError("eps: not negative; gain: finite")
+        n = rotary_dim // 2
+        turns = (ctypes.c_uint64 * max(n, 1))()
+        if frequencies is not None:
+            f = [float(x) for x in frequencies]
+            if len(f) != n or scaling is not None:
+                raise ValueError("frequencies: rotary_dim / 2 values, without scaling")
+            st = moe_mxfp4_rotary_from((ctypes.c_double * max(n, 1))(*f), n, turns)
+            _check(st, "moe_mxfp4_rotary_from")
+        else:
+            if scaling is not None:
+                extra = ("original", "low", "high") if scaling.get("kind") == "parts" else ()
+                if scaling.get("kind") not in self.KINDS or set(scaling) != {"kind", "factor", *extra}:
+                    raise ValueError("scaling: kind ('linear', 'ntk', 'parts') and factor; for 'parts' original, low, high too")
+                scaling = moe_mxfp4_rotary_scaling(self.KINDS[scaling["kind"]], scaling["factor"],
+                                                   *(scaling[x] for x in extra))
+            _check(moe_mxfp4_rotary_turns(rotary_dim, base, scaling, turns), "moe_mxfp4_rotary_turns")
+        self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns[:n]], dtype=torch.int64).to(device)
+        self.device, self.dtype, self.head_dim = self.turns.device, dtype, head_dim
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None and (tuple(w.shape) != (head_dim,) or w.dtype is not dtype or w.device != self.device
+                                  or not w.is_contiguous()):
+                raise ValueError(f"{name}: contiguous {dtype} [head_dim] on {self.device}")
+        norm = (q_norm is not None or k_norm is not None) if norm is None else norm
+        if not norm and (q_norm is not None or k_norm is not None):
+            raise ValueError("norm: weights are given")
+        self._keep = (q_norm, k_norm)
+        self.desc = moe_mxfp4_rotary(self.turns.data_ptr() or None, None if q_norm is None else q_norm.data_ptr(),
+                                     None if k_norm is None else k_norm.data_ptr(), head_dim, rotary_dim,
+                                     MOE_DTYPE_BF16 if dtype is torch.bfloat16 else MOE_DTYPE_FP16,
+                                     (MOE_ROTARY_INTERLEAVED if interleaved else 0) | (MOE_ROTARY_NORM if norm else 0), eps, gain)
+        self._layouts = {}
+
+    def rotate(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """q: [..., q_heads, head_dim] and k: [..., kv_heads, head_dim] (or None) of one number of tokens, each with its
+        tokens one stride apart (the parts of a fused projection's output are); positions: int32, contiguous, one for each
+        token.  Returns (q_out, k_out): made here, contiguous; given; or the inputs themselves (in place)."""
+        import torch
+        on = _OnDevice(self.device, stream)
+        n, q_heads, q_row = self._rows("q", q)
+        m, kv_heads, k_row = (n, 0, 0) if k is None else self._rows("k", k)
+        if m != n or positions.numel() != n or positions.dtype is not torch.int32 or positions.device != self.device \
+                or not positions.is_contiguous():
+            raise ValueError(f"positions: contiguous int32 on {self.device}, one for each token of q and of k")
+        if q_out is None:
+            q_out = on.new(q.shape, self.dtype)
+        if k_out is None and k is not None:
+            k_out = on.new(k.shape, self.dtype)
+        qo_row = self._out("q_out", q_out, q)
+        ko_row = 0 if k is None else self._out("k_out", k_out, k)
+        a = moe_mxfp4_rotate_args(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                                  None if k is None else k_out.data_ptr(), positions.data_ptr(), q_row, k_row, qo_row, ko_row,
+                                  n, q_heads, kv_heads)
+        if n:
+            _check(on.call(load_library().moe_mxfp4_rotate, self.desc, a, on.stream), "moe_mxfp4_rotate")
+        return q_out, k_out
+
+    def _out(self, name, out, x):
+        if out.shape != x.shape:
+            raise ValueError(f"{name}: of its input's shape")
+        return self._rows(name, out)[2]
+
+    def _rows(self, name, t):
+        """(tokens, heads, elements between tokens) of a tensor of rows; remembered by shape and stride."""
+        if t.dtype is not self.dtype or t.device != self.device:
+            raise ValueError(f"{name}: a {self.dtype} tensor on {self.device}")
+        key = (t.shape, t.stride())
+        rows = self._layouts.get(key)
+        if rows is None:
+            if t.dim() < 2 or t.shape[-1] != self.head_dim:
+                raise ValueError(f"{name}: [..., heads, head_dim]")
+            H, D = t.shape[-2:]
+            n, row = math.prod(t.shape[:-2]), H * D
+            if t.numel():
+                if (t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+                    raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
+                step = None                           # the leading dimensions run through the tokens with one stride
+                for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+                    if size == 1:
+                        continue
+                    if step is None:
+                        row = step = stride
+                    elif stride != step:
+                        raise ValueError(f"{name}: heads are contiguous, tokens one stride apart")
+                    step = step * size
+                if n > 1 and row < H * D:
+                    raise ValueError(f"{name}: tokens do not share memory")
+            if len(self._layouts) >= 1024:
+                self._layouts.clear()
+            rows = self._layouts[key] = (n, H, row)
+        return rows
 
 
 def _layer_desc(L) -> moe_mxfp4_layer:
@@ -580,13 +1010,39 @@ class KvCache:
         if st:
             _check(st, "moe_mxfp4_cache_reserve")
 
-    def commit(self, accepted, stream=None):
+    def commit(self, accepted, stream=None, *, path=None, tokens=None, history=None):
         """length += accepted (int32 [num_streams]); the pages behind are given back.  accept()'s output has a value for
         each stream of the batch: slots that are not in it need one too (0: what was reserved there is given back,
-        negative: left alone)."""
+        negative: left alone).  path (int32 [streams, block], accept_edited()'s): the accepted positions of a tree, whose
+        keys and values are moved together first.  tokens (int32 [streams, block]) and history (int32 [streams, room]): the
+        accepted tokens are written behind the first `length` of each history (moe_mxfp4_cache_commit_path)."""
+        if path is not None or history is not None:
+            return self._commit_path(accepted, path, tokens, history, self._stream(stream))
+        if tokens is not None:
+            raise ValueError("tokens: with a history")
         _check(self._lib.moe_mxfp4_cache_commit(self.handle, self._state_ptr,
                                                 self._books("accepted", accepted, self.num_streams), self._stream(stream)),
                "moe_mxfp4_cache_commit")
+
+    def _commit_path(self, accepted, path, tokens, history, stream):
+        accepted = self._books("accepted", accepted, self.num_streams)
+        of = path if path is not None else tokens
+        if of is None or of.dim() != 2 or of.shape[0] > self.num_streams:
+            raise ValueError("path, tokens: int32 [streams, block]")
+        S, B = of.shape
+        path = None if path is None else self._books("path", path, S * B)
+        h, room = None, 0
+        if history is not None:
+            if tokens is None or tokens.shape != of.shape:
+                raise ValueError("tokens: int32 [streams, block], with a history")
+            if (history.dim() != 2 or history.shape[0] != S or history.dtype is not self._i32 or history.get_device() != self._index
+                    or not history.is_contiguous()):
+                raise ValueError(f"history: contiguous int32 [streams, room] on {self.device}")
+            h, room, tokens = history.data_ptr(), history.shape[1], self._books("tokens", tokens, S * B)
+        elif tokens is not None:
+            raise ValueError("tokens: with a history")
+        a = moe_mxfp4_commit_args(accepted, path, tokens, h, room, S if B else 0, B)
+        _check(self._lib.moe_mxfp4_cache_commit_path(self.handle, self._state_ptr, a, stream), "moe_mxfp4_cache_commit_path")
 
     def truncate(self, new_length, stream=None):
         """length = new_length (int32 [num_streams]; negative: left alone); the pages behind are given back."""
@@ -626,6 +1082,45 @@ class KvCache:
                           self._current_stream(self._index) if stream is None else stream)
         if st:
             _check(st, "moe_mxfp4_cache_append")
+
+    def append_rotated(self, layer, q, k, v, rotary, mask=None, lengths=None, out=None, stream=None):
+        """append() of keys that are normed and rotated on the way, with the block's queries
+        (moe_mxfp4_cache_append_rotated).  q: [streams, block, q_heads, head_dim], as k and v (or None: keys and values
+        alone); mask: int64 [streams, block], as in attend: a position turns as many places behind the stream's length as it
+        sees block positions before itself (default: causal).  Returns the queries for attend: out (contiguous; may be q), or
+        a tensor made here, where tokens that `lengths` leaves out are zero."""
+        layout = self._pairs.get((k.shape, k.stride(), v.shape, v.stride()))
+        if (layout is None or k.dtype is not self.dtype or v.dtype is not self.dtype or k.get_device() != self._index
+                or v.get_device() != self._index):
+            layout = self._pair(k, v)
+        S, B, row = layout
+        if type(rotary) is not Rotary or rotary.device != self.device:
+            raise ValueError(f"rotary: a Rotary on {self.device}")
+        if stream is None:
+            stream = self._current_stream(self._index)
+        q_heads, q_row, q_ptr, o_ptr = 0, 0, None, None
+        if q is not None:
+            n, m, q_heads, D, q_row = self._rows("q", q)
+            if (n, m, D) != (S, B, self.head_dim):
+                raise ValueError("q is [streams, block, q_heads, head_dim]")
+            if out is None:
+                out = self._new((S, B, q_heads, D), self.dtype, stream, zero=lengths is not None)
+            elif (out.shape != (S, B, q_heads, D) or out.dtype is not self.dtype or out.get_device() != self._index
+                  or not out.is_contiguous()):
+                raise ValueError("out: contiguous, of q's shape and type")
+            q_ptr, o_ptr = q.data_ptr(), out.data_ptr()
+        elif out is not None:
+            raise ValueError("out: with q")
+        if mask is not None and (mask.shape != (S, B) or mask.dtype not in self._mask_types
+                                 or mask.get_device() != self._index or not mask.is_contiguous()):
+            raise ValueError("mask: contiguous int64 [streams, block]")
+        a = moe_mxfp4_append_args(q_ptr, k.data_ptr(), v.data_ptr(), o_ptr, q_row, row,
+                                  None if lengths is None else self._books("lengths", lengths, S),
+                                  None if mask is None else mask.data_ptr(), S, B, q_heads)
+        st = self._lib.moe_mxfp4_cache_append_rotated(self.handle, self._state_ptr, layer, rotary.desc, a, stream)
+        if st:
+            _check(st, "moe_mxfp4_cache_append_rotated")
+        return out
 
     def attend(self, layer, q, lengths=None, mask=None, shared_stream=0, shared_tokens=0, scale=None, out=None, lse=None,
                workspace=None, stream=None):

@@ -300,6 +300,91 @@ __global__ void __launch_bounds__(256) cache_truncate_kernel(CacheView c, const 
     }
 }
 
+// ---- accepted paths --------------------------------------------------------------------
+
+struct PathView {
+    moe_mxfp4_commit_args a;
+};
+
+// How many positions stream s keeps: accepted[s], or -1 where it is left alone; *bad: because what it was
+// given is not allowed.  The books are not changed before all warps of the call have asked.
+__device__ __forceinline__ int path_count(const CacheView& c, const moe_mxfp4_commit_args& a, int s, int lane, bool* bad) {
+    *bad = false;
+    const int n = a.accepted_dev[s];
+    if (n < 0) return -1;
+    const int len = c.length()[s], held = c.held()[s];
+    const long long room = (long long)held << c.page_shift;
+    bool ok = len >= 0 && held >= 0 && held <= c.L.M && (long long)len + n <= room;
+    if (ok && s < a.streams && n > 0) {
+        ok = n <= a.block && (!a.history_dev || (long long)len + n <= a.history_stride);
+        if (ok && a.path_dev) {
+            const int* path = a.path_dev + (int64_t)s * a.block;
+            for (int i = lane; i < n; i += 32) {
+                const int p = path[i];
+                ok = ok && p < a.block && p > (i ? path[i - 1] : -1);
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                const long long last = (long long)len + path[n - 1];
+                ok = last < room;
+                if (ok)
+                    for (int i = (len >> c.page_shift) + lane; i <= (int)(last >> c.page_shift); i += 32) {
+                        const int page = c.table(s)[i];
+                        ok = ok && (unsigned)page < (unsigned)c.L.P && c.refcount()[page] <= 1;
+                    }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+            }
+        }
+    }
+    *bad = !ok;
+    return ok ? n : -1;
+}
+
+// A warp has 32 16-byte words of a token of one pool, of one stream, and moves them along the path.  Positions
+// ascend and path[i] >= i, so what a step writes lies below all that later steps read: eight are read, then
+// written.  What each stream keeps goes to the state's `need`, for the truncation that follows.
+__global__ void __launch_bounds__(256) cache_path_kernel(CacheView c, const __grid_constant__ PoolList pools, int n_pools, PathView v) {
+    const moe_mxfp4_commit_args& a = v.a;
+    const int lane = threadIdx.x & 31, log_head = c.D == 128 ? 4 : 3;        // words of a head: 16 or 8
+    const int words = c.Hkv << log_head, parts = (words + 31) / 32;
+    grid_dependency_wait();
+    const int64_t n_units = (int64_t)c.L.S * n_pools * parts;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n_units; u += (int64_t)gridDim.x * 8) {
+        const int s = (int)(u / (n_pools * parts)), w = (int)(u - (int64_t)s * (n_pools * parts));
+        const int pool = w / parts, word = (w - pool * parts) * 32 + lane;
+        if (s >= a.streams && w > 0) continue;
+        bool bad;
+        const int n = path_count(c, a, s, lane, &bad);
+        const int len = c.length()[s];
+        const int* path = a.path_dev ? a.path_dev + (int64_t)s * a.block : nullptr;
+        if (w == 0) {
+            if (lane == 0) {
+                c.state[c.L.need + s] = n;
+                if (bad) cache_error(c, MOE_ERR_CACHE_STATE, s);
+            }
+            if (a.history_dev && s < a.streams)
+                for (int i = lane; i < n; i += 32)
+                    a.history_dev[s * a.history_stride + len + i] = a.tokens_dev[(int64_t)s * a.block + (path ? path[i] : i)];
+        }
+        if (!path || s >= a.streams || word >= words) continue;
+        char* const base = static_cast<char*>(pools.base[pool]) +
+                           ((int64_t)(word >> log_head) * c.page * c.D + (word & ((1 << log_head) - 1)) * 8) * 2;
+        auto at = [&](int i) {
+            const int pos = len + i;
+            return reinterpret_cast<uint4*>(base + (c.table(s)[pos >> c.page_shift] * c.page_stride + (int64_t)(pos & (c.page - 1)) * c.D) * 2);
+        };
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n && path[i0 + i] != i0 + i) x[i] = *at(path[i0 + i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n && path[i0 + i] != i0 + i) *at(i0 + i) = x[i];
+        }
+    }
+}
+
 // ---- fork ----------------------------------------------------------------------------
 
 // A CTA per pair.  Every CTA checks the whole list (against the lengths and the pages held,
@@ -572,6 +657,34 @@ int moe_mxfp4_cache_truncate(moe_mxfp4_cache* c, void* state_dev, const int32_t*
 
 int moe_mxfp4_cache_commit(moe_mxfp4_cache* c, void* state_dev, const int32_t* accepted_dev, void* stream) {
     return cache_truncate(c, state_dev, accepted_dev, 1, stream);
+}
+
+int moe_mxfp4_cache_commit_path(moe_mxfp4_cache* c, void* state_dev, const moe_mxfp4_commit_args* args, void* stream) {
+    if (!good_state(c, state_dev) || !args) return MOE_ERR_INVALID_ARG;
+    const moe_mxfp4_commit_args& a = *args;
+    if (!a.accepted_dev || !aligned4(a.accepted_dev) || !aligned4(a.path_dev) || !aligned4(a.tokens_dev) || !aligned4(a.history_dev))
+        return MOE_ERR_INVALID_ARG;
+    if (a.streams < 0 || a.streams > c->cfg.num_streams || (a.streams && a.block < 1)) return MOE_ERR_INVALID_ARG;
+    if (a.history_dev && (!a.tokens_dev || a.history_stride < 0)) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const moe::CacheView v = moe::cache_view(c, state_dev);
+    const int64_t parts = (c->cfg.kv_heads * c->cfg.head_dim / 8 + 31) / 32;
+    for (int l0 = 0; l0 < (a.path_dev ? c->cfg.num_layers : 1); l0 += moe::kMaxPools / 2) {
+        moe::PoolList pools = {};
+        int n = 0;
+        for (int l = l0; l < c->cfg.num_layers && n < moe::kMaxPools; ++l) {
+            pools.base[n++] = c->layers[l].k_dev;
+            pools.base[n++] = c->layers[l].v_dev;
+        }
+        if (!a.path_dev) n = 1;                    // (no token moves)
+        const int64_t want = (c->cfg.num_streams * n * parts + 7) / 8, most = 64 * (int64_t)c->sm_count;
+        if (moe::launch_dependent(moe::cache_path_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, v, pools, n,
+                                  moe::PathView{a}) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    return cache_truncate(c, state_dev, static_cast<int32_t*>(state_dev) + v.L.need, 1, stream);
 }
 
 int moe_mxfp4_cache_fork(moe_mxfp4_cache* c, void* state_dev, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,

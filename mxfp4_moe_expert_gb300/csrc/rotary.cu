@@ -1,0 +1,298 @@
+// Norms of query and key heads with the position rotation, in one pass: on their own (moe_mxfp4_rotate), and
+// on the way into the paged cache (moe_mxfp4_cache_append_rotated).
+//
+// Mathematics.  A head x at position p: x_e <- x_e w_e / sqrt(mean(x^2) + eps), then each pair (a, b) turns by
+// p f_i.  The angle is kept as a fraction of a turn in 64 bits, T_i = 2^64 f_i / 2 pi: p T_i modulo 2^64 is
+// exact, and its upper 32 bits, as half turns in [-1, 1), are what the sine and cosine are taken of.  In fp32
+// radians an angle of 10^5 would be off by up to 0.004.
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "cache.cuh"
+
+namespace moe {
+
+struct RotaryView {
+    const unsigned long long* turns;
+    const uint16_t *q_norm, *k_norm;
+    int R, norm, interleaved;
+    float eps, gain;
+};
+
+// What a call reads and writes: rows of heads, `in` and `out` elements between rows.
+struct HeadRows {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t in, out;
+    int heads;
+};
+
+// Where the keys and values of a token go.
+struct PagePlace {
+    CacheView c;
+    uint16_t *kp, *vp;
+    const int* lengths;
+    const unsigned long long* mask;
+    int block;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float half_to_f32(uint16_t x) {
+    return kBf16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint16_t f32_to_half(float x) {
+    return kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+
+// gain * (cos, sin) of position p's angle in pair i.
+__device__ __forceinline__ float2 turn_of(unsigned long long turns, int p, float gain) {
+    const unsigned long long phase = (unsigned long long)(long long)p * turns;
+    float s, c;
+    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
+    return make_float2(gain * c, gain * s);
+}
+
+// A token of a block on its way into the cache.
+struct TokenPlace {
+    bool used, stored;     // in use; its position is reserved in a page of the stream's own
+    int position;          // of the rotation
+    int64_t at;            // element of head 0 in a pool
+};
+__device__ __forceinline__ TokenPlace token_place(const PagePlace& p, int tok) {
+    TokenPlace t{false, false, 0, 0};
+    const int s = tok / p.block, i = tok - s * p.block;
+    if (p.lengths && i >= p.lengths[s]) return t;
+    t.used = true;
+    const int len = p.c.length()[s], held = min(p.c.held()[s], p.c.L.M);
+    t.position = len + (p.mask ? __popcll(p.mask[tok] & ((1ull << i) - 1)) : i);
+    const int64_t pos = (int64_t)len + i;
+    int page = -1;
+    if (len >= 0 && (pos >> p.c.page_shift) < held) page = p.c.table(s)[pos >> p.c.page_shift];
+    if ((unsigned)page >= (unsigned)p.c.L.P || p.c.refcount()[page] > 1) {
+        raise_status(p.c.state + kCacheStatus, MOE_ERR_CACHE_STATE, s);
+        return t;
+    }
+    t.stored = true;
+    t.at = page * p.c.page_stride + (pos & (p.c.page - 1)) * p.c.D;
+    return t;
+}
+
+// A warp per head of a token: queries, keys, and (into a cache) values.
+template <int D, bool kBf16, bool kCache>
+__global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
+                                                           const int* __restrict__ positions, int tokens, PagePlace pages) {
+    __shared__ float rows[8][D];
+    const int lane = threadIdx.x & 31;
+    float* const row = rows[threadIdx.x >> 5];
+    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
+    grid_dependency_wait();
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < (int64_t)tokens * heads; u += (int64_t)gridDim.x * 8) {
+        const int tok = (int)(u / heads), h = (int)(u - (int64_t)tok * heads);
+        int p;
+        TokenPlace place{true, true, 0, 0};
+        if (kCache) {
+            place = token_place(pages, tok);
+            if (!place.used) continue;
+            p = place.position;
+        } else {
+            p = positions[tok];
+        }
+        const uint16_t* src;
+        uint16_t* dst;
+        const bool is_q = h < q.heads, is_v = h >= q.heads + k.heads;
+        if (is_q) {
+            src = q.src + tok * q.in + (int64_t)h * D;
+            dst = q.dst + tok * q.out + (int64_t)h * D;
+        } else {
+            const int j = h - q.heads - (is_v ? k.heads : 0);
+            if (!place.stored) continue;
+            src = (is_v ? v : k.src) + tok * k.in + (int64_t)j * D;
+            dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)j * pages.c.page * D : k.dst + tok * k.out + (int64_t)j * D;
+        }
+        if (is_v) {
+            for (int e = lane; e < D; e += 32) dst[e] = src[e];
+            continue;
+        }
+        float x[D / 32], sum = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            x[i] = half_to_f32<kBf16>(src[i * 32 + lane]);
+            sum = fmaf(x[i], x[i], sum);
+        }
+        const uint16_t* w = is_q ? r.q_norm : r.k_norm;
+        const float scale = r.norm ? rsqrtf(warp_sum(sum) * (1.0f / D) + r.eps) : 1.0f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            row[i * 32 + lane] = x[i] * scale * (r.norm && w ? half_to_f32<kBf16>(w[i * 32 + lane]) : 1.0f);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int e = i * 32 + lane;
+            float y = row[e];
+            if (e < r.R) {
+                const int half = r.R / 2, pair = r.interleaved ? e >> 1 : e < half ? e : e - half;
+                const float a = row[r.interleaved ? 2 * pair : pair], b = row[r.interleaved ? 2 * pair + 1 : pair + half];
+                const float2 t = turn_of(r.turns[pair], p, r.gain);
+                y = (r.interleaved ? e & 1 : e >= half) ? a * t.y + b * t.x : a * t.x - b * t.y;
+            }
+            dst[e] = f32_to_half<kBf16>(y);
+        }
+    }
+}
+
+}  // namespace moe
+
+namespace {
+
+template <class T>
+bool aligned(const void* p, T n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool good_rotary(const moe_mxfp4_rotary* r) {
+    if (!r || (r->head_dim != 64 && r->head_dim != 128)) return false;
+    if (r->rotary_dim < 0 || r->rotary_dim > r->head_dim || r->rotary_dim % 2) return false;
+    if (r->dtype != MOE_DTYPE_BF16 && r->dtype != MOE_DTYPE_FP16) return false;
+    if (r->flags & ~(MOE_ROTARY_INTERLEAVED | MOE_ROTARY_NORM)) return false;
+    if (!(r->eps >= 0.0f) || !std::isfinite(r->eps) || !std::isfinite(r->gain)) return false;
+    if (r->rotary_dim && !r->turns_dev) return false;
+    return aligned(r->turns_dev, 8) && aligned(r->q_norm_dev, 16) && aligned(r->k_norm_dev, 16);
+}
+
+moe::RotaryView rotary_view(const moe_mxfp4_rotary* r) {
+    moe::RotaryView v;
+    v.turns = reinterpret_cast<const unsigned long long*>(r->turns_dev);
+    v.q_norm = static_cast<const uint16_t*>(r->q_norm_dev);
+    v.k_norm = static_cast<const uint16_t*>(r->k_norm_dev);
+    v.R = r->rotary_dim;
+    v.norm = (r->flags & MOE_ROTARY_NORM) != 0;
+    v.interleaved = (r->flags & MOE_ROTARY_INTERLEAVED) != 0;
+    v.eps = r->eps;
+    v.gain = r->gain;
+    return v;
+}
+
+// Resolves a stride of rows; false for one that is too short or not a multiple of 16 bytes.
+bool good_stride(int64_t* stride, int64_t row) {
+    if (*stride == 0) *stride = row;
+    return *stride >= row && *stride % 8 == 0;
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+template <bool kCache>
+int launch_rotate(const moe_mxfp4_rotary* r, const moe::HeadRows& q, const moe::HeadRows& k, const uint16_t* v,
+                  const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
+    const int64_t units = (int64_t)tokens * (q.heads + k.heads * (kCache ? 2 : 1));
+    const int64_t want = (units + 7) / 8, most = 64 * (int64_t)sms;
+    const dim3 grid((unsigned)(want < most ? want : most));
+    const bool bf16 = r->dtype == MOE_DTYPE_BF16;
+    auto go = [&](auto kern) {
+        return moe::launch_dependent(kern, grid, dim3(256), 0, st, rotary_view(r), q, k, v, positions, tokens, pages);
+    };
+    cudaError_t e;
+    if (r->head_dim == 64)
+        e = bf16 ? go(moe::rotate_heads_kernel<64, true, kCache>) : go(moe::rotate_heads_kernel<64, false, kCache>);
+    else
+        e = bf16 ? go(moe::rotate_heads_kernel<128, true, kCache>) : go(moe::rotate_heads_kernel<128, false, kCache>);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// 2^64 f / 2 pi, |f| <= 2 pi, modulo 2^64: the product with 1 / 2 pi in two doubles.
+bool turns_of(double f, uint64_t* turns) {
+    if (!(std::fabs(f) <= 6.283185307179587)) return false;
+    const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
+    const double x = std::fabs(f), t = x * hi, rest = std::fma(x, hi, -t) + x * lo;
+    const double a = std::ldexp(t, 64), whole = std::floor(a);
+    const uint64_t n = whole >= 0x1p64 ? 0 : (uint64_t)whole;
+    const uint64_t v = n + (uint64_t)(int64_t)std::llround((a - whole) + std::ldexp(rest, 64));
+    *turns = f < 0 ? 0 - v : v;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_mxfp4_rotary_from(const double* frequencies, int32_t n, uint64_t* turns) {
+    if (n < 0 || (n && (!frequencies || !turns))) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!turns_of(frequencies[i], turns + i)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+int moe_mxfp4_rotary_turns(int32_t rotary_dim, double base, const moe_mxfp4_rotary_scaling* scaling, uint64_t* turns) {
+    if (rotary_dim < 0 || rotary_dim % 2 || !(base > 0) || !std::isfinite(base) || (rotary_dim && !turns)) return MOE_ERR_INVALID_ARG;
+    const int kind = scaling ? scaling->kind : MOE_ROTARY_NONE;
+    if (kind < MOE_ROTARY_NONE || kind > MOE_ROTARY_PARTS) return MOE_ERR_INVALID_ARG;
+    const double factor = kind == MOE_ROTARY_NONE ? 1 : scaling->factor;
+    if (!(factor > 0) || !std::isfinite(factor)) return MOE_ERR_INVALID_ARG;
+    if (kind == MOE_ROTARY_PARTS && (!(scaling->original > 0) || !std::isfinite(scaling->original) || !std::isfinite(scaling->low) ||
+                                     !std::isfinite(scaling->high) || scaling->high <= scaling->low))
+        return MOE_ERR_INVALID_ARG;
+    if (kind == MOE_ROTARY_NTK && rotary_dim > 2) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rotary_dim);
+        if (kind == MOE_ROTARY_LINEAR) f /= factor;
+        if (kind == MOE_ROTARY_PARTS) {
+            const double turned = scaling->original * f / 6.283185307179586;
+            const double g = std::fmin(std::fmax((turned - scaling->low) / (scaling->high - scaling->low), 0.0), 1.0);
+            f = g * f + (1 - g) * f / factor;
+        }
+        if (!turns_of(f, turns + i)) return MOE_ERR_INVALID_ARG;
+    }
+    return MOE_OK;
+}
+
+int moe_mxfp4_rotate(const moe_mxfp4_rotary* r, const moe_mxfp4_rotate_args* args, void* stream) {
+    if (!good_rotary(r) || !args) return MOE_ERR_INVALID_ARG;
+    const moe_mxfp4_rotate_args& a = *args;
+    if (a.tokens < 0 || a.q_heads < 0 || a.q_heads > 65536 || a.kv_heads < 0 || a.kv_heads > 65536) return MOE_ERR_INVALID_ARG;
+    moe::HeadRows q{static_cast<const uint16_t*>(a.q_dev), static_cast<uint16_t*>(a.q_out_dev), a.q_stride, a.q_out_stride, a.q_heads};
+    moe::HeadRows k{static_cast<const uint16_t*>(a.k_dev), static_cast<uint16_t*>(a.k_out_dev), a.k_stride, a.k_out_stride, a.kv_heads};
+    for (moe::HeadRows* x : {&q, &k}) {
+        const int64_t row = (int64_t)x->heads * r->head_dim;
+        if (!good_stride(&x->in, row) || !good_stride(&x->out, row)) return MOE_ERR_INVALID_ARG;
+        if (a.tokens && x->heads && (!x->src || !x->dst || !aligned(x->src, 16) || !aligned(x->dst, 16))) return MOE_ERR_INVALID_ARG;
+    }
+    if (a.tokens == 0 || a.q_heads + a.kv_heads == 0) return MOE_OK;
+    if (!a.positions_dev || !aligned(a.positions_dev, 4)) return MOE_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (!sms) return MOE_ERR_CUDA;
+    return launch_rotate<false>(r, q, k, nullptr, a.positions_dev, a.tokens, moe::PagePlace{}, sms, static_cast<cudaStream_t>(stream));
+}
+
+int moe_mxfp4_cache_append_rotated(moe_mxfp4_cache* c, void* state_dev, int32_t layer, const moe_mxfp4_rotary* r,
+                                   const moe_mxfp4_append_args* args, void* stream) {
+    if (!c || !state_dev || !aligned(state_dev, 16) || layer < 0 || layer >= c->cfg.num_layers) return MOE_ERR_INVALID_ARG;
+    if (!good_rotary(r) || r->head_dim != c->cfg.head_dim || r->dtype != c->cfg.dtype || !args) return MOE_ERR_INVALID_ARG;
+    const moe_mxfp4_append_args& a = *args;
+    if (a.streams < 0 || a.streams > c->cfg.num_streams || a.block < 0 || (int64_t)a.streams * a.block > 0x7FFFFFFF) return MOE_ERR_INVALID_ARG;
+    if (a.q_heads < 0 || a.q_heads > 65536 || !aligned(a.lengths_dev, 4) || !aligned(a.mask_dev, 8)) return MOE_ERR_INVALID_ARG;
+    if (a.mask_dev && a.block > 64) return MOE_ERR_INVALID_ARG;
+    const int64_t D = c->cfg.head_dim;
+    moe::HeadRows q{static_cast<const uint16_t*>(a.q_dev), static_cast<uint16_t*>(a.q_out_dev), a.q_stride, a.q_heads * D, a.q_heads};
+    moe::HeadRows k{static_cast<const uint16_t*>(a.k_dev), nullptr, a.row_stride, 0, c->cfg.kv_heads};
+    if (!good_stride(&q.in, q.heads * D) || !good_stride(&k.in, k.heads * D)) return MOE_ERR_INVALID_ARG;
+    if (a.streams == 0 || a.block == 0) return MOE_OK;
+    if (!a.k_dev || !a.v_dev || !aligned(a.k_dev, 16) || !aligned(a.v_dev, 16)) return MOE_ERR_INVALID_ARG;
+    if (a.q_heads && (!a.q_dev || !a.q_out_dev || !aligned(a.q_dev, 16) || !aligned(a.q_out_dev, 16))) return MOE_ERR_INVALID_ARG;
+    const moe::DeviceScope on(c->device);
+    if (!on.ok()) return MOE_ERR_CUDA;
+    moe::PagePlace pages;
+    pages.c = moe::cache_view(c, state_dev);
+    pages.kp = static_cast<uint16_t*>(c->layers[layer].k_dev);
+    pages.vp = static_cast<uint16_t*>(c->layers[layer].v_dev);
+    pages.lengths = a.lengths_dev;
+    pages.mask = reinterpret_cast<const unsigned long long*>(a.mask_dev);
+    pages.block = a.block;
+    return launch_rotate<true>(r, q, k, static_cast<const uint16_t*>(a.v_dev), nullptr, a.streams * a.block, pages, c->sm_count,
+                               static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
