@@ -143,6 +143,139 @@ __global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRow
     }
 }
 
+// Two 16-bit values of a word as fp32, and back.
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (kBf16) return make_float2(bf16_lo(v), bf16_hi(v));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t v;
+    if (kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// Heads whose pairs come in eights (rotary_dim a multiple of 16).  A lane has 16 elements of a head in two
+// 16-byte words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at a time: words that hold both
+// sides of the lane's 8 pairs (8 j.. and rotary_dim / 2 + 8 j.., or side by side), so no element crosses lanes.
+// Each lane takes the sine and cosine of one or two of the token's pairs, and the others from its neighbours;
+// they stay in registers for the token's heads.  `part` of a token's heads go to a warp: all, where there are tokens enough.
+template <int D, bool kBf16, bool kInter, bool kCache>
+__global__ void __launch_bounds__(256) rotate_words_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
+                                                           const int* __restrict__ positions, int tokens, int parts, int steps,
+                                                           PagePlace pages) {
+    constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+    const int lane = threadIdx.x & 31, j = lane % kLanes, g = lane / kLanes;
+    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
+    const bool turns = j < r.R / 16;
+    const int o0 = kInter || !turns ? 16 * j : 8 * j, o1 = kInter || !turns ? 16 * j + 8 : r.R / 2 + 8 * j;
+    grid_dependency_wait();
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < (int64_t)tokens * parts; u += (int64_t)gridDim.x * 8) {
+        const int tok = (int)(u / parts), h0 = (int)(u - (int64_t)tok * parts) * steps * kHeads;
+        const int h_end = min(heads, h0 + steps * kHeads);
+        int p;
+        TokenPlace place{true, true, 0, 0};
+        if (kCache) {
+            place = token_place(pages, tok);
+            if (!place.used) continue;
+            p = place.position;
+        } else {
+            p = positions[tok];
+        }
+        float c[8], s[8];
+        if (r.R) {
+            float2 t0 = make_float2(0, 0), t1 = t0;
+            if (lane < r.R / 2) t0 = turn_of(r.turns[lane], p, r.gain);
+            if (D == 128 && r.R > 64 && lane + 32 < r.R / 2) t1 = turn_of(r.turns[lane + 32], p, r.gain);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = (8 * j + i) & 31;
+                c[i] = __shfl_sync(0xFFFFFFFFu, t0.x, from);
+                s[i] = __shfl_sync(0xFFFFFFFFu, t0.y, from);
+            }
+            if (D == 128 && r.R > 64)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int from = (8 * j + i) & 31;
+                    const float c1 = __shfl_sync(0xFFFFFFFFu, t1.x, from), s1 = __shfl_sync(0xFFFFFFFFu, t1.y, from);
+                    if (j >= 4) {
+                        c[i] = c1;
+                        s[i] = s1;
+                    }
+                }
+        }
+        for (int hb = h0; hb < h_end; hb += kHeads) {
+            const int h = hb + g;
+            const bool is_q = h < q.heads, is_v = h >= q.heads + k.heads;
+            const bool mine = h < h_end && (is_q || place.stored);
+            uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+            uint16_t* dst = nullptr;
+            if (mine) {
+                const uint16_t* src;
+                if (is_q) {
+                    src = q.src + tok * q.in + (int64_t)h * D;
+                    dst = q.dst + tok * q.out + (int64_t)h * D;
+                } else {
+                    const int i = h - q.heads - (is_v ? k.heads : 0);
+                    src = (is_v ? v : k.src) + tok * k.in + (int64_t)i * D;
+                    dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)i * pages.c.page * D : k.dst + tok * k.out + (int64_t)i * D;
+                }
+                w0 = __ldcs(reinterpret_cast<const uint4*>(src + o0));
+                w1 = __ldcs(reinterpret_cast<const uint4*>(src + o1));
+            }
+            float x[16];
+            {
+                const uint32_t in[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = unpack2<kBf16>(in[i]);
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                }
+            }
+            if (r.norm) {
+                float sum = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                const float scale = rsqrtf(sum * (1.0f / D) + r.eps);
+                const uint16_t* w = is_q ? r.q_norm : r.k_norm;
+                if (w) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(w + o0), b = *reinterpret_cast<const uint4*>(w + o1);
+                    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = unpack2<kBf16>(in[i]);
+                        x[2 * i] *= scale * f.x;
+                        x[2 * i + 1] *= scale * f.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] *= scale;
+                }
+            }
+            if (!mine) continue;
+            if (!is_v) {
+                if (turns)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float &a = x[kInter ? 2 * i : i], &b = x[kInter ? 2 * i + 1 : i + 8];
+                        const float y = a * c[i] - b * s[i];
+                        b = fmaf(a, s[i], b * c[i]);
+                        a = y;
+                    }
+                w0 = make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
+                w1 = make_uint4(pack2<kBf16>(x[8], x[9]), pack2<kBf16>(x[10], x[11]), pack2<kBf16>(x[12], x[13]), pack2<kBf16>(x[14], x[15]));
+            }
+            *reinterpret_cast<uint4*>(dst + o0) = w0;
+            *reinterpret_cast<uint4*>(dst + o1) = w1;
+        }
+    }
+}
+
 }  // namespace moe
 
 namespace {
@@ -185,21 +318,35 @@ int sm_count() {
     return sms;
 }
 
+template <bool kCache, int D, bool kBf16>
+cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, const moe::HeadRows& k, const uint16_t* v,
+                          const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
+    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
+    const int64_t most = 64 * (int64_t)sms;
+    if (r.R % 16) {                            // a warp a head, elements through shared memory
+        const int64_t want = ((int64_t)tokens * heads + 7) / 8;
+        return moe::launch_dependent(moe::rotate_heads_kernel<D, kBf16, kCache>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
+                                     r, q, k, v, positions, tokens, pages);
+    }
+    const int rounds = (heads * (D / 16) + 31) / 32;
+    int64_t parts = 24 * (int64_t)sms / tokens;
+    parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
+    const int steps = (int)((rounds + parts - 1) / parts);
+    parts = (rounds + steps - 1) / steps;
+    const int64_t want = ((int64_t)tokens * parts + 7) / 8;
+    auto kern = r.interleaved ? moe::rotate_words_kernel<D, kBf16, true, kCache> : moe::rotate_words_kernel<D, kBf16, false, kCache>;
+    return moe::launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, r, q, k, v, positions, tokens,
+                                 (int)parts, steps, pages);
+}
+
 template <bool kCache>
 int launch_rotate(const moe_mxfp4_rotary* r, const moe::HeadRows& q, const moe::HeadRows& k, const uint16_t* v,
                   const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
-    const int64_t units = (int64_t)tokens * (q.heads + k.heads * (kCache ? 2 : 1));
-    const int64_t want = (units + 7) / 8, most = 64 * (int64_t)sms;
-    const dim3 grid((unsigned)(want < most ? want : most));
+    const moe::RotaryView view = rotary_view(r);
     const bool bf16 = r->dtype == MOE_DTYPE_BF16;
-    auto go = [&](auto kern) {
-        return moe::launch_dependent(kern, grid, dim3(256), 0, st, rotary_view(r), q, k, v, positions, tokens, pages);
-    };
-    cudaError_t e;
-    if (r->head_dim == 64)
-        e = bf16 ? go(moe::rotate_heads_kernel<64, true, kCache>) : go(moe::rotate_heads_kernel<64, false, kCache>);
-    else
-        e = bf16 ? go(moe::rotate_heads_kernel<128, true, kCache>) : go(moe::rotate_heads_kernel<128, false, kCache>);
+    auto go = [&](auto launch) { return launch(view, q, k, v, positions, tokens, pages, sms, st); };
+    const cudaError_t e = r->head_dim == 64 ? (bf16 ? go(launch_rotate<kCache, 64, true>) : go(launch_rotate<kCache, 64, false>))
+                                            : (bf16 ? go(launch_rotate<kCache, 128, true>) : go(launch_rotate<kCache, 128, false>));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
