@@ -56,27 +56,30 @@ __device__ __forceinline__ float2 turn_of(unsigned long long turns, int p, float
 
 // A token of a block on its way into the cache.
 struct TokenPlace {
-    bool used, stored;     // in use; its position is reserved in a page of the stream's own
+    int s, i, len, held;
     int position;          // of the rotation
-    int64_t at;            // element of head 0 in a pool
+    bool used;             // in use
+    int64_t at;            // element of head 0 in a pool, -1: not to be stored
 };
 __device__ __forceinline__ TokenPlace token_place(const PagePlace& p, int tok) {
-    TokenPlace t{false, false, 0, 0};
-    const int s = tok / p.block, i = tok - s * p.block;
-    if (p.lengths && i >= p.lengths[s]) return t;
-    t.used = true;
-    const int len = p.c.length()[s], held = min(p.c.held()[s], p.c.L.M);
-    t.position = len + (p.mask ? __popcll(p.mask[tok] & ((1ull << i) - 1)) : i);
-    const int64_t pos = (int64_t)len + i;
-    int page = -1;
-    if (len >= 0 && (pos >> p.c.page_shift) < held) page = p.c.table(s)[pos >> p.c.page_shift];
-    if ((unsigned)page >= (unsigned)p.c.L.P || p.c.refcount()[page] > 1) {
-        raise_status(p.c.state + kCacheStatus, MOE_ERR_CACHE_STATE, s);
-        return t;
-    }
-    t.stored = true;
-    t.at = page * p.c.page_stride + (pos & (p.c.page - 1)) * p.c.D;
+    TokenPlace t;
+    t.s = tok / p.block;
+    t.i = tok - t.s * p.block;
+    t.len = p.c.length()[t.s];
+    t.held = p.c.held()[t.s];
+    t.position = t.len + (p.mask ? __popcll(p.mask[tok] & ((1ull << t.i) - 1)) : t.i);
+    t.used = !p.lengths || t.i < p.lengths[t.s];
+    t.at = -1;
     return t;
+}
+// Looks the token's page up: its position has to be reserved, in a page of the stream's own.
+__device__ __forceinline__ void token_page(const PagePlace& p, TokenPlace* t) {
+    if (!t->used) return;
+    const int64_t pos = (int64_t)t->len + t->i;
+    int page = -1;
+    if (t->len >= 0 && (pos >> p.c.page_shift) < min(t->held, p.c.L.M)) page = p.c.table(t->s)[pos >> p.c.page_shift];
+    if ((unsigned)page >= (unsigned)p.c.L.P || p.c.refcount()[page] > 1) raise_status(p.c.state + kCacheStatus, MOE_ERR_CACHE_STATE, t->s);
+    else t->at = page * p.c.page_stride + (pos & (p.c.page - 1)) * p.c.D;
 }
 
 // A warp per head of a token: queries, keys, and (into a cache) values.
@@ -91,10 +94,11 @@ __global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRow
     for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < (int64_t)tokens * heads; u += (int64_t)gridDim.x * 8) {
         const int tok = (int)(u / heads), h = (int)(u - (int64_t)tok * heads);
         int p;
-        TokenPlace place{true, true, 0, 0};
+        TokenPlace place{};
         if (kCache) {
             place = token_place(pages, tok);
             if (!place.used) continue;
+            token_page(pages, &place);
             p = place.position;
         } else {
             p = positions[tok];
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRow
             dst = q.dst + tok * q.out + (int64_t)h * D;
         } else {
             const int j = h - q.heads - (is_v ? k.heads : 0);
-            if (!place.stored) continue;
+            if (kCache && place.at < 0) continue;
             src = (is_v ? v : k.src) + tok * k.in + (int64_t)j * D;
             dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)j * pages.c.page * D : k.dst + tok * k.out + (int64_t)j * D;
         }
@@ -157,74 +161,91 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return v;
 }
 
-// Heads whose pairs come in eights (rotary_dim a multiple of 16).  A lane has 16 elements of a head in two
-// 16-byte words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at a time: words that hold both
-// sides of the lane's 8 pairs (8 j.. and rotary_dim / 2 + 8 j.., or side by side), so no element crosses lanes.
-// Each lane takes the sine and cosine of one or two of the token's pairs, and the others from its neighbours;
-// they stay in registers for the token's heads.  `part` of a token's heads go to a warp: all, where there are tokens enough.
+__device__ __forceinline__ void copy_16(void* smem, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Heads whose pairs fill 16-byte words (rotary_dim a multiple of 16, or of 8 where pairs are side by side).  A
+// lane has 16 elements of a head in two words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at
+// a time: words that hold both sides of the lane's 8 pairs, so no element crosses lanes, neighbours' words side
+// by side in memory (with both words of a lane side by side, each touched half of every 32-byte sector).  Each lane takes the sine and
+// cosine of one or two of the token's pairs, and the others from its neighbours; they stay in registers for the
+// token's heads.  A warp takes `steps` rounds of a token's heads.  Every lane copies its own words kStages - 1 rounds
+// ahead into its own places of shared memory, across tokens, so memory is kept busy without registers and without barriers.
+constexpr int kStages = 6;
+
 template <int D, bool kBf16, bool kInter, bool kCache>
-__global__ void __launch_bounds__(256) rotate_words_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
-                                                           const int* __restrict__ positions, int tokens, int parts, int steps,
-                                                           PagePlace pages) {
+__global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
+                                                              const int* __restrict__ positions, int tokens, int parts, int steps,
+                                                              PagePlace pages) {
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
-    const int lane = threadIdx.x & 31, j = lane % kLanes, g = lane / kLanes;
+    __shared__ uint4 ring[8][kStages][2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane % kLanes, g = lane / kLanes;
     const int heads = q.heads + k.heads * (kCache ? 2 : 1);
-    const bool turns = j < r.R / 16;
-    const int o0 = kInter || !turns ? 16 * j : 8 * j, o1 = kInter || !turns ? 16 * j + 8 : r.R / 2 + 8 * j;
-    grid_dependency_wait();
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < (int64_t)tokens * parts; u += (int64_t)gridDim.x * 8) {
-        const int tok = (int)(u / parts), h0 = (int)(u - (int64_t)tok * parts) * steps * kHeads;
-        const int h_end = min(heads, h0 + steps * kHeads);
-        int p;
-        TokenPlace place{true, true, 0, 0};
-        if (kCache) {
-            place = token_place(pages, tok);
-            if (!place.used) continue;
-            p = place.position;
-        } else {
-            p = positions[tok];
+    // the lane's words: elements o0.. and o1.., and whether the pairs c[0..3], c[4..7] turn
+    const bool turns0 = kInter ? 8 * j < r.R : 16 * j < r.R, turns1 = kInter ? 8 * j + D / 2 < r.R : turns0;
+    const int o0 = kInter || turns0 ? 8 * j : r.R / 2 + 8 * j, o1 = kInter ? D / 2 + 8 * j : turns0 ? r.R / 2 + 8 * j : D / 2 + 8 * j;
+    // the pairs whose sine and cosine the lane takes (first, second), and from which lanes it gets those of its own
+    const int first = kInter || D == 64 ? lane : 8 * (lane / 4) + lane % 4, second = kInter ? lane + 32 : first + 4;
+    const int64_t units = (int64_t)tokens * parts, stride = (int64_t)gridDim.x * 8;
+    const int64_t u0 = (int64_t)blockIdx.x * 8 + warp;
+    int64_t ahead_u = u0;
+    int ahead_step = 0, ahead_slot = 0, slot = 0;
+    auto ahead = [&] {
+        if (ahead_u < units) {
+            const int tok = (int)(ahead_u / parts), h = ((int)(ahead_u - (int64_t)tok * parts) * steps + ahead_step) * kHeads + g;
+            if (h < heads) {
+                const uint16_t* src;
+                if (h < q.heads) {
+                    src = q.src + tok * q.in + (int64_t)h * D;
+                } else {
+                    const bool is_v = h >= q.heads + k.heads;
+                    src = (is_v ? v : k.src) + tok * k.in + (int64_t)(h - q.heads - (is_v ? k.heads : 0)) * D;
+                }
+                copy_16(&ring[warp][ahead_slot][0][lane], src + o0);
+                copy_16(&ring[warp][ahead_slot][1][lane], src + o1);
+            }
+            if (++ahead_step == steps) {
+                ahead_step = 0;
+                ahead_u += stride;
+            }
         }
+        copies_commit();
+        if (++ahead_slot == kStages) ahead_slot = 0;
+    };
+    grid_dependency_wait();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ahead();
+    for (int64_t u = u0; u < units; u += stride) {
+        const int tok = (int)(u / parts), h0 = (int)(u - (int64_t)tok * parts) * steps * kHeads;
+        TokenPlace place{};
+        if (kCache) place = token_place(pages, tok);
+        const int p = kCache ? place.position : positions[tok];
         float c[8], s[8];
         if (r.R) {
             float2 t0 = make_float2(0, 0), t1 = t0;
-            if (lane < r.R / 2) t0 = turn_of(r.turns[lane], p, r.gain);
-            if (D == 128 && r.R > 64 && lane + 32 < r.R / 2) t1 = turn_of(r.turns[lane + 32], p, r.gain);
+            if (first < r.R / 2) t0 = turn_of(r.turns[first], p, r.gain);
+            if (D == 128 && second < r.R / 2) t1 = turn_of(r.turns[second], p, r.gain);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int from = (8 * j + i) & 31;
-                c[i] = __shfl_sync(0xFFFFFFFFu, t0.x, from);
-                s[i] = __shfl_sync(0xFFFFFFFFu, t0.y, from);
+                const int from = D == 128 ? 4 * j + i % 4 : kInter ? 4 * j + i % 4 + 16 * (i / 4) : 8 * j + i;
+                c[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.x : t0.x, from);
+                s[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.y : t0.y, from);
             }
-            if (D == 128 && r.R > 64)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int from = (8 * j + i) & 31;
-                    const float c1 = __shfl_sync(0xFFFFFFFFu, t1.x, from), s1 = __shfl_sync(0xFFFFFFFFu, t1.y, from);
-                    if (j >= 4) {
-                        c[i] = c1;
-                        s[i] = s1;
-                    }
-                }
         }
-        for (int hb = h0; hb < h_end; hb += kHeads) {
-            const int h = hb + g;
+        if (kCache) token_page(pages, &place);
+        for (int step = 0; step < steps; ++step) {
+            ahead();
+            copies_wait<kStages - 1>();
+            uint4 w0 = ring[warp][slot][0][lane], w1 = ring[warp][slot][1][lane];
+            if (++slot == kStages) slot = 0;
+            const int h = h0 + step * kHeads + g;
             const bool is_q = h < q.heads, is_v = h >= q.heads + k.heads;
-            const bool mine = h < h_end && (is_q || place.stored);
-            uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-            uint16_t* dst = nullptr;
-            if (mine) {
-                const uint16_t* src;
-                if (is_q) {
-                    src = q.src + tok * q.in + (int64_t)h * D;
-                    dst = q.dst + tok * q.out + (int64_t)h * D;
-                } else {
-                    const int i = h - q.heads - (is_v ? k.heads : 0);
-                    src = (is_v ? v : k.src) + tok * k.in + (int64_t)i * D;
-                    dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)i * pages.c.page * D : k.dst + tok * k.out + (int64_t)i * D;
-                }
-                w0 = __ldcs(reinterpret_cast<const uint4*>(src + o0));
-                w1 = __ldcs(reinterpret_cast<const uint4*>(src + o1));
-            }
             float x[16];
             {
                 const uint32_t in[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -257,11 +278,11 @@ __global__ void __launch_bounds__(256) rotate_words_kernel(RotaryView r, HeadRow
                     for (int i = 0; i < 16; ++i) x[i] *= scale;
                 }
             }
-            if (!mine) continue;
+            if (h >= heads || (kCache && (!place.used || !(is_q || place.at >= 0)))) continue;
             if (!is_v) {
-                if (turns)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 8; ++i)
+                    if (kInter && i >= 4 ? turns1 : turns0) {
                         float &a = x[kInter ? 2 * i : i], &b = x[kInter ? 2 * i + 1 : i + 8];
                         const float y = a * c[i] - b * s[i];
                         b = fmaf(a, s[i], b * c[i]);
@@ -269,6 +290,13 @@ __global__ void __launch_bounds__(256) rotate_words_kernel(RotaryView r, HeadRow
                     }
                 w0 = make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
                 w1 = make_uint4(pack2<kBf16>(x[8], x[9]), pack2<kBf16>(x[10], x[11]), pack2<kBf16>(x[12], x[13]), pack2<kBf16>(x[14], x[15]));
+            }
+            uint16_t* dst;
+            if (is_q) {
+                dst = q.dst + tok * q.out + (int64_t)h * D;
+            } else {
+                const int i = h - q.heads - (is_v ? k.heads : 0);
+                dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)i * pages.c.page * D : k.dst + tok * k.out + (int64_t)i * D;
             }
             *reinterpret_cast<uint4*>(dst + o0) = w0;
             *reinterpret_cast<uint4*>(dst + o1) = w1;
@@ -323,20 +351,30 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
                           const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
     const int heads = q.heads + k.heads * (kCache ? 2 : 1);
     const int64_t most = 64 * (int64_t)sms;
-    if (r.R % 16) {                            // a warp a head, elements through shared memory
+    if (r.R % (r.interleaved ? 8 : 16)) {      // a warp a head, elements through shared memory
         const int64_t want = ((int64_t)tokens * heads + 7) / 8;
         return moe::launch_dependent(moe::rotate_heads_kernel<D, kBf16, kCache>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
                                      r, q, k, v, positions, tokens, pages);
     }
+    // Rounds of heads of a token, dealt out to warps in parts of `steps` each: as many parts as give the busiest warp
+    // of the resident CTAs the least to do, a part's start (its page, its sines and cosines) taken for a round's work.
     const int rounds = (heads * (D / 16) + 31) / 32;
-    int64_t parts = 24 * (int64_t)sms / tokens;
-    parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
-    const int steps = (int)((rounds + parts - 1) / parts);
-    parts = (rounds + steps - 1) / steps;
+    const int64_t resident = 3 * (int64_t)sms;
+    int parts = 1, steps = rounds;
+    int64_t least = INT64_MAX;
+    for (int n = 1; n <= rounds && n <= 64; ++n) {
+        const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
+        const int64_t cost = ((int64_t)tokens * made + resident * 8 - 1) / (resident * 8) * (each + 1);
+        if (cost < least) {
+            least = cost;
+            parts = made;
+            steps = each;
+        }
+    }
     const int64_t want = ((int64_t)tokens * parts + 7) / 8;
     auto kern = r.interleaved ? moe::rotate_words_kernel<D, kBf16, true, kCache> : moe::rotate_words_kernel<D, kBf16, false, kCache>;
-    return moe::launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, r, q, k, v, positions, tokens,
-                                 (int)parts, steps, pages);
+    return moe::launch_dependent(kern, dim3((unsigned)(want < resident ? want : resident)), dim3(256), 0, st, r, q, k, v, positions, tokens,
+                                 parts, steps, pages);
 }
 
 template <bool kCache>
