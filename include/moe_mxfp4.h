@@ -616,7 +616,8 @@ typedef struct {
     const int32_t* lengths_dev;           /* [streams] or NULL: all of the block */
     const int32_t* history_dev;           /* [streams, history_stride] or NULL */
     int64_t history_stride;               /* tokens between the histories of two streams */
-    int64_t history_room;                 /* tokens of each that may be read, 0..history_stride: longer lengths are cut */
+    int64_t history_room;                 /* tokens of each that may be read, 0..history_stride and below 2^29:
+                                           * longer lengths are cut */
     const int32_t* history_lengths_dev;   /* [streams], with history_dev */
     const int32_t* prompt_lengths_dev;    /* [streams] or NULL: no prompt */
     const float* repetition_dev;          /* [streams], above 0, or NULL = 1 */

@@ -3,7 +3,8 @@
 // grammar masks.
 //
 // How often a token was said is counted where it is needed: a CTA has a run of tokens of the vocabulary and
-// counts those of the stream's history that lie in it in shared memory, so nothing is kept from call to call.
+// counts those of the stream's history that lie in it in shared memory, once for some positions of the block, so
+// nothing is kept from call to call.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -13,39 +14,33 @@
 namespace moe {
 
 constexpr int kEditThreads = 256;
-constexpr int kEditRun = 4096;              // tokens of the vocabulary of a CTA
-constexpr uint32_t kPrompted = 1u << 31;    // of a count: the prompt has the token
+constexpr int kEach = 16;                          // tokens of the vocabulary of a thread, the same ones for every position
+constexpr int kEditRun = kEach * kEditThreads;     // ... and of a CTA
+constexpr int kMostRows = 16;                      // positions of a CTA, at most
+constexpr uint32_t kPrompted = 1u << 31;           // of a count: the prompt has the token, ...
+constexpr uint32_t kInBlock = 1u << 30;            // ... and so has the block, at positions that not all of the CTA's see
 
 struct EditView {
     moe_mxfp4_edit_args a;
     void* out;
     int64_t out_stride;
-    unsigned long long* best;               // acceptance: [rows, runs] largest (key, ~token) of a run, 0 = none
-    int runs;
+    unsigned long long* best;                      // acceptance: [rows, runs] largest (key, ~token) of a run, 0 = none
+    int runs, rows, groups;                        // of a CTA's positions: how many, and groups of them in a block
 };
-
-template <int kType>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-    if (kType == MOE_DTYPE_FP32) return static_cast<const float*>(p)[i];
-    const uint16_t x = static_cast<const uint16_t*>(p)[i];
-    return kType == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
-}
-template <int kType>
-__device__ __forceinline__ void store_logit(void* p, int64_t i, float z) {
-    if (kType == MOE_DTYPE_FP32) static_cast<float*>(p)[i] = z;
-    else static_cast<uint16_t*>(p)[i] = kType == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(z)) : __half_as_ushort(__float2half_rn(z));
-}
 
 struct Penalty {
-    float repetition, frequency, presence;
+    float repetition, inverse, frequency, presence;
 };
 
-// The order of the operations and their roundings are fixed: both entry points give the same value.
-__device__ __forceinline__ float edited(float z, uint32_t count, const Penalty& p) {
-    if (count) z = z > 0 ? __fdiv_rn(z, p.repetition) : __fmul_rn(z, p.repetition);
-    const uint32_t c = count & ~kPrompted;
-    if (c) z = __fsub_rn(__fmaf_rn(-p.frequency, (float)c, z), p.presence);
-    return z;
+// What is taken off a token that was said c times.
+__device__ __forceinline__ float penalty_of(uint32_t c, const Penalty& p) {
+    return c ? __fmaf_rn(p.frequency, (float)c, p.presence) : 0.0f;
+}
+// z / r as z (1 / r): half a step more than a division, and a fifth of its instructions.  The operations and their
+// roundings are fixed: both entry points give the same value.
+__device__ __forceinline__ float edited(float z, bool seen, float off, const Penalty& p) {
+    const float factor = seen ? (z > 0 ? p.inverse : p.repetition) : 1.0f;
+    return __fsub_rn(__fmul_rn(z, factor), off);
 }
 
 // Orderable key of a logit (larger logit, larger key; equal ones, -0 and +0 among them, have one key; NaN ranks as -inf).
@@ -55,83 +50,297 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ bool aligned_to_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 __device__ __forceinline__ int used_positions(const moe_mxfp4_edit_args& a, int s) {
     return a.lengths_dev ? min(a.lengths_dev[s], a.block) : a.block;
 }
-// Block positions before b that b sees.
-__device__ __forceinline__ bool sees(const moe_mxfp4_edit_args& a, int64_t row, int b, int j) {
-    return j == b || (j < b && (!a.mask_dev || (a.mask_dev[row] >> j & 1)));
+
+// What a CTA knows of its run of the vocabulary.
+struct EditRun {
+    uint32_t count[kEditRun];
+    union {
+        int entry[kEditRun];                       // 1 + the last entry of the stream's biases for the token, then
+        float off[kEditRun];                       // what is taken off it (of one in the block: the bias alone)
+    };
+    int block_token[64], block_at[64], n_block;    // tokens of the block in the run that only some of the CTA's positions see
+    unsigned long long best[kMostRows][kEditThreads / 32];
+};
+
+// A token of the block: its edited logit at position b.
+__device__ __noinline__ float edited_in_block(const EditView& e, const EditRun& r, const Penalty& p, float z, int i, int64_t row, int b) {
+    uint32_t count = r.count[i] & ~kInBlock;
+    const bool tree = e.a.mask_dev != nullptr;
+    const unsigned long long seen = tree ? (e.a.mask_dev[row] & ((1ull << b) - 1)) | 1ull << b : 0;
+    for (int k = 0; k < r.n_block; ++k)
+        if (r.block_token[k] == i && (tree ? seen >> r.block_at[k] & 1 : r.block_at[k] <= b)) ++count;
+    return edited(z, count != 0, __fadd_rn(penalty_of(count & ~kPrompted, p), r.off[i]), p);
 }
 
-// A CTA per (position, run of the vocabulary).
-template <int kType, bool kAccept>
-__global__ void __launch_bounds__(kEditThreads) edit_kernel(EditView e) {
-    __shared__ uint32_t count[kEditRun];
-    __shared__ int entry[kEditRun];         // 1 + the last entry of the stream's biases for the token
-    __shared__ unsigned long long red[kEditThreads / 32];
+// Counts a token of the history.
+__device__ __forceinline__ void count_token(EditRun& r, int token, int64_t v0, int n, bool prompt) {
+    const uint32_t v = (uint32_t)token - (uint32_t)v0;
+    if (v >= (uint32_t)n) return;
+    if (prompt) atomicOr(r.count + v, kPrompted);
+    else atomicAdd(r.count + v, 1u);
+}
+
+template <int kType>
+__device__ __forceinline__ float to_f32(uint16_t x) {
+    return kType == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+template <int kType>
+__device__ __forceinline__ uint16_t from_f32(float x) {
+    return kType == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+
+// A thread's kEach tokens of the run, as bits of the logits' type: words of 16 bytes that lie kEditThreads apart
+// (kWords, where rows begin on 16 bytes), or single ones.
+template <int kType, bool kWords>
+struct Mine {
+    static constexpr int kSize = kType == MOE_DTYPE_FP32 ? 4 : 2, kPer = 16 / kSize;
+    uint32_t bits[kEach * kSize / 4];
+    static __device__ __forceinline__ int at(int i) {      // ascending in i
+        return kWords ? (i / kPer * kEditThreads + (int)threadIdx.x) * kPer + i % kPer : i * kEditThreads + (int)threadIdx.x;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if (kType == MOE_DTYPE_FP32) return __uint_as_float(bits[i]);
+        return to_f32<kType>((uint16_t)(i & 1 ? bits[i / 2] >> 16 : bits[i / 2]));
+    }
+    __device__ __forceinline__ void raw(int i, uint32_t x) {
+        if (kType == MOE_DTYPE_FP32) bits[i] = x;
+        else bits[i / 2] = i & 1 ? (bits[i / 2] & 0xFFFFu) | x << 16 : (bits[i / 2] & 0xFFFF0000u) | x;
+    }
+    __device__ __forceinline__ void set(int i, float z) {
+        if (kType == MOE_DTYPE_FP32) bits[i] = __float_as_uint(z);
+        else raw(i, from_f32<kType>(z));
+    }
+    __device__ __forceinline__ void load(const void* p, int64_t first, int n) {   // first: of the run's first token; n: tokens in it
+        if (kWords) {
+#pragma unroll
+            for (int w = 0; w < kEach / kPer; ++w) {
+                const int v = at(w * kPer);
+                if (v + kPer <= n) {
+                    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (first + v) * kSize));
+                    bits[4 * w] = x.x;
+                    bits[4 * w + 1] = x.y;
+                    bits[4 * w + 2] = x.z;
+                    bits[4 * w + 3] = x.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) one(p, first, n, w * kPer + i);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) one(p, first, n, i);
+        }
+    }
+    __device__ __forceinline__ void one(const void* p, int64_t first, int n, int i) {
+        const int v = at(i);
+        if (kType == MOE_DTYPE_FP32) raw(i, v < n ? __ldcs(static_cast<const uint32_t*>(p) + first + v) : 0);
+        else raw(i, v < n ? __ldcs(static_cast<const uint16_t*>(p) + first + v) : 0);
+    }
+    // The words (tokens) that have changed, or all.
+    __device__ __forceinline__ void store(void* p, int64_t first, int n, uint32_t which) const {
+        if (kWords) {
+#pragma unroll
+            for (int w = 0; w < kEach / kPer; ++w) {
+                const int v = at(w * kPer);
+                if (!(which >> (w * kPer) & ((1u << kPer) - 1))) continue;
+                if (v + kPer <= n) {
+                    *reinterpret_cast<uint4*>(static_cast<char*>(p) + (first + v) * kSize) =
+                        make_uint4(bits[4 * w], bits[4 * w + 1], bits[4 * w + 2], bits[4 * w + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) put(p, first, n, w * kPer + i);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (which >> i & 1) put(p, first, n, i);
+        }
+    }
+    __device__ __forceinline__ void put(void* p, int64_t first, int n, int i) const {
+        const int v = at(i);
+        if (v >= n) return;
+        if (kType == MOE_DTYPE_FP32) static_cast<uint32_t*>(p)[first + v] = bits[i];
+        else static_cast<uint16_t*>(p)[first + v] = (uint16_t)(i & 1 ? bits[i / 2] >> 16 : bits[i / 2]);
+    }
+    // A bit for each token that the grammar allows and the vocabulary has.
+    static __device__ __forceinline__ uint32_t allowed(const uint32_t* words, int n) {   // words: of the run
+        uint32_t ok = 0;
+        if (kWords) {
+#pragma unroll
+            for (int w = 0; w < kEach / kPer; ++w) {
+                const int v = at(w * kPer);
+                if (v < n) ok |= (__ldg(words + (v >> 5)) >> (v & 31) & ((1u << kPer) - 1)) << (w * kPer);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int v = at(i);
+                if (v < n) ok |= (__ldg(words + (v >> 5)) >> (v & 31) & 1) << i;
+            }
+        }
+        return ok & in_run(n);
+    }
+    static __device__ __forceinline__ uint32_t in_run(int n) {
+        if (n == kEditRun) return (1u << kEach) - 1;
+        uint32_t in = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) in |= (uint32_t)(at(i) < n) << i;
+        return in;
+    }
+};
+
+// A CTA per stream, group of positions and run of the vocabulary.  The next position's logits are under way while
+// one's are edited.
+template <int kType, bool kWords, bool kAccept>
+__global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
+    using M = Mine<kType, kWords>;
+    __shared__ EditRun r;
     const moe_mxfp4_edit_args& a = e.a;
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x / e.runs;
-    const int run = blockIdx.x - row * e.runs;
-    const int s = row / a.block, b = row - (int64_t)s * a.block;
-    const int64_t v0 = (int64_t)run * kEditRun;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = blockIdx.x % e.runs, sg = blockIdx.x / e.runs, s = sg / e.groups, b0 = (sg - s * e.groups) * e.rows;
+    const int64_t v0 = (int64_t)run * kEditRun, row0 = (int64_t)s * a.block;
     const int n = (int)min((int64_t)kEditRun, a.vocab - v0);
     grid_dependency_wait();
-    if (b >= used_positions(a, s)) return;
-    for (int i = tid; i < kEditRun; i += kEditThreads) {
-        count[i] = 0;
-        entry[i] = 0;
+    const int b1 = min(min(b0 + e.rows, a.block), used_positions(a, s));
+    if (b0 >= b1) return;
+    M next;
+    uint32_t next_ok = M::in_run(n);
+    auto fetch = [&](int b) {
+        next.load(a.logits_dev, (row0 + b) * a.row_stride + v0, n);
+        if (a.allowed_dev) next_ok = M::allowed(a.allowed_dev + (row0 + b) * a.allowed_stride + (v0 >> 5), n);
+    };
+    fetch(b0);
+    // what is known of the run's tokens
+    for (int i = tid; i < kEditRun / 4; i += kEditThreads) {
+        reinterpret_cast<uint4*>(r.count)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(r.entry)[i] = make_uint4(0, 0, 0, 0);
     }
+    if (tid == 0) r.n_block = 0;
     __syncthreads();
     if (a.history_dev) {
-        const int64_t len = min((int64_t)a.history_lengths_dev[s], a.history_room);
-        const int64_t prompt = a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0;
-        for (int64_t i = tid; i < len; i += kEditThreads) {
-            const int64_t v = a.history_dev[s * a.history_stride + i] - v0;
-            if (v < 0 || v >= n) continue;
-            if (i < prompt) atomicOr(count + v, kPrompted);
-            else atomicAdd(count + v, 1u);
+        const int len = (int)min((int64_t)a.history_lengths_dev[s], a.history_room);
+        const int prompt = a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0;
+        const int* h = a.history_dev + s * a.history_stride;
+        // (many loads at once, before any of them is counted: one after the other takes a round trip each)
+        int i0 = 0;
+        if (aligned_to_16(h))
+            for (; i0 + 16 * kEditThreads <= len; i0 += 16 * kEditThreads) {
+                int4 t[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t[k] = reinterpret_cast<const int4*>(h + i0)[k * kEditThreads + tid];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + 4 * (k * kEditThreads + tid);
+                    count_token(r, t[k].x, v0, n, i < prompt);
+                    count_token(r, t[k].y, v0, n, i + 1 < prompt);
+                    count_token(r, t[k].z, v0, n, i + 2 < prompt);
+                    count_token(r, t[k].w, v0, n, i + 3 < prompt);
+                }
+            }
+        for (; i0 < len; i0 += 8 * kEditThreads) {
+            int t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = i0 + k * kEditThreads + tid < len ? h[i0 + k * kEditThreads + tid] : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) count_token(r, t[k], v0, n, i0 + k * kEditThreads + tid < prompt);
         }
     }
     if (a.tokens_dev)
-        for (int j = tid; j <= b; j += kEditThreads) {
-            const int64_t v = a.tokens_dev[(int64_t)s * a.block + j] - v0;
-            if (v >= 0 && v < n && sees(a, row, b, j)) atomicAdd(count + v, 1u);
+        for (int j = tid; j < b1; j += kEditThreads) {
+            const int64_t v = a.tokens_dev[row0 + j] - v0;
+            if (v < 0 || v >= n) continue;
+            if (!a.mask_dev && j <= b0) {
+                atomicAdd(r.count + v, 1u);        // all positions here see it
+            } else {
+                atomicOr(r.count + v, kInBlock);
+                const int k = atomicAdd(&r.n_block, 1);
+                r.block_token[k] = (int)v;
+                r.block_at[k] = j;
+            }
         }
     if (a.bias_begin_dev) {
         const int64_t end = min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries);
         for (int64_t i = (int64_t)max(a.bias_begin_dev[s], 0) + tid; i < end; i += kEditThreads) {
             const int64_t v = a.bias_ids_dev[i] - v0;
-            if (v >= 0 && v < n) atomicMax(entry + v, (int)i + 1);
+            if (v >= 0 && v < n) atomicMax(r.entry + v, (int)i + 1);
         }
     }
     __syncthreads();
-    const Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
-                    a.presence_dev ? a.presence_dev[s] : 0.0f};
-    unsigned long long best = 0;
-    for (int i = tid; i < n; i += kEditThreads) {
-        const int64_t v = v0 + i;
-        const bool ok = !a.allowed_dev || (a.allowed_dev[row * a.allowed_stride + (v >> 5)] >> (v & 31) & 1);
-        float z = edited(load_logit<kType>(a.logits_dev, row * a.row_stride + v), count[i], p);
-        if (entry[i]) z += a.bias_dev[entry[i] - 1];
-        if (!kAccept) {
-            store_logit<kType>(e.out, row * e.out_stride + v, ok ? z : -INFINITY);
-        } else if (ok) {
-            const unsigned long long cand = (unsigned long long)logit_key(z) << 32 | (0xFFFFFFFFu - (uint32_t)v);
-            best = cand > best ? cand : best;
+    Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
+              a.presence_dev ? a.presence_dev[s] : 0.0f};
+    p.inverse = __frcp_rn(p.repetition);
+    uint32_t known = 0, seen = 0, in_block = 0;    // bits of the thread's tokens
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = M::at(i);
+        const uint32_t c = r.count[at];
+        const int entry = r.entry[at];
+        const float bias = entry ? a.bias_dev[entry - 1] : 0.0f;
+        known |= (uint32_t)((c | entry) != 0) << i;
+        seen |= (uint32_t)(c != 0) << i;
+        in_block |= (c >> 30 & 1) << i;
+        r.off[at] = __fsub_rn(c & kInBlock ? 0.0f : penalty_of(c & ~kPrompted, p), bias);
+    }
+    auto edit = [&](float z, int i, int64_t row, int b) {
+        return in_block >> i & 1 ? edited_in_block(e, r, p, z, M::at(i), row, b) : edited(z, seen >> i & 1, r.off[M::at(i)], p);
+    };
+    for (int b = b0; b < b1; ++b) {
+        M z = next;
+        const uint32_t ok = next_ok;
+        if (b + 1 < b1) fetch(b + 1);
+        const int64_t row = row0 + b;
+        if (kAccept) {
+            float x[kEach], most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) x[i] = z.get(i);
+            if (known)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (known >> i & 1) x[i] = edit(x[i], i, row, b);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (!(ok >> i & 1)) x[i] = -INFINITY;
+                most = fmaxf(most, x[i]);          // (a NaN is not taken)
+            }
+            const uint32_t key = ok ? logit_key(most) : 0, top = __reduce_max_sync(0xFFFFFFFFu, key);
+            uint32_t v = 0xFFFFFFFFu;
+            if (key == top && key) {               // the first of the thread's largest; of no numbers, the first that is allowed
+                uint32_t is = ok;
+                if (most > -INFINITY) {
+                    is = 0;
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) is |= (uint32_t)(x[i] == most) << i;
+                }
+                const int i = __ffs(is) - 1;
+                v = (uint32_t)(v0 + M::at(i));
+            }
+            v = __reduce_min_sync(0xFFFFFFFFu, v);
+            if (lane == 0) r.best[b - b0][warp] = top ? (unsigned long long)top << 32 | (0xFFFFFFFFu - v) : 0;
+        } else {
+            if (known)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (known >> i & 1) z.set(i, edit(z.get(i), i, row, b));
+            if (ok != (1u << kEach) - 1)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (!(ok >> i & 1)) z.raw(i, kType == MOE_DTYPE_FP32 ? 0xFF800000u : kType == MOE_DTYPE_BF16 ? 0xFF80u : 0xFC00u);
+            const bool in_place = e.out == a.logits_dev;
+            z.store(e.out, row * e.out_stride + v0, n, in_place ? known | ~ok : ~0u);
         }
     }
     if (!kAccept) return;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-        best = other > best ? other : best;
-    }
-    if ((tid & 31) == 0) red[tid >> 5] = best;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kEditThreads / 32; ++w) best = red[w] > best ? red[w] : best;
-        e.best[blockIdx.x] = best;
+    if (tid < b1 - b0) {
+        unsigned long long best = 0;
+        for (int w = 0; w < kEditThreads / 32; ++w) best = r.best[tid][w] > best ? r.best[tid][w] : best;
+        e.best[(row0 + b0 + tid) * e.runs + run] = best;
     }
 }
 
@@ -211,7 +420,9 @@ int check_edit(moe_mxfp4_edit_args* a) {
     if (a->row_stride < a->vocab || a->allowed_stride < (a->vocab + 31) / 32) return MOE_ERR_INVALID_ARG;
     if (a->streams == 0) return MOE_OK;
     if (!a->logits_dev || !aligned(a->logits_dev, a->dtype == MOE_DTYPE_FP32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
-    if (a->history_dev && (!a->history_lengths_dev || a->history_room < 0 || a->history_stride < a->history_room)) return MOE_ERR_INVALID_ARG;
+    if (a->history_dev && (!a->history_lengths_dev || a->history_room < 0 || a->history_room >= 1 << 29 ||
+                           a->history_stride < a->history_room))
+        return MOE_ERR_INVALID_ARG;
     if (a->bias_begin_dev && (a->bias_entries < 0 || a->bias_entries > 0x7FFFFFFF)) return MOE_ERR_INVALID_ARG;
     if (a->bias_begin_dev && a->bias_entries && (!a->bias_ids_dev || !a->bias_dev)) return MOE_ERR_INVALID_ARG;
     if (!aligned(a->mask_dev, 8)) return MOE_ERR_INVALID_ARG;
@@ -223,13 +434,31 @@ int check_edit(moe_mxfp4_edit_args* a) {
     return (int64_t)a->streams * a->block * edit_runs(a->vocab) > 0x7FFFFFFF ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// Positions of a CTA: as many as leave four CTAs for every SM.
+void group_rows(moe::EditView* e) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 1;
+    e->runs = edit_runs(e->a.vocab);
+    const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (4 * sms);
+    e->rows = (int)(most < 1 ? 1 : most > moe::kMostRows ? moe::kMostRows : most);
+    if (e->rows > e->a.block) e->rows = e->a.block;
+    e->groups = (e->a.block + e->rows - 1) / e->rows;
+}
+
 template <bool kAccept>
 int launch_edit(const moe::EditView& e, cudaStream_t st) {
-    const dim3 grid((unsigned)(e.a.streams * (int64_t)e.a.block * e.runs));
+    const dim3 grid((unsigned)((int64_t)e.a.streams * e.groups * e.runs));
+    const int size = e.a.dtype == MOE_DTYPE_FP32 ? 4 : 2;
+    const bool words = aligned(e.a.logits_dev, 16) && e.a.row_stride * size % 16 == 0 &&
+                       (kAccept || (aligned(e.out, 16) && e.out_stride * size % 16 == 0));
     auto go = [&](auto kern) { return moe::launch_dependent(kern, grid, dim3(moe::kEditThreads), 0, st, e); };
-    const cudaError_t r = e.a.dtype == MOE_DTYPE_FP32   ? go(moe::edit_kernel<MOE_DTYPE_FP32, kAccept>)
-                          : e.a.dtype == MOE_DTYPE_BF16 ? go(moe::edit_kernel<MOE_DTYPE_BF16, kAccept>)
-                                                        : go(moe::edit_kernel<MOE_DTYPE_FP16, kAccept>);
+    cudaError_t r;
+    if (e.a.dtype == MOE_DTYPE_FP32)
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP32, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP32, false, kAccept>);
+    else if (e.a.dtype == MOE_DTYPE_BF16)
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_BF16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_BF16, false, kAccept>);
+    else
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP16, false, kAccept>);
     return r == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -250,7 +479,7 @@ int moe_mxfp4_edit_logits(const moe_mxfp4_edit_args* args, void* out_dev, int64_
     if (out_dev == e.a.logits_dev && out_stride != e.a.row_stride) return MOE_ERR_INVALID_ARG;
     e.out = out_dev;
     e.out_stride = out_stride;
-    e.runs = edit_runs(e.a.vocab);
+    group_rows(&e);
     return launch_edit<false>(e, static_cast<cudaStream_t>(stream));
 }
 
@@ -274,7 +503,7 @@ int moe_mxfp4_accept_edited(const moe_mxfp4_edit_args* args, int32_t* target_dev
     moe_mxfp4_accept_edited_bytes(e.a.streams, e.a.block, e.a.vocab, &need);
     if (!workspace_dev || !aligned(workspace_dev, 8) || workspace_bytes < need) return MOE_ERR_WORKSPACE;
     e.best = static_cast<unsigned long long*>(workspace_dev);
-    e.runs = edit_runs(e.a.vocab);
+    group_rows(&e);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     st = launch_edit<true>(e, cs);
     if (st != MOE_OK) return st;
