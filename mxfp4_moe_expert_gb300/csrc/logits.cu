@@ -64,7 +64,8 @@ struct EditRun {
         float off[kEditRun];                       // what is taken off it (of one in the block: the bias alone)
     };
     int block_token[64], block_at[64], n_block;    // tokens of the block in the run that only some of the CTA's positions see
-    unsigned long long best[kMostRows][kEditThreads / 32];
+    uint32_t top[kMostRows];                       // acceptance: largest key so far of a position,
+    unsigned long long best[kMostRows][kEditThreads / 32];   // and each warp's with its token (0: another warp has a larger one)
 };
 
 // A token of the block: its edited logit at position b.
@@ -106,6 +107,46 @@ struct Mine {
     __device__ __forceinline__ float get(int i) const {
         if (kType == MOE_DTYPE_FP32) return __uint_as_float(bits[i]);
         return to_f32<kType>((uint16_t)(i & 1 ? bits[i / 2] >> 16 : bits[i / 2]));
+    }
+    // The largest of the tokens of `which` (-inf: of none; NaN is not taken).  16-bit logits in pairs: -inf is added to those left out.
+    __device__ __forceinline__ float most(uint32_t which) const {
+        constexpr uint32_t all = (1u << kEach) - 1;
+        if (kType == MOE_DTYPE_FP32) {
+            float m = -INFINITY;
+            if (__all_sync(0xFFFFFFFFu, which == all)) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) m = fmaxf(m, get(i));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (which >> i & 1) m = fmaxf(m, get(i));
+            }
+            return m;
+        }
+        uint32_t m = kNone * 0x10001u;
+        if (__all_sync(0xFFFFFFFFu, which == all)) {
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) m = max2(m, bits[i]);
+        } else {
+#pragma unroll
+            for (int w = 0; w < kEach / 8; ++w) {
+                const uint32_t out = (~which >> (8 * w) & 0xFFu) * 0x8001u;      // bits 2 p and 2 p + 1 of eight, 16 apart
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = max2(m, add2(bits[4 * w + i], (out >> (2 * i) & 0x10001u) * kNone));
+            }
+        }
+        return fmaxf(to_f32<kType>((uint16_t)m), to_f32<kType>((uint16_t)(m >> 16)));
+    }
+    static constexpr uint32_t kNone = kType == MOE_DTYPE_FP32 ? 0xFF800000u : kType == MOE_DTYPE_BF16 ? 0xFF80u : 0xFC00u;   // -inf
+    static __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+        if (kType == MOE_DTYPE_BF16) asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+        else asm("max.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+        return x;
+    }
+    static __device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
+        if (kType == MOE_DTYPE_BF16) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+        else asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+        return x;
     }
     __device__ __forceinline__ void raw(int i, uint32_t x) {
         if (kType == MOE_DTYPE_FP32) bits[i] = x;
@@ -219,8 +260,9 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
     // what is known of the run's tokens
     for (int i = tid; i < kEditRun / 4; i += kEditThreads) {
         reinterpret_cast<uint4*>(r.count)[i] = make_uint4(0, 0, 0, 0);
-        reinterpret_cast<uint4*>(r.entry)[i] = make_uint4(0, 0, 0, 0);
+        if (a.bias_begin_dev) reinterpret_cast<uint4*>(r.entry)[i] = make_uint4(0, 0, 0, 0);
     }
+    if (tid < kMostRows) r.top[tid] = 0;
     if (tid == 0) r.n_block = 0;
     __syncthreads();
     if (a.history_dev) {
@@ -278,14 +320,20 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
     uint32_t known = 0, seen = 0, in_block = 0;    // bits of the thread's tokens
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int at = M::at(i);
-        const uint32_t c = r.count[at];
-        const int entry = r.entry[at];
-        const float bias = entry ? a.bias_dev[entry - 1] : 0.0f;
-        known |= (uint32_t)((c | entry) != 0) << i;
+        const uint32_t c = r.count[M::at(i)];
         seen |= (uint32_t)(c != 0) << i;
         in_block |= (c >> 30 & 1) << i;
-        r.off[at] = __fsub_rn(c & kInBlock ? 0.0f : penalty_of(c & ~kPrompted, p), bias);
+    }
+    known = seen;
+    if (a.bias_begin_dev)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) known |= (uint32_t)(r.entry[M::at(i)] != 0) << i;
+    // where no lane of the warp knows anything of its i-th token, the warp passes it over together
+    const uint32_t warp_knows = __reduce_or_sync(0xFFFFFFFFu, known);
+    for (uint32_t left = known; left; left &= left - 1) {
+        const int i = __ffs(left) - 1, at = M::at(i), entry = a.bias_begin_dev ? r.entry[at] : 0;
+        const float bias = entry ? a.bias_dev[entry - 1] : 0.0f;
+        r.off[at] = __fsub_rn(in_block >> i & 1 ? 0.0f : penalty_of(r.count[at] & ~kPrompted, p), bias);
     }
     auto edit = [&](float z, int i, int64_t row, int b) {
         return in_block >> i & 1 ? edited_in_block(e, r, p, z, M::at(i), row, b) : edited(z, seen >> i & 1, r.off[M::at(i)], p);
@@ -296,41 +344,52 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
         if (b + 1 < b1) fetch(b + 1);
         const int64_t row = row0 + b;
         if (kAccept) {
-            float x[kEach], most = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) x[i] = z.get(i);
-            if (known)
+            // what is known of is edited one by one, in fp32; the rest is compared as it is
+            const uint32_t rest = ok & ~known;
+            float most = -INFINITY;
+            int which = -1;
+            if (warp_knows)
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
-                    if (known >> i & 1) x[i] = edit(x[i], i, row, b);
+                    if (warp_knows >> i & 1)
+                        if ((known & ok) >> i & 1) {
+                            const float x = edit(z.get(i), i, row, b);
+                            if (x > most) {
+                                most = x;
+                                which = i;
+                            }
+                        }
+            const float clean = z.most(rest);
+            const float all = fmaxf(clean, most);
+            const uint32_t key = ok ? logit_key(all) : 0, top = __reduce_max_sync(0xFFFFFFFFu, key);
+            unsigned long long best = 0;
+            if (top && top >= *static_cast<volatile uint32_t*>(r.top + (b - b0))) {
+                uint32_t v = 0xFFFFFFFFu;
+                if (key == top) {                  // the first of the thread's largest; of no numbers, the first that is allowed
+                    uint32_t is = ok;
+                    if (all > -INFINITY) {
+                        is = most == all ? 1u << which : 0;
+                        if (clean == all)
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                if (!(ok >> i & 1)) x[i] = -INFINITY;
-                most = fmaxf(most, x[i]);          // (a NaN is not taken)
-            }
-            const uint32_t key = ok ? logit_key(most) : 0, top = __reduce_max_sync(0xFFFFFFFFu, key);
-            uint32_t v = 0xFFFFFFFFu;
-            if (key == top && key) {               // the first of the thread's largest; of no numbers, the first that is allowed
-                uint32_t is = ok;
-                if (most > -INFINITY) {
-                    is = 0;
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) is |= (uint32_t)(x[i] == most) << i;
+                            for (int i = 0; i < kEach; ++i) is |= (uint32_t)(z.get(i) == all) << i & rest;
+                    }
+                    v = (uint32_t)(v0 + M::at(__ffs(is) - 1));
                 }
-                const int i = __ffs(is) - 1;
-                v = (uint32_t)(v0 + M::at(i));
+                v = __reduce_min_sync(0xFFFFFFFFu, v);
+                best = (unsigned long long)top << 32 | (0xFFFFFFFFu - v);
+                if (lane == 0) atomicMax(r.top + (b - b0), top);
             }
-            v = __reduce_min_sync(0xFFFFFFFFu, v);
-            if (lane == 0) r.best[b - b0][warp] = top ? (unsigned long long)top << 32 | (0xFFFFFFFFu - v) : 0;
+            if (lane == 0) r.best[b - b0][warp] = best;
         } else {
-            if (known)
+            if (warp_knows)
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
-                    if (known >> i & 1) z.set(i, edit(z.get(i), i, row, b));
+                    if (warp_knows >> i & 1)
+                        if (known >> i & 1) z.set(i, edit(z.get(i), i, row, b));
             if (ok != (1u << kEach) - 1)
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
-                    if (!(ok >> i & 1)) z.raw(i, kType == MOE_DTYPE_FP32 ? 0xFF800000u : kType == MOE_DTYPE_BF16 ? 0xFF80u : 0xFC00u);
+                    if (!(ok >> i & 1)) z.raw(i, M::kNone);
             const bool in_place = e.out == a.logits_dev;
             z.store(e.out, row * e.out_stride + v0, n, in_place ? known | ~ok : ~0u);
         }
