@@ -7,7 +7,6 @@
 // nothing is kept from call to call.
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <cmath>
 
 #include "cache.cuh"
@@ -15,11 +14,9 @@
 namespace moe {
 
 constexpr int kEditThreads = 256;
-constexpr int kEach = 16;                          // tokens of the vocabulary of a thread, the same ones for every position
-constexpr int kEditRun = kEach * kEditThreads;     // ... and of a CTA
+constexpr int kEditRun = 4096;                     // tokens of the vocabulary of a CTA
+constexpr int kParts = 4;                          // of a run, at most: a warp's work at a time
 constexpr int kMostRows = 16;                      // positions of a CTA, at most
-constexpr int kMostStages = 5;                     // of the ring of logits on their way
-constexpr int kEditShared = 70 * 1024;             // shared memory of a CTA, at most: three fit an SM
 constexpr uint32_t kPrompted = 1u << 31;           // of a count: the prompt has the token, ...
 constexpr uint32_t kInBlock = 1u << 30;            // ... and so has the block, at positions that not all of the CTA's see
 
@@ -29,7 +26,7 @@ struct EditView {
     int64_t out_stride;
     unsigned long long* best;                      // acceptance: [rows, runs] largest (key, ~token) of a run, 0 = none
     int runs, rows, groups;                        // of a CTA's positions: how many, and groups of them in a block
-    int stages;                                    // rows of the ring
+    int parts;                                     // of a run: a power of two up to kParts
 };
 
 struct Penalty {
@@ -69,209 +66,135 @@ __device__ __forceinline__ uint16_t from_f32(float x) {
     return kType == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
 }
 
-__device__ __forceinline__ void copy_16(void* smem, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_4(void* smem, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits for the oldest stage of a ring that is full.
-__device__ __forceinline__ void copies_wait(int stages) {
-    if (stages == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else asm volatile("cp.async.wait_group 4;" ::: "memory");
-}
-
-// A position's logits of the run, in shared memory: token v at place v.
+// Logits as bits of their type.
 template <int kType>
-struct Row {
+struct Bits {
     static constexpr int kSize = kType == MOE_DTYPE_FP32 ? 4 : 2;
     static constexpr uint32_t kNone = kType == MOE_DTYPE_FP32 ? 0xFF800000u : kType == MOE_DTYPE_BF16 ? 0xFF80u : 0xFC00u;   // -inf
-    char* p;
-    __device__ __forceinline__ float get(int v) const {
-        if (kType == MOE_DTYPE_FP32) return reinterpret_cast<const float*>(p)[v];
-        return to_f32<kType>(reinterpret_cast<const uint16_t*>(p)[v]);
+    static __device__ __forceinline__ uint32_t read(const char* row, int v) {
+        return kType == MOE_DTYPE_FP32 ? reinterpret_cast<const uint32_t*>(row)[v] : reinterpret_cast<const uint16_t*>(row)[v];
     }
-    __device__ __forceinline__ void put(int v, float z) const {
-        if (kType == MOE_DTYPE_FP32) reinterpret_cast<float*>(p)[v] = z;
-        else reinterpret_cast<uint16_t*>(p)[v] = from_f32<kType>(z);
+    static __device__ __forceinline__ void write(char* row, int v, uint32_t bits) {
+        if (kType == MOE_DTYPE_FP32) reinterpret_cast<uint32_t*>(row)[v] = bits;
+        else reinterpret_cast<uint16_t*>(row)[v] = (uint16_t)bits;
     }
-    __device__ __forceinline__ void put_none(int v) const {
-        if (kType == MOE_DTYPE_FP32) reinterpret_cast<uint32_t*>(p)[v] = kNone;
-        else reinterpret_cast<uint16_t*>(p)[v] = (uint16_t)kNone;
+    static __device__ __forceinline__ float value(uint32_t bits) {
+        return kType == MOE_DTYPE_FP32 ? __uint_as_float(bits) : to_f32<kType>((uint16_t)bits);
+    }
+    static __device__ __forceinline__ uint32_t of(float z) { return kType == MOE_DTYPE_FP32 ? __float_as_uint(z) : from_f32<kType>(z); }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        if (kType == MOE_DTYPE_BF16) asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        else asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        return a;
+    }
+    static __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+        if (kType == MOE_DTYPE_BF16) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        else asm("add.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        return a;
     }
 };
 
-// A thread's kEach tokens of the run, as bits of the logits' type: words of 16 bytes that lie kEditThreads apart
-// (kWords, where rows begin on 16 bytes), or single ones.  Pointers are of the run's first token; n: tokens of the run.
-template <int kType, bool kWords>
-struct Mine {
-    static constexpr int kSize = Row<kType>::kSize, kPer = 16 / kSize, kWarps = kEditThreads / 32;
-    static constexpr uint32_t kAll = (1u << kEach) - 1, kNone = Row<kType>::kNone;
-    uint32_t bits[kEach * kSize / 4];
-    static __device__ __forceinline__ int at(int i) {      // ascending in i
-        return kWords ? (i / kPer * kEditThreads + (int)threadIdx.x) * kPer + i % kPer : i * kEditThreads + (int)threadIdx.x;
-    }
-    __device__ __forceinline__ float get(int i) const {
-        if (kType == MOE_DTYPE_FP32) return __uint_as_float(bits[i]);
-        return to_f32<kType>((uint16_t)(i & 1 ? bits[i / 2] >> 16 : bits[i / 2]));
-    }
-    __device__ __forceinline__ void raw(int i, uint32_t x) {
-        if (kType == MOE_DTYPE_FP32) bits[i] = x;
-        else bits[i / 2] = i & 1 ? (bits[i / 2] & 0xFFFFu) | x << 16 : (bits[i / 2] & 0xFFFF0000u) | x;
-    }
-    __device__ __forceinline__ uint32_t raw(int i) const {
-        return kType == MOE_DTYPE_FP32 ? bits[i] : i & 1 ? bits[i / 2] >> 16 : bits[i / 2] & 0xFFFFu;
-    }
-    static __device__ __forceinline__ uint32_t read(const void* p, int v) {
-        return kType == MOE_DTYPE_FP32 ? static_cast<const uint32_t*>(p)[v] : static_cast<const uint16_t*>(p)[v];
-    }
-    static __device__ __forceinline__ void write(void* p, int v, uint32_t x) {
-        if (kType == MOE_DTYPE_FP32) static_cast<uint32_t*>(p)[v] = x;
-        else static_cast<uint16_t*>(p)[v] = (uint16_t)x;
-    }
-
-    // kWords: the thread's words into a row of the ring.
-    static __device__ __forceinline__ void copy(char* row, const char* src, int n) {
+// A warp's four loads of 512 bytes of a row that begins on 16 bytes: a lane has 4 words of kPer tokens, and a bit for each
+// of its tokens (token i of word w: bit w kPer + i).
+template <int kType>
+struct Batch {
+    using B = Bits<kType>;
+    static constexpr int kPer = 16 / B::kSize, kTokens = 4 * 32 * kPer, kLane = 4 * kPer;
+    static constexpr uint32_t kAll = kLane == 32 ? 0xFFFFFFFFu : (1u << (kLane & 31)) - 1;
+    uint4 x[4];
+    uint32_t ok;                                   // allowed
+    static __device__ __forceinline__ int token(int w, int lane) { return (w * 32 + lane) * kPer; }
+    // row, allowed: of the batch's first token.
+    __device__ __forceinline__ void load(const char* row, const uint32_t* allowed, int lane) {
+        const uint4* p = reinterpret_cast<const uint4*>(row) + lane;
 #pragma unroll
-        for (int w = 0; w < kEach / kPer; ++w) {
-            const int v = at(w * kPer);
-            if (n == kEditRun || v + kPer <= n) copy_16(row + v * kSize, src + v * kSize);
-            else
-                for (int i = v; i < n; ++i) write(row, i, read(src, i));   // (the vocabulary's last word)
-        }
-    }
-    __device__ __forceinline__ void take(const char* row) {
-        if (kWords) {
+        for (int w = 0; w < 4; ++w) x[w] = __ldcs(p + 32 * w);
+        ok = kAll;
+        if (allowed) {
+            const uint8_t* q = reinterpret_cast<const uint8_t*>(allowed) + (kPer == 8 ? lane : lane / 2);
+            ok = 0;
 #pragma unroll
-            for (int w = 0; w < kEach / kPer; ++w) {
-                const uint4 x = *reinterpret_cast<const uint4*>(row + at(w * kPer) * kSize);
-                bits[4 * w] = x.x;
-                bits[4 * w + 1] = x.y;
-                bits[4 * w + 2] = x.z;
-                bits[4 * w + 3] = x.w;
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t t = __ldg(q + 4 * kPer * w);
+                ok |= (kPer == 8 ? t : t >> (4 * (lane & 1)) & 15u) << (kPer * w);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) raw(i, read(row, at(i)));
         }
     }
-    // Single tokens: from memory into registers, and on into the ring.
-    __device__ __forceinline__ void load(const char* src, int n) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) raw(i, at(i) < n ? read(src, at(i)) : 0);
+    static __device__ __forceinline__ uint32_t part(const uint4& t, int i) { return i == 0 ? t.x : i == 1 ? t.y : i == 2 ? t.z : t.w; }
+    __device__ __forceinline__ uint32_t get(int w, int i) const {
+        if (kType == MOE_DTYPE_FP32) return part(x[w], i);
+        const uint32_t t = part(x[w], i / 2);
+        return i & 1 ? t >> 16 : t & 0xFFFFu;
     }
-    __device__ __forceinline__ void spill(char* row) const {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) write(row, at(i), raw(i));
-    }
-    // To the output: the tokens of `which`, and what shares a word with them.
-    __device__ __forceinline__ void store(char* dst, int n, uint32_t which) const {
-        if (kWords) {
-#pragma unroll
-            for (int w = 0; w < kEach / kPer; ++w) {
-                const int v = at(w * kPer);
-                if (!(which >> (w * kPer) & ((1u << kPer) - 1))) continue;
-                if (n == kEditRun || v + kPer <= n) {
-                    *reinterpret_cast<uint4*>(dst + v * kSize) = make_uint4(bits[4 * w], bits[4 * w + 1], bits[4 * w + 2], bits[4 * w + 3]);
-                } else {
-#pragma unroll
-                    for (int i = w * kPer; i < w * kPer + kPer; ++i)
-                        if (at(i) < n) write(dst, at(i), raw(i));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if ((which >> i & 1) && at(i) < n) write(dst, at(i), raw(i));
-        }
-    }
-
-    // The grammar's words of a warp's tokens: kEach of them, on their way (kWords) ...
-    static __device__ __forceinline__ int word_of(int k) { return (k / kPer * kWarps + (int)(threadIdx.x >> 5)) * kPer + k % kPer; }
-    static __device__ __forceinline__ void copy_allowed(uint32_t* to, const uint32_t* words, int n) {
-        const int lane = threadIdx.x & 31;
-        if (lane < kEach && 32 * word_of(lane) < n) copy_4(to + lane, words + word_of(lane));
-    }
-    // ... and a bit for each of the thread's tokens, ...
-    static __device__ __forceinline__ uint32_t take_allowed(const uint32_t* from) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int w = 0; w < kEach / kPer; ++w) {
-            const int bit = (threadIdx.x & 31) * kPer;
-            x |= (from[w * kPer + bit / 32] >> (bit & 31) & ((1u << kPer) - 1)) << (w * kPer);
-        }
-        return x;
-    }
-    // ... or for token v of the warp's.
-    static __device__ __forceinline__ bool is_allowed(const uint32_t* from, int v) {
-        return from[(v >> 5) / (kPer * kWarps) * kPer + (v >> 5) % kPer] >> (v & 31) & 1;
-    }
-    static __device__ __forceinline__ uint32_t load_allowed(const uint32_t* words, int n) {
-        uint32_t ok = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (at(i) < n) ok |= (__ldg(words + (at(i) >> 5)) >> (at(i) & 31) & 1) << i;
-        return ok;
-    }
-    static __device__ __forceinline__ uint32_t in_run(int n) {
-        if (n == kEditRun) return kAll;
-        uint32_t in = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) in |= (uint32_t)(at(i) < n) << i;
-        return in;
-    }
-
-    // The largest of the tokens of `which` (-inf: of none; NaN is not taken).  16-bit logits in pairs: -inf is added to those left out.
-    __device__ __forceinline__ float most(uint32_t which) const {
-        const bool all = __all_sync(0xFFFFFFFFu, which == kAll);
+    // The largest of those with their bit (-inf: of none; NaN is not taken).  16-bit logits in pairs: -inf is added to those left out.
+    __device__ __forceinline__ float most(uint32_t bits) const {
+        const bool all = __all_sync(0xFFFFFFFFu, bits == kAll);
         if (kType == MOE_DTYPE_FP32) {
             float m = -INFINITY;
+            if (all) {
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (all || (which >> i & 1)) m = fmaxf(m, get(i));
+                for (int w = 0; w < 4; ++w)
+                    m = fmaxf(m, fmaxf(fmaxf(B::value(x[w].x), B::value(x[w].y)), fmaxf(B::value(x[w].z), B::value(x[w].w))));
+            } else {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (bits >> (4 * w + i) & 1) m = fmaxf(m, B::value(part(x[w], i)));
+            }
             return m;
         }
-        uint32_t m = kNone * 0x10001u;
+        uint32_t m = B::kNone * 0x10001u;
         if (all) {
 #pragma unroll
-            for (int i = 0; i < kEach / 2; ++i) m = max2(m, bits[i]);
+            for (int w = 0; w < 4; ++w) m = B::max2(m, B::max2(B::max2(x[w].x, x[w].y), B::max2(x[w].z, x[w].w)));
         } else {
 #pragma unroll
-            for (int w = 0; w < kEach / 8; ++w) {
-                const uint32_t out = (~which >> (8 * w) & 0xFFu) * 0x8001u;      // bits 2 p and 2 p + 1 of eight, 16 apart
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t out = (~bits >> (8 * w) & 0xFFu) * 0x8001u;       // bits 2 i and 2 i + 1, 16 apart
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m = max2(m, add2(bits[4 * w + i], (out >> (2 * i) & 0x10001u) * kNone));
+                for (int i = 0; i < 4; ++i) m = B::max2(m, B::add2(part(x[w], i), (out >> (2 * i) & 0x10001u) * B::kNone));
             }
         }
         return fmaxf(to_f32<kType>((uint16_t)m), to_f32<kType>((uint16_t)(m >> 16)));
     }
-    static __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
-        if (kType == MOE_DTYPE_BF16) asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
-        else asm("max.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
-        return x;
+    // The first token with its bit and the value z; -1: none.
+    __device__ __forceinline__ int find(uint32_t bits, float z, int lane) const {
+        uint32_t is = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) is |= (uint32_t)(B::value(get(w, i)) == z) << (w * kPer + i);
+        is &= bits;
+        const int k = __ffs(is) - 1;
+        return k < 0 ? -1 : token(k / kPer, lane) + k % kPer;
     }
-    static __device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
-        if (kType == MOE_DTYPE_BF16) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
-        else asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
-        return x;
+    // Those without their bit as -inf.
+    __device__ __forceinline__ void hide() {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (kType == MOE_DTYPE_FP32) {
+                if (!(ok >> (4 * w) & 1)) x[w].x = B::kNone;
+                if (!(ok >> (4 * w + 1) & 1)) x[w].y = B::kNone;
+                if (!(ok >> (4 * w + 2) & 1)) x[w].z = B::kNone;
+                if (!(ok >> (4 * w + 3) & 1)) x[w].w = B::kNone;
+            } else {
+                const uint32_t out = (~ok >> (8 * w) & 0xFFu) * 0x8001u;
+                auto masked = [&](uint32_t t, int i) {
+                    const uint32_t m = (out >> (2 * i) & 0x10001u) * 0xFFFFu;
+                    return (t & ~m) | (B::kNone * 0x10001u & m);
+                };
+                x[w] = make_uint4(masked(x[w].x, 0), masked(x[w].y, 1), masked(x[w].z, 2), masked(x[w].w, 3));
+            }
+        }
     }
 };
 
-// Counts a token of the history.
-__device__ __forceinline__ void count_token(uint32_t* count, int token, int64_t v0, int n, bool prompt) {
-    const uint32_t v = (uint32_t)token - (uint32_t)v0;
-    if (v >= (uint32_t)n) return;
-    if (prompt) atomicOr(count + v, kPrompted);
-    else atomicAdd(count + v, 1u);
-}
-__device__ __forceinline__ void count_history(uint32_t* count, const int* h, int len, int prompt, int64_t v0, int n) {
-    // (many loads at once, before any of them is counted: one after the other takes a round trip each)
+// Calls f(token, whether the prompt has it) for the tokens of the history from place i0 on that fall to this thread.  (Many loads at
+// once, before any of them is looked at: one after the other takes a round trip each.)
+template <class F>
+__device__ __forceinline__ void for_history(const int* h, int i0, int len, int prompt, F f) {
     const int tid = threadIdx.x;
-    int i0 = 0;
     if (aligned_to_16(h))
         for (; i0 + 16 * kEditThreads <= len; i0 += 16 * kEditThreads) {
             int4 t[4];
@@ -280,10 +203,10 @@ __device__ __forceinline__ void count_history(uint32_t* count, const int* h, int
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = i0 + 4 * (k * kEditThreads + tid);
-                count_token(count, t[k].x, v0, n, i < prompt);
-                count_token(count, t[k].y, v0, n, i + 1 < prompt);
-                count_token(count, t[k].z, v0, n, i + 2 < prompt);
-                count_token(count, t[k].w, v0, n, i + 3 < prompt);
+                f(t[k].x, i < prompt);
+                f(t[k].y, i + 1 < prompt);
+                f(t[k].z, i + 2 < prompt);
+                f(t[k].w, i + 3 < prompt);
             }
         }
     for (; i0 < len; i0 += 8 * kEditThreads) {
@@ -291,78 +214,93 @@ __device__ __forceinline__ void count_history(uint32_t* count, const int* h, int
 #pragma unroll
         for (int k = 0; k < 8; ++k) t[k] = i0 + k * kEditThreads + tid < len ? h[i0 + k * kEditThreads + tid] : -1;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) count_token(count, t[k], v0, n, i0 + k * kEditThreads + tid < prompt);
+        for (int k = 0; k < 8; ++k) f(t[k], i0 + k * kEditThreads + tid < prompt);
     }
 }
+__device__ __forceinline__ void prefetch_run(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
-// A CTA per stream, group of positions and run of the vocabulary.  It counts the run's tokens of the history once;
-// each warp lists those of its tokens that something is known of, with what is taken off them.  The logits of the
-// positions to come are on their way meanwhile, into a ring of rows in shared memory, which each thread copies its own
-// words of (rows that do not begin on 16 bytes: the next one, in registers).  Of each position a warp edits the tokens on its
-// list in the ring, a lane a token, and then takes its row as it is: a vocabulary has few tokens that a stream has
-// said, and looking for them in every row took four times what the rest does.
+__device__ __forceinline__ bool bit_at(const uint32_t* words, int v) { return words[v >> 5] >> (v & 31) & 1; }
+
+// A CTA per run of the vocabulary, stream and group of positions.  It counts the run's tokens of the history once and
+// lists those that something is known of, with what is taken off them: few of a vocabulary, so they are edited apart
+// from the rest, a lane a token, and passing them over costs a bit each.  Then a warp takes a position's run, or a part of it,
+// at a time: the rest is copied, or compared, as it is.  Low tokens are the common ones and have the longest lists, so their
+// CTAs come first.
 template <int kType, bool kWords, bool kAccept>
 __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
-    using M = Mine<kType, kWords>;
-    constexpr int kWarps = kEditThreads / 32, kRowBytes = kEditRun * M::kSize;
+    using B = Bits<kType>;
+    using X = Batch<kType>;
+    constexpr int kWarps = kEditThreads / 32, kSpan = kEditRun / kParts;
     constexpr uint32_t kListSeen = 1u << 15, kListInBlock = 1u << 14;
     extern __shared__ uint4 dynamic[];
-    __shared__ int block_token[64], block_at[64], n_block;      // tokens of the block that only some of the CTA's positions see
-    __shared__ uint32_t top_key[kMostRows];                     // acceptance: largest key so far of a position,
-    __shared__ unsigned long long warp_best[kMostRows][kWarps]; // and each warp's with its token (0: another warp has a larger one)
-    __shared__ uint32_t grammar[kMostStages][kWarps][kEach];
+    __shared__ int block_token[64], block_at[64], n_block;       // tokens of the block that only some of the CTA's positions see
+    __shared__ int listed[kParts];                               // tokens on the list, by parts of the run
+    __shared__ uint32_t known[kEditRun / 32];                    // a bit for each of them,
+    __shared__ uint32_t known_lane[kEditRun / X::kTokens][32];   // and as the lanes have them
+    __shared__ unsigned long long part_best[kMostRows * kParts]; // acceptance: (key, ~token)
     const moe_mxfp4_edit_args& a = e.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int run = blockIdx.x % e.runs, sg = blockIdx.x / e.runs, s = sg / e.groups, b0 = (sg - s * e.groups) * e.rows;
+    const int sgs = a.streams * e.groups, run = blockIdx.x / sgs, sg = blockIdx.x - run * sgs, s = sg / e.groups, b0 = (sg - s * e.groups) * e.rows;
     const int64_t v0 = (int64_t)run * kEditRun, row0 = (int64_t)s * a.block;
     const int n = (int)min((int64_t)kEditRun, a.vocab - v0);
     uint32_t* const count = reinterpret_cast<uint32_t*>(dynamic);              // later, as fp32: what is taken off the token
-    uint16_t* const list = reinterpret_cast<uint16_t*>(count + kEditRun) + warp * 32 * kEach;
-    int* const entry = a.bias_begin_dev ? reinterpret_cast<int*>(dynamic + kEditRun / 4 + kEditRun / 8) : nullptr;
-    float* const bias = reinterpret_cast<float*>(entry);       // 1 + the last entry of a token, then its bias
-    char* const ring = reinterpret_cast<char*>(dynamic + kEditRun / 4 + kEditRun / 8 + (entry ? kEditRun / 4 : 0));
+    uint16_t* const list = reinterpret_cast<uint16_t*>(count + kEditRun);
+    int* const entry = a.bias_begin_dev ? reinterpret_cast<int*>(list + kEditRun) : nullptr;
+    float* const bias = reinterpret_cast<float*>(entry);         // 1 + the last entry of a token, then its bias
     grid_dependency_wait();
     const int b1 = min(min(b0 + e.rows, a.block), used_positions(a, s));
     if (b0 >= b1) return;
-    // rows on their way
-    const char* src = static_cast<const char*>(a.logits_dev) + ((row0 + b0) * a.row_stride + v0) * M::kSize;
-    const uint32_t* words = a.allowed_dev ? a.allowed_dev + (row0 + b0) * a.allowed_stride + (v0 >> 5) : nullptr;
-    const uint32_t in_run = M::in_run(n);
-    M next;
-    uint32_t next_ok = in_run;
-    int ahead = b0, ahead_stage = 0, stage = 0;
-    auto fetch = [&] {
-        if (ahead < b1) {
-            if (kWords) {
-                M::copy(ring + ahead_stage * kRowBytes, src, n);
-                if (words) M::copy_allowed(grammar[ahead_stage][warp], words, n);
-                if (++ahead_stage == e.stages) ahead_stage = 0;
-            } else {
-                next.load(src, n);
-                if (words) next_ok = M::load_allowed(words, n);
-            }
-            src += a.row_stride * M::kSize;
-            if (words) words += a.allowed_stride;
-            ++ahead;
-        }
-        if (kWords) copies_commit();
-    };
-    for (int i = 0; i < (kWords ? e.stages : 1); ++i) fetch();
-    // what is known of the run's tokens
-    for (int i = tid; i < kEditRun / 4; i += kEditThreads) {
-        reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
-        if (entry) reinterpret_cast<uint4*>(entry)[i] = make_uint4(0, 0, 0, 0);
-    }
-    if (tid < kMostRows) top_key[tid] = 0;
+    // the rows are on their way to L2 meanwhile
+    if (kWords && tid < b1 - b0 && n * B::kSize >= 16)
+        prefetch_run(static_cast<const char*>(a.logits_dev) + ((row0 + b0 + tid) * a.row_stride + v0) * B::kSize, (uint32_t)(n * B::kSize) & ~15u);
+    // what is known of the run's tokens: which they are, then how often they were said, then what is taken off them
+    if (tid < kEditRun / 32) known[tid] = 0;
+    for (int i = tid; i < kEditRun / X::kTokens * 32; i += kEditThreads) known_lane[0][i] = 0;
+    if (tid < kParts) listed[tid] = 0;
     if (tid == 0) n_block = 0;
+    const int* const history = a.history_dev ? a.history_dev + s * a.history_stride : nullptr;
+    const int len = history ? (int)min((int64_t)a.history_lengths_dev[s], a.history_room) : 0;
+    const int prompt = history && a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0;
+    const int bias_end = entry ? (int)min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries) : 0;
+    const int bias_begin = entry ? max(a.bias_begin_dev[s], 0) + tid : 0;
+    int early[8];                                  // the first of the history stay in registers
+#pragma unroll
+    for (int k = 0; k < 8; ++k) early[k] = k * kEditThreads + tid < len ? history[k * kEditThreads + tid] : -1;
     __syncthreads();
-    if (a.history_dev)
-        count_history(count, a.history_dev + s * a.history_stride, (int)min((int64_t)a.history_lengths_dev[s], a.history_room),
-                      a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0, v0, n);
+    auto mark = [&](int token) {
+        const uint32_t v = (uint32_t)token - (uint32_t)v0;
+        if (v >= (uint32_t)n) return;
+        const uint32_t bit = 1u << (v & 31);
+        if (*static_cast<volatile uint32_t*>(known + (v >> 5)) & bit) return;
+        if (atomicOr(known + (v >> 5), bit) & bit) return;
+        count[v] = 0;
+        if (entry) entry[v] = 0;
+        const int part = v / kSpan, in = v % X::kTokens, word = in / X::kPer;
+        list[part * kSpan + atomicAdd(listed + part, 1)] = (uint16_t)v;
+        atomicOr(&known_lane[v / X::kTokens][word % 32], 1u << (word / 32 * X::kPer + in % X::kPer));
+    };
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mark(early[k]);
+    for_history(history, 8 * kEditThreads, len, prompt, [&](int token, bool) { mark(token); });
+    if (a.tokens_dev)
+        for (int j = tid; j < b1; j += kEditThreads) mark(a.tokens_dev[row0 + j]);
+    for (int i = bias_begin; i < bias_end; i += kEditThreads) mark(a.bias_ids_dev[i]);
+    __syncthreads();
+    auto said = [&](int token, bool prompted) {
+        const uint32_t v = (uint32_t)token - (uint32_t)v0;
+        if (v >= (uint32_t)n) return;
+        if (prompted) atomicOr(count + v, kPrompted);
+        else atomicAdd(count + v, 1u);
+    };
+#pragma unroll
+    for (int k = 0; k < 8; ++k) said(early[k], k * kEditThreads + tid < prompt);
+    for_history(history, 8 * kEditThreads, len, prompt, said);
     if (a.tokens_dev)
         for (int j = tid; j < b1; j += kEditThreads) {
-            const int64_t v = a.tokens_dev[row0 + j] - v0;
-            if (v < 0 || v >= n) continue;
+            const uint32_t v = (uint32_t)a.tokens_dev[row0 + j] - (uint32_t)v0;
+            if (v >= (uint32_t)n) continue;
             if (!a.mask_dev && j <= b0) {
                 atomicAdd(count + v, 1u);          // all positions here see it
             } else {
@@ -372,128 +310,141 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
                 block_at[k] = j;
             }
         }
-    if (entry) {
-        const int64_t end = min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries);
-        for (int64_t i = (int64_t)max(a.bias_begin_dev[s], 0) + tid; i < end; i += kEditThreads) {
-            const int64_t v = a.bias_ids_dev[i] - v0;
-            if (v >= 0 && v < n) atomicMax(entry + v, (int)i + 1);
-        }
+    for (int i = bias_begin; i < bias_end; i += kEditThreads) {
+        const uint32_t v = (uint32_t)a.bias_ids_dev[i] - (uint32_t)v0;
+        if (v < (uint32_t)n) atomicMax(entry + v, i + 1);
     }
     Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
               a.presence_dev ? a.presence_dev[s] : 0.0f};
     p.inverse = __frcp_rn(p.repetition);
     __syncthreads();
-    uint32_t known = 0;                            // bits of the thread's tokens
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) known |= (uint32_t)(count[M::at(i)] != 0) << i;
-    if (entry)
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) known |= (uint32_t)(entry[M::at(i)] != 0) << i;
-    int place = __popc(known), listed;             // of the thread's tokens in the warp's list
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, place, o);
-        if (lane >= o) place += x;
-    }
-    listed = __shfl_sync(0xFFFFFFFFu, place, 31);
-    place -= __popc(known);
-    for (uint32_t left = known; left; left &= left - 1) {
-        const int v = M::at(__ffs(left) - 1);
-        const uint32_t c = count[v];
-        if (entry && entry[v]) bias[v] = a.bias_dev[entry[v] - 1];
-        list[place++] = (uint16_t)(v | (c ? kListSeen : 0) | (c & kInBlock ? kListInBlock : 0));
-        if (!(c & kInBlock)) reinterpret_cast<float*>(count)[v] = __fsub_rn(penalty_of(c & ~kPrompted, p), entry ? bias[v] : 0.0f);
-    }
-    __syncwarp();
-    char* dst = static_cast<char*>(e.out) + ((row0 + b0) * e.out_stride + v0) * M::kSize;
-    const uint32_t changed = e.out == a.logits_dev ? known : M::kAll;
-    for (int b = b0; b < b1; ++b) {
-        M z;
-        uint32_t ok = in_run;
-        const Row<kType> row{ring + stage * kRowBytes};
-        const uint32_t* const allowed = grammar[stage][warp];
-        if (kWords) {
-            copies_wait(e.stages);
-            __syncwarp();
-            if (a.allowed_dev) ok &= M::take_allowed(allowed);
-        } else {
-            next.spill(row.p);
-            ok = next_ok;
-            __syncwarp();
+    for (int part = 0; part < kParts; ++part)
+        for (int k = tid; k < listed[part]; k += kEditThreads) {
+            const int v = list[part * kSpan + k];
+            const uint32_t c = count[v];
+            const float add = entry && entry[v] ? a.bias_dev[entry[v] - 1] : 0.0f;
+            if (entry) bias[v] = add;
+            list[part * kSpan + k] = (uint16_t)(v | (c ? kListSeen : 0) | (c & kInBlock ? kListInBlock : 0));
+            if (!(c & kInBlock)) reinterpret_cast<float*>(count)[v] = __fsub_rn(penalty_of(c & ~kPrompted, p), add);
         }
-        float most = -INFINITY;                    // of the tokens on the list
-        int which = kEditRun;
-        for (int k = lane; k < listed; k += 32) {
-            const uint32_t item = list[k];
-            const int v = item & (kEditRun - 1);
-            float off = reinterpret_cast<const float*>(count)[v];
-            bool seen = item & kListSeen;
-            if (item & kListInBlock) {
-                uint32_t c = count[v] & ~kInBlock;
-                const bool tree = a.mask_dev != nullptr;
-                const unsigned long long sees = tree ? (a.mask_dev[row0 + b] & ((1ull << b) - 1)) | 1ull << b : 0;
-                for (int j = 0; j < n_block; ++j)
-                    if (block_token[j] == v && (tree ? sees >> block_at[j] & 1 : block_at[j] <= b)) ++c;
-                seen = c != 0;
-                off = __fsub_rn(penalty_of(c & ~kPrompted, p), entry ? bias[v] : 0.0f);
-            }
-            const float x = edited(row.get(v), seen, off, p);
-            if (!kAccept) {
-                row.put(v, x);
-            } else {
-                row.put_none(v);
-                const bool may = !a.allowed_dev || (kWords ? M::is_allowed(allowed, v)
-                                                           : a.allowed_dev[(row0 + b) * a.allowed_stride + ((v0 + v) >> 5)] >> (v & 31) & 1);
-                if (may && (x > most || (x == most && v < which))) {
-                    most = x;
-                    which = v;
-                }
-            }
-        }
-        __syncwarp();
-        z.take(row.p);
-        if (kWords) {
-            if (++stage == e.stages) stage = 0;
-            __syncwarp();                          // (the grammar's words are copied by other lanes)
-        }
-        fetch();
-        if (kAccept) {
-            const float rest = z.most(ok), all = fmaxf(rest, most);
-            const uint32_t key = ok || which < kEditRun ? logit_key(all) : 0, top = __reduce_max_sync(0xFFFFFFFFu, key);
-            unsigned long long best = 0;
-            if (top && top >= *static_cast<volatile uint32_t*>(top_key + (b - b0))) {
-                uint32_t v = 0xFFFFFFFFu;
-                if (key == top) {                  // the first of the largest; of no numbers, the first that is allowed
-                    uint32_t is = ok;
-                    if (all > -INFINITY) {
-                        is = 0;
-#pragma unroll
-                        for (int i = 0; i < kEach; ++i) is |= (uint32_t)(z.get(i) == all) << i;
-                        is &= ok;
+    __syncthreads();
+    const int parts = e.parts, span = kEditRun / parts;
+    for (int item = warp; item < (b1 - b0) * parts; item += kWarps) {
+        const int b = b0 + item / parts, first = (item - (b - b0) * parts) * span, last = min(first + span, n);
+        const char* const row = static_cast<const char*>(a.logits_dev) + ((row0 + b) * a.row_stride + v0) * B::kSize;
+        char* const out = static_cast<char*>(e.out) + ((row0 + b) * e.out_stride + v0) * B::kSize;
+        const uint32_t* const allowed = a.allowed_dev ? a.allowed_dev + (row0 + b) * a.allowed_stride + (v0 >> 5) : nullptr;
+        float most = -INFINITY;                    // of the rest,
+        int where = -1;                            // and the batch, or the token (~) that it is in
+        uint32_t some = 0;                         // whether the lane has a token that is allowed
+        int base = first;
+        if (kWords && base + X::kTokens <= last) {
+            X next;
+            next.load(row + base * B::kSize, allowed ? allowed + base / 32 : nullptr, lane);
+            for (; base + X::kTokens <= last; base += X::kTokens) {
+                X x = next;
+                if (base + 2 * X::kTokens <= last)
+                    next.load(row + (base + X::kTokens) * B::kSize, allowed ? allowed + (base + X::kTokens) / 32 : nullptr, lane);
+                if (kAccept) {
+                    some |= x.ok;
+                    const float m = x.most(x.ok & ~known_lane[base / X::kTokens][lane]);
+                    if (m > most) {
+                        most = m;
+                        where = base;
                     }
-                    if (is) v = (uint32_t)M::at(__ffs(is) - 1);
-                    if (which < kEditRun && most == all) v = min(v, (uint32_t)which);
-                    v += (uint32_t)v0;
-                }
-                v = __reduce_min_sync(0xFFFFFFFFu, v);
-                best = (unsigned long long)top << 32 | (0xFFFFFFFFu - v);
-                if (lane == 0) atomicMax(top_key + (b - b0), top);
-            }
-            if (lane == 0) warp_best[b - b0][warp] = best;
-        } else {
-            if (ok != M::kAll)
+                } else {
+                    const bool all = x.ok == X::kAll;
+                    if (!all) x.hide();
+                    uint4* const to = reinterpret_cast<uint4*>(out + base * B::kSize) + lane;
+                    if (!all || e.out != a.logits_dev)
 #pragma unroll
-                for (int i = 0; i < kEach; ++i)
-                    if (!(ok >> i & 1)) z.raw(i, M::kNone);
-            z.store(dst, n, changed | ~ok);
-            dst += e.out_stride * M::kSize;
+                        for (int w = 0; w < 4; ++w) to[32 * w] = x.x[w];
+                }
+            }
         }
+#pragma unroll 4
+        for (int v = base + lane; v < last; v += 32) {   // what is less than a batch, and rows that do not begin on 16 bytes
+            const uint32_t x = B::read(row, v);
+            const bool ok = !allowed || bit_at(allowed, v);
+            if (kAccept) {
+                some |= ok;
+                if (ok && !bit_at(known, v) && B::value(x) > most) {
+                    most = B::value(x);
+                    where = ~v;
+                }
+            } else if (!ok || e.out != a.logits_dev) {
+                B::write(out, v, ok ? x : B::kNone);
+            }
+        }
+        // the tokens on the list
+        if (!kAccept) __syncwarp();
+        float best = -INFINITY;
+        int which = kEditRun;
+        for (int part = first / kSpan; part * kSpan < last; ++part)
+            for (int k0 = 0; k0 < listed[part]; k0 += 128) {
+                uint32_t tokens[4], x[4];          // (four at once: each comes from memory)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = k0 + 32 * i + lane;
+                    tokens[i] = k < listed[part] ? list[part * kSpan + k] : 0xFFFFFFFFu;
+                    if (tokens[i] != 0xFFFFFFFFu) x[i] = B::read(row, tokens[i] & (kEditRun - 1));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (tokens[i] == 0xFFFFFFFFu) continue;
+                    const int v = tokens[i] & (kEditRun - 1);
+                    if (allowed && !bit_at(allowed, v)) continue;
+                    float off = reinterpret_cast<const float*>(count)[v];
+                    bool seen = tokens[i] & kListSeen;
+                    if (tokens[i] & kListInBlock) {
+                        uint32_t c = count[v] & ~kInBlock;
+                        const bool tree = a.mask_dev != nullptr;
+                        const unsigned long long sees = tree ? (a.mask_dev[row0 + b] & ((1ull << b) - 1)) | 1ull << b : 0;
+                        for (int j = 0; j < n_block; ++j)
+                            if (block_token[j] == v && (tree ? sees >> block_at[j] & 1 : block_at[j] <= b)) ++c;
+                        seen = c != 0;
+                        off = __fsub_rn(penalty_of(c & ~kPrompted, p), entry ? bias[v] : 0.0f);
+                    }
+                    const float z = edited(B::value(x[i]), seen, off, p);
+                    if (!kAccept) {
+                        B::write(out, v, B::of(z));
+                    } else if (z > best || (z == best && v < which)) {
+                        best = z;
+                        which = v;
+                    }
+                }
+            }
+        if (!kAccept) continue;
+        const float all = fmaxf(most, best);
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, some || which < kEditRun ? logit_key(all) : 0);
+        uint32_t v = 0xFFFFFFFFu;
+        if (top == logit_key(-INFINITY)) {         // no numbers: the first that is allowed
+            for (int i = (first >> 5) + lane; 32 * i < last; i += 32) {
+                uint32_t word = allowed ? allowed[i] : 0xFFFFFFFFu;
+                if (32 * i + 32 > n) word &= (1u << (n - 32 * i)) - 1;
+                if (word && v == 0xFFFFFFFFu) v = 32 * i + __ffs(word) - 1;
+            }
+        } else if (top && logit_key(all) == top) { // the first of the largest (a lane without any has -inf here)
+            if (best == all) v = which;
+            if (most == all) {
+                int at = ~where;
+                if (kWords && where >= 0) {        // its words once more
+                    X x;
+                    x.load(row + where * B::kSize, allowed ? allowed + where / 32 : nullptr, lane);
+                    at = where + x.find(x.ok & ~known_lane[where / X::kTokens][lane], all, lane);
+                }
+                v = min(v, (uint32_t)at);
+            }
+        }
+        v = __reduce_min_sync(0xFFFFFFFFu, v);
+        if (lane == 0) part_best[item] = top ? (unsigned long long)top << 32 | (0xFFFFFFFFu - (uint32_t)(v0 + v)) : 0;
     }
     if (!kAccept) return;
     __syncthreads();
     if (tid < b1 - b0) {
         unsigned long long best = 0;
-        for (int w = 0; w < kWarps; ++w) best = warp_best[tid][w] > best ? warp_best[tid][w] : best;
+        for (int k = 0; k < parts; ++k) best = part_best[tid * parts + k] > best ? part_best[tid * parts + k] : best;
         e.best[(row0 + b0 + tid) * e.runs + run] = best;
     }
 }
@@ -588,51 +539,38 @@ int check_edit(moe_mxfp4_edit_args* a) {
     return (int64_t)a->streams * a->block * edit_runs(a->vocab) > 0x7FFFFFFF ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// Positions of a CTA: as many as leave four CTAs for every SM.
+// Positions of a CTA: as many as leave eight CTAs for every SM.
 void group_rows(moe::EditView* e) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 1;
     e->runs = edit_runs(e->a.vocab);
-    const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (4 * sms);
+    const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (8 * sms);
     e->rows = (int)(most < 1 ? 1 : most > moe::kMostRows ? moe::kMostRows : most);
     if (e->rows > e->a.block) e->rows = e->a.block;
     e->groups = (e->a.block + e->rows - 1) / e->rows;
-}
-
-template <int kType, bool kWords, bool kAccept>
-cudaError_t launch_edit(const moe::EditView& e, dim3 grid, size_t shared, cudaStream_t st) {
-    static std::atomic<uint64_t> allowed{0};       // devices on which the kernel may have its shared memory
-    int dev = 0;
-    cudaError_t r = cudaGetDevice(&dev);
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (r == cudaSuccess && !(allowed.load(std::memory_order_acquire) & bit)) {
-        r = cudaFuncSetAttribute(moe::edit_kernel<kType, kWords, kAccept>, cudaFuncAttributeMaxDynamicSharedMemorySize, moe::kEditShared);
-        if (r == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
+    // parts of a run: the fewest that leave the CTA's last round of warps less than an eighth of the work short
+    constexpr int warps = moe::kEditThreads / 32;
+    for (e->parts = 1; e->parts < moe::kParts; e->parts *= 2) {
+        const int items = e->rows * e->parts, rounds = (items + warps - 1) / warps;
+        if (8 * items >= 7 * warps * rounds) break;
     }
-    return r != cudaSuccess ? r : moe::launch_dependent(moe::edit_kernel<kType, kWords, kAccept>, grid, dim3(moe::kEditThreads), shared, st, e);
 }
 
 template <bool kAccept>
-int launch_edit(moe::EditView e, cudaStream_t st) {
+int launch_edit(const moe::EditView& e, cudaStream_t st) {
     const dim3 grid((unsigned)((int64_t)e.a.streams * e.groups * e.runs));
     const int size = e.a.dtype == MOE_DTYPE_FP32 ? 4 : 2;
     const bool words = aligned(e.a.logits_dev, 16) && e.a.row_stride * size % 16 == 0 &&
                        (kAccept || (aligned(e.out, 16) && e.out_stride * size % 16 == 0));
-    // the counts and lists, the biases if there are any, and as many rows of logits as there is room and positions for
-    const int arrays = moe::kEditRun * (4 + 2 + (e.a.bias_begin_dev ? 4 : 0)), stage = moe::kEditRun * size;
-    e.stages = (moe::kEditShared - arrays) / stage;
-    if (e.stages > moe::kMostStages) e.stages = moe::kMostStages;
-    if (e.stages > e.rows) e.stages = e.rows;
-    if (!words) e.stages = 1;
-    const size_t shared = arrays + (size_t)e.stages * stage;
-    auto go = [&](auto launch) { return launch(e, grid, shared, st); };
+    const size_t shared = moe::kEditRun * (4 + 2 + (e.a.bias_begin_dev ? 4 : 0));   // the counts and the list, the biases if there are any
+    auto go = [&](auto kern) { return moe::launch_dependent(kern, grid, dim3(moe::kEditThreads), shared, st, e); };
     cudaError_t r;
     if (e.a.dtype == MOE_DTYPE_FP32)
-        r = words ? go(launch_edit<MOE_DTYPE_FP32, true, kAccept>) : go(launch_edit<MOE_DTYPE_FP32, false, kAccept>);
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP32, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP32, false, kAccept>);
     else if (e.a.dtype == MOE_DTYPE_BF16)
-        r = words ? go(launch_edit<MOE_DTYPE_BF16, true, kAccept>) : go(launch_edit<MOE_DTYPE_BF16, false, kAccept>);
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_BF16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_BF16, false, kAccept>);
     else
-        r = words ? go(launch_edit<MOE_DTYPE_FP16, true, kAccept>) : go(launch_edit<MOE_DTYPE_FP16, false, kAccept>);
+        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP16, false, kAccept>);
     return r == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
