@@ -511,90 +511,85 @@ def moe_mxfp4_accept_edited(args: moe_mxfp4_edit_args, target_ptr, accepted_ptr,
 # ----------------------------------------------------------------------------- torch convenience
 
 
-class _OnDevice:
-    """Makes tensors on a call's stream, and has the stream's device current for the calls that have no handle."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.device, self.index = device, device.index
-        self.now = torch._C._cuda_getCurrentRawStream(self.index)
-        self.stream = self.now if stream is None else stream
-        self.other = torch.cuda.current_device() != self.index
-
-    def new(self, shape, dtype, zero=False):
-        """Its fill is ordered with the call, and so is what still uses its memory."""
-        import torch
-        make = torch.zeros if zero else torch.empty
-        if self.stream == self.now:
-            return make(shape, dtype=dtype, device=self.device)
-        on = torch.cuda.ExternalStream(self.stream, self.device) if self.stream else torch.cuda.default_stream(self.device)
-        with torch.cuda.stream(on):
-            return make(shape, dtype=dtype, device=self.device)
-
-    def call(self, fn, *args):
-        if not self.other:
-            return fn(*args)
-        import torch
-        with torch.cuda.device(self.device):
-            return fn(*args)
+def _new(shape, dtype, device, stream, now, zero=False):
+    """A tensor made on a call's stream (`now`: the current one): its fill is ordered with the call, and so is what still
+    uses its memory."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream == now:
+        return make(shape, dtype=dtype, device=device)
+    on = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(on):
+        return make(shape, dtype=dtype, device=device)
 
 
-class _Edits:
-    """The arguments that edit_logits and accept_edited share, checked and laid out."""
+def _call_on(index, fn, *args):
+    """Calls a C entry point that has no handle with the device `index` current."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
-    def __init__(self, logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency,
-                 presence, bias, allowed):
-        import torch
-        i32, f32 = torch.int32, torch.float32
-        kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, f32: MOE_DTYPE_FP32}
-        if not logits.is_cuda or logits.dim() != 3 or logits.dtype not in kinds:
-            raise ValueError("logits: a bf16, fp16 or fp32 CUDA tensor [streams, block, vocab]")
-        S, B, V = self.shape = tuple(logits.shape)
-        self.device, self.dtype = logits.device, logits.dtype
-        self.row = _logit_rows("logits", logits)
 
-        def ptr(name, t, dtype, shape):
-            if t is None:
-                return None
-            if t.dtype is not dtype and not (dtype is torch.int64 and t.dtype is torch.uint64):
-                raise ValueError(f"{name}: {dtype}")
-            if t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name}: contiguous {list(shape)} on {self.device}")
-            return t.data_ptr()
+_LOGIT_TYPES = {}
 
-        hist, stride, room, entries = None, 0, 0, 0
-        if history is not None:
-            if history.dim() != 2 or history.shape[0] != S or history.dtype is not i32 or history.device != self.device \
-                    or (history.shape[1] > 1 and history.stride(1) != 1):
-                raise ValueError("history: int32 [streams, tokens], tokens contiguous")
-            if history_lengths is None:
-                raise ValueError("history_lengths: int32 [streams], with history")
-            room = history.shape[1]
-            stride = room if S <= 1 else history.stride(0)
-            if stride < room:
-                raise ValueError("history: streams do not share memory")
-            hist = history.data_ptr()
-        elif history_lengths is not None or prompt_lengths is not None:
-            raise ValueError("history_lengths and prompt_lengths go with history")
-        begin = ids = values = None
-        if bias is not None:
-            begin, ids, values = bias
-            entries = ids.numel()
-            begin, ids, values = (ptr("bias begin", begin, i32, (S + 1,)), ptr("bias ids", ids, i32, (entries,)),
-                                  ptr("bias values", values, f32, (entries,)))
-        words = 0
-        if allowed is not None:
-            if allowed.dim() != 3 or tuple(allowed.shape[:2]) != (S, B) or allowed.shape[2] < (V + 31) // 32 \
-                    or allowed.dtype is not i32 or allowed.device != self.device or not allowed.is_contiguous():
-                raise ValueError("allowed: contiguous int32 [streams, block, (vocab + 31) // 32]")
-            words = allowed.shape[2]
-        self.args = moe_mxfp4_edit_args(
-            logits.data_ptr(), self.row, kinds[logits.dtype], S, B, V, ptr("tokens", tokens, i32, (S, B)),
-            ptr("mask", mask, torch.int64, (S, B)), ptr("lengths", lengths, i32, (S,)), hist, stride, room,
-            ptr("history_lengths", history_lengths, i32, (S,)), ptr("prompt_lengths", prompt_lengths, i32, (S,)),
-            ptr("repetition", repetition, f32, (S,)), ptr("frequency", frequency, f32, (S,)),
-            ptr("presence", presence, f32, (S,)), begin, ids, values, entries,
-            None if allowed is None else allowed.data_ptr(), words)
+
+def _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
+               bias, allowed):
+    """The arguments that edit_logits and accept_edited share, checked and laid out: (moe_mxfp4_edit_args, streams, block,
+    vocab, elements between positions, device index)."""
+    import torch
+    if not _LOGIT_TYPES:
+        _LOGIT_TYPES.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32})
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError("logits: a bf16, fp16 or fp32 CUDA tensor [streams, block, vocab]")
+    S, B, V = logits.shape
+    row = V if logits.is_contiguous() else _logit_rows("logits", logits)
+    index, i32, f32 = logits.get_device(), torch.int32, torch.float32
+
+    def values(name, t, dtype, n):
+        if t.dtype is not dtype or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: {n} contiguous {dtype} values on {logits.device}")
+        return t.data_ptr()
+
+    if mask is not None and (mask.dtype is not torch.int64 and mask.dtype is not torch.uint64):
+        raise ValueError("mask: int64 [streams, block]")
+    hist, stride, room, begin, ids, added, entries, words = None, 0, 0, None, None, None, 0, 0
+    if history is not None:
+        if (history.dtype is not i32 or history.get_device() != index or history.dim() != 2 or history.shape[0] != S
+                or (history.shape[1] > 1 and history.stride(1) != 1)):
+            raise ValueError("history: int32 [streams, tokens], tokens contiguous")
+        if history_lengths is None:
+            raise ValueError("history_lengths: int32 [streams], with history")
+        hist, room = history.data_ptr(), history.shape[1]
+        stride = room if S <= 1 else history.stride(0)
+        if stride < room:
+            raise ValueError("history: streams do not share memory")
+    elif history_lengths is not None or prompt_lengths is not None:
+        raise ValueError("history_lengths and prompt_lengths go with history")
+    if bias is not None:
+        begin, ids, added = bias
+        entries = ids.numel()
+        begin, ids, added = (values("bias begin", begin, i32, S + 1), values("bias ids", ids, i32, entries),
+                             values("bias values", added, f32, entries))
+    if allowed is not None:
+        words = allowed.shape[-1] if allowed.dim() else 0
+        if words < (V + 31) // 32:
+            raise ValueError("allowed: int32 [streams, block, (vocab + 31) // 32]")
+        allowed = values("allowed", allowed, i32, S * B * words)
+    args = moe_mxfp4_edit_args(
+        logits.data_ptr(), row, kind, S, B, V,
+        None if tokens is None else values("tokens", tokens, i32, S * B),
+        None if mask is None else values("mask", mask, mask.dtype, S * B),
+        None if lengths is None else values("lengths", lengths, i32, S), hist, stride, room,
+        None if history_lengths is None else values("history_lengths", history_lengths, i32, S),
+        None if prompt_lengths is None else values("prompt_lengths", prompt_lengths, i32, S),
+        None if repetition is None else values("repetition", repetition, f32, S),
+        None if frequency is None else values("frequency", frequency, f32, S),
+        None if presence is None else values("presence", presence, f32, S), begin, ids, added, entries, allowed, words)
+    return args, S, B, V, row, index
 
 
 def _logit_rows(name, t):
@@ -617,19 +612,21 @@ def edit_logits(logits, tokens=None, *, mask=None, lengths=None, history=None, h
     int32, values fp32), stream s having the entries begin[s] .. begin[s + 1]; allowed: int32 [streams, block, words], a bit
     per token.  Returns out (made here: like logits, contiguous, positions that `lengths` leaves out zero; `logits` itself:
     in place)."""
-    e = _Edits(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
-               bias, allowed)
-    on = _OnDevice(e.device, stream)
+    args, S, B, V, row, index = _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths,
+                                           repetition, frequency, presence, bias, allowed)
+    import torch
+    now = torch._C._cuda_getCurrentRawStream(index)
+    stream = now if stream is None else stream
     if out is None:
-        out, row = on.new(e.shape, e.dtype, zero=lengths is not None), e.shape[2]
-    elif out is logits:
-        row = e.row
-    else:
-        if tuple(out.shape) != e.shape or out.dtype is not e.dtype or out.device != e.device:
+        out, row = _new((S, B, V), logits.dtype, logits.device, stream, now, zero=lengths is not None), V
+    elif out is not logits:
+        if out.shape != logits.shape or out.dtype is not logits.dtype or out.get_device() != index:
             raise ValueError("out: of the logits' shape and type")
-        row = _logit_rows("out", out)
-    if out.numel():
-        _check(on.call(load_library().moe_mxfp4_edit_logits, e.args, out.data_ptr(), row, on.stream), "moe_mxfp4_edit_logits")
+        row = V if out.is_contiguous() else _logit_rows("out", out)
+    if S * B * V:
+        st = _call_on(index, load_library().moe_mxfp4_edit_logits, args, out.data_ptr(), row, stream)
+        if st:
+            _check(st, "moe_mxfp4_edit_logits")
     return out
 
 
@@ -640,23 +637,36 @@ def accept_edited(logits, tokens, *, mask=None, lengths=None, history=None, hist
     path lists the accepted block positions, then -1 (KvCache.commit takes it).  Calls make their workspace on their stream;
     one that is given is 8-byte aligned and moe_mxfp4_accept_edited_bytes long."""
     import torch
-    e = _Edits(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
-               bias, allowed)
-    S, B, V = e.shape
-    on = _OnDevice(e.device, stream)
-    lib = load_library()
-    made = on.new((2 * S * B + 2 * S,), torch.int32)
-    target, path, accepted, next_token = made.split([S * B, S * B, S, S])
+    args, S, B, V, _, index = _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition,
+                                         frequency, presence, bias, allowed)
+    now = torch._C._cuda_getCurrentRawStream(index)
+    stream = now if stream is None else stream
+    device, lib = logits.device, load_library()
+    rows, ends = _new((2, S, B), torch.int32, device, stream, now), _new((2, S), torch.int32, device, stream, now)
     if workspace is None:
-        st, n = moe_mxfp4_accept_edited_bytes(S, B, V)
-        _check(st, "moe_mxfp4_accept_edited_bytes")
-        workspace = on.new((max(n // 8, 1),), torch.int64)
-    elif workspace.device != e.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: contiguous, on {e.device}")
-    _check(on.call(lib.moe_mxfp4_accept_edited, e.args, target.data_ptr(), accepted.data_ptr(), next_token.data_ptr(),
-                   path.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.stream),
-           "moe_mxfp4_accept_edited")
-    return target.view(S, B), accepted, next_token, path.view(S, B)
+        need = _ACCEPT_BYTES.get((S, B, V))
+        if need is None:
+            st, need = moe_mxfp4_accept_edited_bytes(S, B, V)
+            _check(st, "moe_mxfp4_accept_edited_bytes")
+            if len(_ACCEPT_BYTES) >= 1024:
+                _ACCEPT_BYTES.clear()
+            _ACCEPT_BYTES[S, B, V] = need
+        workspace, room = _new((need // 8 + 1,), torch.int64, device, stream, now), need
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on {device}")
+    else:
+        room = workspace.numel() * workspace.element_size()
+    target, accepted = rows.data_ptr(), ends.data_ptr()
+    st = _call_on(index, lib.moe_mxfp4_accept_edited, args, target, accepted, accepted + 4 * S, target + 4 * S * B,
+                  workspace.data_ptr(), room, stream)
+    if st:
+        _check(st, "moe_mxfp4_accept_edited")
+    target, path = rows.unbind(0)
+    accepted, next_token = ends.unbind(0)
+    return target, accepted, next_token, path
+
+
+_ACCEPT_BYTES = {}      # (streams, block, vocab) -> moe_mxfp4_accept_edited_bytes
 
 
 class Rotary:
@@ -714,30 +724,51 @@ class Rotary:
                                      None if k_norm is None else k_norm.data_ptr(), head_dim, rotary_dim,
                                      MOE_DTYPE_BF16 if dtype is torch.bfloat16 else MOE_DTYPE_FP16,
                                      (MOE_ROTARY_INTERLEAVED if interleaved else 0) | (MOE_ROTARY_NORM if norm else 0), eps, gain)
-        self._layouts = {}
+        self._layouts, self._pairs = {}, {}     # shapes and strides seen so far -> how a call lays them out
+        self._index, self._i32, self._lib = self.turns.get_device(), torch.int32, load_library()
+        self._current_stream = torch._C._cuda_getCurrentRawStream if self._index >= 0 else None
 
     def rotate(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """q: [..., q_heads, head_dim] and k: [..., kv_heads, head_dim] (or None) of one number of tokens, each with its
         tokens one stride apart (the parts of a fused projection's output are); positions: int32, contiguous, one for each
         token.  Returns (q_out, k_out): made here, contiguous; given; or the inputs themselves (in place)."""
-        import torch
-        on = _OnDevice(self.device, stream)
-        n, q_heads, q_row = self._rows("q", q)
-        m, kv_heads, k_row = (n, 0, 0) if k is None else self._rows("k", k)
-        if m != n or positions.numel() != n or positions.dtype is not torch.int32 or positions.device != self.device \
-                or not positions.is_contiguous():
+        qs, qt = q.shape, q.stride()
+        key = (qs, qt) if k is None else (qs, qt, k.shape, k.stride())
+        layout = self._pairs.get(key)
+        if layout is None:
+            n, q_heads, q_row = self._rows("q", q)
+            m, kv_heads, k_row = (n, 0, 0) if k is None else self._rows("k", k)
+            if m != n:
+                raise ValueError("q and k have one number of tokens")
+            if len(self._pairs) >= 1024:
+                self._pairs.clear()
+            layout = self._pairs[key] = (n, q_heads, kv_heads, q_row, k_row)
+        n, q_heads, kv_heads, q_row, k_row = layout
+        dtype, index = self.dtype, self._index
+        if q.dtype is not dtype or q.get_device() != index or (k is not None and (k.dtype is not dtype or k.get_device() != index)):
+            raise ValueError(f"q and k: {dtype} on {self.device}")
+        if (positions.dtype is not self._i32 or positions.numel() != n or positions.get_device() != index
+                or not positions.is_contiguous()):
             raise ValueError(f"positions: contiguous int32 on {self.device}, one for each token of q and of k")
+        now = self._current_stream(index)
+        if stream is None:
+            stream = now
+        qo_row = ko_row = 0
         if q_out is None:
-            q_out = on.new(q.shape, self.dtype)
-        if k_out is None and k is not None:
-            k_out = on.new(k.shape, self.dtype)
-        qo_row = self._out("q_out", q_out, q)
-        ko_row = 0 if k is None else self._out("k_out", k_out, k)
-        a = moe_mxfp4_rotate_args(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                                  None if k is None else k_out.data_ptr(), positions.data_ptr(), q_row, k_row, qo_row, ko_row,
-                                  n, q_heads, kv_heads)
+            q_out = _new(qs, dtype, self.device, stream, now)
+        else:
+            qo_row = self._out("q_out", q_out, q)
+        if k is not None and k_out is None:
+            k_out = _new(k.shape, dtype, self.device, stream, now)
+        elif k is not None:
+            ko_row = self._out("k_out", k_out, k)
         if n:
-            _check(on.call(load_library().moe_mxfp4_rotate, self.desc, a, on.stream), "moe_mxfp4_rotate")
+            a = moe_mxfp4_rotate_args(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                                      None if k is None else k_out.data_ptr(), positions.data_ptr(), q_row, k_row, qo_row, ko_row,
+                                      n, q_heads, kv_heads)
+            st = _call_on(index, self._lib.moe_mxfp4_rotate, self.desc, a, stream)
+            if st:
+                _check(st, "moe_mxfp4_rotate")
         return q_out, k_out
 
     def _out(self, name, out, x):
@@ -747,7 +778,7 @@ class Rotary:
 
     def _rows(self, name, t):
         """(tokens, heads, elements between tokens) of a tensor of rows; remembered by shape and stride."""
-        if t.dtype is not self.dtype or t.device != self.device:
+        if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name}: a {self.dtype} tensor on {self.device}")
         key = (t.shape, t.stride())
         rows = self._layouts.get(key)
@@ -1094,7 +1125,7 @@ class KvCache:
                 or v.get_device() != self._index):
             layout = self._pair(k, v)
         S, B, row = layout
-        if type(rotary) is not Rotary or rotary.device != self.device:
+        if type(rotary) is not Rotary or rotary._index != self._index:
             raise ValueError(f"rotary: a Rotary on {self.device}")
         if stream is None:
             stream = self._current_stream(self._index)
@@ -1210,14 +1241,7 @@ class KvCache:
         return rows
 
     def _new(self, shape, dtype, stream, zero=False):
-        """A tensor made on a call's stream: its fill is ordered with the call, and so is what still uses its memory."""
-        import torch
-        make = torch.zeros if zero else torch.empty
-        if stream == self._current_stream(self._index):
-            return make(shape, dtype=dtype, device=self.device)
-        on = torch.cuda.ExternalStream(stream, self.device) if stream else torch.cuda.default_stream(self.device)
-        with torch.cuda.stream(on):
-            return make(shape, dtype=dtype, device=self.device)
+        return _new(shape, dtype, self.device, stream, self._current_stream(self._index), zero)
 
     def _workspace(self, S, B, H, stream):
         """The cache's own workspace, at least doubled when a call needs more; earlier ones are kept, since captured

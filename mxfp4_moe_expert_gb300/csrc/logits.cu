@@ -232,8 +232,8 @@ template <int kType, bool kWords, bool kAccept>
 __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
     using B = Bits<kType>;
     using X = Batch<kType>;
-    constexpr int kWarps = kEditThreads / 32, kSpan = kEditRun / kParts;
-    constexpr uint32_t kListSeen = 1u << 15, kListInBlock = 1u << 14;
+    constexpr int kWarps = kEditThreads / 32;
+    constexpr uint32_t kListSeen = 1u << 15, kListInBlock = 1u << 14, kNoToken = 0xFFFFFFFFu;
     extern __shared__ uint4 dynamic[];
     __shared__ int block_token[64], block_at[64], n_block;       // tokens of the block that only some of the CTA's positions see
     __shared__ int listed[kParts];                               // tokens on the list, by parts of the run
@@ -255,51 +255,41 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
     // the rows are on their way to L2 meanwhile
     if (kWords && tid < b1 - b0 && n * B::kSize >= 16)
         prefetch_run(static_cast<const char*>(a.logits_dev) + ((row0 + b0 + tid) * a.row_stride + v0) * B::kSize, (uint32_t)(n * B::kSize) & ~15u);
-    // what is known of the run's tokens: which they are, then how often they were said, then what is taken off them
-    if (tid < kEditRun / 32) known[tid] = 0;
-    for (int i = tid; i < kEditRun / X::kTokens * 32; i += kEditThreads) known_lane[0][i] = 0;
-    if (tid < kParts) listed[tid] = 0;
-    if (tid == 0) n_block = 0;
+    // what the stream's part of the arguments says, all of it asked for at once
+    const int parts = e.parts, span = kEditRun / parts, log_span = 31 - __clz(span);
     const int* const history = a.history_dev ? a.history_dev + s * a.history_stride : nullptr;
     const int len = history ? (int)min((int64_t)a.history_lengths_dev[s], a.history_room) : 0;
     const int prompt = history && a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0;
     const int bias_end = entry ? (int)min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries) : 0;
     const int bias_begin = entry ? max(a.bias_begin_dev[s], 0) + tid : 0;
-    int early[8];                                  // the first of the history stay in registers
-#pragma unroll
-    for (int k = 0; k < 8; ++k) early[k] = k * kEditThreads + tid < len ? history[k * kEditThreads + tid] : -1;
+    Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
+              a.presence_dev ? a.presence_dev[s] : 0.0f};
+    const int token = a.tokens_dev && tid < b1 ? a.tokens_dev[row0 + tid] : -1;
+    for (int i = tid; i < kEditRun / 4; i += kEditThreads) {
+        reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+        if (entry) reinterpret_cast<uint4*>(entry)[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (tid < kEditRun / 32) known[tid] = 0;
+    for (int i = tid; i < kEditRun / X::kTokens * 32; i += kEditThreads) known_lane[0][i] = 0;
+    if (tid < kParts) listed[tid] = 0;
+    if (tid == 0) n_block = 0;
     __syncthreads();
-    auto mark = [&](int token) {
-        const uint32_t v = (uint32_t)token - (uint32_t)v0;
-        if (v >= (uint32_t)n) return;
+    auto mark = [&](uint32_t v) {                  // puts a token on the list of its part, once
         const uint32_t bit = 1u << (v & 31);
-        if (*static_cast<volatile uint32_t*>(known + (v >> 5)) & bit) return;
         if (atomicOr(known + (v >> 5), bit) & bit) return;
-        count[v] = 0;
-        if (entry) entry[v] = 0;
-        const int part = v / kSpan, in = v % X::kTokens, word = in / X::kPer;
-        list[part * kSpan + atomicAdd(listed + part, 1)] = (uint16_t)v;
+        const int part = v >> log_span, in = v % X::kTokens, word = in / X::kPer;
+        list[(part << log_span) + atomicAdd(listed + part, 1)] = (uint16_t)v;
         atomicOr(&known_lane[v / X::kTokens][word % 32], 1u << (word / 32 * X::kPer + in % X::kPer));
     };
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mark(early[k]);
-    for_history(history, 8 * kEditThreads, len, prompt, [&](int token, bool) { mark(token); });
-    if (a.tokens_dev)
-        for (int j = tid; j < b1; j += kEditThreads) mark(a.tokens_dev[row0 + j]);
-    for (int i = bias_begin; i < bias_end; i += kEditThreads) mark(a.bias_ids_dev[i]);
-    __syncthreads();
-    auto said = [&](int token, bool prompted) {
-        const uint32_t v = (uint32_t)token - (uint32_t)v0;
+    for_history(history, 0, len, prompt, [&](int t, bool prompted) {
+        const uint32_t v = (uint32_t)t - (uint32_t)v0;
         if (v >= (uint32_t)n) return;
-        if (prompted) atomicOr(count + v, kPrompted);
-        else atomicAdd(count + v, 1u);
-    };
-#pragma unroll
-    for (int k = 0; k < 8; ++k) said(early[k], k * kEditThreads + tid < prompt);
-    for_history(history, 8 * kEditThreads, len, prompt, said);
+        const uint32_t was = prompted ? atomicOr(count + v, kPrompted) : atomicAdd(count + v, 1u);
+        if (!was) mark(v);
+    });
     if (a.tokens_dev)
         for (int j = tid; j < b1; j += kEditThreads) {
-            const uint32_t v = (uint32_t)a.tokens_dev[row0 + j] - (uint32_t)v0;
+            const uint32_t v = (uint32_t)(j == tid ? token : a.tokens_dev[row0 + j]) - (uint32_t)v0;
             if (v >= (uint32_t)n) continue;
             if (!a.mask_dev && j <= b0) {
                 atomicAdd(count + v, 1u);          // all positions here see it
@@ -309,32 +299,33 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
                 block_token[k] = (int)v;
                 block_at[k] = j;
             }
+            mark(v);
         }
     for (int i = bias_begin; i < bias_end; i += kEditThreads) {
         const uint32_t v = (uint32_t)a.bias_ids_dev[i] - (uint32_t)v0;
-        if (v < (uint32_t)n) atomicMax(entry + v, i + 1);
+        if (v < (uint32_t)n && !atomicMax(entry + v, i + 1)) mark(v);
     }
-    Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
-              a.presence_dev ? a.presence_dev[s] : 0.0f};
     p.inverse = __frcp_rn(p.repetition);
     __syncthreads();
-#pragma unroll
-    for (int part = 0; part < kParts; ++part)
+    for (int part = 0; part < parts; ++part)
         for (int k = tid; k < listed[part]; k += kEditThreads) {
-            const int v = list[part * kSpan + k];
+            const int v = list[(part << log_span) + k];
             const uint32_t c = count[v];
             const float add = entry && entry[v] ? a.bias_dev[entry[v] - 1] : 0.0f;
             if (entry) bias[v] = add;
-            list[part * kSpan + k] = (uint16_t)(v | (c ? kListSeen : 0) | (c & kInBlock ? kListInBlock : 0));
+            list[(part << log_span) + k] = (uint16_t)(v | (c ? kListSeen : 0) | (c & kInBlock ? kListInBlock : 0));
             if (!(c & kInBlock)) reinterpret_cast<float*>(count)[v] = __fsub_rn(penalty_of(c & ~kPrompted, p), add);
         }
     __syncthreads();
-    const int parts = e.parts, span = kEditRun / parts;
     for (int item = warp; item < (b1 - b0) * parts; item += kWarps) {
-        const int b = b0 + item / parts, first = (item - (b - b0) * parts) * span, last = min(first + span, n);
+        const int b = b0 + item / parts, part = item - (b - b0) * parts, first = part * span, last = min(first + span, n);
         const char* const row = static_cast<const char*>(a.logits_dev) + ((row0 + b) * a.row_stride + v0) * B::kSize;
         char* const out = static_cast<char*>(e.out) + ((row0 + b) * e.out_stride + v0) * B::kSize;
         const uint32_t* const allowed = a.allowed_dev ? a.allowed_dev + (row0 + b) * a.allowed_stride + (v0 >> 5) : nullptr;
+        const uint16_t* const mine = list + first; // the first tokens on the list are asked for before the rest is looked at
+        const int n_mine = listed[part];
+        uint32_t token0 = lane < n_mine ? mine[lane] : kNoToken, x0 = 0;
+        if (token0 != kNoToken) x0 = B::read(row, token0 & (kEditRun - 1));
         float most = -INFINITY;                    // of the rest,
         int where = -1;                            // and the batch, or the token (~) that it is in
         uint32_t some = 0;                         // whether the lane has a token that is allowed
@@ -381,40 +372,41 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
         if (!kAccept) __syncwarp();
         float best = -INFINITY;
         int which = kEditRun;
-        for (int part = first / kSpan; part * kSpan < last; ++part)
-            for (int k0 = 0; k0 < listed[part]; k0 += 128) {
-                uint32_t tokens[4], x[4];          // (four at once: each comes from memory)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = k0 + 32 * i + lane;
-                    tokens[i] = k < listed[part] ? list[part * kSpan + k] : 0xFFFFFFFFu;
-                    if (tokens[i] != 0xFFFFFFFFu) x[i] = B::read(row, tokens[i] & (kEditRun - 1));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (tokens[i] == 0xFFFFFFFFu) continue;
-                    const int v = tokens[i] & (kEditRun - 1);
-                    if (allowed && !bit_at(allowed, v)) continue;
-                    float off = reinterpret_cast<const float*>(count)[v];
-                    bool seen = tokens[i] & kListSeen;
-                    if (tokens[i] & kListInBlock) {
-                        uint32_t c = count[v] & ~kInBlock;
-                        const bool tree = a.mask_dev != nullptr;
-                        const unsigned long long sees = tree ? (a.mask_dev[row0 + b] & ((1ull << b) - 1)) | 1ull << b : 0;
-                        for (int j = 0; j < n_block; ++j)
-                            if (block_token[j] == v && (tree ? sees >> block_at[j] & 1 : block_at[j] <= b)) ++c;
-                        seen = c != 0;
-                        off = __fsub_rn(penalty_of(c & ~kPrompted, p), entry ? bias[v] : 0.0f);
-                    }
-                    const float z = edited(B::value(x[i]), seen, off, p);
-                    if (!kAccept) {
-                        B::write(out, v, B::of(z));
-                    } else if (z > best || (z == best && v < which)) {
-                        best = z;
-                        which = v;
-                    }
-                }
+        auto edit = [&](uint32_t token, uint32_t x) {
+            const int v = token & (kEditRun - 1);
+            if (allowed && !bit_at(allowed, v)) return;
+            float off = reinterpret_cast<const float*>(count)[v];
+            bool seen = token & kListSeen;
+            if (token & kListInBlock) {
+                uint32_t c = count[v] & ~kInBlock;
+                const bool tree = a.mask_dev != nullptr;
+                const unsigned long long sees = tree ? (a.mask_dev[row0 + b] & ((1ull << b) - 1)) | 1ull << b : 0;
+                for (int j = 0; j < n_block; ++j)
+                    if (block_token[j] == v && (tree ? sees >> block_at[j] & 1 : block_at[j] <= b)) ++c;
+                seen = c != 0;
+                off = __fsub_rn(penalty_of(c & ~kPrompted, p), entry ? bias[v] : 0.0f);
             }
+            const float z = edited(B::value(x), seen, off, p);
+            if (!kAccept) {
+                B::write(out, v, B::of(z));
+            } else if (z > best || (z == best && v < which)) {
+                best = z;
+                which = v;
+            }
+        };
+        if (token0 != kNoToken) edit(token0, x0);
+        for (int k0 = 32; k0 < n_mine; k0 += 128) {
+            uint32_t tokens[4], x[4];              // (four at once: each comes from memory)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + 32 * i + lane;
+                tokens[i] = k < n_mine ? mine[k] : kNoToken;
+                x[i] = tokens[i] != kNoToken ? B::read(row, tokens[i] & (kEditRun - 1)) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tokens[i] != kNoToken) edit(tokens[i], x[i]);
+        }
         if (!kAccept) continue;
         const float all = fmaxf(most, best);
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, some || which < kEditRun ? logit_key(all) : 0);
@@ -441,6 +433,7 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
         if (lane == 0) part_best[item] = top ? (unsigned long long)top << 32 | (0xFFFFFFFFu - (uint32_t)(v0 + v)) : 0;
     }
     if (!kAccept) return;
+    grid_dependency_launch();
     __syncthreads();
     if (tid < b1 - b0) {
         unsigned long long best = 0;
@@ -449,20 +442,25 @@ __global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
     }
 }
 
-// A CTA per stream: the targets of its positions, and the path of accepted nodes.
+// A CTA per stream: the targets of its positions, and the path of accepted nodes.  It starts while the edits end (each of
+// their CTAs has waited for what came before), and reads what they do not write before it waits for them.
 __global__ void __launch_bounds__(256) accept_path_kernel(EditView e, int* __restrict__ target, int* __restrict__ accepted,
                                                           int* __restrict__ next_token, int* __restrict__ path) {
     __shared__ int s_target[1024], s_token[1024], s_parent[1024];
     const moe_mxfp4_edit_args& a = e.a;
     const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    grid_dependency_wait();
     const int used = used_positions(a, s);
     const int64_t row0 = (int64_t)s * a.block;
+    for (int b = tid; b < a.block; b += 256) {
+        s_token[b] = a.tokens_dev[row0 + b];
+        s_parent[b] = a.mask_dev ? 63 - __clzll(a.mask_dev[row0 + b] & ((1ull << b) - 1)) : b - 1;
+    }
+    grid_dependency_wait();
     for (int b = tid >> 5; b < a.block; b += 8) {
         unsigned long long best = 0;
         if (b < used)
             for (int i = lane; i < e.runs; i += 32) {
-                const unsigned long long x = e.best[(row0 + b) * e.runs + i];
+                const unsigned long long x = __ldcg(e.best + (row0 + b) * e.runs + i);
                 best = x > best ? x : best;
             }
 #pragma unroll
@@ -473,13 +471,6 @@ __global__ void __launch_bounds__(256) accept_path_kernel(EditView e, int* __res
         if (lane == 0) {
             s_target[b] = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -1;
             target[row0 + b] = s_target[b];
-            s_token[b] = a.tokens_dev[row0 + b];
-            int up = b - 1;
-            if (a.mask_dev) {
-                const unsigned long long below = a.mask_dev[row0 + b] & ((1ull << b) - 1);
-                up = 63 - __clzll(below);
-            }
-            s_parent[b] = up;
         }
     }
     __syncthreads();

@@ -102,7 +102,7 @@ def test_calls_of_the_cache_refuse_a_null_handle():
 
 def bare(D=64):
     r = pkg.Rotary.__new__(pkg.Rotary)
-    r.device, r.dtype, r.head_dim, r._layouts = torch.device("cpu"), torch.bfloat16, D, {}
+    r.device, r.dtype, r.head_dim, r._layouts, r._index = torch.device("cpu"), torch.bfloat16, D, {}, -1
     return r
 
 
