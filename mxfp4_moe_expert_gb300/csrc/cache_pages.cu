@@ -302,17 +302,12 @@ __global__ void __launch_bounds__(256) cache_truncate_kernel(CacheView c, const 
 
 // ---- accepted paths --------------------------------------------------------------------
 
-struct PathView {
-    moe_mxfp4_commit_args a;
-};
-
 // How many positions stream s keeps: accepted[s], or -1 where it is left alone; *bad: because what it was
 // given is not allowed.  The books are not changed before all warps of the call have asked.
 __device__ __forceinline__ int path_count(const CacheView& c, const moe_mxfp4_commit_args& a, int s, int lane, bool* bad) {
+    const int n = a.accepted_dev[s], len = c.length()[s], held = c.held()[s];
     *bad = false;
-    const int n = a.accepted_dev[s];
     if (n < 0) return -1;
-    const int len = c.length()[s], held = c.held()[s];
     const long long room = (long long)held << c.page_shift;
     bool ok = len >= 0 && held >= 0 && held <= c.L.M && (long long)len + n <= room;
     if (ok && s < a.streams && n > 0) {
@@ -320,31 +315,27 @@ __device__ __forceinline__ int path_count(const CacheView& c, const moe_mxfp4_co
         if (ok && a.path_dev) {
             const int* path = a.path_dev + (int64_t)s * a.block;
             for (int i = lane; i < n; i += 32) {
-                const int p = path[i];
-                ok = ok && p < a.block && p > (i ? path[i - 1] : -1);
+                const int p = path[i], before = i ? path[i - 1] : -1;
+                if (p <= before || p >= a.block || (long long)len + p >= room) {
+                    ok = false;
+                } else {
+                    const int from = c.table(s)[(len + p) >> c.page_shift], to = c.table(s)[(len + i) >> c.page_shift];
+                    ok = ok && (unsigned)from < (unsigned)c.L.P && (unsigned)to < (unsigned)c.L.P && c.refcount()[from] <= 1 && c.refcount()[to] <= 1;
+                }
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (ok) {
-                const long long last = (long long)len + path[n - 1];
-                ok = last < room;
-                if (ok)
-                    for (int i = (len >> c.page_shift) + lane; i <= (int)(last >> c.page_shift); i += 32) {
-                        const int page = c.table(s)[i];
-                        ok = ok && (unsigned)page < (unsigned)c.L.P && c.refcount()[page] <= 1;
-                    }
-                ok = __all_sync(0xFFFFFFFFu, ok);
-            }
         }
     }
     *bad = !ok;
     return ok ? n : -1;
 }
 
-// A warp has 32 16-byte words of a token of one pool, of one stream, and moves them along the path.  Positions
-// ascend and path[i] >= i, so what a step writes lies below all that later steps read: eight are read, then
-// written.  What each stream keeps goes to the state's `need`, for the truncation that follows.
-__global__ void __launch_bounds__(256) cache_path_kernel(CacheView c, const __grid_constant__ PoolList pools, int n_pools, PathView v) {
-    const moe_mxfp4_commit_args& a = v.a;
+// A warp has 32 16-byte words of a token of one pool, of one stream, and moves them along the path.  The lanes look up 32
+// positions of it at once.  Positions ascend and path[i] >= i, so what a step writes lies below all that later steps
+// read: eight are read, then written.  What each stream keeps goes to the state's `need`, for the truncation that follows.
+// Bound by the chain of look-ups (the count, the path, its pages, their counts, the tokens): each position looked up on
+// its own took two more round trips for each eight.
+__global__ void __launch_bounds__(256) cache_path_kernel(CacheView c, const __grid_constant__ PoolList pools, int n_pools, moe_mxfp4_commit_args a) {
     const int lane = threadIdx.x & 31, log_head = c.D == 128 ? 4 : 3;        // words of a head: 16 or 8
     const int words = c.Hkv << log_head, parts = (words + 31) / 32;
     grid_dependency_wait();
@@ -366,21 +357,40 @@ __global__ void __launch_bounds__(256) cache_path_kernel(CacheView c, const __gr
                 for (int i = lane; i < n; i += 32)
                     a.history_dev[s * a.history_stride + len + i] = a.tokens_dev[(int64_t)s * a.block + (path ? path[i] : i)];
         }
-        if (!path || s >= a.streams || word >= words) continue;
+        if (!path || s >= a.streams) continue;
         char* const base = static_cast<char*>(pools.base[pool]) +
                            ((int64_t)(word >> log_head) * c.page * c.D + (word & ((1 << log_head) - 1)) * 8) * 2;
-        auto at = [&](int i) {
+        auto at = [&](int i) {                     // bytes of block position i's token from head 0's start
             const int pos = len + i;
-            return reinterpret_cast<uint4*>(base + (c.table(s)[pos >> c.page_shift] * c.page_stride + (int64_t)(pos & (c.page - 1)) * c.D) * 2);
+            return (c.table(s)[pos >> c.page_shift] * c.page_stride + (int64_t)(pos & (c.page - 1)) * c.D) * 2;
         };
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            uint4 x[8];
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            int64_t from = 0, to = 0;
+            bool moves = false;
+            if (i0 + lane < n) {
+                const int p = path[i0 + lane];
+                moves = p != i0 + lane;
+                from = at(p);
+                to = at(i0 + lane);
+            }
+            unsigned left = __ballot_sync(0xFFFFFFFFu, moves);
+            while (left) {
+                uint4 x[8];
+                int64_t dst[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < n && path[i0 + i] != i0 + i) x[i] = *at(path[i0 + i]);
+                for (int i = 0; i < 8; ++i) {
+                    dst[i] = -1;
+                    if (!left) continue;
+                    const int k = __ffs(left) - 1;
+                    left &= left - 1;
+                    dst[i] = __shfl_sync(0xFFFFFFFFu, to, k);
+                    const int64_t src = __shfl_sync(0xFFFFFFFFu, from, k);
+                    if (word < words) x[i] = *reinterpret_cast<const uint4*>(base + src);
+                }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < n && path[i0 + i] != i0 + i) *at(i0 + i) = x[i];
+                for (int i = 0; i < 8; ++i)
+                    if (dst[i] >= 0 && word < words) *reinterpret_cast<uint4*>(base + dst[i]) = x[i];
+            }
         }
     }
 }
@@ -681,7 +691,7 @@ int moe_mxfp4_cache_commit_path(moe_mxfp4_cache* c, void* state_dev, const moe_m
         if (!a.path_dev) n = 1;                    // (no token moves)
         const int64_t want = (c->cfg.num_streams * n * parts + 7) / 8, most = 64 * (int64_t)c->sm_count;
         if (moe::launch_dependent(moe::cache_path_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, v, pools, n,
-                                  moe::PathView{a}) != cudaSuccess)
+                                  a) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     return cache_truncate(c, state_dev, static_cast<int32_t*>(state_dev) + v.L.need, 1, stream);

@@ -229,7 +229,7 @@ __device__ __forceinline__ bool bit_at(const uint32_t* words, int v) { return wo
 // at a time: the rest is copied, or compared, as it is.  Low tokens are the common ones and have the longest lists, so their
 // CTAs come first.
 template <int kType, bool kWords, bool kAccept>
-__global__ void __launch_bounds__(kEditThreads, 3) edit_kernel(EditView e) {
+__global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(EditView e) {
     using B = Bits<kType>;
     using X = Batch<kType>;
     constexpr int kWarps = kEditThreads / 32;

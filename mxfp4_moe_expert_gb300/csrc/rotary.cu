@@ -54,32 +54,37 @@ __device__ __forceinline__ float2 turn_of(unsigned long long turns, int p, float
     return make_float2(gain * c, gain * s);
 }
 
-// A token of a block on its way into the cache.
+// A token of a block on its way into the cache.  Its page and the page's count are asked for early and looked at
+// late, when a key or a value is to be stored: the queries do not wait for them.
 struct TokenPlace {
-    int s, i, len, held;
+    int s, i, len;
     int position;          // of the rotation
     bool used;             // in use
-    int64_t at;            // element of head 0 in a pool, -1: not to be stored
+    int page, holders;     // -1: not reserved
 };
 __device__ __forceinline__ TokenPlace token_place(const PagePlace& p, int tok) {
     TokenPlace t;
     t.s = tok / p.block;
     t.i = tok - t.s * p.block;
     t.len = p.c.length()[t.s];
-    t.held = p.c.held()[t.s];
-    t.position = t.len + (p.mask ? __popcll(p.mask[tok] & ((1ull << t.i) - 1)) : t.i);
+    const int held = p.c.held()[t.s];
+    const unsigned long long sees = p.mask ? p.mask[tok] : 0;
     t.used = !p.lengths || t.i < p.lengths[t.s];
-    t.at = -1;
+    t.position = t.len + (p.mask ? __popcll(sees & ((1ull << t.i) - 1)) : t.i);
+    const int64_t at = ((int64_t)t.len + t.i) >> p.c.page_shift;
+    t.page = t.used && t.len >= 0 && at < min(held, p.c.L.M) ? p.c.table(t.s)[at] : -1;
     return t;
 }
-// Looks the token's page up: its position has to be reserved, in a page of the stream's own.
-__device__ __forceinline__ void token_page(const PagePlace& p, TokenPlace* t) {
-    if (!t->used) return;
-    const int64_t pos = (int64_t)t->len + t->i;
-    int page = -1;
-    if (t->len >= 0 && (pos >> p.c.page_shift) < min(t->held, p.c.L.M)) page = p.c.table(t->s)[pos >> p.c.page_shift];
-    if ((unsigned)page >= (unsigned)p.c.L.P || p.c.refcount()[page] > 1) raise_status(p.c.state + kCacheStatus, MOE_ERR_CACHE_STATE, t->s);
-    else t->at = page * p.c.page_stride + (pos & (p.c.page - 1)) * p.c.D;
+__device__ __forceinline__ void token_holders(const PagePlace& p, TokenPlace* t) {
+    t->holders = (unsigned)t->page < (unsigned)p.c.L.P ? p.c.refcount()[t->page] : 2;
+}
+// The token's place in a pool (element of head 0), -1: its position is not reserved, or in a page that others hold too.
+__device__ __forceinline__ int64_t token_at(const PagePlace& p, const TokenPlace& t) {
+    if (t.holders > 1) {
+        raise_status(p.c.state + kCacheStatus, MOE_ERR_CACHE_STATE, t.s);
+        return -1;
+    }
+    return t.page * p.c.page_stride + ((t.len + t.i) & (p.c.page - 1)) * p.c.D;
 }
 
 // A warp per head of a token: queries, keys, and (into a cache) values.
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRow
         if (kCache) {
             place = token_place(pages, tok);
             if (!place.used) continue;
-            token_page(pages, &place);
+            token_holders(pages, &place);
             p = place.position;
         } else {
             p = positions[tok];
@@ -111,9 +116,13 @@ __global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRow
             dst = q.dst + tok * q.out + (int64_t)h * D;
         } else {
             const int j = h - q.heads - (is_v ? k.heads : 0);
-            if (kCache && place.at < 0) continue;
             src = (is_v ? v : k.src) + tok * k.in + (int64_t)j * D;
-            dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)j * pages.c.page * D : k.dst + tok * k.out + (int64_t)j * D;
+            dst = k.dst + tok * k.out + (int64_t)j * D;
+            if (kCache) {
+                const int64_t at = token_at(pages, place);
+                if (at < 0) continue;
+                dst = (is_v ? pages.vp : pages.kp) + at + (int64_t)j * pages.c.page * D;
+            }
         }
         if (is_v) {
             for (int e = lane; e < D; e += 32) dst[e] = src[e];
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
                 s[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.y : t0.y, from);
             }
         }
-        if (kCache) token_page(pages, &place);
+        if (kCache) token_holders(pages, &place);
         for (int step = 0; step < steps; ++step) {
             ahead();
             copies_wait<kStages - 1>();
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
                     for (int i = 0; i < 16; ++i) x[i] *= scale;
                 }
             }
-            if (h >= heads || (kCache && (!place.used || !(is_q || place.at >= 0)))) continue;
+            if (h >= heads || (kCache && !place.used)) continue;
             if (!is_v) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -296,7 +305,12 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
                 dst = q.dst + tok * q.out + (int64_t)h * D;
             } else {
                 const int i = h - q.heads - (is_v ? k.heads : 0);
-                dst = kCache ? (is_v ? pages.vp : pages.kp) + place.at + (int64_t)i * pages.c.page * D : k.dst + tok * k.out + (int64_t)i * D;
+                dst = k.dst + tok * k.out + (int64_t)i * D;
+                if (kCache) {
+                    const int64_t at = token_at(pages, place);
+                    if (at < 0) continue;
+                    dst = (is_v ? pages.vp : pages.kp) + at + (int64_t)i * pages.c.page * D;
+                }
             }
             *reinterpret_cast<uint4*>(dst + o0) = w0;
             *reinterpret_cast<uint4*>(dst + o1) = w1;
