@@ -1020,8 +1020,9 @@ class KvCache:
         self.refcount = self.state[at:at + pages]
         self._lib = load_library()
         self._index, self._append = k0.get_device(), self._lib.moe_mxfp4_cache_append
+        self._append_rotated = self._lib.moe_mxfp4_cache_append_rotated
         self._ws, self._ws_bytes, self._ws_kept = None, {}, []
-        self._layouts, self._pairs = {}, {}     # shapes and strides seen so far -> how a call lays them out
+        self._layouts, self._pairs, self._triples = {}, {}, {}     # shapes and strides seen so far -> how a call lays them out
         self._i32, self._f32, self._u8, self._mask_types = torch.int32, torch.float32, torch.uint8, (torch.int64, torch.uint64)
         # the raw handle of the current stream (torch.cuda.current_stream() builds a Stream object around it)
         self._current_stream = torch._C._cuda_getCurrentRawStream
@@ -1120,35 +1121,35 @@ class KvCache:
         alone); mask: int64 [streams, block], as in attend: a position turns as many places behind the stream's length as it
         sees block positions before itself (default: causal).  Returns the queries for attend: out (contiguous; may be q), or
         a tensor made here, where tokens that `lengths` leaves out are zero."""
-        layout = self._pairs.get((k.shape, k.stride(), v.shape, v.stride()))
-        if (layout is None or k.dtype is not self.dtype or v.dtype is not self.dtype or k.get_device() != self._index
-                or v.get_device() != self._index):
-            layout = self._pair(k, v)
-        S, B, row = layout
-        if type(rotary) is not Rotary or rotary._index != self._index:
+        dtype, index = self.dtype, self._index
+        key = ((k.shape, k.stride(), v.shape, v.stride()) if q is None
+               else (k.shape, k.stride(), v.shape, v.stride(), q.shape, q.stride()))
+        layout = self._triples.get(key)
+        if (layout is None or k.dtype is not dtype or v.dtype is not dtype or k.get_device() != index or v.get_device() != index
+                or (q is not None and (q.dtype is not dtype or q.get_device() != index))):
+            layout = self._triple(key, q, k, v)
+        S, B, row, q_heads, q_row = layout
+        if type(rotary) is not Rotary or rotary._index != index:
             raise ValueError(f"rotary: a Rotary on {self.device}")
         if stream is None:
-            stream = self._current_stream(self._index)
-        q_heads, q_row, q_ptr, o_ptr = 0, 0, None, None
+            stream = self._current_stream(index)
+        q_ptr = o_ptr = None
         if q is not None:
-            n, m, q_heads, D, q_row = self._rows("q", q)
-            if (n, m, D) != (S, B, self.head_dim):
-                raise ValueError("q is [streams, block, q_heads, head_dim]")
             if out is None:
-                out = self._new((S, B, q_heads, D), self.dtype, stream, zero=lengths is not None)
-            elif (out.shape != (S, B, q_heads, D) or out.dtype is not self.dtype or out.get_device() != self._index
-                  or not out.is_contiguous()):
+                out = self._new(q.shape, dtype, stream, zero=lengths is not None)
+            elif out.shape != q.shape or out.dtype is not dtype or out.get_device() != index or not out.is_contiguous():
                 raise ValueError("out: contiguous, of q's shape and type")
             q_ptr, o_ptr = q.data_ptr(), out.data_ptr()
         elif out is not None:
             raise ValueError("out: with q")
         if mask is not None and (mask.shape != (S, B) or mask.dtype not in self._mask_types
-                                 or mask.get_device() != self._index or not mask.is_contiguous()):
+                                 or mask.get_device() != index or not mask.is_contiguous()):
             raise ValueError("mask: contiguous int64 [streams, block]")
-        a = moe_mxfp4_append_args(q_ptr, k.data_ptr(), v.data_ptr(), o_ptr, q_row, row,
+        st = self._append_rotated(
+            self.handle, self._state_ptr, layer, rotary.desc,
+            moe_mxfp4_append_args(q_ptr, k.data_ptr(), v.data_ptr(), o_ptr, q_row, row,
                                   None if lengths is None else self._books("lengths", lengths, S),
-                                  None if mask is None else mask.data_ptr(), S, B, q_heads)
-        st = self._lib.moe_mxfp4_cache_append_rotated(self.handle, self._state_ptr, layer, rotary.desc, a, stream)
+                                  None if mask is None else mask.data_ptr(), S, B, q_heads), stream)
         if st:
             _check(st, "moe_mxfp4_cache_append_rotated")
         return out
@@ -1218,6 +1219,19 @@ class KvCache:
         if len(self._pairs) >= 1024:
             self._pairs.clear()
         layout = self._pairs[(k.shape, k.stride(), v.shape, v.stride())] = (S, B, row)
+        return layout
+
+    def _triple(self, key, q, k, v):
+        """(streams, block, elements between tokens of k and v, query heads, elements between tokens of q), remembered."""
+        S, B, row = self._pair(k, v)
+        q_heads = q_row = 0
+        if q is not None:
+            n, m, q_heads, D, q_row = self._rows("q", q)
+            if (n, m, D) != (S, B, self.head_dim):
+                raise ValueError("q is [streams, block, q_heads, head_dim]")
+        if len(self._triples) >= 1024:
+            self._triples.clear()
+        layout = self._triples[key] = (S, B, row, q_heads, q_row)
         return layout
 
     def _rows(self, name, t):

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
     const int b1 = min(min(b0 + e.rows, a.block), used_positions(a, s));
     if (b0 >= b1) return;
     // the rows are on their way to L2 meanwhile
-    if (kWords && tid < b1 - b0 && n * B::kSize >= 16)
+    if (kWords && !kAccept && tid < b1 - b0 && n * B::kSize >= 16)
         prefetch_run(static_cast<const char*>(a.logits_dev) + ((row0 + b0 + tid) * a.row_stride + v0) * B::kSize, (uint32_t)(n * B::kSize) & ~15u);
     // what the stream's part of the arguments says, all of it asked for at once
     const int parts = e.parts, span = kEditRun / parts, log_span = 31 - __clz(span);
@@ -543,7 +543,7 @@ void group_rows(moe::EditView* e) {
     constexpr int warps = moe::kEditThreads / 32;
     for (e->parts = 1; e->parts < moe::kParts; e->parts *= 2) {
         const int items = e->rows * e->parts, rounds = (items + warps - 1) / warps;
-        if (8 * items >= 7 * warps * rounds) break;
+        if (8 * items >= 5 * warps * rounds) break;
     }
 }
 
