@@ -745,7 +745,7 @@ class Rotary:
             layout = self._pairs[key] = (n, q_heads, kv_heads, q_row, k_row)
         n, q_heads, kv_heads, q_row, k_row = layout
         dtype, index = self.dtype, self._index
-        if q.dtype is not dtype or q.get_device() != index or (k is not None and (k.dtype is not dtype or k.get_device() != index)):
+        if index < 0 or q.dtype is not dtype or q.get_device() != index or (k is not None and (k.dtype is not dtype or k.get_device() != index)):
             raise ValueError(f"q and k: {dtype} on {self.device}")
         if (positions.dtype is not self._i32 or positions.numel() != n or positions.get_device() != index
                 or not positions.is_contiguous()):

@@ -449,11 +449,11 @@ __global__ void __launch_bounds__(256) accept_path_kernel(EditView e, int* __res
     __shared__ int s_target[1024], s_token[1024], s_parent[1024];
     const moe_mxfp4_edit_args& a = e.a;
     const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    const int used = used_positions(a, s);
+    const int used = a.lengths_dev ? min(__ldcg(a.lengths_dev + s), a.block) : a.block;
     const int64_t row0 = (int64_t)s * a.block;
     for (int b = tid; b < a.block; b += 256) {
-        s_token[b] = a.tokens_dev[row0 + b];
-        s_parent[b] = a.mask_dev ? 63 - __clzll(a.mask_dev[row0 + b] & ((1ull << b) - 1)) : b - 1;
+        s_token[b] = __ldcg(a.tokens_dev + row0 + b);
+        s_parent[b] = a.mask_dev ? 63 - __clzll(__ldcg(reinterpret_cast<const unsigned long long*>(a.mask_dev) + row0 + b) & ((1ull << b) - 1)) : b - 1;
     }
     grid_dependency_wait();
     for (int b = tid >> 5; b < a.block; b += 8) {

@@ -113,6 +113,7 @@ def edit_reference(logits, tokens=None, masks=None, lengths=None, history=None, 
                 if c:
                     x = x - f * c - p
                 z[s, b, t] = x
+                # z times the rounded reciprocal: two steps; f c + p: one; the difference: one of the result
                 err[s, b, t] = 4 * 2.0 ** -24 * mag if math.isfinite(mag) else 0.0
             if bias is not None:
                 for t, value in dict(bias[s]).items():

@@ -77,8 +77,9 @@ class Case:
             on["bias"] = (i32(begin), i32([t for t, _ in flat]), f32([v for _, v in flat]))
         self.allowed = None
         if "g" in what:
-            self.allowed = [[rng.choice([None, set(), {token()}, {token() for _ in range(20)}, set(range(V)) - {token()},
-                                         {t for t in range(V) if rng.random() < 0.5}]) for _ in range(B)] for _ in range(S)]
+            kinds = [None, set(), {token()}, {token() for _ in range(20)}, set(range(V)) - {token()},
+                     {t for t in range(V) if rng.random() < 0.5}, {t for t in range(V) if rng.random() < 0.9}]
+            self.allowed = [[rng.choice(kinds) for _ in range(B)] for _ in range(S)]
             on["allowed"] = pack_allowed(self.allowed, S, B, V, extra).cuda()
             plain["allowed"] = self.allowed
         self.on, self.plain = on, plain
@@ -129,6 +130,18 @@ def test_edits_and_acceptance(kw, dtype):
     if c.lengths is not None:                                                  # rows behind are left as they were
         y = torch.full_like(out, 7.0)
         c.check_edit(pkg.edit_logits(c.logits.cuda(), out=y, **c.on), unused=7.0)
+
+
+@pytest.mark.parametrize("dtype,kw", [
+    (torch.bfloat16, dict(S=100, B=17, V=9000)), (torch.float32, dict(S=100, B=17, V=9001, what="hpbt")),
+    (torch.float16, dict(S=60, B=40, V=8192 + 40, ragged=True, tree=True)), (torch.bfloat16, dict(S=60, B=40, V=8192, ragged=True, what="hpt")),
+    (torch.float32, dict(S=150, B=64, V=4104, tree=True, what="hpbt")), (torch.bfloat16, dict(S=30, B=300, V=4099, what="hpt"))])
+def test_many_positions_of_a_stream_at_once(kw, dtype):
+    """Batches whose CTAs take several positions: groups that end with the block, tokens that only some of them see."""
+    c = Case(**kw, dtype=dtype, seed=kw["S"])
+    x = c.logits.cuda()
+    c.check_edit(pkg.edit_logits(x, **c.on))
+    c.check_accept(pkg.accept_edited(x, **c.on))
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -100,6 +100,14 @@ def test_sizes(N, Hq, Hkv, D, R):
         assert two[0].shape == (5, N // 5, Hq, D) and torch.equal(two[0].flatten(0, 1), out[0]) and torch.equal(two[1].flatten(0, 1), out[1])
 
 
+def test_nothing_to_rotate():
+    r = pkg.Rotary(head_dim=64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((0, 3, 64), dtype=torch.bfloat16, device="cuda")
+    assert r.rotate(q, q, i32([]))[0].shape == (0, 3, 64)
+    q = torch.zeros((4, 0, 64), dtype=torch.bfloat16, device="cuda")
+    assert r.rotate(q, None, i32([0, 1, 2, 3]))[0].shape == (4, 0, 64)
+
+
 def test_values_that_are_not_finite_stay_in_their_head():
     r = pkg.Rotary(head_dim=64, norm=True, dtype=torch.bfloat16, device="cuda")
     q = torch.randn((4, 6, 64), dtype=torch.bfloat16, device="cuda")

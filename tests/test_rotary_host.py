@@ -133,5 +133,8 @@ def test_the_rotary_refuses():
             pkg.Rotary(**{**dict(head_dim=64, device="cpu"), **kw})
     with pytest.raises(pkg.MoeError):
         pkg.Rotary(head_dim=64, base=-1.0, device="cpu")
+    r = pkg.Rotary(head_dim=64, device="cpu")
+    with pytest.raises(ValueError, match="cpu"):
+        r.rotate(torch.zeros((1, 2, 64), dtype=torch.bfloat16), None, torch.zeros(1, dtype=torch.int32))
     r = pkg.Rotary(head_dim=64, rotary_dim=0, device="cpu")
     assert r.turns.numel() == 0 and r.desc.flags == 0
