@@ -186,7 +186,7 @@ __device__ __forceinline__ void copies_wait() {
 // cosine of one or two of the token's pairs, and the others from its neighbours; they stay in registers for the
 // token's heads.  A warp takes `steps` rounds of a token's heads.  Every lane copies its own words kStages - 1 rounds
 // ahead into its own places of shared memory, across tokens, so memory is kept busy without registers and without barriers.
-constexpr int kStages = 6;
+constexpr int kStages = 4;
 
 template <int D, bool kBf16, bool kInter, bool kCache>
 __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
@@ -203,18 +203,24 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
     const int first = kInter || D == 64 ? lane : 8 * (lane / 4) + lane % 4, second = kInter ? lane + 32 : first + 4;
     const int64_t units = (int64_t)tokens * parts, stride = (int64_t)gridDim.x * 8;
     const int64_t u0 = (int64_t)blockIdx.x * 8 + warp;
+    // unit u: a token, and the first of its heads that the warp takes (a 64-bit division costs as much as half a round)
+    auto unit = [&](int64_t u, int* tok, int* head) {
+        *tok = parts == 1 ? (int)u : (int)(u / parts);
+        *head = parts == 1 ? 0 : (int)(u - (int64_t)*tok * parts) * steps * kHeads;
+    };
     int64_t ahead_u = u0;
-    int ahead_step = 0, ahead_slot = 0, slot = 0;
+    int ahead_step = 0, ahead_slot = 0, slot = 0, ahead_tok, ahead_head;
+    unit(u0, &ahead_tok, &ahead_head);
     auto ahead = [&] {
         if (ahead_u < units) {
-            const int tok = (int)(ahead_u / parts), h = ((int)(ahead_u - (int64_t)tok * parts) * steps + ahead_step) * kHeads + g;
+            const int h = ahead_head + ahead_step * kHeads + g;
             if (h < heads) {
                 const uint16_t* src;
                 if (h < q.heads) {
-                    src = q.src + tok * q.in + (int64_t)h * D;
+                    src = q.src + ahead_tok * q.in + (int64_t)h * D;
                 } else {
                     const bool is_v = h >= q.heads + k.heads;
-                    src = (is_v ? v : k.src) + tok * k.in + (int64_t)(h - q.heads - (is_v ? k.heads : 0)) * D;
+                    src = (is_v ? v : k.src) + ahead_tok * k.in + (int64_t)(h - q.heads - (is_v ? k.heads : 0)) * D;
                 }
                 copy_16(&ring[warp][ahead_slot][0][lane], src + o0);
                 copy_16(&ring[warp][ahead_slot][1][lane], src + o1);
@@ -222,6 +228,7 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
             if (++ahead_step == steps) {
                 ahead_step = 0;
                 ahead_u += stride;
+                unit(ahead_u, &ahead_tok, &ahead_head);
             }
         }
         copies_commit();
@@ -231,7 +238,8 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) ahead();
     for (int64_t u = u0; u < units; u += stride) {
-        const int tok = (int)(u / parts), h0 = (int)(u - (int64_t)tok * parts) * steps * kHeads;
+        int tok, h0;
+        unit(u, &tok, &h0);
         TokenPlace place{};
         if (kCache) place = token_place(pages, tok);
         const int p = kCache ? place.position : positions[tok];
@@ -370,24 +378,27 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
         return moe::launch_dependent(moe::rotate_heads_kernel<D, kBf16, kCache>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
                                      r, q, k, v, positions, tokens, pages);
     }
-    // Rounds of heads of a token, dealt out to warps in parts of `steps` each: as many parts as give the busiest warp
-    // of the resident CTAs the least to do, a part's start (its page, its sines and cosines) taken for a round's work.
+    // Rounds of heads of a token, dealt out to warps in parts of `steps` each, by two or three CTAs on every SM: what gives
+    // the busiest warps the least to do, a part's start (its page, its sines and cosines) taken for a round's work.  Where
+    // both do as well two do better, whose loads and stores come in longer runs of memory (47976 tokens of 36 narrow heads: 67 us
+    // with two, 76 with three); three serve where two leave warps idle (2560 tokens of 48 heads: 127 us for 8 layers, 140 with two).
     const int rounds = (heads * (D / 16) + 31) / 32;
-    const int64_t resident = 3 * (int64_t)sms;
-    int parts = 1, steps = rounds;
+    int parts = 1, steps = rounds, resident = 2;
     int64_t least = INT64_MAX;
-    for (int n = 1; n <= rounds && n <= 64; ++n) {
-        const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
-        const int64_t cost = ((int64_t)tokens * made + resident * 8 - 1) / (resident * 8) * (each + 1);
-        if (cost < least) {
-            least = cost;
-            parts = made;
-            steps = each;
+    for (int ctas = 2; ctas <= 3; ++ctas)
+        for (int n = 1; n <= rounds && n <= 64; ++n) {
+            const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
+            const int64_t warps = 8 * (int64_t)ctas * sms, cost = ((int64_t)tokens * made + warps - 1) / warps * (each + 1) * ctas;
+            if (cost < least) {
+                least = cost;
+                parts = made;
+                steps = each;
+                resident = ctas;
+            }
         }
-    }
     const int64_t want = ((int64_t)tokens * parts + 7) / 8;
     auto kern = r.interleaved ? moe::rotate_words_kernel<D, kBf16, true, kCache> : moe::rotate_words_kernel<D, kBf16, false, kCache>;
-    return moe::launch_dependent(kern, dim3((unsigned)(want < resident ? want : resident)), dim3(256), 0, st, r, q, k, v, positions, tokens,
+    return moe::launch_dependent(kern, dim3((unsigned)(want < (int64_t)resident * sms ? want : (int64_t)resident * sms)), dim3(256), 0, st, r, q, k, v, positions, tokens,
                                  parts, steps, pages);
 }
 
