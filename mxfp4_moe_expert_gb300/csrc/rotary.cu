@@ -37,15 +37,6 @@ struct PagePlace {
     int block;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ float half_to_f32(uint16_t x) {
-    return kBf16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
-}
-template <bool kBf16>
-__device__ __forceinline__ uint16_t f32_to_half(float x) {
-    return kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
-}
-
 // gain * (cos, sin) of position p's angle in pair i.
 __device__ __forceinline__ float2 turn_of(unsigned long long turns, int p, float gain) {
     const unsigned long long phase = (unsigned long long)(long long)p * turns;
@@ -87,75 +78,6 @@ __device__ __forceinline__ int64_t token_at(const PagePlace& p, const TokenPlace
     return t.page * p.c.page_stride + ((t.len + t.i) & (p.c.page - 1)) * p.c.D;
 }
 
-// A warp per head of a token: queries, keys, and (into a cache) values.
-template <int D, bool kBf16, bool kCache>
-__global__ void __launch_bounds__(256) rotate_heads_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
-                                                           const int* __restrict__ positions, int tokens, PagePlace pages) {
-    __shared__ float rows[8][D];
-    const int lane = threadIdx.x & 31;
-    float* const row = rows[threadIdx.x >> 5];
-    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
-    grid_dependency_wait();
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < (int64_t)tokens * heads; u += (int64_t)gridDim.x * 8) {
-        const int tok = (int)(u / heads), h = (int)(u - (int64_t)tok * heads);
-        int p;
-        TokenPlace place{};
-        if (kCache) {
-            place = token_place(pages, tok);
-            if (!place.used) continue;
-            token_holders(pages, &place);
-            p = place.position;
-        } else {
-            p = positions[tok];
-        }
-        const uint16_t* src;
-        uint16_t* dst;
-        const bool is_q = h < q.heads, is_v = h >= q.heads + k.heads;
-        if (is_q) {
-            src = q.src + tok * q.in + (int64_t)h * D;
-            dst = q.dst + tok * q.out + (int64_t)h * D;
-        } else {
-            const int j = h - q.heads - (is_v ? k.heads : 0);
-            src = (is_v ? v : k.src) + tok * k.in + (int64_t)j * D;
-            dst = k.dst + tok * k.out + (int64_t)j * D;
-            if (kCache) {
-                const int64_t at = token_at(pages, place);
-                if (at < 0) continue;
-                dst = (is_v ? pages.vp : pages.kp) + at + (int64_t)j * pages.c.page * D;
-            }
-        }
-        if (is_v) {
-            for (int e = lane; e < D; e += 32) dst[e] = src[e];
-            continue;
-        }
-        float x[D / 32], sum = 0;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            x[i] = half_to_f32<kBf16>(src[i * 32 + lane]);
-            sum = fmaf(x[i], x[i], sum);
-        }
-        const uint16_t* w = is_q ? r.q_norm : r.k_norm;
-        const float scale = r.norm ? rsqrtf(warp_sum(sum) * (1.0f / D) + r.eps) : 1.0f;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            row[i * 32 + lane] = x[i] * scale * (r.norm && w ? half_to_f32<kBf16>(w[i * 32 + lane]) : 1.0f);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int e = i * 32 + lane;
-            float y = row[e];
-            if (e < r.R) {
-                const int half = r.R / 2, pair = r.interleaved ? e >> 1 : e < half ? e : e - half;
-                const float a = row[r.interleaved ? 2 * pair : pair], b = row[r.interleaved ? 2 * pair + 1 : pair + half];
-                const float2 t = turn_of(r.turns[pair], p, r.gain);
-                y = (r.interleaved ? e & 1 : e >= half) ? a * t.y + b * t.x : a * t.x - b * t.y;
-            }
-            dst[e] = f32_to_half<kBf16>(y);
-        }
-    }
-}
-
 // Two 16-bit values of a word as fp32, and back.
 template <bool kBf16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
@@ -179,28 +101,50 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// Heads whose pairs fill 16-byte words (rotary_dim a multiple of 16, or of 8 where pairs are side by side).  A
-// lane has 16 elements of a head in two words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at
-// a time: words that hold both sides of the lane's 8 pairs, so no element crosses lanes, neighbours' words side
-// by side in memory (with both words of a lane side by side, each touched half of every 32-byte sector).  Each lane takes the sine and
-// cosine of one or two of the token's pairs, and the others from its neighbours; they stay in registers for the
-// token's heads.  A warp takes `steps` rounds of a token's heads.  Every lane copies its own words kStages - 1 rounds
-// ahead into its own places of shared memory, across tokens, so memory is kept busy without registers and without barriers.
-constexpr int kStages = 4;
+// How a head's pairs lie in its 16-byte words.
+enum : int {
+    kHalves,   // i and rotary_dim / 2 + i, rotary_dim a multiple of 16: word against word
+    kPairs,    // side by side: within a word
+    kAnywhere, // i and rotary_dim / 2 + i, any other rotary_dim
+};
 
-template <int D, bool kBf16, bool kInter, bool kCache>
-__global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
-                                                              const int* __restrict__ positions, int tokens, int parts, int steps,
-                                                              PagePlace pages) {
-    constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+// A lane has 16 elements of a head in two words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at a time.  The
+// words are chosen so that they hold both sides of the lane's 8 pairs, with neighbours' words side by side in memory (with both words
+// of a lane side by side, each touched half of every 32-byte sector: 92 us for what takes 77).  Each lane takes the sine and
+// cosine of one or two of the token's pairs, and the others from its neighbours; they stay in registers for the
+// token's heads.  kAnywhere: the lanes exchange the normed elements through shared memory, laid out so that neither side has
+// conflicts.  A warp takes `steps` rounds of a token's heads.  Every lane copies its own words some rounds ahead into its
+// own places of shared memory, across tokens, so memory is kept busy without registers and without barriers.
+// Bound by HBM: 16381 tokens of 56 + 8 heads of 128 (537 MB read and written) in 86 us, 6.3 TB/s, 0.92 of the copy rate;
+// 47976 tokens of 32 + 4 heads of 64 in 67 us, 0.97; 2 layers of those into the cache with their values in 154 us, 0.94.  Of few
+// tokens by the launch and the chain of look-ups: 8 tokens of one layer in 2.6 us, 3.2 into the cache.
+template <int D, bool kBf16, int kLayout, bool kCache>
+__global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
+                                                                                  const int* __restrict__ positions, int tokens, int parts,
+                                                                                  int steps, PagePlace pages) {
+    constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kStages = kLayout == kAnywhere ? 3 : 4;
+    constexpr int kColumn = D / 8, kHeadRow = D + kLanes;        // kAnywhere: element e of a head at place (e % 8) kColumn + e / 8
+    constexpr int kTurns = kLayout == kAnywhere ? 16 : 8;
     __shared__ uint4 ring[8][kStages][2][32];
+    __shared__ float normed[kLayout == kAnywhere ? 8 : 1][kHeads * kHeadRow];
+    __shared__ float2 turned[kLayout == kAnywhere ? 8 : 1][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane % kLanes, g = lane / kLanes;
-    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
-    // the lane's words: elements o0.. and o1.., and whether the pairs c[0..3], c[4..7] turn
-    const bool turns0 = kInter ? 8 * j < r.R : 16 * j < r.R, turns1 = kInter ? 8 * j + D / 2 < r.R : turns0;
-    const int o0 = kInter || turns0 ? 8 * j : r.R / 2 + 8 * j, o1 = kInter ? D / 2 + 8 * j : turns0 ? r.R / 2 + 8 * j : D / 2 + 8 * j;
-    // the pairs whose sine and cosine the lane takes (first, second), and from which lanes it gets those of its own
-    const int first = kInter || D == 64 ? lane : 8 * (lane / 4) + lane % 4, second = kInter ? lane + 32 : first + 4;
+    const int heads = q.heads + k.heads * (kCache ? 2 : 1), half = r.R / 2;
+    // the lane's words: elements o0.. and o1..
+    const bool across = kLayout == kHalves && 16 * j < r.R;
+    const int o0 = kLayout != kHalves || across ? 8 * j : half + 8 * j, o1 = across ? half + 8 * j : D / 2 + 8 * j;
+    // the pairs whose sine and cosine the lane takes (first, second)
+    const int first = kLayout == kPairs || D == 64 ? lane : 8 * (lane / 4) + lane % 4, second = kLayout == kPairs ? lane + 32 : first + 4;
+    // which of its pairs (kAnywhere: elements) turn
+    uint32_t turns = across ? 0xFF : 0;
+    if (kLayout != kHalves) {
+        turns = 0;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int e = kLayout == kPairs ? (i < 4 ? o0 + 2 * i : o1 + 2 * (i - 4)) : (i < 8 ? o0 + i : o1 + i - 8);
+            turns |= (uint32_t)(e < r.R) << i;
+        }
+    }
     const int64_t units = (int64_t)tokens * parts, stride = (int64_t)gridDim.x * 8;
     const int64_t u0 = (int64_t)blockIdx.x * 8 + warp;
     // unit u: a token, and the first of its heads that the warp takes (a 64-bit division costs as much as half a round)
@@ -243,14 +187,25 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
         TokenPlace place{};
         if (kCache) place = token_place(pages, tok);
         const int p = kCache ? place.position : positions[tok];
-        float c[8], s[8];
-        if (r.R) {
-            float2 t0 = make_float2(0, 0), t1 = t0;
-            if (first < r.R / 2) t0 = turn_of(r.turns[first], p, r.gain);
-            if (D == 128 && second < r.R / 2) t1 = turn_of(r.turns[second], p, r.gain);
+        float c[kTurns], s[kTurns];
+        if (kLayout == kAnywhere) {
+            __syncwarp();
+            for (int i = lane; i < half; i += 32) turned[warp][i] = turn_of(r.turns[i], p, r.gain);
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int from = D == 128 ? 4 * j + i % 4 : kInter ? 4 * j + i % 4 + 16 * (i / 4) : 8 * j + i;
+            for (int i = 0; i < kTurns; ++i) {     // element e against e + half (the sine's sign with it) or e - half
+                const int e = i < 8 ? o0 + i : o1 + i - 8;
+                const float2 t = e < r.R ? turned[warp][e < half ? e : e - half] : make_float2(0, 0);
+                c[i] = t.x;
+                s[i] = e < half ? -t.y : t.y;
+            }
+        } else if (r.R) {
+            float2 t0 = make_float2(0, 0), t1 = t0;
+            if (first < half) t0 = turn_of(r.turns[first], p, r.gain);
+            if (D == 128 && second < half) t1 = turn_of(r.turns[second], p, r.gain);
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+                const int from = D == 128 ? 4 * j + i % 4 : kLayout == kPairs ? 4 * j + i % 4 + 16 * (i / 4) : (8 * j + i) & 31;
                 c[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.x : t0.x, from);
                 s[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.y : t0.y, from);
             }
@@ -295,16 +250,29 @@ __global__ void __launch_bounds__(256, 3) rotate_words_kernel(RotaryView r, Head
                     for (int i = 0; i < 16; ++i) x[i] *= scale;
                 }
             }
+            if (kLayout == kAnywhere) {
+                float* const head = normed[warp] + g * kHeadRow;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) head[i % 8 * kColumn + (i < 8 ? o0 : o1) / 8] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = i < 8 ? o0 + i : o1 + i - 8, with = e < half ? e + half : e - half;
+                    if (turns >> i & 1) x[i] = fmaf(head[with % 8 * kColumn + with / 8], s[i], x[i] * c[i]);
+                }
+                __syncwarp();
+            }
             if (h >= heads || (kCache && !place.used)) continue;
             if (!is_v) {
+                if (kLayout != kAnywhere)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (kInter && i >= 4 ? turns1 : turns0) {
-                        float &a = x[kInter ? 2 * i : i], &b = x[kInter ? 2 * i + 1 : i + 8];
-                        const float y = a * c[i] - b * s[i];
-                        b = fmaf(a, s[i], b * c[i]);
-                        a = y;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        if (kLayout == kHalves ? across : turns >> i & 1) {
+                            float &a = x[kLayout == kPairs ? 2 * i : i], &b = x[kLayout == kPairs ? 2 * i + 1 : i + 8];
+                            const float y = a * c[i] - b * s[i];
+                            b = fmaf(a, s[i], b * c[i]);
+                            a = y;
+                        }
                 w0 = make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
                 w1 = make_uint4(pack2<kBf16>(x[8], x[9]), pack2<kBf16>(x[10], x[11]), pack2<kBf16>(x[12], x[13]), pack2<kBf16>(x[14], x[15]));
             }
@@ -371,13 +339,7 @@ int sm_count() {
 template <bool kCache, int D, bool kBf16>
 cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, const moe::HeadRows& k, const uint16_t* v,
                           const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
-    const int heads = q.heads + k.heads * (kCache ? 2 : 1);
-    const int64_t most = 64 * (int64_t)sms;
-    if (r.R % (r.interleaved ? 8 : 16)) {      // a warp a head, elements through shared memory
-        const int64_t want = ((int64_t)tokens * heads + 7) / 8;
-        return moe::launch_dependent(moe::rotate_heads_kernel<D, kBf16, kCache>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
-                                     r, q, k, v, positions, tokens, pages);
-    }
+    const int heads = q.heads + k.heads * (kCache ? 2 : 1), layout = r.interleaved ? moe::kPairs : r.R % 16 ? moe::kAnywhere : moe::kHalves;
     // Rounds of heads of a token, dealt out to warps in parts of `steps` each, by two or three CTAs on every SM: what gives
     // the busiest warps the least to do, a part's start (its page, its sines and cosines) taken for a round's work.  Where
     // both do as well two do better, whose loads and stores come in longer runs of memory (47976 tokens of 36 narrow heads: 67 us
@@ -385,7 +347,7 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
     const int rounds = (heads * (D / 16) + 31) / 32;
     int parts = 1, steps = rounds, resident = 2;
     int64_t least = INT64_MAX;
-    for (int ctas = 2; ctas <= 3; ++ctas)
+    for (int ctas = 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
         for (int n = 1; n <= rounds && n <= 64; ++n) {
             const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
             const int64_t warps = 8 * (int64_t)ctas * sms, cost = ((int64_t)tokens * made + warps - 1) / warps * (each + 1) * ctas;
@@ -397,7 +359,9 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
             }
         }
     const int64_t want = ((int64_t)tokens * parts + 7) / 8;
-    auto kern = r.interleaved ? moe::rotate_words_kernel<D, kBf16, true, kCache> : moe::rotate_words_kernel<D, kBf16, false, kCache>;
+    auto kern = layout == moe::kPairs    ? moe::rotate_kernel<D, kBf16, moe::kPairs, kCache>
+                : layout == moe::kHalves ? moe::rotate_kernel<D, kBf16, moe::kHalves, kCache>
+                                         : moe::rotate_kernel<D, kBf16, moe::kAnywhere, kCache>;
     return moe::launch_dependent(kern, dim3((unsigned)(want < (int64_t)resident * sms ? want : (int64_t)resident * sms)), dim3(256), 0, st, r, q, k, v, positions, tokens,
                                  parts, steps, pages);
 }
