@@ -76,8 +76,9 @@ def test_given_frequencies():
     assert_rounded(r.rotate(q, None, pos)[0], want, err)
 
 
-@pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 0), (1, 0, 1), (1, 56, 8), (3, 7, 1), (2000, 2, 1), (701, 33, 5), (40000, 1, 1), (5, 300, 17)])
-@pytest.mark.parametrize("D,R", [(128, 128), (64, 32), (64, 34)])
+@pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 0), (1, 0, 1), (1, 56, 8), (3, 7, 1), (2000, 2, 1), (701, 33, 5), (40000, 1, 1), (5, 300, 17), (70001, 1, 0),
+                                      (9999, 3, 1), (30001, 5, 2)])
+@pytest.mark.parametrize("D,R", [(128, 128), (64, 32), (64, 34), (128, 90)])
 def test_sizes(N, Hq, Hkv, D, R):
     """Few and many tokens, few and many heads; tokens of a wider tensor; two leading dimensions."""
     dtype = torch.bfloat16
@@ -193,7 +194,9 @@ def status(c):
     (dict(), 8, 4, 64, False, True, False, False), (dict(dtype=torch.float16, page=32, Hkv=1), 3, 8, 32, True, False, False, True),
     (dict(D=128, Hkv=3, page=64, M=4), 11, 6, 128, False, True, True, False), (dict(D=128, Hkv=8, dtype=torch.float16), 1, 56, 64, True, True, False, False),
     (dict(S=3, page=128, M=3, Hkv=5), 64, 5, 20, False, False, True, True), (dict(S=2, M=40, P=90), 300, 2, 64, True, True, False, True),
-    (dict(S=1, D=128, Hkv=2), 1, 0, 128, False, True, False, False), (dict(S=5, Hkv=33, M=4), 7, 33, 50, True, True, True, True)])
+    (dict(S=1, D=128, Hkv=2), 1, 0, 128, False, True, False, False), (dict(S=5, M=20, P=110, Hkv=1), 64, 2, 64, False, True, True, True),
+    (dict(S=4, D=128, M=20, P=90, Hkv=1), 100, 0, 20, False, False, False, True), (dict(S=2, M=20, P=50, Hkv=1), 200, 0, 64, True, True, False, False),
+    (dict(S=3, M=20, P=70, Hkv=1, dtype=torch.float16), 90, 1, 64, False, True, False, True), (dict(S=5, Hkv=33, M=4), 7, 33, 50, True, True, True, True)])
 def test_a_block_on_its_way_into_the_cache(kw, B, Hq, R, inter, norm, tree, ragged):
     c, mem, b = make(**kw, seed=B, room=B)
     S, D, Hkv, dtype, L = b.S, c.head_dim, c.kv_heads, c.dtype, c.num_layers
