@@ -94,31 +94,58 @@ struct Bits {
     }
 };
 
-// A warp's four loads of 512 bytes of a row that begins on 16 bytes: a lane has 4 words of kPer tokens, and a bit for each
-// of its tokens (token i of word w: bit w kPer + i).
-template <int kType>
+// A warp's four loads of 512 bytes of a row, from a token that lies on 16 bytes: a lane has 4 words of kPer tokens, and a bit
+// for each of its tokens (token i of word w: bit w kPer + i).  kShift: the first of them is any token of the run (rows that do not
+// begin on 16 bytes), and its bits lie anywhere in the grammar's words.
+template <int kType, bool kShift>
 struct Batch {
     using B = Bits<kType>;
     static constexpr int kPer = 16 / B::kSize, kTokens = 4 * 32 * kPer, kLane = 4 * kPer;
-    static constexpr uint32_t kAll = kLane == 32 ? 0xFFFFFFFFu : (1u << (kLane & 31)) - 1;
+    static constexpr uint32_t kAll = kLane == 32 ? 0xFFFFFFFFu : (1u << (kLane & 31)) - 1, kWord = (1u << kPer) - 1;
     uint4 x[4];
     uint32_t ok;                                   // allowed
     static __device__ __forceinline__ int token(int w, int lane) { return (w * 32 + lane) * kPer; }
-    // row, allowed: of the batch's first token.
-    __device__ __forceinline__ void load(const char* row, const uint32_t* allowed, int lane) {
-        const uint4* p = reinterpret_cast<const uint4*>(row) + lane;
+    // The bits of the tokens from base on in a row of bits: the words' tokens lie a whole number of its words apart, kPer.
+    static __device__ __forceinline__ uint32_t bits_from(const uint32_t* bits, int base, int w, int lane) {
+        const int v = base + token(0, lane);
+        if (!kShift) {                             // (a byte holds them)
+            const uint32_t t = reinterpret_cast<const uint8_t*>(bits)[v / 8 + 4 * kPer * w];
+            return kPer == 8 ? t : t >> (v & 7) & kWord;
+        }
+        const uint32_t lo = bits[(v >> 5) + kPer * w], hi = (v & 31) + kPer > 32 ? bits[(v >> 5) + kPer * w + 1] : 0;
+        return __funnelshift_r(lo, hi, v & 31) & kWord;
+    }
+    // The run's row and grammar, tokens base .. last; words that reach beyond are left out.
+    __device__ __forceinline__ void load(const char* row, const uint32_t* allowed, int base, int last, int lane) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + base * B::kSize) + lane;
+        if (base + kTokens <= last) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) x[w] = __ldcs(p + 32 * w);
-        ok = kAll;
-        if (allowed) {
-            const uint8_t* q = reinterpret_cast<const uint8_t*>(allowed) + (kPer == 8 ? lane : lane / 2);
+            for (int w = 0; w < 4; ++w) x[w] = __ldcs(p + 32 * w);
+            ok = kAll;
+            if (allowed) {
+                ok = 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) ok |= bits_from(allowed, base, w, lane) << (kPer * w);
+            }
+        } else {
             ok = 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t t = __ldg(q + 4 * kPer * w);
-                ok |= (kPer == 8 ? t : t >> (4 * (lane & 1)) & 15u) << (kPer * w);
+                x[w] = make_uint4(0, 0, 0, 0);
+                if (base + token(w, lane) + kPer > last) continue;
+                x[w] = __ldcs(p + 32 * w);
+                ok |= (allowed ? bits_from(allowed, base, w, lane) : kWord) << (kPer * w);
             }
         }
+    }
+    // Those of the tokens that something is known of.
+    static __device__ __forceinline__ uint32_t known_bits(const uint32_t* known, const uint32_t (*known_lane)[32], int base, int last, int lane) {
+        if (!kShift) return known_lane[base / kTokens][lane];
+        uint32_t t = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (base + token(w, lane) + kPer <= last) t |= bits_from(known, base, w, lane) << (kPer * w);
+        return t;
     }
     static __device__ __forceinline__ uint32_t part(const uint4& t, int i) { return i == 0 ? t.x : i == 1 ? t.y : i == 2 ? t.z : t.w; }
     __device__ __forceinline__ uint32_t get(int w, int i) const {
@@ -228,10 +255,10 @@ __device__ __forceinline__ bool bit_at(const uint32_t* words, int v) { return wo
 // from the rest, a lane a token, and passing them over costs a bit each.  Then a warp takes a position's run, or a part of it,
 // at a time: the rest is copied, or compared, as it is.  Low tokens are the common ones and have the longest lists, so their
 // CTAs come first.
-template <int kType, bool kWords, bool kAccept>
+template <int kType, bool kShift, bool kAccept>
 __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(EditView e) {
     using B = Bits<kType>;
-    using X = Batch<kType>;
+    using X = Batch<kType, kShift>;
     constexpr int kWarps = kEditThreads / 32;
     constexpr uint32_t kListSeen = 1u << 15, kListInBlock = 1u << 14, kNoToken = 0xFFFFFFFFu;
     extern __shared__ uint4 dynamic[];
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
     const int b1 = min(min(b0 + e.rows, a.block), used_positions(a, s));
     if (b0 >= b1) return;
     // the rows are on their way to L2 meanwhile
-    if (kWords && !kAccept && tid < b1 - b0 && n * B::kSize >= 16)
+    if (!kShift && !kAccept && tid < b1 - b0 && n * B::kSize >= 16)
         prefetch_run(static_cast<const char*>(a.logits_dev) + ((row0 + b0 + tid) * a.row_stride + v0) * B::kSize, (uint32_t)(n * B::kSize) & ~15u);
     // what the stream's part of the arguments says, all of it asked for at once
     const int parts = e.parts, span = kEditRun / parts, log_span = 31 - __clz(span);
@@ -327,35 +354,13 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
         uint32_t token0 = lane < n_mine ? mine[lane] : kNoToken, x0 = 0;
         if (token0 != kNoToken) x0 = B::read(row, token0 & (kEditRun - 1));
         float most = -INFINITY;                    // of the rest,
-        int where = -1;                            // and the batch, or the token (~) that it is in
+        int where = -1;                            // and the first token of its batch, or (~) itself
         uint32_t some = 0;                         // whether the lane has a token that is allowed
-        int base = first;
-        if (kWords && base + X::kTokens <= last) {
-            X next;
-            next.load(row + base * B::kSize, allowed ? allowed + base / 32 : nullptr, lane);
-            for (; base + X::kTokens <= last; base += X::kTokens) {
-                X x = next;
-                if (base + 2 * X::kTokens <= last)
-                    next.load(row + (base + X::kTokens) * B::kSize, allowed ? allowed + (base + X::kTokens) / 32 : nullptr, lane);
-                if (kAccept) {
-                    some |= x.ok;
-                    const float m = x.most(x.ok & ~known_lane[base / X::kTokens][lane]);
-                    if (m > most) {
-                        most = m;
-                        where = base;
-                    }
-                } else {
-                    const bool all = x.ok == X::kAll;
-                    if (!all) x.hide();
-                    uint4* const to = reinterpret_cast<uint4*>(out + base * B::kSize) + lane;
-                    if (!all || e.out != a.logits_dev)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) to[32 * w] = x.x[w];
-                }
-            }
-        }
-#pragma unroll 4
-        for (int v = base + lane; v < last; v += 32) {   // what is less than a batch, and rows that do not begin on 16 bytes
+        // the words of 16 bytes of first .. last, and the few tokens before and behind them
+        const int lead = kShift ? (int)(-(reinterpret_cast<uintptr_t>(row + first * B::kSize) / B::kSize) & (X::kPer - 1)) : 0;
+        const int begin = min(first + lead, last), end = begin + (last - begin) / X::kPer * X::kPer;
+        const bool whole = !kShift || ((reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(row)) & 15) == 0;   // words of the output too
+        auto single = [&](int v) {
             const uint32_t x = B::read(row, v);
             const bool ok = !allowed || bit_at(allowed, v);
             if (kAccept) {
@@ -367,7 +372,42 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
             } else if (!ok || e.out != a.logits_dev) {
                 B::write(out, v, ok ? x : B::kNone);
             }
+        };
+        if (kShift && first + lane < begin) single(first + lane);
+        if (begin < end) {
+            X next;
+            next.load(row, allowed, begin, end, lane);
+            for (int base = begin; base < end; base += X::kTokens) {
+                X x = next;
+                if (base + X::kTokens < end) next.load(row, allowed, base + X::kTokens, end, lane);
+                if (kAccept) {
+                    some |= x.ok;
+                    const float m = x.most(x.ok & ~X::known_bits(known, known_lane, base, end, lane));
+                    if (m > most) {
+                        most = m;
+                        where = base;
+                    }
+                } else {
+                    const bool all = x.ok == X::kAll;
+                    if (!all) x.hide();
+                    if (all && e.out == a.logits_dev) continue;
+                    char* const to = out + (base + X::token(0, lane)) * B::kSize;
+                    const bool full = base + X::kTokens <= end;
+                    if (whole) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            if (full || base + X::token(w, lane) + X::kPer <= end) reinterpret_cast<uint4*>(to)[32 * w] = x.x[w];
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int i = 0; i < X::kPer; ++i)
+                                if (full || base + X::token(w, lane) + X::kPer <= end) B::write(to + 512 * w, i, x.get(w, i));
+                    }
+                }
+            }
         }
+        if (end + lane < last) single(end + lane);
         // the tokens on the list
         if (!kAccept) __syncwarp();
         float best = -INFINITY;
@@ -421,10 +461,10 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
             if (best == all) v = which;
             if (most == all) {
                 int at = ~where;
-                if (kWords && where >= 0) {        // its words once more
+                if (where >= 0) {                  // its words once more
                     X x;
-                    x.load(row + where * B::kSize, allowed ? allowed + where / 32 : nullptr, lane);
-                    at = where + x.find(x.ok & ~known_lane[where / X::kTokens][lane], all, lane);
+                    x.load(row, allowed, where, end, lane);
+                    at = where + x.find(x.ok & ~X::known_bits(known, known_lane, where, end, lane), all, lane);
                 }
                 v = min(v, (uint32_t)at);
             }
@@ -530,12 +570,12 @@ int check_edit(moe_mxfp4_edit_args* a) {
     return (int64_t)a->streams * a->block * edit_runs(a->vocab) > 0x7FFFFFFF ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// Positions of a CTA: as many as leave eight CTAs for every SM.
+// Positions of a CTA: as many as leave four CTAs for every SM.
 void group_rows(moe::EditView* e) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 1;
     e->runs = edit_runs(e->a.vocab);
-    const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (8 * sms);
+    const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (4 * sms);
     e->rows = (int)(most < 1 ? 1 : most > moe::kMostRows ? moe::kMostRows : most);
     if (e->rows > e->a.block) e->rows = e->a.block;
     e->groups = (e->a.block + e->rows - 1) / e->rows;
@@ -551,17 +591,17 @@ template <bool kAccept>
 int launch_edit(const moe::EditView& e, cudaStream_t st) {
     const dim3 grid((unsigned)((int64_t)e.a.streams * e.groups * e.runs));
     const int size = e.a.dtype == MOE_DTYPE_FP32 ? 4 : 2;
-    const bool words = aligned(e.a.logits_dev, 16) && e.a.row_stride * size % 16 == 0 &&
-                       (kAccept || (aligned(e.out, 16) && e.out_stride * size % 16 == 0));
+    const bool shift = !aligned(e.a.logits_dev, 16) || e.a.row_stride * size % 16 ||
+                       (!kAccept && (!aligned(e.out, 16) || e.out_stride * size % 16));
     const size_t shared = moe::kEditRun * (4 + 2 + (e.a.bias_begin_dev ? 4 : 0));   // the counts and the list, the biases if there are any
     auto go = [&](auto kern) { return moe::launch_dependent(kern, grid, dim3(moe::kEditThreads), shared, st, e); };
     cudaError_t r;
     if (e.a.dtype == MOE_DTYPE_FP32)
-        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP32, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP32, false, kAccept>);
+        r = shift ? go(moe::edit_kernel<MOE_DTYPE_FP32, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP32, false, kAccept>);
     else if (e.a.dtype == MOE_DTYPE_BF16)
-        r = words ? go(moe::edit_kernel<MOE_DTYPE_BF16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_BF16, false, kAccept>);
+        r = shift ? go(moe::edit_kernel<MOE_DTYPE_BF16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_BF16, false, kAccept>);
     else
-        r = words ? go(moe::edit_kernel<MOE_DTYPE_FP16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP16, false, kAccept>);
+        r = shift ? go(moe::edit_kernel<MOE_DTYPE_FP16, true, kAccept>) : go(moe::edit_kernel<MOE_DTYPE_FP16, false, kAccept>);
     return r == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
