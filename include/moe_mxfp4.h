@@ -603,7 +603,7 @@ int moe_mxfp4_cache_append_rotated(moe_mxfp4_cache* c, void* state_dev, int32_t 
  *   z <- z - frequency[s] * c - presence[s] * [c > 0]
  *   z <- z + the bias of v                               (of a token given twice, the last one counts)
  *   z <- -inf                                            where bit v of allowed[s, b] is 0
- * in fp32.  Tokens outside [0, vocab) (padding) count nowhere.  Positions lengths[s] and behind are not
+ * in fp32, z / r as the product with the rounded 1 / r.  Tokens outside [0, vocab) (padding) count nowhere.  Positions lengths[s] and behind are not
  * read, and left as they were in the output. */
 typedef struct {
     const void* logits_dev;               /* [streams, block, vocab], row_stride elements between positions */
@@ -626,7 +626,7 @@ typedef struct {
     const int32_t* bias_begin_dev;        /* [streams + 1]: stream s has entries begin[s] .. begin[s + 1], or NULL */
     const int32_t* bias_ids_dev;          /* tokens, ... */
     const float* bias_dev;                /* ... and what is added to their logits */
-    int64_t bias_entries;                 /* entries in all, 0..2^31 - 1: what bias_begin names beyond them is not read */
+    int64_t bias_entries;                 /* entries in all, 0..2^31 - 2: what bias_begin names beyond them is not read */
     const uint32_t* allowed_dev;          /* [streams, block, allowed_stride] or NULL: bit v % 32 of word v / 32 */
     int64_t allowed_stride;               /* words between positions; 0 = (vocab + 31) / 32 */
 } moe_mxfp4_edit_args;

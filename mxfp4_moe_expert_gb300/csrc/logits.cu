@@ -2,8 +2,9 @@
 // them (moe_mxfp4_accept_edited): penalties for tokens that a stream has said or was prompted with, biases and
 // grammar masks.
 //
-// How often a token was said is counted where it is needed: a CTA has a run of tokens of the vocabulary and
-// counts those of the stream's history that lie in it in shared memory, once for some positions of the block, so
+// A vocabulary has few tokens that a stream has said, and the rest is copied, or compared, as it is.  How
+// often a token was said is counted where it is needed: a CTA has a run of tokens of the vocabulary and counts
+// those of the stream's history that lie in it in shared memory, once for some positions of the block, so
 // nothing is kept from call to call.
 #include <cuda_fp16.h>
 
@@ -250,11 +251,19 @@ __device__ __forceinline__ void prefetch_run(const void* p, uint32_t bytes) {
 
 __device__ __forceinline__ bool bit_at(const uint32_t* words, int v) { return words[v >> 5] >> (v & 31) & 1; }
 
-// A CTA per run of the vocabulary, stream and group of positions.  It counts the run's tokens of the history once and
-// lists those that something is known of, with what is taken off them: few of a vocabulary, so they are edited apart
-// from the rest, a lane a token, and passing them over costs a bit each.  Then a warp takes a position's run, or a part of it,
-// at a time: the rest is copied, or compared, as it is.  Low tokens are the common ones and have the longest lists, so their
-// CTAs come first.
+// A CTA per run of the vocabulary, stream and group of positions.  It counts the run's tokens of the history once
+// and lists those that something is known of, with what is taken off them: few of a vocabulary, so they are edited
+// apart from the rest, a lane a token, and passing them over costs a bit each.  Then a warp takes a position's run, or
+// a part of it, at a time: the rest is copied, or compared, as it is.  Low tokens are the common ones and have the
+// longest lists, so their CTAs come first.
+//
+// Bound by HBM where rows are written: 32 x 8 positions of 151936 fp32 logits (311 MB read and written) in 56 us,
+// 5.6 TB/s, 0.83 of the copy rate.  By instructions, half of them the masks', where 16-bit logits under a grammar are
+// compared: 48 x 11 positions of 151936 in bf16 (171 MB) in 54 us, 3.2 TB/s, where 32 x 8 in fp32 without one take
+// 34 us, 4.6 TB/s.  By its start (the look-ups, the history) where a CTA has one position: 96 x 1 of 32000 in 14 us.
+// Measured on those trees: a CTA's tokens dealt out to all of its warps for every position, each looking for its own,
+// 86 us where this took 74; counters of all tokens cleared and looked through 94; 128 and 512 threads 66 and 62 where
+// 256 took 58.  Rows prefetched to L2 during the start: edits 58 -> 56, acceptance 58 -> 61 (left out there).
 template <int kType, bool kShift, bool kAccept>
 __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(EditView e) {
     using B = Bits<kType>;
@@ -287,8 +296,8 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
     const int* const history = a.history_dev ? a.history_dev + s * a.history_stride : nullptr;
     const int len = history ? (int)min((int64_t)a.history_lengths_dev[s], a.history_room) : 0;
     const int prompt = history && a.prompt_lengths_dev ? a.prompt_lengths_dev[s] : 0;
-    const int bias_end = entry ? (int)min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries) : 0;
-    const int bias_begin = entry ? max(a.bias_begin_dev[s], 0) + tid : 0;
+    const int64_t bias_end = entry ? min((int64_t)a.bias_begin_dev[s + 1], a.bias_entries) : 0;
+    const int64_t bias_begin = entry ? (int64_t)max(a.bias_begin_dev[s], 0) + tid : 0;
     Penalty p{a.repetition_dev ? a.repetition_dev[s] : 1.0f, 1.0f, a.frequency_dev ? a.frequency_dev[s] : 0.0f,
               a.presence_dev ? a.presence_dev[s] : 0.0f};
     const int token = a.tokens_dev && tid < b1 ? a.tokens_dev[row0 + tid] : -1;
@@ -328,9 +337,9 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
             }
             mark(v);
         }
-    for (int i = bias_begin; i < bias_end; i += kEditThreads) {
+    for (int64_t i = bias_begin; i < bias_end; i += kEditThreads) {
         const uint32_t v = (uint32_t)a.bias_ids_dev[i] - (uint32_t)v0;
-        if (v < (uint32_t)n && !atomicMax(entry + v, i + 1)) mark(v);
+        if (v < (uint32_t)n && !atomicMax(entry + v, (int)i + 1)) mark(v);
     }
     p.inverse = __frcp_rn(p.repetition);
     __syncthreads();
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(Edi
     }
 }
 
-// A CTA per stream: the targets of its positions, and the path of accepted nodes.  It starts while the edits end (each of
+// A CTA per stream: the targets of its positions, and the path of accepted nodes; some 3 us of the launch and its look-ups.  It starts while the edits end (each of
 // their CTAs has waited for what came before), and reads what they do not write before it waits for them.
 __global__ void __launch_bounds__(256) accept_path_kernel(EditView e, int* __restrict__ target, int* __restrict__ accepted,
                                                           int* __restrict__ next_token, int* __restrict__ path) {
@@ -559,7 +568,7 @@ int check_edit(moe_mxfp4_edit_args* a) {
     if (a->history_dev && (!a->history_lengths_dev || a->history_room < 0 || a->history_room >= 1 << 29 ||
                            a->history_stride < a->history_room))
         return MOE_ERR_INVALID_ARG;
-    if (a->bias_begin_dev && (a->bias_entries < 0 || a->bias_entries > 0x7FFFFFFF)) return MOE_ERR_INVALID_ARG;
+    if (a->bias_begin_dev && (a->bias_entries < 0 || a->bias_entries >= 0x7FFFFFFF)) return MOE_ERR_INVALID_ARG;
     if (a->bias_begin_dev && a->bias_entries && (!a->bias_ids_dev || !a->bias_dev)) return MOE_ERR_INVALID_ARG;
     if (!aligned(a->mask_dev, 8)) return MOE_ERR_INVALID_ARG;
     for (const void* p : {(const void*)a->tokens_dev, (const void*)a->lengths_dev, (const void*)a->history_dev, (const void*)a->history_lengths_dev,
