@@ -554,8 +554,10 @@ def _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_l
             raise ValueError(f"{name}: {n} contiguous {dtype} values on {logits.device}")
         return t.data_ptr()
 
-    if mask is not None and (mask.dtype is not torch.int64 and mask.dtype is not torch.uint64):
+    if mask is not None and (mask.shape != (S, B) or (mask.dtype is not torch.int64 and mask.dtype is not torch.uint64)):
         raise ValueError("mask: int64 [streams, block]")
+    if tokens is not None and tokens.shape != (S, B):
+        raise ValueError("tokens: int32 [streams, block]")
     hist, stride, room, begin, ids, added, entries, words = None, 0, 0, None, None, None, 0, 0
     if history is not None:
         if (history.dtype is not i32 or history.get_device() != index or history.dim() != 2 or history.shape[0] != S
@@ -575,8 +577,8 @@ def _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_l
         begin, ids, added = (values("bias begin", begin, i32, S + 1), values("bias ids", ids, i32, entries),
                              values("bias values", added, f32, entries))
     if allowed is not None:
-        words = allowed.shape[-1] if allowed.dim() else 0
-        if words < (V + 31) // 32:
+        words = allowed.shape[-1] if allowed.dim() == 3 else 0
+        if words < (V + 31) // 32 or allowed.shape[:2] != (S, B):
             raise ValueError("allowed: int32 [streams, block, (vocab + 31) // 32]")
         allowed = values("allowed", allowed, i32, S * B * words)
     args = moe_mxfp4_edit_args(

@@ -343,11 +343,12 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
     // Rounds of heads of a token, dealt out to warps in parts of `steps` each, by two or three CTAs on every SM: what gives
     // the busiest warps the least to do, a part's start (its page, its sines and cosines) taken for a round's work.  Where
     // both do as well two do better, whose loads and stores come in longer runs of memory (47976 tokens of 36 narrow heads: 67 us
-    // with two, 76 with three); three serve where two leave warps idle (2560 tokens of 48 heads: 127 us for 8 layers, 140 with two).
+    // with two, 76 with three); three serve where two leave warps idle (2560 tokens of 48 heads: 127 us for 8 layers, 140 with
+    // two), and where a token has a round or two, and warps wait for its look-ups (two heads: 154 us, 195 with two).
     const int rounds = (heads * (D / 16) + 31) / 32;
     int parts = 1, steps = rounds, resident = 2;
     int64_t least = INT64_MAX;
-    for (int ctas = 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
+    for (int ctas = rounds <= 2 && layout != moe::kAnywhere ? 3 : 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
         for (int n = 1; n <= rounds && n <= 64; ++n) {
             const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
             const int64_t warps = 8 * (int64_t)ctas * sms, cost = ((int64_t)tokens * made + warps - 1) / warps * (each + 1) * ctas;

@@ -299,7 +299,8 @@ def test_the_binding_refuses_wrong_tensors():
     x, t = torch.zeros((2, 3, 50), device="cuda"), torch.zeros((2, 3), dtype=torch.int32, device="cuda")
     one = torch.zeros(2, dtype=torch.int32, device="cuda")
     h = torch.zeros((2, 9), dtype=torch.int32, device="cuda")
-    bad = [dict(mask=t), dict(mask=torch.zeros((2, 3), dtype=torch.int64)), dict(lengths=one.long()), dict(lengths=one[:1]), dict(history=h),
+    bad = [dict(mask=torch.zeros((3, 2), dtype=torch.int64, device="cuda")), dict(allowed=torch.zeros((3, 2, 2), dtype=torch.int32, device="cuda")),
+           dict(mask=t), dict(mask=torch.zeros((2, 3), dtype=torch.int64)), dict(lengths=one.long()), dict(lengths=one[:1]), dict(history=h),
            dict(history_lengths=one), dict(prompt_lengths=one), dict(history=h.long(), history_lengths=one),
            dict(history=h[:1], history_lengths=one), dict(history=h.T, history_lengths=one), dict(repetition=one),
            dict(history=h[:1].expand(2, 9), history_lengths=one), dict(frequency=torch.zeros(3, device="cuda")),
@@ -313,8 +314,9 @@ def test_the_binding_refuses_wrong_tensors():
     for out in (torch.zeros((2, 3, 49), device="cuda"), x.half(), x.cpu()):
         with pytest.raises(ValueError):
             pkg.edit_logits(x, t, out=out)
-    with pytest.raises(ValueError):
-        pkg.edit_logits(x, t[:1])
+    for tokens in (t[:1], t.T.contiguous(), t.view(6)):
+        with pytest.raises(ValueError):
+            pkg.edit_logits(x, tokens)
     with pytest.raises(ValueError):
         pkg.edit_logits(x.long(), t)
     with pytest.raises(ValueError):
