@@ -118,7 +118,9 @@ enum : int {
 // Bound by HBM: 16381 tokens of 56 + 8 heads of 128 (537 MB read and written) in 86 us, 6.3 TB/s, 0.92 of the copy rate;
 // 47976 tokens of 32 + 4 heads of 64 in 67 us, 0.97; 2 layers of those into the cache with their values in 154 us, 0.94.  Of few
 // tokens by the launch and the chain of look-ups: 8 tokens of one layer in 2.6 us, 3.2 into the cache.
-template <int D, bool kBf16, int kLayout, bool kCache>
+// Few heads: a round has the heads of kPack tokens, and a token's sines and cosines are shared by its lanes alone (two heads of
+// 128, 300000 tokens: 96 us, 154 with a token a round; 46 are the bytes').
+template <int D, bool kBf16, int kLayout, bool kCache, int kPack>
 __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kernel(RotaryView r, HeadRows q, HeadRows k, const uint16_t* v,
                                                                                   const int* __restrict__ positions, int tokens, int parts,
                                                                                   int steps, PagePlace pages) {
@@ -133,8 +135,11 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
     // the lane's words: elements o0.. and o1..
     const bool across = kLayout == kHalves && 16 * j < r.R;
     const int o0 = kLayout != kHalves || across ? 8 * j : half + 8 * j, o1 = across ? half + 8 * j : D / 2 + 8 * j;
-    // the pairs whose sine and cosine the lane takes (first, second)
-    const int first = kLayout == kPairs || D == 64 ? lane : 8 * (lane / 4) + lane % 4, second = kLayout == kPairs ? lane + 32 : first + 4;
+    // a token's lanes, and how many of them take the sines and cosines of eight pairs: pair i of the lane's eight is
+    // taken by the (i % kSharers)-th of the lanes that share them, as its (i / kSharers)-th
+    constexpr int kTokenLanes = 32 / kPack, kSharers = kTokenLanes / kLanes, kTaken = 8 / kSharers;
+    const int member = lane / kTokenLanes;         // of the unit's tokens
+    auto pair_of = [&](int j, int i) { return kLayout == kPairs ? 4 * j + (i < 4 ? i : D / 4 + i - 4) : 8 * j + i; };
     // which of its pairs (kAnywhere: elements) turn
     uint32_t turns = across ? 0xFF : 0;
     if (kLayout != kHalves) {
@@ -145,12 +150,12 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
             turns |= (uint32_t)(e < r.R) << i;
         }
     }
-    const int64_t units = (int64_t)tokens * parts, stride = (int64_t)gridDim.x * 8;
+    const int64_t units = kPack > 1 ? ((int64_t)tokens + kPack - 1) / kPack : (int64_t)tokens * parts, stride = (int64_t)gridDim.x * 8;
     const int64_t u0 = (int64_t)blockIdx.x * 8 + warp;
-    // unit u: a token, and the first of its heads that the warp takes (a 64-bit division costs as much as half a round)
+    // unit u: the lane's token, and the first of its heads that the warp takes (a 64-bit division costs as much as half a round)
     auto unit = [&](int64_t u, int* tok, int* head) {
-        *tok = parts == 1 ? (int)u : (int)(u / parts);
-        *head = parts == 1 ? 0 : (int)(u - (int64_t)*tok * parts) * steps * kHeads;
+        *tok = kPack > 1 ? (int)u * kPack + member : parts == 1 ? (int)u : (int)(u / parts);
+        *head = kPack > 1 ? -member * (kHeads / kPack) : parts == 1 ? 0 : (int)(u - (int64_t)*tok * parts) * steps * kHeads;
     };
     int64_t ahead_u = u0;
     int ahead_step = 0, ahead_slot = 0, slot = 0, ahead_tok, ahead_head;
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
     auto ahead = [&] {
         if (ahead_u < units) {
             const int h = ahead_head + ahead_step * kHeads + g;
-            if (h < heads) {
+            if (h < heads && (kPack == 1 || ahead_tok < tokens)) {
                 const uint16_t* src;
                 if (h < q.heads) {
                     src = q.src + ahead_tok * q.in + (int64_t)h * D;
@@ -185,8 +190,9 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
         int tok, h0;
         unit(u, &tok, &h0);
         TokenPlace place{};
-        if (kCache) place = token_place(pages, tok);
-        const int p = kCache ? place.position : positions[tok];
+        const bool real = kPack == 1 || tok < tokens;            // (the last unit may have fewer tokens)
+        if (kCache && real) place = token_place(pages, tok);
+        const int p = kCache ? place.position : real ? positions[tok] : 0;
         float c[kTurns], s[kTurns];
         if (kLayout == kAnywhere) {
             __syncwarp();
@@ -200,17 +206,21 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
                 s[i] = e < half ? -t.y : t.y;
             }
         } else if (r.R) {
-            float2 t0 = make_float2(0, 0), t1 = t0;
-            if (first < half) t0 = turn_of(r.turns[first], p, r.gain);
-            if (D == 128 && second < half) t1 = turn_of(r.turns[second], p, r.gain);
+            float2 t[kTaken];
+            const int in = lane % kTokenLanes;
+#pragma unroll
+            for (int i = 0; i < kTaken; ++i) {
+                const int pair = pair_of(in / kSharers, i * kSharers + in % kSharers);
+                t[i] = pair < half ? turn_of(r.turns[pair], p, r.gain) : make_float2(0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < kTurns; ++i) {
-                const int from = D == 128 ? 4 * j + i % 4 : kLayout == kPairs ? 4 * j + i % 4 + 16 * (i / 4) : (8 * j + i) & 31;
-                c[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.x : t0.x, from);
-                s[i] = __shfl_sync(0xFFFFFFFFu, D == 128 && i >= 4 ? t1.y : t0.y, from);
+                const int from = member * kTokenLanes + (kSharers * j + i % kSharers) % kTokenLanes;
+                c[i] = __shfl_sync(0xFFFFFFFFu, t[i / kSharers % kTaken].x, from);
+                s[i] = __shfl_sync(0xFFFFFFFFu, t[i / kSharers % kTaken].y, from);
             }
         }
-        if (kCache) token_holders(pages, &place);
+        if (kCache && real) token_holders(pages, &place);
         for (int step = 0; step < steps; ++step) {
             ahead();
             copies_wait<kStages - 1>();
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(256, kLayout == kAnywhere ? 2 : 3) rotate_kern
                 }
                 __syncwarp();
             }
-            if (h >= heads || (kCache && !place.used)) continue;
+            if (h >= heads || !real || (kCache && !place.used)) continue;
             if (!is_v) {
                 if (kLayout != kAnywhere)
 #pragma unroll
@@ -359,10 +369,17 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
                 resident = ctas;
             }
         }
-    const int64_t want = ((int64_t)tokens * parts + 7) / 8;
-    auto kern = layout == moe::kPairs    ? moe::rotate_kernel<D, kBf16, moe::kPairs, kCache>
-                : layout == moe::kHalves ? moe::rotate_kernel<D, kBf16, moe::kHalves, kCache>
-                                         : moe::rotate_kernel<D, kBf16, moe::kAnywhere, kCache>;
+    // few heads: as many tokens a round as it has room for, up to four
+    const int pack = layout == moe::kAnywhere || heads * (D / 16) > 16 ? 1 : heads * (D / 16) > 8 ? 2 : 4;
+    if (pack > 1) resident = 3;
+    const int64_t want = (pack > 1 ? ((int64_t)tokens + pack - 1) / pack + 7 : (int64_t)tokens * parts + 7) / 8;
+    auto kern = moe::rotate_kernel<D, kBf16, moe::kAnywhere, kCache, 1>;
+    if (layout == moe::kHalves)
+        kern = pack == 4 ? moe::rotate_kernel<D, kBf16, moe::kHalves, kCache, 4> : pack == 2 ? moe::rotate_kernel<D, kBf16, moe::kHalves, kCache, 2>
+                                                                                            : moe::rotate_kernel<D, kBf16, moe::kHalves, kCache, 1>;
+    if (layout == moe::kPairs)
+        kern = pack == 4 ? moe::rotate_kernel<D, kBf16, moe::kPairs, kCache, 4> : pack == 2 ? moe::rotate_kernel<D, kBf16, moe::kPairs, kCache, 2>
+                                                                                           : moe::rotate_kernel<D, kBf16, moe::kPairs, kCache, 1>;
     return moe::launch_dependent(kern, dim3((unsigned)(want < (int64_t)resident * sms ? want : (int64_t)resident * sms)), dim3(256), 0, st, r, q, k, v, positions, tokens,
                                  parts, steps, pages);
 }
