@@ -288,6 +288,26 @@ def test_two_calls_at_once():
             c.check_accept(x)
 
 
+def test_two_captured_graphs_and_a_given_workspace():
+    """Graphs whose calls make their workspaces do not share them; one that is given serves calls one after the other."""
+    cases = [Case(S=5, B=6, V=9000, seed=s, tree=s == 1) for s in range(2)]
+    xs = [c.logits.cuda() for c in cases]
+    ws = torch.empty(max(pkg.moe_mxfp4_accept_edited_bytes(5, 6, 9000)[1], 8), dtype=torch.uint8, device="cuda")
+    for given in (None, ws):
+        graphs, got = [], []
+        for c, x in zip(cases, xs):
+            pkg.accept_edited(x, workspace=given, **c.on)
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                got.append(pkg.accept_edited(x, workspace=given, **c.on))
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for c, g in zip(cases, got):
+            c.check_accept(g)
+
+
 def test_empty_batches():
     x = torch.zeros((0, 3, 50), device="cuda")
     tokens = torch.zeros((0, 3), dtype=torch.int32, device="cuda")

@@ -159,6 +159,19 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
 
 
+def test_two_calls_at_once():
+    r = pkg.Rotary(head_dim=128, norm=True, dtype=torch.bfloat16, device="cuda")
+    xs = [torch.randn((3000, 9, 128), device="cuda").bfloat16() for _ in range(2)]
+    pos = [torch.arange(3000, dtype=torch.int32, device="cuda") + 1000 * i for i in range(2)]
+    want = [r.rotate(x, None, p)[0] for x, p in zip(xs, pos)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[r.rotate(x, None, p, stream=s.cuda_stream)[0] for _ in range(4)] for x, p, s in zip(xs, pos, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(t, w) for t in g)
+
+
 def test_the_binding_refuses_wrong_tensors():
     r = pkg.Rotary(head_dim=64, dtype=torch.bfloat16, device="cuda")
     q, pos = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda"), i32([0, 1, 2, 3])
@@ -329,7 +342,8 @@ def paths_of(masks, rng):
 
 
 @pytest.mark.parametrize("kw,B,streams", [(dict(), 8, 5), (dict(D=128, Hkv=8, page=32, L=3), 40, 4), (dict(Hkv=1, dtype=torch.float16), 2, 5),
-                                          (dict(Hkv=5, page=128, M=3, L=1), 64, 3), (dict(L=130, Hkv=1, P=20, M=4), 9, 5)])
+                                          (dict(Hkv=5, page=128, M=3, L=1), 64, 3), (dict(L=130, Hkv=1, P=20, M=4), 9, 5),
+                                          (dict(S=300, M=5, P=1500, L=1, Hkv=1), 5, 297)])
 @pytest.mark.parametrize("history", [False, True])
 def test_accepted_paths_are_moved_together(kw, B, streams, history):
     c, mem, b = make(**kw, seed=B, room=B)
@@ -360,6 +374,28 @@ def test_accepted_paths_are_moved_together(kw, B, streams, history):
     assert torch.equal(mem.cpu().view(torch.int16), b.pool.view(torch.int16))
     if history:
         assert torch.equal(dev.cpu(), said)
+    c.close()
+
+
+@pytest.mark.parametrize("D,Hkv,page", [(64, 3, 16), (128, 2, 32)])
+def test_long_paths_move_by_any_distance(D, Hkv, page):
+    """Paths of more positions than are looked up at once, over many pages, whose moves overlap: each node goes to where
+    another one came from."""
+    B = 64
+    paths = [[0] + list(range(2, B)), list(range(5, B)), list(range(B)), [B - 1], list(range(0, B, 2)), list(range(1, B)),
+             [0, 1, 2] + list(range(31, B)), list(range(32)) + list(range(33, B))]
+    c, mem, b = make(L=2, S=len(paths), M=10, P=90, Hkv=Hkv, page=page, D=D, room=B)
+    assert b.reserve([B] * b.S)
+    c.reserve(B)
+    c.commit(i32([len(p) for p in paths]), path=i32([p + [-1] * (B - len(p)) for p in paths]))
+    assert status(c) == pkg.MOE_OK
+    for s, path in enumerate(paths):
+        for i, x in enumerate(path):
+            (a, x), (d, y) = divmod(b.length[s] + x, page), divmod(b.length[s] + i, page)
+            b.pool[:, :, b.table[s][d], :, y] = b.pool[:, :, b.table[s][a], :, x]
+    b.truncate([b.length[s] + len(p) for s, p in enumerate(paths)])
+    assert_books(c, b)
+    assert torch.equal(mem.cpu().view(torch.int16), b.pool.view(torch.int16))
     c.close()
 
 
