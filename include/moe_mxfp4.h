@@ -542,7 +542,8 @@ typedef struct {
  *                      pairs that turn at least `high` times in the original length keep their frequency
  * moe_mxfp4_rotary_from does the same from a caller's own f_i in radians per position (n host doubles;
  * |f_i| <= 2 pi).  MOE_ERR_INVALID_ARG for a NULL pointer, an odd or negative size, base or factor not
- * positive and finite, original not positive, high <= low (PARTS), or a frequency that is not finite. */
+ * positive and finite, original not positive, high <= low (PARTS), or a frequency that is not finite or
+ * beyond 2 pi. */
 #define MOE_ROTARY_NONE   0
 #define MOE_ROTARY_LINEAR 1
 #define MOE_ROTARY_NTK    2

@@ -244,6 +244,18 @@ def test_lengths_beyond_the_history_and_the_biases_are_cut():
     assert torch.equal(got.cpu(), want)
 
 
+def test_offsets_beyond_32_bits():
+    """Positions whose elements, and bytes, lie beyond 2^31 of the tensor's start."""
+    S, B, V, stride = 2, 5, 5003, (1 << 28) + 3
+    c = Case(S=S, B=B, V=V, dtype=torch.bfloat16, seed=11, tree=True)
+    x = torch.empty((S * B - 1) * stride + V, dtype=torch.bfloat16, device="cuda").as_strided((S, B, V), (B * stride, stride, 1))
+    x.copy_(c.logits)
+    c.check_accept(pkg.accept_edited(x, **c.on))
+    c.check_edit(pkg.edit_logits(x, **c.on))
+    pkg.edit_logits(x, out=x, **c.on)
+    c.check_edit(x)
+
+
 def test_on_another_stream_in_a_graph_and_with_a_workspace():
     c = Case(S=4, B=6, V=30000, seed=3, tree=True)
     x = c.logits.cuda()

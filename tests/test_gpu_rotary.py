@@ -272,6 +272,32 @@ def test_alone_and_into_the_cache_give_the_same_bits():
     c.close()
 
 
+def test_pages_beyond_32_bits():
+    """Pages whose elements lie beyond 2^31 of the pool's start: appending into them, and moving a path there."""
+    S, M, P, Hkv, page, D, B = 2, 3, 10, 2, 16, 64, 12
+    stride = (1 << 28) + 8
+    pools = [torch.empty((P - 1) * stride + Hkv * page * D, dtype=torch.bfloat16, device="cuda").as_strided(
+        (P, Hkv, page, D), (stride, page * D, D, 1)) for _ in range(2)]
+    c = pkg.KvCache(layers=[tuple(pools)], num_streams=S, max_pages=M)
+    b = Books(S, M, P, page)
+    b.length, b.held = [13, 30], [2, 3]
+    b.table, b.ref = [[9, 8, -1], [1, 7, 6]], [0, 1, 0, 0, 0, 0, 1, 1, 1, 1]
+    write_books(c, b)
+    r = pkg.Rotary(head_dim=D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.randn((S, B, Hkv, D), device="cuda").bfloat16() for _ in range(2))
+    c.append_rotated(0, None, k, v, r)
+    path = [[0, 2, 3, 5, 11], [1, 2, 4, 8, 9]]
+    pos = (c.length[:, None] + torch.arange(B, device="cuda", dtype=torch.int32)).int().contiguous()
+    rk = r.rotate(k, None, pos)[0]
+    c.commit(i32([5, 5]), path=i32([p + [-1] * (B - 5) for p in path]))
+    assert status(c) == pkg.MOE_OK and c.length.tolist() == [18, 35]
+    for s in range(S):
+        for i, x in enumerate(path[s]):
+            at, off = divmod(b.length[s] + i, page)
+            assert torch.equal(pools[0][b.table[s][at], :, off], rk[s, x]) and torch.equal(pools[1][b.table[s][at], :, off], v[s, x])
+    c.close()
+
+
 def test_positions_that_are_not_reserved_or_shared_are_skipped():
     """The queries are rotated all the same; the first error is kept."""
     c, mem, b = make(S=4, P=30, M=4)
