@@ -511,10 +511,22 @@ def moe_mxfp4_accept_edited(args: moe_mxfp4_edit_args, target_ptr, accepted_ptr,
 # ----------------------------------------------------------------------------- torch convenience
 
 
+_torch = None           # torch, once a call has needed it (an import statement costs a small call a tenth of its time)
+_LOGIT_TYPES = {}
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _LOGIT_TYPES.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32})
+    _torch = torch
+    return torch
+
+
 def _new(shape, dtype, device, stream, now, zero=False):
     """A tensor made on a call's stream (`now`: the current one): its fill is ordered with the call, and so is what still
     uses its memory."""
-    import torch
+    torch = _torch or _import_torch()
     make = torch.zeros if zero else torch.empty
     if stream == now:
         return make(shape, dtype=dtype, device=device)
@@ -525,23 +537,18 @@ def _new(shape, dtype, device, stream, now, zero=False):
 
 def _call_on(index, fn, *args):
     """Calls a C entry point that has no handle with the device `index` current."""
-    import torch
+    torch = _torch or _import_torch()
     if torch._C._cuda_getDevice() == index:
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)
 
 
-_LOGIT_TYPES = {}
-
-
 def _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition, frequency, presence,
                bias, allowed):
     """The arguments that edit_logits and accept_edited share, checked and laid out: (moe_mxfp4_edit_args, streams, block,
     vocab, elements between positions, device index)."""
-    import torch
-    if not _LOGIT_TYPES:
-        _LOGIT_TYPES.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32})
+    torch = _torch or _import_torch()
     kind = _LOGIT_TYPES.get(logits.dtype)
     if kind is None or not logits.is_cuda or logits.dim() != 3:
         raise ValueError("logits: a bf16, fp16 or fp32 CUDA tensor [streams, block, vocab]")
@@ -616,7 +623,7 @@ def edit_logits(logits, tokens=None, *, mask=None, lengths=None, history=None, h
     in place)."""
     args, S, B, V, row, index = _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths,
                                            repetition, frequency, presence, bias, allowed)
-    import torch
+    torch = _torch
     now = torch._C._cuda_getCurrentRawStream(index)
     stream = now if stream is None else stream
     if out is None:
@@ -626,7 +633,7 @@ def edit_logits(logits, tokens=None, *, mask=None, lengths=None, history=None, h
             raise ValueError("out: of the logits' shape and type")
         row = V if out.is_contiguous() else _logit_rows("out", out)
     if S * B * V:
-        st = _call_on(index, load_library().moe_mxfp4_edit_logits, args, out.data_ptr(), row, stream)
+        st = _call_on(index, (_lib or load_library()).moe_mxfp4_edit_logits, args, out.data_ptr(), row, stream)
         if st:
             _check(st, "moe_mxfp4_edit_logits")
     return out
@@ -638,33 +645,31 @@ def accept_edited(logits, tokens, *, mask=None, lengths=None, history=None, hist
     edit_logits.  Returns (target [streams, block], accepted [streams], next_token [streams], path [streams, block]), int32:
     path lists the accepted block positions, then -1 (KvCache.commit takes it).  Calls make their workspace on their stream;
     one that is given is 8-byte aligned and moe_mxfp4_accept_edited_bytes long."""
-    import torch
     args, S, B, V, _, index = _edit_args(logits, tokens, mask, lengths, history, history_lengths, prompt_lengths, repetition,
                                          frequency, presence, bias, allowed)
+    torch = _torch
     now = torch._C._cuda_getCurrentRawStream(index)
     stream = now if stream is None else stream
-    device, lib = logits.device, load_library()
-    rows, ends = _new((2, S, B), torch.int32, device, stream, now), _new((2, S), torch.int32, device, stream, now)
+    device, i32 = logits.device, torch.int32
+    target, path = _new((S, B), i32, device, stream, now), _new((S, B), i32, device, stream, now)
+    accepted, next_token = _new((S,), i32, device, stream, now), _new((S,), i32, device, stream, now)
     if workspace is None:
-        need = _ACCEPT_BYTES.get((S, B, V))
-        if need is None:
-            st, need = moe_mxfp4_accept_edited_bytes(S, B, V)
+        room = _ACCEPT_BYTES.get((S, B, V))
+        if room is None:
+            st, room = moe_mxfp4_accept_edited_bytes(S, B, V)
             _check(st, "moe_mxfp4_accept_edited_bytes")
             if len(_ACCEPT_BYTES) >= 1024:
                 _ACCEPT_BYTES.clear()
-            _ACCEPT_BYTES[S, B, V] = need
-        workspace, room = _new((need // 8 + 1,), torch.int64, device, stream, now), need
+            _ACCEPT_BYTES[S, B, V] = room
+        workspace = _new((room // 8 + 1,), torch.int64, device, stream, now)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace: contiguous, on {device}")
     else:
         room = workspace.numel() * workspace.element_size()
-    target, accepted = rows.data_ptr(), ends.data_ptr()
-    st = _call_on(index, lib.moe_mxfp4_accept_edited, args, target, accepted, accepted + 4 * S, target + 4 * S * B,
-                  workspace.data_ptr(), room, stream)
+    st = _call_on(index, (_lib or load_library()).moe_mxfp4_accept_edited, args, target.data_ptr(), accepted.data_ptr(),
+                  next_token.data_ptr(), path.data_ptr(), workspace.data_ptr(), room, stream)
     if st:
         _check(st, "moe_mxfp4_accept_edited")
-    target, path = rows.unbind(0)
-    accepted, next_token = ends.unbind(0)
     return target, accepted, next_token, path
 
 

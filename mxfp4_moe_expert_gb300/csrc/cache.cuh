@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 #include "common.cuh"
@@ -90,6 +91,17 @@ inline CacheView cache_view(const moe_mxfp4_cache* c, void* state) {
 
 // Allows the attention's kernels their shared memory on the current device, once for each.
 bool attend_prepare(int device);
+
+// SMs of the current device (0: an error), asked for once for each.
+inline int current_sm_count() {
+    static std::atomic<int> counts[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (sms = counts[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) counts[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
 
 // The handle's device for the duration of a call.
 class DeviceScope {

@@ -581,8 +581,7 @@ int check_edit(moe_mxfp4_edit_args* a) {
 
 // Positions of a CTA: as many as leave four CTAs for every SM.
 void group_rows(moe::EditView* e) {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 1;
+    const int known = moe::current_sm_count(), sms = known ? known : 1;
     e->runs = edit_runs(e->a.vocab);
     const int64_t ctas = (int64_t)e->a.streams * e->a.block * e->runs, most = ctas / (4 * sms);
     e->rows = (int)(most < 1 ? 1 : most > moe::kMostRows ? moe::kMostRows : most);

@@ -340,12 +340,6 @@ bool good_stride(int64_t* stride, int64_t row) {
     return *stride >= row && *stride % 8 == 0;
 }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
 template <bool kCache, int D, bool kBf16>
 cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, const moe::HeadRows& k, const uint16_t* v,
                           const int* positions, int tokens, const moe::PagePlace& pages, int sms, cudaStream_t st) {
@@ -454,7 +448,7 @@ int moe_mxfp4_rotate(const moe_mxfp4_rotary* r, const moe_mxfp4_rotate_args* arg
     }
     if (a.tokens == 0 || a.q_heads + a.kv_heads == 0) return MOE_OK;
     if (!a.positions_dev || !aligned(a.positions_dev, 4)) return MOE_ERR_INVALID_ARG;
-    const int sms = sm_count();
+    const int sms = moe::current_sm_count();
     if (!sms) return MOE_ERR_CUDA;
     return launch_rotate<false>(r, q, k, nullptr, a.positions_dev, a.tokens, moe::PagePlace{}, sms, static_cast<cudaStream_t>(stream));
 }
