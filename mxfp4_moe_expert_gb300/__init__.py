@@ -765,13 +765,15 @@ class Rotary:
             q_out = _new(qs, dtype, self.device, stream, now)
         else:
             qo_row = self._out("q_out", q_out, q)
-        if k is not None and k_out is None:
-            k_out = _new(k.shape, dtype, self.device, stream, now)
-        elif k is not None:
-            ko_row = self._out("k_out", k_out, k)
+        k_ptr = ko_ptr = None
+        if k is not None:
+            if k_out is None:
+                k_out = _new(key[2], dtype, self.device, stream, now)
+            else:
+                ko_row = self._out("k_out", k_out, k)
+            k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
         if n:
-            a = moe_mxfp4_rotate_args(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                                      None if k is None else k_out.data_ptr(), positions.data_ptr(), q_row, k_row, qo_row, ko_row,
+            a = moe_mxfp4_rotate_args(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, positions.data_ptr(), q_row, k_row, qo_row, ko_row,
                                       n, q_heads, kv_heads)
             st = _call_on(index, self._lib.moe_mxfp4_rotate, self.desc, a, stream)
             if st:

@@ -350,19 +350,21 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
     // with two, 76 with three); three serve where two leave warps idle (2560 tokens of 48 heads: 127 us for 8 layers, 140 with
     // two), and where a token has a round or two, and warps wait for its look-ups (two heads: 154 us, 195 with two).
     const int rounds = (heads * (D / 16) + 31) / 32;
-    int parts = 1, steps = rounds, resident = 2;
-    int64_t least = INT64_MAX;
-    for (int ctas = rounds <= 2 && layout != moe::kAnywhere ? 3 : 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
-        for (int n = 1; n <= rounds && n <= 64; ++n) {
-            const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
-            const int64_t warps = 8 * (int64_t)ctas * sms, cost = ((int64_t)tokens * made + warps - 1) / warps * (each + 1) * ctas;
-            if (cost < least) {
-                least = cost;
-                parts = made;
-                steps = each;
-                resident = ctas;
+    int parts = rounds, steps = 1, resident = 2;
+    if (rounds <= 2 || (int64_t)tokens * rounds > 16 * (int64_t)sms) {   // (else a round for each warp, and no more)
+        int64_t least = INT64_MAX;
+        for (int ctas = rounds <= 2 && layout != moe::kAnywhere ? 3 : 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
+            for (int n = 1; n <= rounds && n <= 64; ++n) {
+                const int each = (rounds + n - 1) / n, made = (rounds + each - 1) / each;
+                const int64_t warps = 8 * (int64_t)ctas * sms, cost = ((int64_t)tokens * made + warps - 1) / warps * (each + 1) * ctas;
+                if (cost < least) {
+                    least = cost;
+                    parts = made;
+                    steps = each;
+                    resident = ctas;
+                }
             }
-        }
+    }
     // few heads: as many tokens a round as it has room for, up to four
     const int pack = layout == moe::kAnywhere || heads * (D / 16) > 16 ? 1 : heads * (D / 16) > 8 ? 2 : 4;
     if (pack > 1) resident = 3;
