@@ -316,7 +316,8 @@ __device__ __forceinline__ int path_count(const CacheView& c, const moe_mxfp4_co
             const int* path = a.path_dev + (int64_t)s * a.block;
             for (int i = lane; i < n; i += 32) {
                 const int p = path[i], before = i ? path[i - 1] : -1;
-                if (p <= before || p >= a.block || (long long)len + p >= room) {
+                // (each lane looks at its own two places and reads before it knows of the others': `before` may be wrong itself)
+                if (p < 0 || p <= before || p >= a.block || (long long)len + p >= room) {
                     ok = false;
                 } else {
                     const int from = c.table(s)[(len + p) >> c.page_shift], to = c.table(s)[(len + i) >> c.page_shift];

@@ -491,6 +491,30 @@ def test_paths_that_are_refused_leave_their_stream_alone(wrong):
     c.close()
 
 
+@pytest.mark.parametrize("first", [[-5, -3, 2], [-2, -1, 0], [-20, -19, -18], [-1, 0, 1], [-1 << 31, -1 << 30, 0]])
+def test_paths_that_begin_below_the_block_are_refused(first):
+    """Ascending all the same.  The other streams' paths are kept."""
+    c, mem, b = make(S=3, M=6)
+    S, B, page = 3, 6, b.page
+    b = Books(3, 6, 30, page, mem.cpu())
+    b.reserve([20, 30, 9])
+    b.length = [20, 30, 9]
+    b.reserve([B] * S)
+    write_books(c, b)
+    path = [[0, 2, 3, -1, -1, -1], first + [-1] * 3, [0, 2, 3, -1, -1, -1]]
+    c.commit(i32([3, 3, 3]), path=i32(path))
+    assert c.state[:2].tolist() == [pkg.MOE_ERR_CACHE_STATE, 1]
+    assert status(c) == pkg.MOE_ERR_CACHE_STATE
+    for s in (0, 2):
+        for i in range(3):
+            (a, x), (d, y) = divmod(b.length[s] + path[s][i], page), divmod(b.length[s] + i, page)
+            b.pool[:, :, b.table[s][d], :, y] = b.pool[:, :, b.table[s][a], :, x]
+    b.truncate([b.length[0] + 3, -1, b.length[2] + 3])
+    assert_books(c, b)
+    assert torch.equal(mem.cpu(), b.pool)
+    c.close()
+
+
 def test_commit_refuses_wrong_tensors():
     c, mem, b = make()
     path = i32([[0, 1]] * 5)
