@@ -604,8 +604,8 @@ int moe_mxfp4_cache_append_rotated(moe_mxfp4_cache* c, void* state_dev, int32_t 
  *   z <- z - frequency[s] * c - presence[s] * [c > 0]
  *   z <- z + the bias of v                               (of a token given twice, the last one counts)
  *   z <- -inf                                            where bit v of allowed[s, b] is 0
- * in fp32, z / r as the product with the rounded 1 / r.  Tokens outside [0, vocab) (padding) count nowhere.  Positions lengths[s] and behind are not
- * read, and left as they were in the output. */
+ * in fp32.  Tokens outside [0, vocab) (padding) count nowhere.  Positions lengths[s] and behind are not read, and left as
+ * they were in the output. */
 typedef struct {
     const void* logits_dev;               /* [streams, block, vocab], row_stride elements between positions */
     int64_t row_stride;                   /* 0 = vocab; at least vocab */
