@@ -539,7 +539,10 @@ typedef struct {
  *   MOE_ROTARY_LINEAR  f_i / factor
  *   MOE_ROTARY_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in base's place (rotary_dim > 2)
  *   MOE_ROTARY_PARTS   g f_i + (1 - g) f_i / factor, g = clamp((original f_i / 2 pi - low) / (high - low), 0, 1):
- *                      pairs that turn at least `high` times in the original length keep their frequency
+ *                      pairs that turn at least `high` times in the original length keep their frequency,
+ *                      those that turn at most `low` times have it divided, g is linear in the turns between them.
+ *                      (Other encodings let g run over the pairs' indices between two rounded bounds: their
+ *                      frequencies go to moe_mxfp4_rotary_from.)
  * moe_mxfp4_rotary_from does the same from a caller's own f_i in radians per position (n host doubles;
  * |f_i| <= 2 pi).  MOE_ERR_INVALID_ARG for a NULL pointer, an odd or negative size, base or factor not
  * positive and finite, original not positive, high <= low (PARTS), or a frequency that is not finite or

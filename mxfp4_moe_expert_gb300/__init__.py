@@ -682,7 +682,7 @@ class Rotary:
 
     rotary_dim: elements of a head that turn (default: all); frequencies from `base` and `scaling` (None, or a dict of
     kind = "linear", "ntk" or "parts", factor, and for "parts" original, low, high), or given: rotary_dim / 2 radians per
-    position.  q_norm, k_norm: weights [head_dim] of `dtype` on the device (kept alive here); norm: whether heads are
+    position ("parts" ramps over the turns in the original length; a ramp over the pairs' indices is given this way).  q_norm, k_norm: weights [head_dim] of `dtype` on the device (kept alive here); norm: whether heads are
     normed (default: where there is a weight; a weight that is missing then is 1).
     """
 

@@ -259,12 +259,12 @@ __device__ __forceinline__ bool bit_at(const uint32_t* words, int v) { return wo
 // longest lists, so their CTAs come first.
 //
 // Bound by HBM where rows are written: 32 x 8 positions of 151936 fp32 logits (311 MB read and written) in 56 us,
-// 5.6 TB/s, 0.83 of the copy rate.  By instructions, half of them the masks', where 16-bit logits under a grammar are
-// compared: 48 x 11 positions of 151936 in bf16 (171 MB) in 54 us, 3.2 TB/s, where 32 x 8 in fp32 without one take
-// 34 us, 4.6 TB/s.  By its start (the look-ups, the history) where a CTA has one position: 96 x 1 of 32000 in 14 us.
-// Measured on those trees: a CTA's tokens dealt out to all of its warps for every position, each looking for its own,
-// 86 us where this took 74; counters of all tokens cleared and looked through 94; 128 and 512 threads 66 and 62 where
-// 256 took 58.  Rows prefetched to L2 during the start: edits 58 -> 56, acceptance 58 -> 61 (left out there).
+// 5.6 TB/s, 0.83 of the copy rate; in 16 bits 30 us, 0.77.  By instructions, half of them the masks', where 16-bit logits under a
+// grammar are compared: 48 x 11 positions of 151936 in bf16 (171 MB) in 55 us, 3.1 TB/s, where 32 x 8 in fp32 without one take
+// 34 us, 4.5 TB/s.  By its start (the look-ups, the history) where a CTA has one position, 96 x 1 of 32000 in 14 us, and behind
+// a long history, which every CTA of the stream reads: 1 x 8 of 151936 behind 4000, 32768 and 131072 tokens in 10, 33 and 78 us,
+// 32 x 8 in 60, 99 and 189.  128 and 512 threads took 66 and 62 us for those trees where 256 took 58.  Rows prefetched to L2 during the
+// start: edits 58 -> 56, acceptance 58 -> 61 (left out there).
 template <int kType, bool kShift, bool kAccept>
 __global__ void __launch_bounds__(kEditThreads, kAccept ? 4 : 3) edit_kernel(EditView e) {
     using B = Bits<kType>;
@@ -587,7 +587,9 @@ void group_rows(moe::EditView* e) {
     e->rows = (int)(most < 1 ? 1 : most > moe::kMostRows ? moe::kMostRows : most);
     if (e->rows > e->a.block) e->rows = e->a.block;
     e->groups = (e->a.block + e->rows - 1) / e->rows;
-    // parts of a run: the fewest that leave the CTA's last round of warps less than an eighth of the work short
+    // parts of a run: the fewest that keep five eighths of the warps of all its rounds busy, up to kParts.  (Six and seven
+    // eighths make more parts, each with a start and a reduction of its own.  Acceptance of 16 x 5 positions of 151936 in bf16 17 us, 22 with
+    // either; of 16 x 9 and 16 x 10 28 and 27, 28 and 30 with six eighths, 34 and 35 with seven.  Edits differ by 3 % either way.)
     constexpr int warps = moe::kEditThreads / 32;
     for (e->parts = 1; e->parts < moe::kParts; e->parts *= 2) {
         const int items = e->rows * e->parts, rounds = (items + warps - 1) / warps;

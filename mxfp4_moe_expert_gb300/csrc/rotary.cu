@@ -110,14 +110,16 @@ enum : int {
 
 // A lane has 16 elements of a head in two words, D / 16 lanes a head, so a warp has 4 heads of 128 or 8 of 64 at a time.  The
 // words are chosen so that they hold both sides of the lane's 8 pairs, with neighbours' words side by side in memory (with both words
-// of a lane side by side, each touched half of every 32-byte sector: 92 us for what takes 77).  Each lane takes the sine and
-// cosine of one or two of the token's pairs, and the others from its neighbours; they stay in registers for the
-// token's heads.  kAnywhere: the lanes exchange the normed elements through shared memory, laid out so that neither side has
-// conflicts.  A warp takes `steps` rounds of a token's heads.  Every lane copies its own words some rounds ahead into its
-// own places of shared memory, across tokens, so memory is kept busy without registers and without barriers.
-// Bound by HBM: 16381 tokens of 56 + 8 heads of 128 (537 MB read and written) in 86 us, 6.3 TB/s, 0.92 of the copy rate;
-// 47976 tokens of 32 + 4 heads of 64 in 67 us, 0.97; 2 layers of those into the cache with their values in 154 us, 0.94.  Of few
-// tokens by the launch and the chain of look-ups: 8 tokens of one layer in 2.6 us, 3.2 into the cache.
+// of a lane side by side each load touched half of every 32-byte sector: narrow heads took 92 us where this took 77, both before
+// the steps that followed).  The lanes that share a token's 8 pairs each take the sine and cosine of some of them, two (heads of 64:
+// one) where the warp has one token and up to eight (four) where it has kPack of them, and the others from their neighbours; they stay in
+// registers for the token's heads.  kAnywhere: a warp takes a token's sines and cosines through shared memory, and the lanes
+// exchange the normed elements there, laid out so that neither side has conflicts.  A warp takes `steps` rounds of a token's heads.
+// Every lane copies its own words three rounds ahead (kAnywhere: two) into its own places of shared memory, across tokens, so
+// memory is kept busy without registers and without barriers.
+// Bound by HBM: 16381 tokens of 56 + 8 heads of 128 (537 MB read and written) in 86 us, 6.2 TB/s, 0.92 of the copy rate;
+// 47976 tokens of 32 + 4 heads of 64 in 67 us, 0.97; 2 layers of those into the cache with their values in 156 us, 0.93.  Of few
+// tokens by the launch and the chain of look-ups: 8 tokens of one layer in 2.5 us, 3.1 into the cache.
 // Few heads: a round has the heads of kPack tokens, and a token's sines and cosines are shared by its lanes alone (two heads of
 // 128, 300000 tokens: 96 us, 154 with a token a round; 46 are the bytes').
 template <int D, bool kBf16, int kLayout, bool kCache, int kPack>
@@ -349,9 +351,13 @@ cudaError_t launch_rotate(const moe::RotaryView& r, const moe::HeadRows& q, cons
     // both do as well two do better, whose loads and stores come in longer runs of memory (47976 tokens of 36 narrow heads: 67 us
     // with two, 76 with three); three serve where two leave warps idle (2560 tokens of 48 heads: 127 us for 8 layers, 140 with
     // two), and where a token has a round or two, and warps wait for its look-ups (two heads: 154 us, 195 with two).
+    // Where two CTAs an SM have a warp for every round, that is the least, and is taken without a search: which finds the same up
+    // to 64 rounds a token, and goes no further (8 tokens of 640 heads: 2.8 us, 3.6 in 64 parts; of 2100 heads of one token: 2.6
+    // and 6.5).  Beyond, parts win over rounds of their own (200, 304 and 600 tokens of 64 heads: 3.6, 3.7 and 5.0 us, 4.0,
+    // 4.5 and 7.3 with a round each).
     const int rounds = (heads * (D / 16) + 31) / 32;
     int parts = rounds, steps = 1, resident = 2;
-    if (rounds <= 2 || (int64_t)tokens * rounds > 16 * (int64_t)sms) {   // (else a round for each warp, and no more)
+    if (rounds <= 2 || (int64_t)tokens * rounds > 2 * 8 * (int64_t)sms) {
         int64_t least = INT64_MAX;
         for (int ctas = rounds <= 2 && layout != moe::kAnywhere ? 3 : 2; ctas <= (layout == moe::kAnywhere ? 2 : 3); ++ctas)
             for (int n = 1; n <= rounds && n <= 64; ++n) {
